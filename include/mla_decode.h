@@ -199,6 +199,112 @@ int mla_decode_run_static_ws(const void* plan_dev, const void* plan_host, size_t
  */
 int mla_device_pair_slots(int device, int* slots);
 
+/*
+ * ---- Block-scaled e4m3 caches ----
+ *
+ * An e4m3 cache may carry an fp32 scale for each block of block_tokens consecutive tokens of
+ * a page instead of one per tensor: kv_scales [num_pages, 64 / block_tokens], block_tokens 1,
+ * 2, 4, .. 64, and code c of a row of that block stands for c * scale. Scales are finite and
+ * >= 0 (0 stands for a block of zeros); between 2^-60 and 2^60 they may lie any distance apart.
+ *
+ * mla_cache_append -- write new latent rows into such a cache.
+ *
+ *   rows          [total_rows, 576] bf16, requests concatenated
+ *   cu_new        device int32 [batch + 1]: request b's rows are cu_new[b] .. cu_new[b + 1] - 1
+ *                 (none is allowed)
+ *   seq_lens      device int32 [batch]: the length of each request with its new rows, which
+ *                 are its last ones
+ *   max_new       host: at least the largest number of new rows of a request
+ *   kv_cache, kv_scales   the cache, written in place
+ *
+ * A block whose first token is new gets the least power of two 2^e, -60 <= e <= 60, with
+ * amax <= 448 * 2^e over the finite entries of its new rows. A block that already holds older
+ * tokens gets the larger of that and its present scale; where that is larger its old codes are
+ * rounded to it. Codes are round-to-nearest-even of x / scale; infinities and larger values
+ * become +-448, NaN stays NaN. Rows behind a request's last token are left as they are.
+ * No two requests of a call may write one page.
+ *
+ * Requests whose lengths do not fit (more than max_new rows, more rows than tokens, more
+ * pages than page_table_stride, cu_new outside rows) write nothing and report
+ * MLA_DEVICE_PLAN_MISMATCH; pages outside [0, num_pages) are skipped and reported as
+ * MLA_DEVICE_BAD_PAGE. Enqueue only, as mla_decode_run.
+ */
+int mla_cache_append(const void* rows, int total_rows, const int32_t* cu_new, const int32_t* seq_lens, int batch,
+                     int max_new, void* kv_cache, float* kv_scales, int block_tokens, const int32_t* page_table,
+                     int page_table_stride, int num_pages, int32_t* status_dev, void* stream);
+
+/*
+ * mla_decode_run_scaled -- mla_decode_run over a block-scaled e4m3 cache: the same plan (of
+ * kv_dtype MLA_KV_FP8_E4M3), buffers and results, with kv_scales and block_tokens in the
+ * place of kv_scale.
+ */
+int mla_decode_run_scaled(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
+                          const void* kv_cache, const float* kv_scales, int block_tokens, const int32_t* page_table,
+                          int page_table_stride, int num_pages, const int32_t* seq_lens, const int32_t* q_lens,
+                          float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                          int32_t* status_dev, void* stream);
+
+/*
+ * mla_key_weights -- add the attention weight that each cached key received from a verify
+ * call to a running sum, what mla_cache_evict goes by:
+ *
+ *   weights[b, j] = decay * weights[b, j]
+ *                   + sum over verify tokens i < counted[b] and heads h with j visible to i
+ *                     of exp(s_ijh - lse[b, i, h])           for j < seq_lens[b]
+ *
+ * with the scores s of mla_decode_run and lse as it wrote it.
+ *
+ *   plan_dev, plan_host   the decode's plan
+ *   kv_scales     NULL, or the scales of a block-scaled e4m3 cache (kv_scale is then ignored)
+ *   counted       device int32 [batch], the verify tokens that count (the accepted ones), or
+ *                 NULL for all; values are cut to [0, q_len]
+ *   decay         finite; with 0 the old sums are not read
+ *   weights       fp32 [batch, weights_stride], weights_stride >= the longest request; entries
+ *                 at and behind seq_lens[b] are left as they are
+ *   workspace     mla_key_weights_workspace bytes (0 for a bf16 plan), 256-byte aligned; calls
+ *                 that may overlap need one each
+ *
+ * Sums are taken in fp32 in a fixed order: equal inputs give equal bits. A row whose lse is
+ * -inf adds nothing. Enqueue only, as mla_decode_run.
+ */
+int mla_key_weights(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
+                    const void* kv_cache, const float* kv_scales, int block_tokens, const int32_t* page_table,
+                    int page_table_stride, int num_pages, const float* lse, const int32_t* counted, float sm_scale,
+                    float kv_scale, float decay, float* weights, long long weights_stride, void* workspace,
+                    size_t workspace_bytes, int32_t* status_dev, void* stream);
+int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* workspace_bytes_out);
+
+/*
+ * mla_cache_evict -- shorten each request to at most `budget` keys and move them, in order,
+ * to new pages. A request of n <= budget keys keeps all. A longer one keeps its first n_first,
+ * its last n_last and, of the others, the budget - n_first - n_last with the largest weights
+ * (ties: the lower index; -0 equals 0; NaN counts as the lowest).
+ *
+ *   weights       fp32 [batch, weights_stride]
+ *   seq_lens      device int32 [batch]; a length outside [0, max_seq] reports
+ *                 MLA_DEVICE_PLAN_MISMATCH and keeps nothing
+ *   max_seq       host: at least the longest length (sizes the launch)
+ *   kv_dtype, kv_cache, kv_scales, page_table, num_pages   the cache; kv_scales NULL for a
+ *                 bf16 cache or an e4m3 cache with one scale
+ *   ..._dst       the cache that receives the rows, its scales and page table. It may be the
+ *                 same cache; its pages named by page_table_dst must not be pages that the
+ *                 call reads, nor be named twice
+ *   kept          int32 [batch, budget]: the kept indices in order, then -1
+ *   seq_lens_dst  int32 [batch]: the new lengths
+ *   weights_dst   NULL, or fp32 [batch, weights_dst_stride]: the kept keys' weights in order
+ *
+ * A new block's scale is the largest among its rows' old ones; codes of a row from a block
+ * with another scale are multiplied by old / new and rounded. Rows of the new pages behind the
+ * new length are left as they are. Pages out of range are skipped and reported as
+ * MLA_DEVICE_BAD_PAGE. Enqueue only, as mla_decode_run; weights_dst must not overlap weights.
+ */
+int mla_cache_evict(const float* weights, long long weights_stride, const int32_t* seq_lens, int batch, int max_seq,
+                    int budget, int n_first, int n_last, int kv_dtype, const void* kv_cache, const float* kv_scales,
+                    int block_tokens, const int32_t* page_table, int page_table_stride, int num_pages,
+                    void* kv_cache_dst, float* kv_scales_dst, const int32_t* page_table_dst,
+                    int page_table_dst_stride, int num_pages_dst, int32_t* kept, int32_t* seq_lens_dst,
+                    float* weights_dst, long long weights_dst_stride, int32_t* status_dev, void* stream);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* mla_last_error(void);
 

@@ -58,6 +58,19 @@ SIGNATURES = {
                                       ctypes.c_float, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "mla_decode_run_static_ws": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P, _P, _P, ctypes.c_int, ctypes.c_int, _P,
                                                  _P, ctypes.c_float, ctypes.c_float, _P, _P, _P, _P]),
+    "mla_decode_run_scaled": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P, _P, _P, ctypes.c_int, _P, ctypes.c_int,
+                                              ctypes.c_int, _P, _P, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P,
+                                              _P]),
+    "mla_cache_append": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, ctypes.c_int, ctypes.c_int, _P, _P, ctypes.c_int, _P,
+                                        ctypes.c_int, ctypes.c_int, _P, _P]),
+    "mla_key_weights": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P, _P, _P, ctypes.c_int, _P, ctypes.c_int,
+                                       ctypes.c_int, _P, _P, ctypes.c_float, ctypes.c_float, ctypes.c_float, _P,
+                                       ctypes.c_longlong, _P, ctypes.c_size_t, _P, _P]),
+    "mla_key_weights_workspace": (ctypes.c_int, [_P, ctypes.c_size_t, _SZP]),
+    "mla_cache_evict": (ctypes.c_int, [_P, ctypes.c_longlong, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                       ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, ctypes.c_int, _P,
+                                       ctypes.c_int, ctypes.c_int, _P, _P, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P,
+                                       ctypes.c_longlong, _P, _P]),
     "mla_device_pair_slots": (ctypes.c_int, [ctypes.c_int, _IP]),
     "mla_last_error": (ctypes.c_char_p, []),
     "mla_version": (ctypes.c_int, []),
@@ -170,6 +183,51 @@ def run_static_ws(plan_dev_ptr: int, plan_host: np.ndarray, q_ptr: int, kv_ptr: 
                                       q_lens_ptr, float(sm_scale), float(kv_scale), out_ptr, lse_ptr, status_ptr,
                                       stream_handle)
     check(rc, lib)
+
+
+def run_scaled(plan_dev_ptr: int, plan_host: np.ndarray, q_ptr: int, kv_ptr: int, scales_ptr: int, block_tokens: int,
+               page_table_ptr: int, page_table_stride: int, num_pages: int, seq_lens_ptr: int, q_lens_ptr: int,
+               sm_scale: float, out_ptr: int, lse_ptr: int | None, workspace_ptr: int | None, workspace_bytes: int,
+               status_ptr: int | None, stream_handle: int) -> None:
+    """mla_decode_run_scaled: the decode over an e4m3 cache with a scale for each block of tokens."""
+    lib = load()
+    check(lib.mla_decode_run_scaled(plan_dev_ptr, plan_host.ctypes.data_as(_P), plan_host.nbytes, q_ptr, kv_ptr,
+                                    scales_ptr, block_tokens, page_table_ptr, page_table_stride, num_pages,
+                                    seq_lens_ptr, q_lens_ptr, sm_scale, out_ptr, lse_ptr, workspace_ptr,
+                                    workspace_bytes, status_ptr, stream_handle), lib)
+
+
+def key_weights_workspace(plan_host: np.ndarray) -> int:
+    """mla_key_weights_workspace: device scratch bytes that mla_key_weights needs with this plan."""
+    lib = load()
+    n = ctypes.c_size_t(0)
+    check(lib.mla_key_weights_workspace(plan_host.ctypes.data_as(_P), plan_host.nbytes, ctypes.byref(n)), lib)
+    return int(n.value)
+
+
+def key_weights(plan_dev_ptr: int, plan_host: np.ndarray, q_ptr: int, kv_ptr: int, scales_ptr: int | None,
+                block_tokens: int, page_table_ptr: int, page_table_stride: int, num_pages: int, lse_ptr: int,
+                counted_ptr: int | None, sm_scale: float, kv_scale: float, decay: float, weights_ptr: int,
+                weights_stride: int, workspace_ptr: int | None, workspace_bytes: int, status_ptr: int | None,
+                stream_handle: int) -> None:
+    """mla_key_weights: accumulate the attention weight of every cached key."""
+    lib = load()
+    check(lib.mla_key_weights(plan_dev_ptr, plan_host.ctypes.data_as(_P), plan_host.nbytes, q_ptr, kv_ptr, scales_ptr,
+                              block_tokens, page_table_ptr, page_table_stride, num_pages, lse_ptr, counted_ptr,
+                              sm_scale, kv_scale, decay, weights_ptr, weights_stride, workspace_ptr, workspace_bytes,
+                              status_ptr, stream_handle), lib)
+
+
+def cache_append(*args) -> None:
+    """mla_cache_append, arguments as in the header (device pointers as ints)."""
+    lib = load()
+    check(lib.mla_cache_append(*args), lib)
+
+
+def cache_evict(*args) -> None:
+    """mla_cache_evict, arguments as in the header (device pointers as ints)."""
+    lib = load()
+    check(lib.mla_cache_evict(*args), lib)
 
 
 def declared_functions(header: str | None = None) -> list[str]:

@@ -1,0 +1,610 @@
+// cache_sm103.cu -- the paged latent cache's own operators: mla_cache_append writes new rows
+// into an e4m3 cache with a scale for each block of tokens, mla_cache_evict keeps the keys
+// with the largest accumulated attention weight and moves them to new pages.
+//
+// Block scales. A block is block_tokens consecutive tokens of a page (1, 2, 4, .. 64); the
+// value of a stored code c is c * scale(block). An append gives a block the least power of
+// two 2^e, e in [-60, 60], with amax <= 448 * 2^e (448 is the largest e4m3 value), so that
+// x / scale and a later change of scale are exact but for e4m3's own rounding. A block that
+// already holds earlier tokens keeps the larger of its old and the new scale, and where that
+// grows its old codes are rounded to the new one.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "mla_decode.h"
+#include "plan_format.h"
+#include "ptx.cuh"
+#include "status.h"
+
+namespace mla {
+
+int current_device_ready(int* dev);   // defined next to the decode kernel
+int block_log2_of(int block_tokens);  // defined with the plan
+
+namespace {
+
+constexpr int kThreads = 256;  // append and gather: one page of 64 rows per CTA
+constexpr int kScaleExpMin = -60, kScaleExpMax = 60;
+
+__device__ __forceinline__ void report(int32_t* status, int bits) {
+  if (status) atomicOr(status, bits);
+}
+
+// The least 2^e, e in [-60, 60], with amax <= 448 * 2^e, from amax's bits: 448 = 1.75 * 2^8, so
+// e is amax's own exponent - 8, one more if its mantissa is above 1.75.
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = max(kScaleExpMin, min(kScaleExpMax, e));
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Four e4m3 codes times `ratio`, rounded to e4m3 again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
+  float f[4];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> (16 * k)), __NV_E4M3);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    f[2 * k] = v.x * ratio;
+    f[2 * k + 1] = v.y * ratio;
+  }
+  return e4m3x4(f[0], f[1], f[2], f[3]);
+}
+
+// ------------------------------------------------------------------ append
+struct AppendArgs {
+  const uint4* rows;  // [total, 576] bf16 as 72 16-byte pieces a row
+  int total;
+  const int32_t* page_table;
+  int pt_stride, num_pages, max_new, block_log2;
+  const int32_t* ends;
+  const int32_t* cu;
+  uint8_t* codes;
+  float* scales;
+  int32_t* status;
+};
+
+// One CTA per page that a request's new rows reach (blockIdx = page within those, request).
+// Eight lanes hold a row (nine 16-byte pieces each, 128 contiguous bytes of a row per load),
+// a warp four rows, so the page's rows are read once, all loads in flight together, and stay
+// in registers between the maximum and the rounding.
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+  __shared__ float row_max[kPage], scale[kPage], ratio[kPage], half_max[2];
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r0 = a.cu[b], n = a.cu[b + 1] - r0, end = a.ends[b];
+  if (n == 0) return;
+  if (r0 < 0 || n < 0 || n > a.max_new || r0 > a.total - n || end < n || (end - 1) / kPage >= a.pt_stride) {
+    if (tid == 0 && blockIdx.x == 0) report(a.status, MLA_DEVICE_PLAN_MISMATCH);
+    return;
+  }
+  const int start = end - n;
+  const int pg = start / kPage + blockIdx.x;
+  if ((long long)pg * kPage >= end) return;
+  const int page = a.page_table[(size_t)b * a.pt_stride + pg];
+  if (page < 0 || page >= a.num_pages) {
+    if (tid == 0) report(a.status, MLA_DEVICE_BAD_PAGE);
+    return;
+  }
+  const int lo = max(start - pg * kPage, 0), hi = min(end - pg * kPage, kPage);  // new rows of the page
+  const int spb_log2 = 6 - a.block_log2;
+  float* page_scales = a.scales + ((size_t)page << spb_log2);
+  // a block whose first row is older than the new ones keeps what it holds
+  const int blk = tid >> a.block_log2, blk_row0 = blk << a.block_log2;
+  float s_old = 0.f;
+  if (tid < kPage && blk_row0 < lo) s_old = page_scales[blk];
+
+  const int sub = lane & 7, row_in = warp * 4 + (lane >> 3);
+  uint4 v[2][9];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 32 * h + row_in;
+    const bool live = r >= lo && r < hi;
+    const uint4* src = a.rows + (size_t)(live ? r0 + (pg * kPage + r - start) : 0) * 72 + sub;
+#pragma unroll
+    for (int j = 0; j < 9; ++j) v[h][j] = live ? __ldcs(src + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    // the largest magnitude from the bits (bf16 magnitudes order as integers); infinities
+    // and NaN are left out, in a second pass that only rows which hold some take
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 9; ++j) {
+      m = __vmaxu2(m, __vmaxu2(v[h][j].x & 0x7FFF7FFFu, v[h][j].y & 0x7FFF7FFFu));
+      m = __vmaxu2(m, __vmaxu2(v[h][j].z & 0x7FFF7FFFu, v[h][j].w & 0x7FFF7FFFu));
+    }
+    uint32_t top = max(m & 0xFFFFu, m >> 16);
+    if (top >= 0x7F80u) {
+      top = 0;
+#pragma unroll
+      for (int j = 0; j < 9; ++j) {
+        const uint32_t w[4] = {v[h][j].x, v[h][j].y, v[h][j].z, v[h][j].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = w[k] & 0x7FFFu, y = (w[k] >> 16) & 0x7FFFu;
+          if (x < 0x7F80u) top = max(top, x);
+          if (y < 0x7F80u) top = max(top, y);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (sub == 0) row_max[32 * h + row_in] = __uint_as_float(top << 16);
+  }
+  __syncthreads();
+  float m = 0.f;
+  if (tid < kPage) {
+    m = row_max[tid];
+    for (int o = 1; o < min(1 << a.block_log2, 32); o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) half_max[warp] = m;
+  }
+  __syncthreads();
+  if (tid < kPage) {
+    if (a.block_log2 == 6) m = fmaxf(half_max[0], half_max[1]);
+    const float s = fmaxf(scale_for(m), s_old);
+    scale[tid] = s;
+    ratio[tid] = s_old / s;
+    // the block's first row writes its scale, if the block has new rows at all
+    if (tid == blk_row0 && blk_row0 < hi && blk_row0 + (1 << a.block_log2) > lo) page_scales[blk] = s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = 32 * h + row_in;
+    uint2* dst = reinterpret_cast<uint2*>(a.codes + ((size_t)page * kPage + r) * kDqk) + sub;
+    if (r >= lo && r < hi) {
+      const float s = scale[r];
+      // a power of two divides exactly through its reciprocal; a block that kept another
+      // writer's scale divides
+      const bool two = (__float_as_uint(s) & 0x7FFFFFu) == 0 && s >= 0x1p-120f && s <= 0x1p120f;
+      const float inv = two ? 1.f / s : 0.f;
+#pragma unroll
+      for (int j = 0; j < 9; ++j) {
+        const uint32_t w[4] = {v[h][j].x, v[h][j].y, v[h][j].z, v[h][j].w};
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[2 * k] = __uint_as_float(w[k] << 16);
+          f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+        if (two) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] *= inv;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = __fdiv_rn(f[k], s);
+        }
+        dst[8 * j] = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+      }
+    } else if (r < lo && (r >> a.block_log2) == (lo >> a.block_log2) && ratio[r] != 1.f) {
+      const float q = ratio[r];
+#pragma unroll
+      for (int j = 0; j < 9; ++j) {
+        const uint2 c = dst[8 * j];
+        dst[8 * j] = make_uint2(rescale4(c.x, q), rescale4(c.y, q));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ eviction: which keys stay
+struct SelectArgs {
+  const float* weights;
+  long long w_stride;
+  const int32_t* lens;
+  int max_seq, budget, n_first, n_last;
+  int32_t* kept;
+  float* weights_dst;
+  long long wd_stride;
+  int32_t* lens_dst;
+  int32_t* status;
+};
+
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kSelBatch = 8;  // weights a lane reads per round trip
+
+// A weight as an unsigned key of the same order; -0 counts as 0, NaN as the lowest.
+__device__ __forceinline__ uint32_t order_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// One cluster of CTAs per request (blockIdx.y). The k-th largest key of the middle is found
+// from its bits, 11, 11 and 10 at a time: every CTA counts its keys by the next bits among
+// those that match the bits found so far, the cluster adds the counts (each CTA reads its
+// peers' through distributed shared memory), and each finds the same bin. Then the kept keys
+// are numbered in order: those above the threshold, and of those equal to it the first ones.
+// Warp g of the cluster owns a contiguous piece of the keys in every pass.
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ uint32_t hist[3][kBins];
+  __shared__ uint32_t warp_sum[kSelWarps], found[2];
+  __shared__ uint32_t gt_of[kSelWarps], eq_of[kSelWarps], totals[2];
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int n = a.lens[b];
+  const float* w = a.weights + (size_t)b * a.w_stride;
+  int32_t* kept = a.kept + (size_t)b * a.budget;
+  float* wd = a.weights_dst ? a.weights_dst + (size_t)b * a.wd_stride : nullptr;
+  const int gtid = rank * kSelThreads + tid, gthreads = ctas * kSelThreads;
+  const bool bad = n < 0 || n > a.max_seq;
+  const int out = bad ? 0 : min(n, a.budget);
+  if (gtid == 0) {
+    a.lens_dst[b] = out;
+    if (bad) report(a.status, MLA_DEVICE_PLAN_MISMATCH);
+  }
+  if (out < a.budget || n == a.budget) {  // everything stays (the whole cluster leaves here)
+    for (int r = gtid; r < a.budget; r += gthreads) {
+      kept[r] = r < out ? r : -1;
+      if (wd && r < out) wd[r] = w[r];
+    }
+    return;
+  }
+  const int lo = a.n_first, m = n - a.n_first - a.n_last, k = a.budget - a.n_first - a.n_last;
+  for (int r = gtid; r < a.n_first; r += gthreads) {
+    kept[r] = r;
+    if (wd) wd[r] = w[r];
+  }
+  for (int r = gtid; r < a.n_last; r += gthreads) {
+    kept[a.budget - a.n_last + r] = n - a.n_last + r;
+    if (wd) wd[a.budget - a.n_last + r] = w[n - a.n_last + r];
+  }
+  if (k == 0) return;  // the whole cluster again
+  const int per = ((m + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) / 32 * 32;
+  const long long p0 = (long long)(rank * kSelWarps + warp) * per;
+  const int i0 = (int)min((long long)m, p0), i1 = (int)min((long long)m, p0 + per);  // this warp's keys
+  const float* wm = w + lo;
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0u;
+  __syncthreads();
+
+  uint32_t prefix = 0, want = (uint32_t)k;  // bits found so far; rank within the keys that match them
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int above = pass == 0 ? 32 : pass == 1 ? 21 : 10;  // the bits above these are found
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    for (int i = i0 + lane; i < i1; i += 32 * kSelBatch) {
+      float x[kSelBatch];
+#pragma unroll
+      for (int u = 0; u < kSelBatch; ++u) x[u] = i + 32 * u < i1 ? wm[i + 32 * u] : 0.f;
+#pragma unroll
+      for (int u = 0; u < kSelBatch; ++u) {
+        const uint32_t key = order_key(x[u]);
+        if (i + 32 * u < i1 && (pass == 0 || (key >> (above & 31)) == prefix)) atomicAdd(&hist[pass][(key >> shift) & mask], 1u);
+      }
+    }
+    cluster.sync();
+    // bins from the top, two per thread
+    const int hb = kBins - 1 - 2 * tid;
+    uint32_t c0 = 0, c1 = 0;
+    for (int r = 0; r < ctas; ++r) {
+      const uint32_t* h = cluster.map_shared_rank(&hist[pass][0], r);
+      const uint2 c = *reinterpret_cast<const uint2*>(h + hb - 1);
+      c0 += c.y;
+      c1 += c.x;
+    }
+    uint32_t incl = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t s = warp_sum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
+      }
+      warp_sum[lane] = s;
+    }
+    __syncthreads();
+    const uint32_t before = (warp ? warp_sum[warp - 1] : 0u) + incl - c0 - c1;
+    if (before < want && before + c0 >= want) {
+      found[0] = (uint32_t)hb;
+      found[1] = want - before;
+    } else if (before + c0 < want && before + c0 + c1 >= want) {
+      found[0] = (uint32_t)(hb - 1);
+      found[1] = want - before - c0;
+    }
+    __syncthreads();
+    prefix = pass == 0 ? found[0] : (prefix << (pass == 1 ? 11 : 10)) | found[0];
+    want = found[1];
+    __syncthreads();
+  }
+  // prefix is the threshold's key; `want` of the keys equal to it stay
+  uint32_t gt = 0, eq = 0;
+  for (int i = i0 + lane; i < i1; i += 32 * kSelBatch) {
+    float x[kSelBatch];
+#pragma unroll
+    for (int u = 0; u < kSelBatch; ++u) x[u] = i + 32 * u < i1 ? wm[i + 32 * u] : 0.f;
+#pragma unroll
+    for (int u = 0; u < kSelBatch; ++u) {
+      const uint32_t key = order_key(x[u]);
+      gt += i + 32 * u < i1 && key > prefix;
+      eq += i + 32 * u < i1 && key == prefix;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    gt += __shfl_xor_sync(0xffffffffu, gt, o);
+    eq += __shfl_xor_sync(0xffffffffu, eq, o);
+  }
+  if (lane == 0) {
+    gt_of[warp] = gt;
+    eq_of[warp] = eq;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t g = 0, e = 0;
+    for (int i = 0; i < kSelWarps; ++i) {
+      const uint32_t gi = gt_of[i], ei = eq_of[i];
+      gt_of[i] = g;
+      eq_of[i] = e;
+      g += gi;
+      e += ei;
+    }
+    totals[0] = g;
+    totals[1] = e;
+  }
+  cluster.sync();
+  gt = gt_of[warp];
+  eq = eq_of[warp];
+  for (int r = 0; r < rank; ++r) {
+    const uint32_t* t = cluster.map_shared_rank(&totals[0], r);
+    gt += t[0];
+    eq += t[1];
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = i0; i < i1; i += 32 * kSelBatch) {
+    float x[kSelBatch];
+#pragma unroll
+    for (int u = 0; u < kSelBatch; ++u) x[u] = i + 32 * u + lane < i1 ? wm[i + 32 * u + lane] : 0.f;
+#pragma unroll
+    for (int u = 0; u < kSelBatch; ++u) {
+      const int j = i + 32 * u + lane;
+      const uint32_t key = order_key(x[u]);
+      const uint32_t bg = __ballot_sync(0xffffffffu, j < i1 && key > prefix);
+      const uint32_t be = __ballot_sync(0xffffffffu, j < i1 && key == prefix);
+      const uint32_t e = eq + __popc(be & below);
+      if (((bg >> lane) & 1u) || (((be >> lane) & 1u) && e < want)) {
+        const uint32_t pos = (uint32_t)a.n_first + gt + __popc(bg & below) + min(e, want);
+        kept[pos] = lo + j;
+        if (wd) wd[pos] = x[u];
+      }
+      gt += __popc(bg);
+      eq += __popc(be);
+    }
+  }
+  cluster.sync();  // no CTA leaves while a peer may still read its counts
+}
+
+// ------------------------------------------------------------------ eviction: moving the rows
+struct GatherArgs {
+  const int32_t* kept;
+  const int32_t* lens_dst;
+  int budget, max_seq;
+  const uint4* src;
+  uint4* dst;
+  const float* scales_src;
+  float* scales_dst;
+  int block_log2;
+  const int32_t* pt_src;
+  const int32_t* pt_dst;
+  int pt_src_stride, pt_dst_stride, pages_src, pages_dst;
+  int32_t* status;
+};
+
+// One CTA per new page. P = 16-byte pieces of a row (72: bf16, 36: e4m3), held by P / 9 lanes
+// with nine pieces each; the page's rows are loaded before any is stored. For a block-scaled
+// cache the new block takes the largest scale of its rows and codes from a block with a
+// smaller one are rounded to it.
+template <int P, bool kScaled>
+__global__ void __launch_bounds__(kThreads) evict_gather_kernel(GatherArgs a) {
+  constexpr int kLanes = P / 9;                        // 8 or 4 lanes to a row
+  constexpr int kPasses = kPage * kLanes / kThreads;   // 2 or 1
+  __shared__ long long src_row[kPage];
+  __shared__ float scale[kPage], ratio[kPage], half_max[2];
+  ptx::pdl_wait_primary();
+  const int b = blockIdx.y, pg = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = a.lens_dst[b];
+  const int rows = min(kPage, n - pg * kPage);
+  if (rows <= 0) return;
+  const int page = a.pt_dst[(size_t)b * a.pt_dst_stride + pg];
+  if (page < 0 || page >= a.pages_dst) {
+    if (tid == 0) report(a.status, MLA_DEVICE_BAD_PAGE);
+    return;
+  }
+  float s = 0.f;
+  if (tid < kPage) {
+    long long row = -1;
+    if (tid < rows) {
+      const int j = a.kept[(size_t)b * a.budget + pg * kPage + tid];
+      const int p = a.pt_src[(size_t)b * a.pt_src_stride + j / kPage];
+      if (p >= 0 && p < a.pages_src) {
+        row = (long long)p * kPage + j % kPage;
+        if (kScaled) s = a.scales_src[row >> a.block_log2];
+      } else {
+        report(a.status, MLA_DEVICE_BAD_PAGE);
+      }
+    }
+    src_row[tid] = row;
+    if constexpr (kScaled) {
+      float m = s;
+      for (int o = 1; o < min(1 << a.block_log2, 32); o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      scale[tid] = m;
+      if (lane == 0) half_max[warp] = m;
+    }
+  }
+  __syncthreads();
+  const int sub = tid % kLanes, row_in = tid / kLanes;
+  uint4 v[kPasses][9];
+#pragma unroll
+  for (int h = 0; h < kPasses; ++h) {
+    const long long row = src_row[h * (kThreads / kLanes) + row_in];
+    const uint4* src = a.src + (row < 0 ? 0 : row) * P + sub;
+#pragma unroll
+    for (int j = 0; j < 9; ++j) v[h][j] = row < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldcs(src + kLanes * j);
+  }
+  if constexpr (kScaled) {
+    if (tid < kPage) {
+      const float m = a.block_log2 == 6 ? fmaxf(half_max[0], half_max[1]) : scale[tid];
+      ratio[tid] = m > 0.f ? s / m : 1.f;
+      const int blk = tid >> a.block_log2;
+      if (tid == blk << a.block_log2 && tid < rows) a.scales_dst[((size_t)page << (6 - a.block_log2)) + blk] = m;
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int h = 0; h < kPasses; ++h) {
+    const int r = h * (kThreads / kLanes) + row_in;
+    if (src_row[r] < 0) continue;
+    uint4* dst = a.dst + ((size_t)page * kPage + r) * P + sub;
+    if (kScaled && ratio[r] != 1.f) {
+      const float q = ratio[r];
+#pragma unroll
+      for (int j = 0; j < 9; ++j) {
+        const uint4 c = v[h][j];
+        v[h][j] = make_uint4(rescale4(c.x, q), rescale4(c.y, q), rescale4(c.z, q), rescale4(c.w, q));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 9; ++j) dst[kLanes * j] = v[h][j];
+  }
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_cache_append(const void* rows, int total_rows, const int32_t* cu_new, const int32_t* seq_lens,
+                                int batch, int max_new, void* kv_cache, float* kv_scales, int block_tokens,
+                                const int32_t* page_table, int page_table_stride, int num_pages, int32_t* status_dev,
+                                void* stream) {
+  clear_error();
+  if (batch < 1 || batch > 65535) return set_error(MLA_ERR_INVALID_ARG, "batch must be in [1, 65535] (got %d)", batch);
+  if (total_rows < 0 || max_new < 0 || max_new > total_rows)
+    return set_error(MLA_ERR_INVALID_ARG, "need 0 <= max_new <= total_rows (got %d and %d)", max_new, total_rows);
+  const int bl = block_log2_of(block_tokens);
+  if (bl < 0) return set_error(MLA_ERR_UNSUPPORTED, "block_tokens must be 1, 2, 4, .. 64 (got %d)", block_tokens);
+  if (num_pages < 1 || page_table_stride < 1)
+    return set_error(MLA_ERR_INVALID_ARG, "num_pages and page_table_stride must be >= 1 (got %d and %d)", num_pages,
+                     page_table_stride);
+  if (max_new == 0) return MLA_OK;
+  if (!rows || !cu_new || !seq_lens || !kv_cache || !kv_scales || !page_table)
+    return set_error(MLA_ERR_INVALID_ARG, "rows, cu_new, seq_lens, kv_cache, kv_scales and page_table must not be NULL");
+  if (!aligned16(rows) || !aligned16(kv_cache))
+    return set_error(MLA_ERR_INVALID_ARG, "rows and kv_cache must be 16-byte aligned");
+  if (!aligned4(cu_new) || !aligned4(seq_lens) || !aligned4(kv_scales) || !aligned4(page_table) || !aligned4(status_dev))
+    return set_error(MLA_ERR_INVALID_ARG, "cu_new, seq_lens, kv_scales, page_table and status_dev must be 4-byte aligned");
+  int dev = 0;
+  const int rc = current_device_ready(&dev);
+  if (rc != MLA_OK) return rc;
+  const AppendArgs a{(const uint4*)rows, total_rows, page_table, page_table_stride, num_pages, max_new, bl,
+                     seq_lens, cu_new, (uint8_t*)kv_cache, kv_scales, status_dev};
+  // max_new rows touch at most this many pages, wherever in a page they start
+  const unsigned pages = (unsigned)(((long long)max_new + kPage - 2) / kPage + 1);
+  append_kernel<<<dim3(pages, (unsigned)batch), kThreads, 0, (cudaStream_t)stream>>>(a);
+  const cudaError_t ce = cudaGetLastError();
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(ce));
+  return MLA_OK;
+}
+
+extern "C" int mla_cache_evict(const float* weights, long long weights_stride, const int32_t* seq_lens, int batch,
+                               int max_seq, int budget, int n_first, int n_last, int kv_dtype, const void* kv_cache,
+                               const float* kv_scales, int block_tokens, const int32_t* page_table,
+                               int page_table_stride, int num_pages, void* kv_cache_dst, float* kv_scales_dst,
+                               const int32_t* page_table_dst, int page_table_dst_stride, int num_pages_dst,
+                               int32_t* kept, int32_t* seq_lens_dst, float* weights_dst, long long weights_dst_stride,
+                               int32_t* status_dev, void* stream) {
+  clear_error();
+  if (batch < 1 || batch > 65535) return set_error(MLA_ERR_INVALID_ARG, "batch must be in [1, 65535] (got %d)", batch);
+  if (max_seq < 0 || max_seq > 1 << 30)
+    return set_error(MLA_ERR_INVALID_ARG, "max_seq must be in [0, 2^30] (got %d)", max_seq);
+  if (budget < 1 || n_first < 0 || n_last < 0 || (long long)n_first + n_last > budget)
+    return set_error(MLA_ERR_INVALID_ARG, "need budget >= 1 and n_first + n_last <= budget (got %d, %d and %d)", budget,
+                     n_first, n_last);
+  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3)
+    return set_error(MLA_ERR_INVALID_ARG, "kv_dtype must be MLA_KV_BF16 or MLA_KV_FP8_E4M3 (got %d)", kv_dtype);
+  if ((kv_scales == nullptr) != (kv_scales_dst == nullptr))
+    return set_error(MLA_ERR_INVALID_ARG, "kv_scales and kv_scales_dst must both be given, or neither");
+  if (kv_scales && kv_dtype != MLA_KV_FP8_E4M3)
+    return set_error(MLA_ERR_INVALID_ARG, "block scales belong to an fp8 e4m3 cache");
+  const int bl = kv_scales ? block_log2_of(block_tokens) : 0;
+  if (bl < 0) return set_error(MLA_ERR_UNSUPPORTED, "block_tokens must be 1, 2, 4, .. 64 (got %d)", block_tokens);
+  if (!weights || !seq_lens || !kv_cache || !page_table || !kv_cache_dst || !page_table_dst || !kept || !seq_lens_dst)
+    return set_error(MLA_ERR_INVALID_ARG, "weights, seq_lens, the caches, their page tables, kept and seq_lens_dst must not be NULL");
+  if (!aligned16(kv_cache) || !aligned16(kv_cache_dst))
+    return set_error(MLA_ERR_INVALID_ARG, "kv_cache and kv_cache_dst must be 16-byte aligned");
+  if (!aligned4(weights) || !aligned4(seq_lens) || !aligned4(kv_scales) || !aligned4(kv_scales_dst) ||
+      !aligned4(page_table) || !aligned4(page_table_dst) || !aligned4(kept) || !aligned4(seq_lens_dst) ||
+      !aligned4(weights_dst) || !aligned4(status_dev))
+    return set_error(MLA_ERR_INVALID_ARG, "every pointer must be aligned to its element");
+  const int most = std::min(budget, max_seq);  // rows of the longest result
+  const long long pages_src = ((long long)max_seq + kPage - 1) / kPage, pages_dst = ((long long)most + kPage - 1) / kPage;
+  if (num_pages < 1 || num_pages_dst < 1 || page_table_stride < pages_src || page_table_dst_stride < pages_dst)
+    return set_error(MLA_ERR_INVALID_ARG, "the page tables have %d and %d entries a row, %lld and %lld are needed",
+                     page_table_stride, page_table_dst_stride, pages_src, pages_dst);
+  if (weights_stride < max_seq || (weights_dst && weights_dst_stride < most))
+    return set_error(MLA_ERR_INVALID_ARG, "weights_stride %lld or weights_dst_stride %lld is smaller than a row",
+                     weights_stride, weights_dst_stride);
+  int dev = 0;
+  const int rc = current_device_ready(&dev);
+  if (rc != MLA_OK) return rc;
+
+  const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last,
+                     kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
+  // CTAs per request: one for every 16384 keys, up to a portable cluster of 8
+  int ctas = 1;
+  while (ctas < 8 && (long long)ctas * 16384 < max_seq) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)batch, 1);
+  cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.stream = (cudaStream_t)stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t ce = cudaLaunchKernelEx(&cfg, evict_select_kernel, s);
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction select kernel launch: %s", cudaGetErrorString(ce));
+  if (pages_dst == 0) return MLA_OK;
+
+  const GatherArgs g{kept, seq_lens_dst, budget, max_seq, (const uint4*)kv_cache, (uint4*)kv_cache_dst, kv_scales,
+                     kv_scales_dst, bl, page_table, page_table_dst, page_table_stride, page_table_dst_stride, num_pages,
+                     num_pages_dst, status_dev};
+  cfg.gridDim = dim3((unsigned)pages_dst, (unsigned)batch, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  auto fn = kv_dtype == MLA_KV_BF16 ? evict_gather_kernel<72, false>
+            : kv_scales             ? evict_gather_kernel<36, true>
+                                    : evict_gather_kernel<36, false>;
+  ce = cudaLaunchKernelEx(&cfg, fn, g);
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction gather kernel launch: %s", cudaGetErrorString(ce));
+  return MLA_OK;
+}

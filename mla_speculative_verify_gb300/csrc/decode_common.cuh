@@ -31,6 +31,8 @@ struct Params {
   int32_t* status;
   long long wait_budget;  // cycles a bounded wait may take (kWaitBudget; kWaitBudgetTest in a timeout test)
   int skip_copy;          // page of the first unit whose copy is never issued (timeout test), or -1
+  const float* kv_scales; // block-scaled e4m3 cache: [num_pages, 64 >> block_log2], else NULL
+  int block_log2;         // log2 of the tokens that share a scale
 };
 
 __device__ __forceinline__ void report(int32_t* status, int bits) {
@@ -42,8 +44,8 @@ __device__ __forceinline__ void report(int32_t* status, int bits) {
 // scope), so the warp never diverges while it waits: a lane-0 spin loop with the other
 // lanes parked at a shuffle cost every role ~10 % of its pace (1M q=8 bf16 392.7 -> 349.2
 // us, q=1 38.9 -> 35.8 us when changed).
-template <bool kCluster = false>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, const Params& p) {
+template <bool kCluster = false, typename P>  // P: a launch's parameters (its wait_budget and status)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, const P& p) {
   auto poll = [&]() { return kCluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
   if (__all_sync(0xffffffffu, poll())) return true;
   const long long t0 = clock64();

@@ -234,7 +234,14 @@ struct SoftmaxArgs {
 // 16 c + cp and 16 c + cp + 1, cp = 8 grp + 2 (t % 4). Element x[4 c + j] is key kr0 + 8 (j / 2),
 // column 16 c + cp + j % 2 (c < NCH, j < 4).
 // Returns whether this thread issued O^T MMAs (lane 0 of softmax warps 0..3).
-template <int NCH, bool kFp8>
+//
+// kScaled (an e4m3 cache with a scale for each block of tokens, value = code * scale[key]):
+// the products run on the raw codes. With s_j the score and v_j the scale of key j, the
+// softmax works on s_j + log2 v_j: P'_j = 2^(s_j + log2 v_j - ref) is what the code of key j
+// is weighted with in O^T, and l adds P'_j / v_j, so out = O / l and the reference follows
+// the terms that O is made of, however far the blocks' scales lie apart. Each thread needs
+// the scales of its two keys; they are read a tile ahead, their page id two tiles ahead.
+template <int NCH, bool kFp8, bool kScaled>
 __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params& p) {
   constexpr int NC = 4 * NCH;
   using G = Geo<kFp8>;
@@ -355,8 +362,38 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
     }
   };
   const float scale = p.score_scale_log2;
+  // kScaled: the block scales of this thread's two keys in the next tile, and the page after it
+  float sc_next[2] = {1.f, 1.f};
+  int page_after = 0;
+  auto page_of = [&](int t) {
+    const int pid = t < a.ntiles ? p.page_table[(size_t)a.b * p.pt_stride + a.kv_begin / kPage + t] : 0;
+    return pid >= 0 && pid < p.num_pages ? pid : 0;
+  };
+  auto load_scales = [&](int t, int page) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int kr = kr0 + 8 * k;
+      const bool live = a.kv_begin + t * kTileKeys + kr < a.kv_end;  // past the range a scale may be anything
+      sc_next[k] = live ? p.kv_scales[((size_t)page * kPage + kr) >> p.block_log2] : 1.f;
+    }
+  };
+  if constexpr (kScaled) {
+    load_scales(0, page_of(0));
+    page_after = page_of(1);
+  }
   for (int t = 0; !stop && t < a.ntiles; ++t) {
     const int sb = t & 1;
+    float ks[2], lks[2], inv_ks[2];
+    if constexpr (kScaled) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        ks[k] = sc_next[k] < 0x1p-60f ? 0x1p-60f : sc_next[k];  // a block of zeros may have the scale 0
+        lks[k] = lg2(ks[k]);
+        inv_ks[k] = 1.f / ks[k];
+      }
+      load_scales(t + 1, page_after);
+      page_after = page_of(t + 2);
+    }
     float x[NC];
     bool need = false;
     bool unmasked = false;  // this tile: every key visible to every row
@@ -405,6 +442,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float v = x[4 * c + j] * csv[j];
+          if constexpr (kScaled) v = fmaf(v, ks[j >> 1], lks[j >> 1]);
           const int key = key0 + 8 * (j >> 1);
           if (!unmasked) v = (key < a.kv_end && key < ms->lim[n0 + (j & 1)]) ? v : -INFINITY;
           x[4 * c + j] = v;
@@ -542,7 +580,12 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
       }
       if (!fail) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) l_acc[i] += pv[i];
+        for (int i = 0; i < NC; ++i) {
+          if constexpr (kScaled)
+            l_acc[i] = fmaf(pv[i], inv_ks[(i >> 1) & 1], l_acc[i]);
+          else
+            l_acc[i] += pv[i];
+        }
         store_p();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&ms->p_full[sb]);
@@ -648,7 +691,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
   return issued_ot;
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kScaled>
 __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
     fold_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv, Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -921,11 +964,11 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
                         kv_begin, kv_end, ntiles, part_row0, ctx, qlen, tok0, abort};
     bool issued_ot;
     if (nch == 1)
-      issued_ot = softmax_role<1, kFp8>(a, p);
+      issued_ot = softmax_role<1, kFp8, kScaled>(a, p);
     else if (nch == 2)
-      issued_ot = softmax_role<2, kFp8>(a, p);
+      issued_ot = softmax_role<2, kFp8, kScaled>(a, p);
     else
-      issued_ot = softmax_role<3, kFp8>(a, p);
+      issued_ot = softmax_role<3, kFp8, kScaled>(a, p);
     // the O^T MMAs this lane issued must retire before TMEM is released
     if (issued_ot) drain_mmas(&ms->mma_done[4 + (warp - 1 - kMma)], p.wait_budget);
     __syncwarp();
@@ -1109,6 +1152,7 @@ int max_splits_for_merge() { return kMergeMaxSplits; }
 
 // ------------------------------------------------------------------ host side
 size_t workspace_bytes_for(int n_part_rows);
+int block_log2_of(int block_tokens);  // defined with the plan
 int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out);
 int launch_pair_kernel(int dev, const PlanHeader* h, const void* q, const void* kv_cache, int num_pages,
                        const Params& prm, cudaStream_t st);
@@ -1148,13 +1192,20 @@ static int prepare_device(int dev) {
     return set_error(MLA_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a (GB300)", dev, d.major,
                      d.minor);
   if (!d.attrs_set) {
-    cudaError_t e1 = cudaFuncSetAttribute(fold_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    cudaError_t e2 = cudaFuncSetAttribute(fold_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e1 != cudaSuccess || e2 != cudaSuccess)
-      return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e1 != cudaSuccess ? e1 : e2));
+    for (auto fn : {fold_decode_kernel<false, false>, fold_decode_kernel<true, false>, fold_decode_kernel<true, true>}) {
+      const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
+    }
     d.attrs_set = true;
   }
   return MLA_OK;
+}
+
+// The current device, checked to be one this library runs on (for the other entry points).
+int current_device_ready(int* dev) {
+  const cudaError_t ce = cudaGetDevice(dev);
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(ce));
+  return prepare_device(*dev);
 }
 
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -1174,18 +1225,13 @@ static CUresult encode_chunked(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMa
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-}  // namespace mla
-
-using namespace mla;
-
-extern "C" int mla_decode_run(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
-                              const void* kv_cache, const int32_t* page_table, int page_table_stride, int num_pages,
-                              const int32_t* seq_lens, const int32_t* q_lens, float sm_scale, float kv_scale, void* out,
-                              float* lse, void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
-  clear_error();
-  const PlanHeader* h = nullptr;
-  int rc = check_plan(plan_host, plan_bytes, &h);
-  if (rc != MLA_OK) return rc;
+// mla_decode_run, and with kv_scales (the caller has checked them) mla_decode_run_scaled.
+static int decode_run(const void* plan_dev, const void* plan_host, const PlanHeader* h, const void* q,
+                      const void* kv_cache, const float* kv_scales, int block_log2, const int32_t* page_table,
+                      int page_table_stride, int num_pages, const int32_t* seq_lens, const int32_t* q_lens,
+                      float sm_scale, float kv_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                      int32_t* status_dev, void* stream) {
+  int rc = MLA_OK;
   if (!plan_dev || !q || !kv_cache || !page_table || !seq_lens || !q_lens || !out)
     return set_error(MLA_ERR_INVALID_ARG, "plan_dev, q, kv_cache, page_table, seq_lens, q_lens and out must not be NULL");
   if (!aligned16(plan_dev) || !aligned16(q) || !aligned16(kv_cache) || !aligned16(out))
@@ -1242,16 +1288,20 @@ extern "C" int mla_decode_run(const void* plan_dev, const void* plan_host, size_
   prm.status = status_dev;
   prm.wait_budget = h->debug_skip_copy > 0 ? kWaitBudgetTest : kWaitBudget;
   prm.skip_copy = h->debug_skip_copy - 1;
+  prm.kv_scales = kv_scales;
+  prm.block_log2 = block_log2;
   cudaStream_t st = (cudaStream_t)stream;
   if (h->cta_pair) {
     if (fp8) return set_error(MLA_ERR_PLAN, "a two-CTA plan needs a bf16 cache");
     rc = launch_pair_kernel(dev, h, q, kv_cache, num_pages, prm, st);
     if (rc != MLA_OK) return rc;
   } else {
-    if (fp8)
-      fold_decode_kernel<true><<<h->n_units, Roles<true>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
+    if (kv_scales)
+      fold_decode_kernel<true, true><<<h->n_units, Roles<true>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
+    else if (fp8)
+      fold_decode_kernel<true, false><<<h->n_units, Roles<true>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
     else
-      fold_decode_kernel<false><<<h->n_units, Roles<false>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
+      fold_decode_kernel<false, false><<<h->n_units, Roles<false>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
     ce = cudaGetLastError();
     if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "fold kernel launch: %s", cudaGetErrorString(ce));
   }
@@ -1291,6 +1341,42 @@ extern "C" int mla_decode_run(const void* plan_dev, const void* plan_host, size_
     if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "merge kernel launch: %s", cudaGetErrorString(ce));
   }
   return MLA_OK;
+}
+
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_decode_run(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
+                              const void* kv_cache, const int32_t* page_table, int page_table_stride, int num_pages,
+                              const int32_t* seq_lens, const int32_t* q_lens, float sm_scale, float kv_scale, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
+  clear_error();
+  const PlanHeader* h = nullptr;
+  const int rc = check_plan(plan_host, plan_bytes, &h);
+  if (rc != MLA_OK) return rc;
+  return decode_run(plan_dev, plan_host, h, q, kv_cache, nullptr, 0, page_table, page_table_stride, num_pages, seq_lens,
+                    q_lens, sm_scale, kv_scale, out, lse, workspace, workspace_bytes, status_dev, stream);
+}
+
+extern "C" int mla_decode_run_scaled(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
+                                     const void* kv_cache, const float* kv_scales, int block_tokens,
+                                     const int32_t* page_table, int page_table_stride, int num_pages,
+                                     const int32_t* seq_lens, const int32_t* q_lens, float sm_scale, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                                     void* stream) {
+  clear_error();
+  const PlanHeader* h = nullptr;
+  const int rc = check_plan(plan_host, plan_bytes, &h);
+  if (rc != MLA_OK) return rc;
+  if (h->kv_dtype != MLA_KV_FP8_E4M3)
+    return set_error(MLA_ERR_INVALID_ARG, "block scales belong to an fp8 e4m3 cache: plan with MLA_KV_FP8_E4M3");
+  const int bl = block_log2_of(block_tokens);
+  if (bl < 0) return set_error(MLA_ERR_UNSUPPORTED, "block_tokens must be 1, 2, 4, .. 64 (got %d)", block_tokens);
+  if (!kv_scales || ((uintptr_t)kv_scales & 3u))
+    return set_error(MLA_ERR_INVALID_ARG, "kv_scales must be a 4-byte aligned pointer and not NULL");
+  return decode_run(plan_dev, plan_host, h, q, kv_cache, kv_scales, bl, page_table, page_table_stride, num_pages,
+                    seq_lens, q_lens, sm_scale, 1.0f, out, lse, workspace, workspace_bytes, status_dev, stream);
 }
 
 extern "C" int mla_device_pair_slots(int device, int* slots) {

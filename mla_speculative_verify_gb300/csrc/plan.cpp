@@ -40,6 +40,13 @@ static int fold_factor(int q, int H) {
 
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// log2 of a block's tokens (1, 2, 4, .. 64, so that a block never leaves its page), or -1.
+int block_log2_of(int block_tokens) {
+  for (int l = 0; (1 << l) <= kPage; ++l)
+    if (block_tokens == 1 << l) return l;
+  return -1;
+}
+
 size_t workspace_bytes_for(int n_part_rows) {
   if (n_part_rows <= 0) return 0;
   return align_up((size_t)n_part_rows * kDv * kPartOElemBytes, 256) + align_up((size_t)n_part_rows * sizeof(float), 256);

@@ -1,0 +1,659 @@
+// weights_sm103.cu -- mla_key_weights: the attention weight that every cached key received
+// from a verify call, added to a running sum (what an eviction goes by):
+//
+//   w[b, j] = decay * w[b, j] + sum over counted rows (i, h) of exp(s_ijh - lse_ih)
+//
+// with the scores s and the log-sum-exp of the decode. No value product and no running
+// maximum are needed, since lse is known, so one pass over the cache does it:
+//
+//   S^T[key, row] = K[key, 0:576] . Q[row, 0:576]^T      (M = 128 keys, N = up to 128 rows)
+//
+// on the tcgen05 tensor cores. In this orientation a key is one lane of tensor memory: a
+// thread reads its key's scores of all rows and adds their exponentials in registers; no sum
+// crosses threads and no order depends on timing, so results repeat bit for bit.
+//
+// Rows. The q * H rows of a request are cut into G groups of at most 128. Keys go through
+// shared memory in tiles of 128 (two pages), 64 of the 576 columns at a time, so that the Q
+// group stays resident (up to 144 KB) beside a ring of K pieces. With G > 1 a CTA takes a few
+// tiles (sub_tiles, which fit L2 over all CTAs) through all groups before it goes on, so the
+// cache leaves HBM once; the sums of those keys wait in shared memory.
+//
+// An e4m3 cache is multiplied as stored (kind::f8f6f4). q_split_kernel first writes each Q row
+// as two e4m3 parts: the row times the power of two that brings its largest entry to [128,
+// 256), rounded, and the remainder. A bf16 entry has 8 significant bits and each part carries
+// 4, so entries down to 2^-9 of the row's largest are exact; below that the error is at most
+// 2^-18 of the largest. N = 2 * rows columns then hold both parts' scores.
+//
+// Warp roles (one CTA per SM): warp 0 loads (TMA), warp 1 issues the products, warps 4-7 and
+// 8-11 take alternate tiles' scores out of two accumulators. All of them walk the same work
+// list (Walk). Waits are bounded as in the decode kernel.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "mla_decode.h"
+#include "plan_format.h"
+#include "decode_common.cuh"
+#include "ptx.cuh"
+#include "status.h"
+
+namespace mla {
+
+int current_device_ready(int* dev);                         // defined next to the decode kernel
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();     // defined next to the decode kernel
+int block_log2_of(int block_tokens);                        // defined with the plan
+int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out);
+
+namespace {
+
+constexpr int kKeys = 128;          // keys per tile (two pages)
+constexpr int kPieces = 9;          // 576 = 9 x 64 columns
+constexpr int kMaxRows = 128;       // rows of a group
+constexpr int kMaxStages = 16;
+constexpr int kMaxSub = 16;         // tiles of one sub-range: 32 page ids, one per lane
+constexpr int kMaxSubSums = 8;      // of those when sums wait in shared memory (G > 1)
+constexpr int kThreads = 384;
+constexpr int kSmemCap = 232448;    // 227 KB per CTA
+
+struct WeightsMisc {
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t q_full[kPieces], q_empty[kPieces];
+  uint64_t d_full[2], d_empty[2], mma_done;
+  uint32_t tmem_base;
+  int abort;
+  alignas(16) float nlse[2][kMaxRows];   // per epilogue warpgroup: -lse * log2(e) of its current group's rows
+  alignas(16) float rscale[2][kMaxRows]; // e4m3: each row's part of its scores' scale
+  alignas(16) int lim[2][kMaxRows];      // keys that each row sees
+  alignas(16) float sums[kMaxSubSums][kKeys];
+};
+constexpr int kMiscBytes = (sizeof(WeightsMisc) + 1023) / 1024 * 1024;
+
+struct WeightsParams {
+  const PlanRequest* reqs;
+  int batch, H, pt_stride, num_pages, block_log2;
+  const int32_t* page_table;
+  const float* kv_scales;  // NULL without block scales
+  const float* lse;
+  const int32_t* counted;  // NULL: every row counts
+  const float* q_scale;    // e4m3: per row, undoes its power of two
+  float* weights;
+  long long w_stride;
+  float decay, scale_log2;
+  int rows_n;              // MMA rows of every group (multiple of 16)
+  int total_rows;
+  int stages, sub_tiles;
+  long long total_work;    // sum over requests of tiles * groups
+  int32_t* status;
+  long long wait_budget;
+};
+
+// This CTA's share of the work list, as every role's warps walk it. The list is request by
+// request, a request's tiles each weighing its groups; CTA i of n takes the tiles whose
+// place in the list lies in [W i / n, W (i + 1) / n). 32 requests are looked at together.
+struct Walk {
+  long long lo, hi, base;  // base: place of request b0
+  int b0;
+  PlanRequest r;           // this lane's request
+  long long at;            // its place
+  uint32_t todo;           // lanes of the current 32 requests that hold work of this CTA
+  bool loaded;
+
+  __device__ __forceinline__ void start(const WeightsParams& p) {
+    lo = p.total_work * blockIdx.x / gridDim.x;
+    hi = p.total_work * (blockIdx.x + 1) / gridDim.x;
+    base = 0;
+    b0 = -32;
+    todo = 0;
+    loaded = false;
+  }
+  static __device__ __forceinline__ int groups(const WeightsParams& p, int q) {
+    return (q * p.H + p.rows_n - 1) / p.rows_n;
+  }
+  // The next request with tiles [t0, t1) for this CTA; false at the end.
+  __device__ __forceinline__ bool next(const WeightsParams& p, int& b, PlanRequest& req, int& t0, int& t1) {
+    const int lane = threadIdx.x & 31;
+    while (todo == 0) {
+      b0 += 32;
+      if (b0 >= p.batch || base >= hi) return false;
+      const bool live = b0 + lane < p.batch;
+      r = live ? p.reqs[b0 + lane] : PlanRequest{0, 0, 0, 1};
+      const long long mine = (long long)((r.ctx + kKeys - 1) / kKeys) * groups(p, r.q);
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      at = base + incl - mine;
+      todo = __ballot_sync(0xffffffffu, mine > 0 && at < hi && at + mine > lo);
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    const int l = __ffs(todo) - 1;
+    todo &= todo - 1;
+    b = b0 + l;
+    req.ctx = __shfl_sync(0xffffffffu, r.ctx, l);
+    req.q = __shfl_sync(0xffffffffu, r.q, l);
+    req.tok0 = __shfl_sync(0xffffffffu, r.tok0, l);
+    req.fold = 1;
+    const long long a = __shfl_sync(0xffffffffu, at, l);
+    const int g = groups(p, req.q), tiles = (req.ctx + kKeys - 1) / kKeys;
+    auto first_tile = [&](long long place) {  // the first tile at or after a place of the list
+      const long long d = place - a;
+      return d <= 0 ? 0 : (int)min((long long)tiles, (d + g - 1) / g);
+    };
+    t0 = first_tile(lo);
+    t1 = first_tile(hi);
+    return true;
+  }
+};
+
+// Rows of request b that count (its first counted[b] tokens).
+__device__ __forceinline__ int counted_rows(const WeightsParams& p, int b, int q) {
+  const int c = p.counted ? max(0, min(q, p.counted[b])) : q;
+  return c * p.H;
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv,
+                       const __grid_constant__ CUtensorMap tmap_page, WeightsParams p) {
+  constexpr int kRowBytes = kFp8 ? 64 : 128;             // a row's bytes in one 64-column piece
+  constexpr int kStageBytes = kKeys * kRowBytes;
+  constexpr int kHalf = kPage * kRowBytes;               // one page of a piece
+  constexpr uint32_t kAccCols = kFp8 ? 256 : 128;        // tensor-memory columns of an accumulator
+  constexpr uint32_t kSwizzle = kFp8 ? ptx::kSwizzle64B : ptx::kSwizzle128B;
+  constexpr uint32_t kSbo = 8 * kRowBytes;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
+  WeightsMisc* ms = (WeightsMisc*)smem;
+  uint8_t* sQ = smem + kMiscBytes;
+  const int n = p.rows_n;
+  const int q_piece = n * 128;                           // bytes of a Q piece (e4m3: n hi rows, then n lo rows)
+  uint8_t* sK = sQ + kPieces * q_piece;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &ms->abort;
+
+  if (warp == 0 && lane == 0) {
+    ms->abort = 0;
+    for (int i = 0; i < p.stages; ++i) {
+      ptx::mbar_init(&ms->kv_full[i], 1);
+      ptx::mbar_init(&ms->kv_empty[i], 1);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      ptx::mbar_init(&ms->q_full[i], 1);
+      ptx::mbar_init(&ms->q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&ms->d_full[i], 1);
+      ptx::mbar_init(&ms->d_empty[i], 4);
+    }
+    ptx::mbar_init(&ms->mma_done, 1);
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmap_q);
+    ptx::prefetch_tmap(&tmap_kv);
+  } else if (warp == 1) {
+    ptx::tmem_alloc(&ms->tmem_base, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ms->tmem_base;
+  Walk walk;
+  walk.start(p);
+  int b, t0, t1;
+  PlanRequest req;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ loads
+    if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
+    uint32_t fill = 0, qfill = 0;       // ring pieces and Q groups loaded so far
+    bool ok = true;
+    while (ok && walk.next(p, b, req, t0, t1)) {
+      const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
+      if (groups == 0 || t0 >= t1) continue;
+      const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
+      const int npages = (req.ctx + kPage - 1) / kPage;
+      const int32_t* ids = p.page_table + (size_t)b * p.pt_stride;
+      auto load_ids = [&](int tile) {
+        const int pg = 2 * tile + lane;
+        int id = pg < min(npages, 2 * t1) && lane < 2 * sub ? ids[pg] : 0;
+        if (id < 0 || id >= p.num_pages) {
+          report(p.status, MLA_DEVICE_BAD_PAGE);
+          id = 0;
+        }
+        return id;
+      };
+      int cur = load_ids(t0);
+      for (int s0 = t0; ok && s0 < t1; s0 += sub) {
+        const int s1 = min(t1, s0 + sub);
+        const int nxt = s1 < t1 ? load_ids(s1) : 0;
+        for (int g = 0; ok && g < groups; ++g) {
+          const bool new_q = groups > 1 || s0 == t0;
+          for (int t = s0; ok && t < s1; ++t) {
+            const int pg = 2 * (t - s0);
+            const bool two = 2 * t + 1 < npages;
+            const int id0 = __shfl_sync(0xffffffffu, cur, pg), id1 = __shfl_sync(0xffffffffu, cur, pg + 1);
+            // ask L2 for whole pages of the next tile that HBM has to deliver
+            const int tn = g == 0 && t + 1 < s1 ? t + 1 : g == groups - 1 && t + 1 == s1 ? s1 : -1;
+            const int pn = t + 1 < s1 ? pg + 2 : 0;
+            const int n0 = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur, pn & 31) : __shfl_sync(0xffffffffu, nxt, 0);
+            const int n1 = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur, (pn + 1) & 31) : __shfl_sync(0xffffffffu, nxt, 1);
+            if (lane == 0 && tn >= 0 && tn < t1) {
+              ptx::tma_prefetch_l2_3d(&tmap_page, 0, n0 * kPage, 0);
+              if (2 * tn + 1 < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, n1 * kPage, 0);
+            }
+            for (int c = 0; ok && c < kPieces; ++c, ++fill) {
+              if (new_q && t == s0) {
+                if (qfill > 0) ok = warp_wait(&ms->q_empty[c], (qfill - 1) & 1, abort, p);
+                if (!ok) break;
+                if (lane == 0) {
+                  const int row = req.tok0 * p.H + g * n;
+                  ptx::mbar_arrive_expect_tx(&ms->q_full[c], q_piece);
+                  ptx::tma_load_3d(sQ + c * q_piece, &tmap_q, &ms->q_full[c], 0, row, c);
+                  if (kFp8) ptx::tma_load_3d(sQ + c * q_piece + n * 64, &tmap_q, &ms->q_full[c], 0, p.total_rows + row, c);
+                }
+                __syncwarp();
+              }
+              const uint32_t st = fill % p.stages, use = fill / p.stages;
+              if (use > 0) ok = warp_wait(&ms->kv_empty[st], (use - 1) & 1, abort, p);
+              if (!ok) break;
+              if (lane == 0) {
+                uint8_t* dst = sK + st * kStageBytes;
+                ptx::mbar_arrive_expect_tx(&ms->kv_full[st], two ? 2 * kHalf : kHalf);
+                ptx::tma_load_3d(dst, &tmap_kv, &ms->kv_full[st], 0, id0 * kPage, c);
+                if (two) ptx::tma_load_3d(dst + kHalf, &tmap_kv, &ms->kv_full[st], 0, id1 * kPage, c);
+              }
+              __syncwarp();
+            }
+          }
+          if (new_q) ++qfill;
+        }
+        cur = nxt;
+      }
+    }
+    // every copy must have landed before the CTA may exit: the last ones of the ring, and of
+    // the Q pieces (a piece that the loop gave up on has none in flight)
+    if (*abort && lane == 0) {
+      for (uint32_t f = fill > (uint32_t)p.stages ? fill - p.stages : 0; f < fill; ++f) {
+        const long long t0c = clock64();
+        while (!ptx::mbar_try_wait(&ms->kv_full[f % p.stages], (f / p.stages) & 1) && clock64() - t0c < p.wait_budget) {
+        }
+      }
+      for (int c = 0; c < kPieces; ++c)
+        for (uint32_t par = 0; par < 2; ++par) {
+          const long long t0c = clock64();
+          while (!ptx::mbar_try_wait(&ms->q_full[c], par) && clock64() - t0c < kWaitBudgetTest) {
+          }
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    const uint32_t sq = ptx::smem_addr(sQ), sk = ptx::smem_addr(sK);
+    const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kKeys, 2 * n, 0, 0) : ptx::idesc_bf16(kKeys, n, 0, 0);
+    uint32_t fill = 0, qfill = 0, used[2] = {0, 0};
+    bool ok = true, issued = false;
+    while (ok && walk.next(p, b, req, t0, t1)) {
+      const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
+      if (groups == 0 || t0 >= t1) continue;
+      const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
+      for (int s0 = t0; ok && s0 < t1; s0 += sub) {
+        const int s1 = min(t1, s0 + sub);
+        for (int g = 0; ok && g < groups; ++g) {
+          const bool new_q = groups > 1 || s0 == t0, last_q = groups > 1 || s1 == t1;
+          for (int t = s0; ok && t < s1; ++t) {
+            const int buf = (t - s0) & 1;
+            if (used[buf] > 0) ok = warp_wait(&ms->d_empty[buf], (used[buf] - 1) & 1, abort, p);
+            for (int c = 0; ok && c < kPieces; ++c, ++fill) {
+              if (new_q && t == s0) ok = warp_wait(&ms->q_full[c], qfill & 1, abort, p);
+              const uint32_t st = fill % p.stages;
+              if (ok) ok = warp_wait(&ms->kv_full[st], (fill / p.stages) & 1, abort, p);
+              if (!ok) break;
+              ptx::tc_fence_after();
+              if (lane == 0) {
+                const uint32_t d = tmem + buf * kAccCols, a0 = sk + st * kStageBytes, b0 = sq + c * q_piece;
+#pragma unroll
+                for (int k = 0; k < kRowBytes / 32; ++k) {
+                  const uint64_t ad = ptx::smem_desc(a0 + 32 * k, 16, kSbo, kSwizzle);
+                  const uint64_t bd = ptx::smem_desc(b0 + 32 * k, 16, kSbo, kSwizzle);
+                  if constexpr (kFp8)
+                    ptx::mma_e4m3_ss(d, ad, bd, idesc, (c | k) != 0 ? 1u : 0u);
+                  else
+                    ptx::mma_bf16_ss(d, ad, bd, idesc, (c | k) != 0 ? 1u : 0u);
+                }
+                ptx::mma_commit(&ms->kv_empty[st]);
+                if (last_q && t == s1 - 1) ptx::mma_commit(&ms->q_empty[c]);
+                if (c == kPieces - 1) ptx::mma_commit(&ms->d_full[buf]);
+              }
+              __syncwarp();
+              issued = true;
+            }
+            ++used[buf];
+          }
+          if (new_q) ++qfill;
+        }
+      }
+    }
+    // every product must retire before tensor memory is released
+    if (issued && lane == 0) drain_mmas(&ms->mma_done, p.wait_budget);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ weights
+    const int wg = (warp - 4) >> 2, qd = warp & 3, key_in = 32 * qd + lane, wtid = tid & 127;
+    const uint32_t acc = tmem + wg * kAccCols + ((uint32_t)(32 * qd) << 16);
+    float* nlse = ms->nlse[wg];
+    float* rscale = ms->rscale[wg];
+    int* lim = ms->lim[wg];
+    if (kFp8) ptx::pdl_wait_primary();  // q_scale comes from the kernel before
+    uint32_t used = 0;
+    bool ok = true;
+    while (walk.next(p, b, req, t0, t1)) {
+      const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
+      const int32_t* ids = p.page_table + (size_t)b * p.pt_stride;
+      float* wrow = p.weights + (size_t)b * p.w_stride;
+      if (groups == 0) {  // no row counts: the sums only decay
+        for (int t = t0 + wg; t < t1; t += 2) {
+          const int key = t * kKeys + wtid;
+          if (key < req.ctx) wrow[key] = p.decay == 0.f ? 0.f : wrow[key] * p.decay;
+        }
+        continue;
+      }
+      const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
+      for (int s0 = t0; s0 < t1; s0 += sub) {
+        const int s1 = min(t1, s0 + sub);
+        for (int g = 0; g < groups; ++g) {
+          const int nrows = min(n, rows - g * n), row0 = req.tok0 * p.H + g * n;
+          if (groups > 1 || s0 == t0) {
+            ptx::bar_sync(1 + wg, 128);  // this warpgroup is done with the old table
+            if (wtid < n) {
+              const bool live = wtid < nrows;
+              const float l = live ? p.lse[row0 + wtid] : INFINITY;
+              nlse[wtid] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;  // a row that saw nothing adds nothing
+              if (kFp8) rscale[wtid] = live ? p.scale_log2 * p.q_scale[row0 + wtid] : 0.f;
+              lim[wtid] = live ? req.ctx - req.q + (g * n + wtid) / p.H + 1 : 0;
+            }
+            ptx::bar_sync(1 + wg, 128);
+          }
+          const int lim_min = lim[0];
+          for (int t = s0 + wg; t < s1; t += 2) {
+            const int key = t * kKeys + key_in;
+            const bool live = key < req.ctx;
+            float old = 0.f, ks = kFp8 ? 1.f : p.scale_log2;  // the key's part of its scores' scale
+            if (g == groups - 1 && live && p.decay != 0.f) old = wrow[key] * p.decay;
+            if (kFp8 && p.kv_scales && live) {
+              int id = ids[key / kPage];
+              id = id >= 0 && id < p.num_pages ? id : 0;
+              ks = p.kv_scales[((size_t)id * kPage + key % kPage) >> p.block_log2];
+            }
+            if (ok) ok = warp_wait(&ms->d_full[wg], used & 1, abort, p);
+            ++used;
+            if (!ok) continue;
+            ptx::tc_fence_after();
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            const bool all = (t + 1) * kKeys <= lim_min;  // every row sees every key of the tile
+            for (int c = 0; 16 * c < nrows; ++c) {
+              float x[16];
+              ptx::tmem_ld16(acc + 16 * c, x);
+              if constexpr (kFp8) {
+                float y[16];
+                ptx::tmem_ld16(acc + n + 16 * c, y);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 r = *reinterpret_cast<const float4*>(rscale + 16 * c + j);
+                  x[j] = (x[j] + y[j]) * r.x;
+                  x[j + 1] = (x[j + 1] + y[j + 1]) * r.y;
+                  x[j + 2] = (x[j + 2] + y[j + 2]) * r.z;
+                  x[j + 3] = (x[j + 3] + y[j + 3]) * r.w;
+                }
+              } else {
+                ptx::tmem_ld_wait();
+              }
+              if (all && 16 * c + 16 <= nrows) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 l = *reinterpret_cast<const float4*>(nlse + 16 * c + j);
+                  s[0] += ex2(fmaf(x[j], ks, l.x));
+                  s[1] += ex2(fmaf(x[j + 1], ks, l.y));
+                  s[2] += ex2(fmaf(x[j + 2], ks, l.z));
+                  s[3] += ex2(fmaf(x[j + 3], ks, l.w));
+                }
+              } else {
+                // a row past the group, or one that does not see this key, holds anything
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[j & 3] += key < lim[16 * c + j] ? ex2(fmaf(x[j], ks, nlse[16 * c + j])) : 0.f;
+              }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ms->d_empty[wg]);
+            float w = (s[0] + s[1]) + (s[2] + s[3]);
+            if (groups > 1) {
+              float* slot = &ms->sums[t - s0][key_in];  // this thread's own, through all groups
+              if (g > 0) w += *slot;
+              *slot = w;
+            }
+            if (g == groups - 1 && live) wrow[key] = old + w;
+          }
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Q [rows, 576] bf16 -> e4m3 parts [2][rows][576] and the factor that undoes each row's power
+// of two. One warp per row: 72 pieces of 8 entries, lane l holds pieces l, l + 32 and (l < 8) 64 + l.
+constexpr int kSplitWarps = 8;
+__global__ void __launch_bounds__(32 * kSplitWarps) q_split_kernel(const uint4* q, int rows, uint8_t* parts,
+                                                                   float* q_scale) {
+  ptx::pdl_launch_dependents();
+  const int row = blockIdx.x * kSplitWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  uint4 v[3];
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) v[i] = 32 * i + lane < 72 ? q[(size_t)row * 72 + 32 * i + lane] : make_uint4(0u, 0u, 0u, 0u);
+  auto entry = [&](int i, int k) {
+    const uint32_t w = k < 2 ? v[i].x : k < 4 ? v[i].y : k < 6 ? v[i].z : v[i].w;
+    return __uint_as_float((k & 1) ? (w & 0xFFFF0000u) : (w << 16));
+  };
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(entry(i, k)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  int e = 0;
+  if (mx > 0.f && mx < INFINITY) e = max(-100, min(100, 7 - ((int)(__float_as_uint(mx) >> 23) - 127)));
+  const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (32 * i + lane >= 72) continue;
+    uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const float a = entry(i, k) * sc, c = entry(i, k + 1) * sc;
+      const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3);
+      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
+      const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+      const __nv_fp8x2_storage_t r = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, c - back.y), __NV_SATFINITE, __NV_E4M3);
+      hi[k >> 2] |= (uint32_t)h << (8 * (k & 3));
+      lo[k >> 2] |= (uint32_t)r << (8 * (k & 3));
+    }
+    const size_t at = (size_t)row * 576 + 8 * (32 * i + lane);
+    *reinterpret_cast<uint2*>(parts + at) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(parts + (size_t)rows * 576 + at) = make_uint2(lo[0], lo[1]);
+  }
+  if (lane == 0) q_scale[row] = __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+size_t weights_workspace(const PlanHeader* h) {
+  if (h->kv_dtype != MLA_KV_FP8_E4M3) return 0;
+  const size_t rows = (size_t)h->total_q * h->num_heads;
+  return (rows * 1152 + 255) / 256 * 256 + (rows * sizeof(float) + 255) / 256 * 256;
+}
+
+// [rows, 576] as (64 columns, rows, 9 pieces), boxes of box_rows rows and box_pieces pieces.
+CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* base, bool fp8, uint64_t rows,
+                uint32_t box_rows, uint32_t box_pieces) {
+  const uint64_t esz = fp8 ? 1 : 2;
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)kPieces};
+  cuuint64_t strides[2] = {(cuuint64_t)(kDqk * esz), (cuuint64_t)(64 * esz)};
+  cuuint32_t box[3] = {64, box_rows, box_pieces};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+}  // namespace
+}  // namespace mla
+
+using namespace mla;
+
+extern "C" int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* workspace_bytes_out) {
+  clear_error();
+  const PlanHeader* h = nullptr;
+  const int rc = check_plan(plan_host, plan_bytes, &h);
+  if (rc != MLA_OK) return rc;
+  if (!workspace_bytes_out) return set_error(MLA_ERR_INVALID_ARG, "workspace_bytes_out must not be NULL");
+  *workspace_bytes_out = weights_workspace(h);
+  return MLA_OK;
+}
+
+extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
+                               const void* kv_cache, const float* kv_scales, int block_tokens,
+                               const int32_t* page_table, int page_table_stride, int num_pages, const float* lse,
+                               const int32_t* counted, float sm_scale, float kv_scale, float decay, float* weights,
+                               long long weights_stride, void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                               void* stream) {
+  clear_error();
+  const PlanHeader* h = nullptr;
+  int rc = check_plan(plan_host, plan_bytes, &h);
+  if (rc != MLA_OK) return rc;
+  if (!plan_dev || !q || !kv_cache || !page_table || !lse || !weights)
+    return set_error(MLA_ERR_INVALID_ARG, "plan_dev, q, kv_cache, page_table, lse and weights must not be NULL");
+  if (((uintptr_t)plan_dev & 15u) || ((uintptr_t)q & 15u) || ((uintptr_t)kv_cache & 15u))
+    return set_error(MLA_ERR_INVALID_ARG, "plan_dev, q and kv_cache must be 16-byte aligned");
+  for (const void* ptr : {(const void*)page_table, (const void*)lse, (const void*)weights, (const void*)counted,
+                          (const void*)kv_scales, (const void*)status_dev})
+    if ((uintptr_t)ptr & 3u)
+      return set_error(MLA_ERR_INVALID_ARG, "page_table, lse, weights, counted, kv_scales and status_dev must be 4-byte aligned");
+  const bool fp8 = h->kv_dtype == MLA_KV_FP8_E4M3;
+  if (kv_scales && !fp8) return set_error(MLA_ERR_INVALID_ARG, "block scales belong to an fp8 e4m3 cache");
+  const int bl = kv_scales ? block_log2_of(block_tokens) : 0;
+  if (bl < 0) return set_error(MLA_ERR_UNSUPPORTED, "block_tokens must be 1, 2, 4, .. 64 (got %d)", block_tokens);
+  if (num_pages < 1 || (long long)num_pages * kPage > 0xFFFFFFFFLL)
+    return set_error(MLA_ERR_INVALID_ARG, "num_pages out of range (got %d)", num_pages);
+  if (page_table_stride < h->max_pages)
+    return set_error(MLA_ERR_INVALID_ARG, "page_table_stride %d is smaller than the %d pages of the longest request",
+                     page_table_stride, h->max_pages);
+  if (!(sm_scale > 0.f) || !isfinite(sm_scale) || !(kv_scale > 0.f) || !isfinite(kv_scale))
+    return set_error(MLA_ERR_INVALID_ARG, "sm_scale and kv_scale must be finite and > 0");
+  if (!isfinite(decay)) return set_error(MLA_ERR_INVALID_ARG, "decay must be finite");
+  // the lengths that the plan was built for
+  const PlanRequest* reqs = (const PlanRequest*)((const uint8_t*)plan_host + h->req_off);
+  int max_ctx = 0, most_rows = 0;
+  for (int i = 0; i < h->batch; ++i) {
+    max_ctx = std::max(max_ctx, reqs[i].ctx);
+    const int r = reqs[i].q * h->num_heads, g = (r + kMaxRows - 1) / kMaxRows;
+    most_rows = std::max(most_rows, ((r + g - 1) / g + 15) / 16 * 16);
+  }
+  if (weights_stride < max_ctx)
+    return set_error(MLA_ERR_INVALID_ARG, "weights_stride %lld is smaller than the longest request's %d keys",
+                     weights_stride, max_ctx);
+  const size_t need = weights_workspace(h);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return set_error(MLA_ERR_BUFFER, "workspace needs %zu bytes (got %zu)", need, workspace ? workspace_bytes : (size_t)0);
+  if (need > 0 && ((uintptr_t)workspace & 255u)) return set_error(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+
+  int dev = 0;
+  rc = current_device_ready(&dev);
+  if (rc != MLA_OK) return rc;
+  int sms = 0;
+  cudaError_t ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(ce));
+  const int stage = fp8 ? 8192 : 16384, tile_bytes = kPieces * stage;
+  const int fixed = 1024 + kMiscBytes + kPieces * most_rows * 128;
+  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / stage);
+  const int smem = fixed + stages * stage;
+  auto fn = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
+  ce = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(ce));
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return set_error(MLA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+
+  WeightsParams prm{};
+  prm.total_rows = h->total_q * h->num_heads;
+  long long tiles = 0;
+  for (int i = 0; i < h->batch; ++i) {
+    const long long t = (reqs[i].ctx + kKeys - 1) / kKeys;
+    tiles += t;
+    prm.total_work += t * ((reqs[i].q * h->num_heads + most_rows - 1) / most_rows);
+  }
+  const unsigned grid = (unsigned)std::min<long long>(tiles, sms);
+  prm.reqs = (const PlanRequest*)((const uint8_t*)plan_dev + h->req_off);
+  prm.batch = h->batch;
+  prm.H = h->num_heads;
+  prm.pt_stride = page_table_stride;
+  prm.num_pages = num_pages;
+  prm.block_log2 = bl;
+  prm.page_table = page_table;
+  prm.kv_scales = kv_scales;
+  prm.lse = lse;
+  prm.counted = counted;
+  prm.weights = weights;
+  prm.w_stride = weights_stride;
+  prm.decay = decay;
+  prm.scale_log2 = sm_scale * (fp8 && !kv_scales ? kv_scale : 1.f) * 1.4426950408889634f;
+  prm.rows_n = most_rows;
+  prm.stages = stages;
+  // tiles that all CTAs together keep in L2 while the groups pass over them
+  prm.sub_tiles = std::max(1, std::min<int>(kMaxSubSums, (int)((80LL << 20) / ((long long)tile_bytes * grid))));
+  prm.status = status_dev;
+  prm.wait_budget = kWaitBudget;
+  const void* q_src = q;
+  if (fp8) {
+    prm.q_scale = (const float*)((uint8_t*)workspace + ((size_t)prm.total_rows * 1152 + 255) / 256 * 256);
+    q_src = workspace;
+  }
+  alignas(64) CUtensorMap tq, tkv, tpage;
+  CUresult r = encode(enc, &tq, q_src, fp8, (uint64_t)prm.total_rows * (fp8 ? 2 : 1), (uint32_t)most_rows, 1);
+  if (r == CUDA_SUCCESS) r = encode(enc, &tkv, kv_cache, fp8, (uint64_t)num_pages * kPage, kPage, 1);
+  if (r == CUDA_SUCCESS) r = encode(enc, &tpage, kv_cache, fp8, (uint64_t)num_pages * kPage, kPage, kPieces);
+  if (r != CUDA_SUCCESS) return set_error(MLA_ERR_CUDA, "tensor map for q or kv_cache failed (CUresult %d)", (int)r);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (fp8) {
+    q_split_kernel<<<(prm.total_rows + kSplitWarps - 1) / kSplitWarps, 32 * kSplitWarps, 0, st>>>(
+        (const uint4*)q, prm.total_rows, (uint8_t*)workspace, const_cast<float*>(prm.q_scale));
+    ce = cudaGetLastError();
+    if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "Q split kernel launch: %s", cudaGetErrorString(ce));
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = fp8 ? 1 : 0;
+  ce = cudaLaunchKernelEx(&cfg, fn, tq, tkv, tpage, prm);
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "key weights kernel launch: %s", cudaGetErrorString(ce));
+  return MLA_OK;
+}

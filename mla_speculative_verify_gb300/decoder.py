@@ -14,6 +14,7 @@ import numpy as np
 import torch
 
 from . import binding
+from .cache import check_scales, check_status, check_tensor, device_guard
 
 KV_DTYPES = {"bf16": binding.MLA_KV_BF16, "fp8": binding.MLA_KV_FP8_E4M3}
 SM_SCALE = 1.0 / math.sqrt(192.0)
@@ -48,6 +49,7 @@ class VerifyDecoder:
         self.plan_host, self.workspace_bytes = binding.plan(self.seq_lens, self.q_lens, self.num_heads,
                                                             KV_DTYPES[kv_dtype], self.num_sms, options)
         self.info = binding.plan_info(self.plan_host)
+        self.weights_workspace_bytes = binding.key_weights_workspace(self.plan_host)
         # the plan runs on clusters of two CTAs (PlanHeader.cta_pair, the int32 at byte 64)
         self.cta_pair = bool(int(self.plan_host[64:68].view(np.int32)[0]))
         self.plan_dev = torch.from_numpy(self.plan_host).to(self.device)
@@ -60,7 +62,10 @@ class VerifyDecoder:
     def run(self, q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor, out: torch.Tensor,
             lse: torch.Tensor | None = None, sm_scale: float = SM_SCALE, kv_scale: float = 1.0,
             status: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None,
-            seq_lens_dev: torch.Tensor | None = None, q_lens_dev: torch.Tensor | None = None) -> None:
+            seq_lens_dev: torch.Tensor | None = None, q_lens_dev: torch.Tensor | None = None,
+            kv_scales: torch.Tensor | None = None) -> None:
+        """The verify decode. With ``kv_scales`` [pages, 64 / block_tokens] fp32 the e4m3 cache
+        is block-scaled: code * scale of its block (``kv_scale`` is then not used)."""
         H = self.num_heads
         want_kv = torch.bfloat16 if self.kv_dtype == "bf16" else torch.uint8
         if q.dtype != torch.bfloat16 or tuple(q.shape) != (self.total_q, H, 576) or not q.is_contiguous():
@@ -82,9 +87,59 @@ class VerifyDecoder:
             if t is not None and t.device != self.device:
                 raise ValueError("all tensors must be on the decoder's device")
         st = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if kv_scales is not None:
+            if self.kv_dtype != "fp8":
+                raise ValueError("block scales belong to an fp8 cache")
+            block = check_scales("kv_scales", kv_scales, rows // 64, self.device)
+            with device_guard(self.device):
+                binding.run_scaled(self.plan_dev.data_ptr(), self.plan_host, q.data_ptr(), kv_cache.data_ptr(),
+                                   kv_scales.data_ptr(), block, page_table.data_ptr(), page_table.shape[1], rows // 64,
+                                   (seq_lens_dev if seq_lens_dev is not None else self.seq_lens_dev).data_ptr(),
+                                   (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(),
+                                   sm_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
+                                   _ptr(status), st.cuda_stream)
+            return
         binding.run(self.plan_dev.data_ptr(), self.plan_host, q.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
                     page_table.shape[1], rows // 64,
                     (seq_lens_dev if seq_lens_dev is not None else self.seq_lens_dev).data_ptr(),
                     (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(),
                     sm_scale, kv_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
                     _ptr(status), st.cuda_stream)
+
+    def key_weights(self, q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor, lse: torch.Tensor,
+                    weights: torch.Tensor, decay: float = 1.0, counted: torch.Tensor | None = None,
+                    sm_scale: float = SM_SCALE, kv_scale: float = 1.0, kv_scales: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> None:
+        """After ``run``: add to ``weights`` [batch, >= longest request] fp32 what every cached
+        key received, weights = decay * weights + sum over rows of exp(score - lse), with the
+        ``lse`` that ``run`` wrote. ``counted`` [batch] int32: only the first so many verify
+        tokens of a request count (the accepted ones). Its scratch comes from torch's allocator,
+        call by call, so calls on several streams or captured in several graphs share none."""
+        H, batch, dev = self.num_heads, self.seq_lens.shape[0], self.device
+        if dev.type != "cuda":
+            raise ValueError("key_weights runs on a CUDA device")
+        check_tensor("q", q, torch.bfloat16, (self.total_q, H, 576), dev)
+        check_tensor("kv_cache", kv_cache,
+                     torch.bfloat16 if self.kv_dtype == "bf16" else (torch.uint8, torch.float8_e4m3fn),
+                     (None,) * (kv_cache.dim() - 1) + (576,), dev)
+        rows = kv_cache.numel() // 576
+        if rows % 64:
+            raise ValueError("kv_cache must hold whole 64-row pages")
+        block = 0 if kv_scales is None else check_scales("kv_scales", kv_scales, rows // 64, dev)
+        check_tensor("page_table", page_table, torch.int32, (batch, None), dev)
+        check_tensor("lse", lse, torch.float32, (self.total_q, H), dev)
+        check_tensor("weights", weights, torch.float32, (batch, None), dev)
+        if counted is not None:
+            check_tensor("counted", counted, torch.int32, (batch,), dev)
+        check_status(status, dev)
+        st = stream if stream is not None else torch.cuda.current_stream(dev)
+        need = self.weights_workspace_bytes
+        with device_guard(dev):
+            scratch = None
+            if need:
+                with torch.cuda.stream(st):
+                    scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+            binding.key_weights(self.plan_dev.data_ptr(), self.plan_host, q.data_ptr(), kv_cache.data_ptr(),
+                                _ptr(kv_scales), block, page_table.data_ptr(), page_table.shape[1], rows // 64,
+                                lse.data_ptr(), _ptr(counted), sm_scale, kv_scale, decay, weights.data_ptr(),
+                                weights.shape[1], _ptr(scratch), need, _ptr(status), st.cuda_stream)

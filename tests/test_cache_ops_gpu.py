@@ -1,0 +1,421 @@
+"""The cache operators on the GPU against plain 64-bit forms: append to a block-scaled e4m3
+cache, the decode over it, the accumulated key weights and the eviction, through the public
+entry points."""
+import numpy as np
+import pytest
+import torch
+
+from mla_speculative_verify_gb300 import binding, cache, inputs
+from mla_speculative_verify_gb300.decoder import VerifyDecoder
+from tests import cache_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+F8 = torch.float8_e4m3fn
+PAGE, D = 64, 576
+
+
+def dev(a):
+    return (torch.from_numpy(np.ascontiguousarray(a)) if isinstance(a, np.ndarray) else a).cuda()
+
+
+def same(got: torch.Tensor, want: np.ndarray):
+    assert np.array_equal(got.cpu().double().numpy(), want, equal_nan=True)
+
+
+# ------------------------------------------------------------------------------- append
+def append_case(lens_new, pasts, block, seed=0, magnitude=1.0):
+    """Host tensors of an append: filled cache, scales (powers of two), table, rows."""
+    g = torch.Generator().manual_seed(seed)
+    ends = np.asarray(lens_new) + np.asarray(pasts)
+    batch = ref.Batch(1, np.maximum(ends, 1), np.ones(len(ends)), "bf16", seed=seed, extra_pages=3, poison=False)
+    codes = (torch.randn((batch.pages, PAGE, D), generator=g) * 60).clamp(-448, 448).to(F8).view(torch.uint8)
+    scales = torch.exp2(torch.randint(-9, -3, (batch.pages, PAGE // block), generator=g).float())
+    rows = torch.randn((int(sum(lens_new)), D), generator=g) * magnitude
+    rows *= torch.exp2(torch.randint(-6, 6, (rows.shape[0], 1), generator=g).float())
+    return batch, codes, scales, rows.to(torch.bfloat16), ends.astype(np.int32), np.concatenate(
+        [[0], np.cumsum(lens_new)]).astype(np.int32)
+
+
+def run_append(batch, codes, scales, rows, ends, cu, max_new=None, stream=None):
+    c, s = codes.clone().cuda(), scales.clone().cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache.append(rows.cuda(), c, s, dev(batch.table), dev(ends), dev(cu),
+                 int(np.diff(cu).max()) if max_new is None else max_new, status, stream)
+    torch.cuda.synchronize()
+    return c, s, int(status.item())
+
+
+@pytest.mark.parametrize("block", [1, 2, 4, 8, 16, 32, 64])
+@pytest.mark.parametrize("lens_new,pasts", [([1], [0]), ([1], [63]), ([4, 1, 0, 7], [61, 64, 30, 5]),
+                                            ([130, 64, 1, 200], [0, 64, 127, 33]), ([63, 65], [1, 62])])
+def test_append(block, lens_new, pasts):
+    batch, codes, scales, rows, ends, cu = append_case(lens_new, pasts, block, seed=block)
+    values, want_s = ref.code_values(codes), scales.double().numpy()
+    ref.append(rows, values, want_s, batch.table, ends, cu, block)
+    c, s, status = run_append(batch, codes, scales, rows, ends, cu)
+    assert status == 0
+    same(c.view(F8), values)
+    same(s, want_s)
+
+
+def test_append_special_values():
+    """Zero rows, infinities, NaN, bf16's largest and least values, another writer's scale."""
+    batch, codes, scales, rows, ends, cu = append_case([40, 24], [10, 64], 16, seed=3)
+    rows[0:6] = 0
+    rows[7, 3], rows[8, 4], rows[9, 5] = float("inf"), float("-inf"), float("nan")
+    rows[30, :8] = torch.tensor([3.0e38, -3.0e38, 1e-40, 0.0, -0.0, 1.0, -1.0, 2e-38])
+    scales[batch.table[0, 0], 0] = 0.37  # not a power of two, and larger than the new rows ask for
+    values, want_s = ref.code_values(codes), scales.double().numpy()
+    ref.append(rows, values, want_s, batch.table, ends, cu, 16)
+    c, s, status = run_append(batch, codes, scales, rows, ends, cu)
+    assert status == 0
+    same(c.view(F8), values)
+    same(s, want_s)
+
+
+def test_append_twice_is_once():
+    """Appending the same rows again changes nothing (a replayed step)."""
+    batch, codes, scales, rows, ends, cu = append_case([5, 9], [60, 3], 32, seed=4)
+    c, s, _ = run_append(batch, codes, scales, rows, ends, cu)
+    c2, s2, _ = run_append(batch, c.cpu(), s.cpu(), rows, ends, cu)
+    assert torch.equal(c, c2) and torch.equal(s, s2)
+
+
+def test_append_bad_requests_write_nothing():
+    batch, codes, scales, rows, ends, cu = append_case([5, 9, 3], [60, 3, 0], 16, seed=5)
+    for bad, bit in (("page", binding.MLA_DEVICE_BAD_PAGE), ("more than max_new", binding.MLA_DEVICE_PLAN_MISMATCH),
+                     ("shorter than its rows", binding.MLA_DEVICE_PLAN_MISMATCH)):
+        table, e, most = batch.table.copy(), ends.copy(), 9
+        b2 = type("B", (), {"table": table})
+        if bad == "page":
+            table[1, 0] = batch.pages
+        elif bad == "more than max_new":
+            most = 8
+        else:
+            e[1] = 8
+        values, want_s = ref.code_values(codes), scales.double().numpy()
+        only = np.array([cu[0], cu[1], cu[1], cu[2]], np.int32)  # request 1 left out
+        ref.append(torch.cat([rows[:5], rows[14:]]), values, want_s, batch.table, np.array([ends[0], 0, ends[2]]),
+                   np.array([0, 5, 5, 8]), 16)
+        c, s, status = run_append(b2, codes, scales, rows, e, cu, max_new=most)
+        assert status == bit, bad
+        same(c.view(F8), values)
+        same(s, want_s)
+
+
+# ------------------------------------------------------------------------------- decode
+def decode(batch, options=None):
+    d = VerifyDecoder(batch.seq_lens, batch.q_lens, batch.H, "bf16" if batch.kind == "bf16" else "fp8", options=options)
+    out = torch.full((batch.q.shape[0], batch.H, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((batch.q.shape[0], batch.H), float("nan"), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    t = {"q": batch.q.cuda(), "kv": batch.kv.cuda(), "table": dev(batch.table),
+         "scales": None if batch.scales is None else batch.scales.cuda()}
+    d.run(t["q"], t["kv"], t["table"], out, lse, kv_scale=batch.kv_scale, status=status, kv_scales=t["scales"])
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    return d, t, out, lse
+
+
+SHAPES = [(12, [1], [1]), (12, [64], [3]), (1, [65], [2]), (12, [700], [8]), (33, [129, 64, 300], [1, 3, 2]),
+          (128, [200, 7], [2, 5]), (48, [513], [4]), (96, [260], [1])]
+
+
+@pytest.mark.parametrize("heads,seq,q", SHAPES)
+@pytest.mark.parametrize("block", [1, 16, 64])
+def test_decode_scaled(heads, seq, q, block):
+    batch = ref.Batch(heads, seq, q, "e4m3", block, seed=heads + block)
+    want, bound, lse, lse_bound = ref.attend(batch)
+    _, _, out, got_lse = decode(batch)
+    assert (np.abs(got_lse.cpu().double().numpy() - lse) <= lse_bound).all()
+    assert (np.abs(out.cpu().double().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("splits", [1, 5, 20])
+@pytest.mark.parametrize("spread", [0.0, 8.0])
+def test_decode_scaled_splits_and_spread(splits, spread):
+    """Split over the keys, and scales that lie up to 2^16 apart: blocks with a small scale hold
+    small values, and keys with a large one win the softmax of many rows."""
+    batch = ref.Batch(12, [64 * 20 + 5], [4], "e4m3", 32, spread=spread, seed=7)
+    want, bound, lse, lse_bound = ref.attend(batch)
+    _, _, out, got_lse = decode(batch, binding.PlanOptions(force_splits=splits))
+    assert (np.abs(got_lse.cpu().double().numpy() - lse) <= lse_bound).all()
+    assert (np.abs(out.cpu().double().numpy() - want) <= bound).all()
+
+
+def test_decode_scaled_zero_blocks_and_far_scales():
+    """Blocks with the scale 0 (values 0, weight as any score of 0) beside scales of 2^-40 and 2^-9."""
+    batch = ref.Batch(12, [640], [2], "e4m3", 64, spread=0.0, seed=8, poison=False)
+    page = batch.table[0]
+    batch.scales[page[1], 0] = 0.0
+    batch.scales[page[2], 0] = 2.0 ** -40
+    batch.scales[page[3], 0] = 2.0 ** -9
+    want, bound, lse, lse_bound = ref.attend(batch)
+    _, _, out, got_lse = decode(batch)
+    assert (np.abs(got_lse.cpu().double().numpy() - lse) <= lse_bound).all()
+    assert (np.abs(out.cpu().double().numpy() - want) <= bound).all()
+
+
+def test_decode_scaled_equal_scales_match_one_scale():
+    """A cache whose blocks all have one scale gives what the per-tensor scale gives, within both bounds."""
+    one = ref.Batch(12, [1000], [4], "e4m3", 0, seed=9, poison=False)
+    many = ref.Batch(12, [1000], [4], "e4m3", 0, seed=9, poison=False)
+    many.block, many.scales = 16, torch.full((many.pages, 4), many.kv_scale)
+    want, bound, _, _ = ref.attend(one)
+    _, _, a, la = decode(one)
+    _, _, b, lb = decode(many)
+    assert (np.abs(a.cpu().double().numpy() - want) <= bound).all()
+    assert (np.abs(b.cpu().double().numpy() - want) <= bound).all()
+    assert (la - lb).abs().max().item() <= 1e-5
+
+
+# ------------------------------------------------------------------------------- key weights
+def run_weights(batch, decay, old, counted=None, lse=None, d=None, t=None, stream=None):
+    if d is None:
+        d, t, _, lse = decode(batch)
+    w = torch.from_numpy(old.astype(np.float32)).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    d.key_weights(t["q"], t["kv"], t["table"], lse, w, decay, None if counted is None else dev(np.asarray(counted, np.int32)),
+                  kv_scale=batch.kv_scale, kv_scales=t["scales"], status=status, stream=stream)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    return w, lse
+
+
+KINDS = [("bf16", 0), ("e4m3", 0), ("e4m3", 1), ("e4m3", 64)]
+
+
+@pytest.mark.parametrize("kind,block", KINDS)
+@pytest.mark.parametrize("heads,seq,q", SHAPES)
+def test_key_weights(heads, seq, q, kind, block):
+    batch = ref.Batch(heads, seq, q, kind, block, seed=heads + block)
+    old = np.random.default_rng(1).random((len(seq), max(seq) + 3)).astype(np.float32)
+    w, lse = run_weights(batch, 0.75, old)
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 0.75, old)
+    got = w.cpu().double().numpy()
+    assert (np.abs(got - want) <= bound + 1e-30).all()
+    for b, n in enumerate(seq):  # behind the last key nothing is touched
+        assert np.array_equal(got[b, n:], old[b, n:].astype(np.float64))
+
+
+@pytest.mark.parametrize("kind,block", KINDS)
+def test_key_weights_many_rows(kind, block):
+    """Several groups of rows (up to 128 each) over several tiles, one of them short."""
+    batch = ref.Batch(96, [64 * 11 + 9, 300], [6, 3], kind, block, seed=21)
+    old = np.zeros((2, 713))
+    w, lse = run_weights(batch, 1.0, old)
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 1.0, old)
+    assert (np.abs(w.cpu().double().numpy() - want) <= bound + 1e-30).all()
+
+
+@pytest.mark.parametrize("kind,block", KINDS)
+def test_key_weights_counted_and_no_decay(kind, block):
+    """Only accepted tokens count; decay 0 does not read the old sums (NaN here)."""
+    batch = ref.Batch(40, [500, 90, 130], [5, 4, 3], kind, block, seed=22)
+    counted = [2, 0, 9]
+    old = np.full((3, 500), np.nan)
+    w, lse = run_weights(batch, 0.0, old, counted)
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 0.0, old, counted)
+    got = w.cpu().double().numpy()
+    for b, n in enumerate(batch.seq_lens):
+        assert (np.abs(got[b, :n] - want[b, :n]) <= bound[b, :n] + 1e-30).all()
+        assert np.isnan(got[b, n:]).all()
+
+
+def test_key_weights_of_hidden_rows():
+    """lse = -inf (a row that saw nothing) adds nothing; rows beside a request's, of another
+    request with NaN in its queries, do not reach it; equal calls give equal bits."""
+    batch = ref.Batch(12, [300, 200], [2, 2], "bf16", 0, seed=23)
+    d, t, _, lse = decode(batch)
+    t["q"][2:] = float("nan")
+    lse[0, :] = float("-inf")
+    old = np.zeros((2, 300))
+    w, _ = run_weights(batch, 1.0, old, lse=lse, d=d, t=t)
+    w2, _ = run_weights(batch, 1.0, old, lse=lse, d=d, t=t)
+    l = lse.cpu().double().numpy()
+    l[0, :] = np.inf
+    batch.seq_lens, batch.q_lens = batch.seq_lens[:1], batch.q_lens[:1]
+    want, bound = ref.weights(batch, l, 1.0, old)
+    assert (np.abs(w.cpu().double().numpy() - want)[0] <= bound[0] + 1e-30).all()
+    assert torch.equal(w[0], w2[0])
+
+
+def test_key_weights_sum_to_the_rows():
+    """Every row's weights sum to one, so a request's sums add up to its rows (a long context)."""
+    batch = ref.Batch(12, [20000, 9000], [4, 2], "bf16", 0, seed=24)
+    w, _ = run_weights(batch, 0.0, np.zeros((2, 20000)))
+    total = w.double().sum(1).cpu().numpy()
+    assert np.abs(total / [48, 24] - 1).max() < 1e-4
+
+
+# ------------------------------------------------------------------------------- evict
+def run_evict(batch, weights, budget, first, last, seed=0, max_seq=None, same_cache=True):
+    """Evicts into free pages of the batch's own cache (or another one); compares everything."""
+    lens = batch.seq_lens
+    kept_n = np.minimum(lens, budget)
+    per = (kept_n + PAGE - 1) // PAGE
+    table_dst = np.zeros((len(lens), max(1, int(per.max(initial=1)))), np.int32)
+    pool = list(batch.free) if same_cache else list(np.random.default_rng(seed).permutation(int(per.sum()) + 2))
+    for b, k in enumerate(per):
+        table_dst[b, :k] = [pool.pop() for _ in range(k)]
+    kv = batch.kv.cuda()
+    scales = None if batch.scales is None else batch.scales.cuda()
+    if same_cache:
+        kv_dst, scales_dst = kv, scales
+    else:
+        kv_dst = torch.zeros((int(per.sum()) + 2, PAGE, D), dtype=kv.dtype, device="cuda")
+        scales_dst = None if scales is None else torch.ones((kv_dst.shape[0], scales.shape[1]), device="cuda")
+    before = kv_dst.cpu(), None if scales is None else scales_dst.cpu()
+    kept = torch.full((len(lens), budget), -7, dtype=torch.int32, device="cuda")
+    lens_dst = torch.full((len(lens),), -7, dtype=torch.int32, device="cuda")
+    w_dst = torch.full((len(lens), budget + 1), -7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache.evict(dev(weights), dev(lens), budget, first, last, kv, dev(batch.table), kv_dst, dev(table_dst), kept,
+                lens_dst, w_dst, scales, scales_dst, max_seq, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    as_values = (lambda x: x.double().numpy()) if batch.kind == "bf16" else ref.code_values
+    values, values_dst = as_values(batch.kv), as_values(before[0])
+    s_dst = None if scales is None else before[1].double().numpy()
+    want = ref.evict(weights, lens, budget, first, last, values, None if scales is None else batch.scales.double().numpy(),
+                     batch.table, values_dst, s_dst, table_dst, batch.block)
+    for b, k in enumerate(want):
+        row = np.full(budget, -1)
+        row[:len(k)] = k
+        assert np.array_equal(kept[b].cpu().numpy(), row), b
+        assert int(lens_dst[b]) == len(k)
+        got_w = w_dst[b].cpu().numpy()
+        assert np.array_equal(got_w[:len(k)], weights[b, k], equal_nan=True) and (got_w[len(k):] == -7).all()
+    same(kv_dst if batch.kind == "bf16" else kv_dst.view(F8), values_dst)
+    if scales is not None:
+        same(scales_dst, s_dst)
+
+
+def evict_batch(seq, kind, block, seed):
+    """Free pages for twice the batch; weights heavy-tailed with many zeros and ties."""
+    pages = int(((np.asarray(seq) + PAGE - 1) // PAGE).sum())
+    batch = ref.Batch(1, seq, np.ones(len(seq)), kind, block, seed=seed, extra_pages=pages, poison=False)
+    g = np.random.default_rng(seed)
+    w = np.exp(2 * g.standard_normal((len(seq), max(seq) + 5))).astype(np.float32)
+    w[g.random(w.shape) < 0.2] = 0.0
+    w[g.random(w.shape) < 0.2] = 0.5
+    return batch, w
+
+
+@pytest.mark.parametrize("kind,block", [("bf16", 0), ("e4m3", 0), ("e4m3", 1), ("e4m3", 8), ("e4m3", 64)])
+@pytest.mark.parametrize("seq,budget,first,last", [([1], 1, 0, 0), ([500, 64, 65, 333], 64, 4, 8),
+                                                   ([300, 1, 100], 100, 0, 100), ([200, 201], 200, 3, 5),
+                                                   ([777], 33, 33, 0), ([130], 129, 0, 0)])
+def test_evict(seq, budget, first, last, kind, block):
+    batch, w = evict_batch(seq, kind, block, seed=budget + block)
+    run_evict(batch, w, budget, first, last)
+    run_evict(batch, w, budget, first, last, same_cache=False)
+
+
+@pytest.mark.parametrize("budget", [100, 9000, 39999])
+def test_evict_long(budget):
+    """Requests that several CTAs select over, beside short ones."""
+    batch, w = evict_batch([40000, 900, 17000], "e4m3", 16, seed=budget)
+    run_evict(batch, w, budget, 4, 50)
+
+
+def test_evict_special_weights():
+    """Ties decided by index, negative weights, infinities, NaN as the lowest, -0 as 0."""
+    batch, w = evict_batch([600, 600, 600, 600, 600], "bf16", 0, seed=31)
+    w[0] = 0.25
+    w[1] = -w[1] - 1
+    w[2, ::3], w[2, 1::3], w[2, 2::3] = np.inf, -np.inf, np.nan
+    w[3] = np.nan
+    w[4, ::2], w[4, 1::2] = 0.0, -0.0
+    run_evict(batch, w, 350, 5, 20)
+    run_evict(batch, w, 150, 0, 0)
+
+
+def test_evict_empty_and_unfit_lengths():
+    """A request without keys, and lengths outside [0, max_seq]."""
+    batch, w = evict_batch([300, 200, 100], "e4m3", 64, seed=32)
+    kept = torch.full((3, 64), -7, dtype=torch.int32, device="cuda")
+    lens_dst = torch.full((3,), -7, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv, scales = batch.kv.cuda(), batch.scales.cuda()
+    table_dst = dev(batch.free[:3].reshape(3, 1))
+    cache.evict(dev(w), dev(np.array([0, 306, -1], np.int32)), 64, 0, 0, kv, dev(batch.table), kv, table_dst, kept,
+                lens_dst, scales=scales, scales_dst=scales, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == binding.MLA_DEVICE_PLAN_MISMATCH
+    assert (kept == -1).all() and (lens_dst == 0).all()
+    assert torch.equal(kv.cpu(), batch.kv)
+
+
+# ------------------------------------------------------------------------------- together
+@pytest.mark.parametrize("block", [16, 64])
+def test_a_server_step(block):
+    """Append verify tokens, decode over them, add up the weights, evict, append again and decode
+    the shortened cache, as one program runs them, on a stream of its own and then from a graph."""
+    heads, q = 12, 4
+    past = np.array([250, 64, 131], np.int32)
+    seq = past + q
+    g = torch.Generator().manual_seed(block)
+    budget, first, last = 128, 4, 16
+    pages = 5 + 2 + 3
+    perm = torch.randperm(pages + 9, generator=g).int()
+    table = torch.zeros((3, 5), dtype=torch.int32)
+    table[0, :], table[1, :2], table[2, :3] = perm[:5], perm[5:7], perm[7:10]
+    table_dst = perm[10:19].view(3, 3)
+    codes = torch.zeros((pages + 9, PAGE, D), dtype=torch.uint8, device="cuda")
+    scales = torch.ones((pages + 9, PAGE // block), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    prompt = torch.randn((int(past.sum()), D), generator=g).to(torch.bfloat16)
+    new = torch.randn((3 * q, D), generator=g).to(torch.bfloat16)
+    queries = torch.randn((3 * q, heads, D), generator=g).to(torch.bfloat16)
+    new2 = torch.randn((3 * q, D), generator=g).to(torch.bfloat16)
+    cu = lambda n: dev(np.concatenate([[0], np.cumsum(n)]).astype(np.int32))  # noqa: E731
+    i32 = lambda n: dev(np.asarray(n, np.int32))  # noqa: E731
+    seq2 = np.minimum(seq, budget) + q
+    d1, d2 = VerifyDecoder(seq, [q] * 3, heads, "fp8"), VerifyDecoder(seq2, [q] * 3, heads, "fp8")
+    t = dict(table=table.cuda(), dst=table_dst.cuda(), prompt=prompt.cuda(), new=new.cuda(), new2=new2.cuda(),
+             q=queries.cuda(), past=i32(past), seq=i32(seq), seq2=i32(seq2), cu0=cu(past), cu=cu([q] * 3))
+    out, lse = torch.empty((3 * q, heads, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((3 * q, heads), device="cuda")
+    out2, w = torch.empty_like(out), torch.zeros((3, 260), device="cuda")
+    kept, lens_dst = torch.empty((3, budget), dtype=torch.int32, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda")
+
+    def step(stream=None):
+        cache.append(t["prompt"], codes, scales, t["table"], t["past"], t["cu0"], int(past.max()), status, stream)
+        cache.append(t["new"], codes, scales, t["table"], t["seq"], t["cu"], q, status, stream)
+        d1.run(t["q"], codes, t["table"], out, lse, status=status, stream=stream, kv_scales=scales)
+        d1.key_weights(t["q"], codes, t["table"], lse, w, decay=0.0, kv_scales=scales, status=status, stream=stream)
+        cache.evict(w, t["seq"], budget, first, last, codes, t["table"], codes, t["dst"], kept, lens_dst, None, scales,
+                    scales, max_seq=int(seq.max()), status=status, stream=stream)
+        cache.append(t["new2"], codes, scales, t["dst"], t["seq2"], t["cu"], q, status, stream)
+        d2.run(t["q"], codes, t["dst"], out2, lse, status=status, stream=stream, kv_scales=scales)
+
+    own = torch.cuda.Stream()
+    own.wait_stream(torch.cuda.current_stream())
+    step(own)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    got = [x.clone() for x in (out, out2, w, kept, lens_dst, codes, scales)]
+    # against the plain forms: the cache as it now stands, its rows' order from `kept`
+    batch = ref.Batch(heads, seq, [q] * 3, "e4m3", block, poison=False)
+    batch.q, batch.kv, batch.scales, batch.table = queries, codes.cpu(), scales.cpu(), table.numpy()
+    want, bound, _, _ = ref.attend(batch)
+    assert (np.abs(out.cpu().double().numpy() - want) <= bound).all()
+    for b, n in enumerate(seq):
+        assert kept[b].cpu().tolist() == list(ref.keep(w[b].cpu().numpy(), n, budget, first, last)) + [-1] * max(0, budget - n)
+    batch.seq_lens, batch.table = seq2, table_dst.numpy()
+    want, bound, _, _ = ref.attend(batch)
+    assert (np.abs(out2.cpu().double().numpy() - want) <= bound).all()
+    # captured, and replayed twice
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(2):
+        for x in (out, out2, w, kept, lens_dst):
+            x.zero_()
+        codes.zero_()
+        scales.fill_(1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (out, out2, w, kept, lens_dst, codes, scales)):
+            assert torch.equal(a, b)
