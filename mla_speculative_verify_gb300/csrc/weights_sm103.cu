@@ -24,9 +24,17 @@
 // 4, so entries down to 2^-9 of the row's largest are exact; below that the error is at most
 // 2^-18 of the largest. N = 2 * rows columns then hold both parts' scores.
 //
-// Warp roles (one CTA per SM): warp 0 loads (TMA), warp 1 issues the products, warps 4-7 and
-// 8-11 take alternate tiles' scores out of two accumulators. All of them walk the same work
-// list (Walk). Waits are bounded as in the decode kernel.
+// The tensor cores cut the bits below an accumulator's last one at every step, always towards
+// zero, so a score of 36 steps in one accumulator is off by ~2^-20 of itself: 1.9e-5 in the
+// weights of a million keys with scores of 20 and more. The columns are therefore summed in
+// parts (three for bf16, two for e4m3, whose steps are half as many), each in an accumulator
+// that starts at zero, and the parts are added in fp32 registers, rounded: 6.8e-6 there. A part
+// has an issuing warp of its own, since one thread issues a product only every ~100 cycles. The
+// accumulators form a ring, so the next tile's products run while this one's are read.
+//
+// Warp roles (one CTA per SM): warp 0 loads (TMA), warps 1-3 (e4m3: 1-2) issue the products, a part each,
+// warps 4-7 and 8-11 take the scores out, each half of the rows. All of them walk the same work list (Walk).
+// Waits are bounded as in the decode kernel.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -56,6 +64,18 @@ constexpr int kKeys = 128;          // keys per tile (two pages)
 constexpr int kPieces = 9;          // 576 = 9 x 64 columns
 constexpr int kMaxRows = 128;       // rows of a group
 constexpr int kMaxStages = 16;
+constexpr int kMaxSlots = 8;        // accumulators of the ring
+constexpr int kIssuers = 3;
+
+// The parts of a score's 576 columns and the ring sizes that go with them. Every ring place
+// belongs to one issuer for good (the ring's length is a multiple of the pieces or parts after
+// which the issuers repeat): a wait for a barrier's phase says nothing if the phase before it
+// may still be open, and only the warp that saw that one end can know that it is not.
+template <bool kFp8>
+struct Parts {
+  static constexpr int kCount = kFp8 ? 2 : 3;
+  static constexpr int kStageUnit = kFp8 ? kPieces : kCount;
+};
 constexpr int kMaxSub = 16;         // tiles of one sub-range: 32 page ids, one per lane
 constexpr int kMaxSubSums = 8;      // of those when sums wait in shared memory (G > 1)
 constexpr int kThreads = 384;
@@ -64,12 +84,13 @@ constexpr int kSmemCap = 232448;    // 227 KB per CTA
 struct WeightsMisc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[kPieces], q_empty[kPieces];
-  uint64_t d_full[2], d_empty[2], mma_done;
+  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done[kIssuers];
   uint32_t tmem_base;
   int abort;
-  alignas(16) float nlse[2][kMaxRows];   // per epilogue warpgroup: -lse * log2(e) of its current group's rows
-  alignas(16) float rscale[2][kMaxRows]; // e4m3: each row's part of its scores' scale
-  alignas(16) int lim[2][kMaxRows];      // keys that each row sees
+  alignas(16) float nlse[kMaxRows];    // -lse * log2(e) of the current group's rows
+  alignas(16) float rscale[kMaxRows];  // e4m3: each row's part of its scores' scale
+  alignas(16) int lim[kMaxRows];       // keys that each row sees
+  float half[2][kKeys];                // one warpgroup's sums of a tile, for the other
   alignas(16) float sums[kMaxSubSums][kKeys];
 };
 constexpr int kMiscBytes = (sizeof(WeightsMisc) + 1023) / 1024 * 1024;
@@ -85,7 +106,8 @@ struct WeightsParams {
   float* weights;
   long long w_stride;
   float decay, scale_log2;
-  int rows_n;              // MMA rows of every group (multiple of 16)
+  int rows_n;              // MMA rows of every group (multiple of 32)
+  int slots;               // accumulators in the ring
   int total_rows;
   int stages, sub_tiles;
   long long total_work;    // sum over requests of tiles * groups
@@ -153,10 +175,154 @@ struct Walk {
   }
 };
 
+// A place in a ring of n barriers and how often it has come round.
+struct Ring {
+  uint32_t n, at, phase;
+  __device__ __forceinline__ Ring(uint32_t n_, uint32_t first) : n(n_), at(0), phase(0) { step(first); }
+  __device__ __forceinline__ void step(uint32_t k) {
+    at += k;
+    while (at >= n) {
+      at -= n;
+      ++phase;
+    }
+  }
+};
+
 // Rows of request b that count (its first counted[b] tokens).
 __device__ __forceinline__ int counted_rows(const WeightsParams& p, int b, int q) {
   const int c = p.counted ? max(0, min(q, p.counted[b])) : q;
   return c * p.H;
+}
+
+// The epilogue warpgroups (wg 0 and 1, warps of quadrant qd): rows [16 NC wg, 16 NC (wg + 1))
+// of each group, N = 32 NC. A thread owns the key of its tensor-memory lane. One warpgroup
+// hands its half of a tile's sums to the other, in turns.
+template <int NC, bool kFp8>
+__device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc* ms, Walk& walk, uint32_t tmem, int wg,
+                                             int qd, int lane) {
+  constexpr int kCols = 16 * NC, n = 32 * NC;
+  constexpr uint32_t kSlotCols = kFp8 ? 2 * n : n;
+  const int key_in = 32 * qd + lane, col0 = kCols * wg;
+  const uint32_t acc0 = tmem + col0 + ((uint32_t)(32 * qd) << 16);
+  const float* nlse = ms->nlse + col0;
+  const float* rscale = ms->rscale + col0;
+  const int* lim = ms->lim + col0;
+  volatile int* abort = &ms->abort;
+  Ring slots(p.slots, 0);
+  uint32_t tiles = 0;  // tiles done so far
+  bool ok = true;
+  int b, t0, t1;
+  PlanRequest req;
+  while (walk.next(p, b, req, t0, t1)) {
+    const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
+    const int32_t* ids = p.page_table + (size_t)b * p.pt_stride;
+    float* wrow = p.weights + (size_t)b * p.w_stride;
+    if (groups == 0) {  // no row counts: the sums only decay
+      for (int t = t0 + wg; t < t1; t += 2) {
+        const int key = t * kKeys + key_in;
+        if (key < req.ctx) wrow[key] = p.decay == 0.f ? 0.f : wrow[key] * p.decay;
+      }
+      continue;
+    }
+    const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
+    for (int s0 = t0; s0 < t1; s0 += sub) {
+      const int s1 = min(t1, s0 + sub);
+      for (int g = 0; g < groups; ++g) {
+        const int mine = min(n, rows - g * n) - col0;  // rows of this warpgroup that are there (or none)
+        if (groups > 1 || s0 == t0) {
+          const int row0 = req.tok0 * p.H + g * n + col0;
+          ptx::bar_sync(1 + wg, 128);  // this warpgroup is done with the old table
+          if (key_in < kCols) {
+            const bool live = key_in < mine;
+            const float l = live ? p.lse[row0 + key_in] : INFINITY;
+            ms->nlse[col0 + key_in] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;  // a row that saw nothing adds nothing
+            if (kFp8) ms->rscale[col0 + key_in] = live ? p.scale_log2 * p.q_scale[row0 + key_in] : 0.f;
+            ms->lim[col0 + key_in] = live ? req.ctx - req.q + (g * n + col0 + key_in) / p.H + 1 : 0;
+          }
+          ptx::bar_sync(1 + wg, 128);
+        }
+        const int lim_min = req.ctx - req.q + g * n / p.H + 1;  // what the group's first row sees
+        for (int t = s0; t < s1; ++t, ++tiles) {
+          const int key = t * kKeys + key_in;
+          const bool live = key < req.ctx, writes = ((t - s0) & 1) == wg;
+          float old = 0.f, ks = kFp8 ? 1.f : p.scale_log2;  // the key's part of its scores' scale
+          if (writes && g == groups - 1 && live && p.decay != 0.f) old = wrow[key] * p.decay;
+          if (kFp8 && p.kv_scales && live) {
+            int id = ids[key / kPage];
+            id = id >= 0 && id < p.num_pages ? id : 0;
+            ks = p.kv_scales[((size_t)id * kPage + key % kPage) >> p.block_log2];
+          }
+          float x[kCols];
+#pragma unroll
+          for (int u = 0; u < Parts<kFp8>::kCount; ++u, slots.step(1)) {
+            const uint32_t slot = slots.at;
+            if (ok) ok = warp_wait(&ms->d_full[slot], slots.phase & 1, abort, p);
+            if (ok && mine > 0) {
+              ptx::tc_fence_after();
+              const uint32_t acc = acc0 + slot * kSlotCols;
+#pragma unroll
+              for (int h = 0; h < (kFp8 ? 2 : 1); ++h) {
+                float y[kCols];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) ptx::tmem_ld16(acc + h * n + 16 * c, y + 16 * c);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) x[j] = u == 0 && h == 0 ? y[j] : x[j] + y[j];
+              }
+              ptx::tc_fence_before();
+            }
+            __syncwarp();
+            if (ok && lane == 0) ptx::mbar_arrive(&ms->d_empty[slot]);
+          }
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+          if (ok && mine > 0) {
+            const bool all = (t + 1) * kKeys <= lim_min;  // every row sees every key of the tile
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              if (16 * c >= mine) break;
+              if constexpr (kFp8) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 r = *reinterpret_cast<const float4*>(rscale + 16 * c + j);
+                  x[16 * c + j] *= r.x;
+                  x[16 * c + j + 1] *= r.y;
+                  x[16 * c + j + 2] *= r.z;
+                  x[16 * c + j + 3] *= r.w;
+                }
+              }
+              if (all && 16 * c + 16 <= mine) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 l = *reinterpret_cast<const float4*>(nlse + 16 * c + j);
+                  s[0] += ex2(fmaf(x[16 * c + j], ks, l.x));
+                  s[1] += ex2(fmaf(x[16 * c + j + 1], ks, l.y));
+                  s[2] += ex2(fmaf(x[16 * c + j + 2], ks, l.z));
+                  s[3] += ex2(fmaf(x[16 * c + j + 3], ks, l.w));
+                }
+              } else {
+                // a row past the group, or one that does not see this key, holds anything
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  s[j & 3] += key < lim[16 * c + j] ? ex2(fmaf(x[16 * c + j], ks, nlse[16 * c + j])) : 0.f;
+              }
+            }
+          }
+          float w = (s[0] + s[1]) + (s[2] + s[3]);
+          if (!writes) ms->half[tiles & 1][key_in] = w;
+          ptx::bar_sync(3, 256);  // alternate buffers: the next tile's barrier closes this one's
+          if (writes) {
+            w += ms->half[tiles & 1][key_in];
+            if (groups > 1) {
+              float* slot = &ms->sums[t - s0][key_in];  // this thread's own, through all groups
+              if (g > 0) w += *slot;
+              *slot = w;
+            }
+            if (ok && g == groups - 1 && live) wrow[key] = old + w;
+          }
+        }
+      }
+    }
+  }
 }
 
 template <bool kFp8>
@@ -166,7 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kRowBytes = kFp8 ? 64 : 128;             // a row's bytes in one 64-column piece
   constexpr int kStageBytes = kKeys * kRowBytes;
   constexpr int kHalf = kPage * kRowBytes;               // one page of a piece
-  constexpr uint32_t kAccCols = kFp8 ? 256 : 128;        // tensor-memory columns of an accumulator
   constexpr uint32_t kSwizzle = kFp8 ? ptx::kSwizzle64B : ptx::kSwizzle128B;
   constexpr uint32_t kSbo = 8 * kRowBytes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -189,11 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ms->q_full[i], 1);
       ptx::mbar_init(&ms->q_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < p.slots; ++i) {
       ptx::mbar_init(&ms->d_full[i], 1);
-      ptx::mbar_init(&ms->d_empty[i], 4);
+      ptx::mbar_init(&ms->d_empty[i], 8);
     }
-    ptx::mbar_init(&ms->mma_done, 1);
+    for (int i = 0; i < kIssuers; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmap_q);
     ptx::prefetch_tmap(&tmap_kv);
@@ -213,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
-    uint32_t fill = 0, qfill = 0;       // ring pieces and Q groups loaded so far
+    Ring ring(p.stages, 0);
+    uint32_t fill = 0, qfill = 0;       // pieces and Q groups loaded so far
     bool ok = true;
     while (ok && walk.next(p, b, req, t0, t1)) {
       const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
@@ -261,9 +427,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
               }
-              const uint32_t st = fill % p.stages, use = fill / p.stages;
-              if (use > 0) ok = warp_wait(&ms->kv_empty[st], (use - 1) & 1, abort, p);
+              const uint32_t st = ring.at;
+              if (ring.phase > 0) ok = warp_wait(&ms->kv_empty[st], (ring.phase - 1) & 1, abort, p);
               if (!ok) break;
+              ring.step(1);
               if (lane == 0) {
                 uint8_t* dst = sK + st * kStageBytes;
                 ptx::mbar_arrive_expect_tx(&ms->kv_full[st], two ? 2 * kHalf : kHalf);
@@ -294,11 +461,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= Parts<kFp8>::kCount) {
     // ------------------------------------------------------------ products
+    // Warp 1 + i issues part i of every tile into an accumulator that no other thread writes.
+    // bf16: a part is pieces i, i + 3, i + 6, so that neighbouring pieces have different issuers
+    // and all three work at once. e4m3: pieces 0-4 and 5-8, so that with up to 128 rows, whose
+    // 2 x 256 columns leave two accumulators, one is read while the other is filled; a product
+    // of 256 columns takes longer than its issue anyway.
+    const int mi = warp - 1;
+    const int count = kFp8 ? 5 - mi : 3;  // pieces of this part
+    auto piece = [&](int i) { return kFp8 ? 5 * mi + i : mi + 3 * i; };
     const uint32_t sq = ptx::smem_addr(sQ), sk = ptx::smem_addr(sK);
     const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kKeys, 2 * n, 0, 0) : ptx::idesc_bf16(kKeys, n, 0, 0);
-    uint32_t fill = 0, qfill = 0, used[2] = {0, 0};
+    const uint32_t slot_cols = kFp8 ? 2 * n : n;
+    const bool leader = ptx::elect_one();
+    Ring ring(p.stages, piece(0)), slots(p.slots, mi);
+    uint32_t qphase = 0;
     bool ok = true, issued = false;
     while (ok && walk.next(p, b, req, t0, t1)) {
       const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
@@ -309,142 +487,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; ok && g < groups; ++g) {
           const bool new_q = groups > 1 || s0 == t0, last_q = groups > 1 || s1 == t1;
           for (int t = s0; ok && t < s1; ++t) {
-            const int buf = (t - s0) & 1;
-            if (used[buf] > 0) ok = warp_wait(&ms->d_empty[buf], (used[buf] - 1) & 1, abort, p);
-            for (int c = 0; ok && c < kPieces; ++c, ++fill) {
-              if (new_q && t == s0) ok = warp_wait(&ms->q_full[c], qfill & 1, abort, p);
-              const uint32_t st = fill % p.stages;
-              if (ok) ok = warp_wait(&ms->kv_full[st], (fill / p.stages) & 1, abort, p);
+            if (slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
+            const uint32_t d = tmem + slots.at * slot_cols;
+            for (int i = 0; i < count; ++i) {
+              const int c = piece(i);
+              if (ok && new_q && t == s0) ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
+              if (ok) ok = warp_wait(&ms->kv_full[ring.at], ring.phase & 1, abort, p);
               if (!ok) break;
               ptx::tc_fence_after();
-              if (lane == 0) {
-                const uint32_t d = tmem + buf * kAccCols, a0 = sk + st * kStageBytes, b0 = sq + c * q_piece;
+              const uint32_t a0 = sk + ring.at * kStageBytes, b0 = sq + c * q_piece;
+              const uint64_t ad = ptx::smem_desc(a0, 16, kSbo, kSwizzle), bd = ptx::smem_desc(b0, 16, kSbo, kSwizzle);
+              if (leader) {
 #pragma unroll
-                for (int k = 0; k < kRowBytes / 32; ++k) {
-                  const uint64_t ad = ptx::smem_desc(a0 + 32 * k, 16, kSbo, kSwizzle);
-                  const uint64_t bd = ptx::smem_desc(b0 + 32 * k, 16, kSbo, kSwizzle);
+                for (int k = 0; k < kRowBytes / 32; ++k) {  // 32 bytes on: 2 in the address field's units
                   if constexpr (kFp8)
-                    ptx::mma_e4m3_ss(d, ad, bd, idesc, (c | k) != 0 ? 1u : 0u);
+                    ptx::mma_e4m3_ss(d, ad + 2 * k, bd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
                   else
-                    ptx::mma_bf16_ss(d, ad, bd, idesc, (c | k) != 0 ? 1u : 0u);
+                    ptx::mma_bf16_ss(d, ad + 2 * k, bd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
                 }
-                ptx::mma_commit(&ms->kv_empty[st]);
+                ptx::mma_commit(&ms->kv_empty[ring.at]);
                 if (last_q && t == s1 - 1) ptx::mma_commit(&ms->q_empty[c]);
-                if (c == kPieces - 1) ptx::mma_commit(&ms->d_full[buf]);
+                if (i == count - 1) ptx::mma_commit(&ms->d_full[slots.at]);
               }
               __syncwarp();
+              ring.step(!kFp8 ? 3 : i < count - 1 ? 1 : kPieces - count + 1);
               issued = true;
             }
-            ++used[buf];
+            slots.step(Parts<kFp8>::kCount);
           }
-          if (new_q) ++qfill;
+          if (new_q) ++qphase;
         }
       }
     }
     // every product must retire before tensor memory is released
-    if (issued && lane == 0) drain_mmas(&ms->mma_done, p.wait_budget);
+    if (issued && leader) drain_mmas(&ms->mma_done[mi], p.wait_budget);
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ weights
-    const int wg = (warp - 4) >> 2, qd = warp & 3, key_in = 32 * qd + lane, wtid = tid & 127;
-    const uint32_t acc = tmem + wg * kAccCols + ((uint32_t)(32 * qd) << 16);
-    float* nlse = ms->nlse[wg];
-    float* rscale = ms->rscale[wg];
-    int* lim = ms->lim[wg];
+    const int wg = (warp - 4) >> 2, qd = warp & 3;
     if (kFp8) ptx::pdl_wait_primary();  // q_scale comes from the kernel before
-    uint32_t used = 0;
-    bool ok = true;
-    while (walk.next(p, b, req, t0, t1)) {
-      const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
-      const int32_t* ids = p.page_table + (size_t)b * p.pt_stride;
-      float* wrow = p.weights + (size_t)b * p.w_stride;
-      if (groups == 0) {  // no row counts: the sums only decay
-        for (int t = t0 + wg; t < t1; t += 2) {
-          const int key = t * kKeys + wtid;
-          if (key < req.ctx) wrow[key] = p.decay == 0.f ? 0.f : wrow[key] * p.decay;
-        }
-        continue;
-      }
-      const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
-      for (int s0 = t0; s0 < t1; s0 += sub) {
-        const int s1 = min(t1, s0 + sub);
-        for (int g = 0; g < groups; ++g) {
-          const int nrows = min(n, rows - g * n), row0 = req.tok0 * p.H + g * n;
-          if (groups > 1 || s0 == t0) {
-            ptx::bar_sync(1 + wg, 128);  // this warpgroup is done with the old table
-            if (wtid < n) {
-              const bool live = wtid < nrows;
-              const float l = live ? p.lse[row0 + wtid] : INFINITY;
-              nlse[wtid] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;  // a row that saw nothing adds nothing
-              if (kFp8) rscale[wtid] = live ? p.scale_log2 * p.q_scale[row0 + wtid] : 0.f;
-              lim[wtid] = live ? req.ctx - req.q + (g * n + wtid) / p.H + 1 : 0;
-            }
-            ptx::bar_sync(1 + wg, 128);
-          }
-          const int lim_min = lim[0];
-          for (int t = s0 + wg; t < s1; t += 2) {
-            const int key = t * kKeys + key_in;
-            const bool live = key < req.ctx;
-            float old = 0.f, ks = kFp8 ? 1.f : p.scale_log2;  // the key's part of its scores' scale
-            if (g == groups - 1 && live && p.decay != 0.f) old = wrow[key] * p.decay;
-            if (kFp8 && p.kv_scales && live) {
-              int id = ids[key / kPage];
-              id = id >= 0 && id < p.num_pages ? id : 0;
-              ks = p.kv_scales[((size_t)id * kPage + key % kPage) >> p.block_log2];
-            }
-            if (ok) ok = warp_wait(&ms->d_full[wg], used & 1, abort, p);
-            ++used;
-            if (!ok) continue;
-            ptx::tc_fence_after();
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            const bool all = (t + 1) * kKeys <= lim_min;  // every row sees every key of the tile
-            for (int c = 0; 16 * c < nrows; ++c) {
-              float x[16];
-              ptx::tmem_ld16(acc + 16 * c, x);
-              if constexpr (kFp8) {
-                float y[16];
-                ptx::tmem_ld16(acc + n + 16 * c, y);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 r = *reinterpret_cast<const float4*>(rscale + 16 * c + j);
-                  x[j] = (x[j] + y[j]) * r.x;
-                  x[j + 1] = (x[j + 1] + y[j + 1]) * r.y;
-                  x[j + 2] = (x[j + 2] + y[j + 2]) * r.z;
-                  x[j + 3] = (x[j + 3] + y[j + 3]) * r.w;
-                }
-              } else {
-                ptx::tmem_ld_wait();
-              }
-              if (all && 16 * c + 16 <= nrows) {
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 l = *reinterpret_cast<const float4*>(nlse + 16 * c + j);
-                  s[0] += ex2(fmaf(x[j], ks, l.x));
-                  s[1] += ex2(fmaf(x[j + 1], ks, l.y));
-                  s[2] += ex2(fmaf(x[j + 2], ks, l.z));
-                  s[3] += ex2(fmaf(x[j + 3], ks, l.w));
-                }
-              } else {
-                // a row past the group, or one that does not see this key, holds anything
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s[j & 3] += key < lim[16 * c + j] ? ex2(fmaf(x[j], ks, nlse[16 * c + j])) : 0.f;
-              }
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&ms->d_empty[wg]);
-            float w = (s[0] + s[1]) + (s[2] + s[3]);
-            if (groups > 1) {
-              float* slot = &ms->sums[t - s0][key_in];  // this thread's own, through all groups
-              if (g > 0) w += *slot;
-              *slot = w;
-            }
-            if (g == groups - 1 && live) wrow[key] = old + w;
-          }
-        }
-      }
-    }
+    if (n == 32)
+      weights_role<1, kFp8>(p, ms, walk, tmem, wg, qd, lane);
+    else if (n == 64)
+      weights_role<2, kFp8>(p, ms, walk, tmem, wg, qd, lane);
+    else if (n == 96)
+      weights_role<3, kFp8>(p, ms, walk, tmem, wg, qd, lane);
+    else
+      weights_role<4, kFp8>(p, ms, walk, tmem, wg, qd, lane);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -571,7 +660,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   for (int i = 0; i < h->batch; ++i) {
     max_ctx = std::max(max_ctx, reqs[i].ctx);
     const int r = reqs[i].q * h->num_heads, g = (r + kMaxRows - 1) / kMaxRows;
-    most_rows = std::max(most_rows, ((r + g - 1) / g + 15) / 16 * 16);
+    most_rows = std::max(most_rows, ((r + g - 1) / g + 31) / 32 * 32);
   }
   if (weights_stride < max_ctx)
     return set_error(MLA_ERR_INVALID_ARG, "weights_stride %lld is smaller than the longest request's %d keys",
@@ -589,7 +678,9 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(ce));
   const int stage = fp8 ? 8192 : 16384, tile_bytes = kPieces * stage;
   const int fixed = 1024 + kMiscBytes + kPieces * most_rows * 128;
-  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / stage);
+  const int unit = fp8 ? Parts<true>::kStageUnit : Parts<false>::kStageUnit;
+  const int parts = fp8 ? Parts<true>::kCount : Parts<false>::kCount;
+  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / stage) / unit * unit;
   const int smem = fixed + stages * stage;
   auto fn = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
   ce = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
@@ -622,6 +713,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   prm.scale_log2 = sm_scale * (fp8 && !kv_scales ? kv_scale : 1.f) * 1.4426950408889634f;
   prm.rows_n = most_rows;
   prm.stages = stages;
+  prm.slots = std::min(kMaxSlots, 512 / (fp8 ? 2 * most_rows : most_rows)) / parts * parts;
   // tiles that all CTAs together keep in L2 while the groups pass over them
   prm.sub_tiles = std::max(1, std::min<int>(kMaxSubSums, (int)((80LL << 20) / ((long long)tile_bytes * grid))));
   prm.status = status_dev;
