@@ -64,18 +64,14 @@ constexpr int kKeys = 128;          // keys per tile (two pages)
 constexpr int kPieces = 9;          // 576 = 9 x 64 columns
 constexpr int kMaxRows = 128;       // rows of a group
 constexpr int kMaxStages = 16;
+constexpr int kParts = 3;           // parts of a score's 576 columns, three pieces each
+constexpr int kPartPieces = kPieces / kParts;
 constexpr int kMaxSlots = 8;        // accumulators of the ring
-constexpr int kIssuers = 3;
-
-// The parts of a score's 576 columns and the ring sizes that go with them. Every ring place
-// belongs to one issuer for good (the ring's length is a multiple of the pieces or parts after
-// which the issuers repeat): a wait for a barrier's phase says nothing if the phase before it
-// may still be open, and only the warp that saw that one end can know that it is not.
-template <bool kFp8>
-struct Parts {
-  static constexpr int kCount = kFp8 ? 2 : 3;
-  static constexpr int kStageUnit = kFp8 ? kPieces : kCount;
-};
+// Pieces that share a stage of the ring. The issuer's waits and commits cost it ~300 cycles a
+// stage, more than the products of an e4m3 piece take, so three of those go together (batch
+// of 128 heads 207 -> 179 us). bf16 pieces are twice as large: two stages of three would be all
+// that fits, and the copies stall (a million keys 202 -> 208 us).
+__host__ __device__ constexpr int pieces_per_stage(bool fp8) { return fp8 ? 3 : 1; }
 constexpr int kMaxSub = 16;         // tiles of one sub-range: 32 page ids, one per lane
 constexpr int kMaxSubSums = 8;      // of those when sums wait in shared memory (G > 1)
 constexpr int kThreads = 384;
@@ -84,7 +80,7 @@ constexpr int kSmemCap = 232448;    // 227 KB per CTA
 struct WeightsMisc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[kPieces], q_empty[kPieces];
-  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done[kIssuers];
+  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done;
   uint32_t tmem_base;
   int abort;
   alignas(16) float nlse[kMaxRows];    // -lse * log2(e) of the current group's rows
@@ -178,11 +174,10 @@ struct Walk {
 // A place in a ring of n barriers and how often it has come round.
 struct Ring {
   uint32_t n, at, phase;
-  __device__ __forceinline__ Ring(uint32_t n_, uint32_t first) : n(n_), at(0), phase(0) { step(first); }
-  __device__ __forceinline__ void step(uint32_t k) {
-    at += k;
-    while (at >= n) {
-      at -= n;
+  __device__ __forceinline__ explicit Ring(uint32_t n_) : n(n_), at(0), phase(0) {}
+  __device__ __forceinline__ void step() {
+    if (++at == n) {
+      at = 0;
       ++phase;
     }
   }
@@ -208,7 +203,7 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
   const float* rscale = ms->rscale + col0;
   const int* lim = ms->lim + col0;
   volatile int* abort = &ms->abort;
-  Ring slots(p.slots, 0);
+  Ring slots(p.slots);
   uint32_t tiles = 0;  // tiles done so far
   bool ok = true;
   int b, t0, t1;
@@ -254,7 +249,7 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
           }
           float x[kCols];
 #pragma unroll
-          for (int u = 0; u < Parts<kFp8>::kCount; ++u, slots.step(1)) {
+          for (int u = 0; u < kParts; ++u, slots.step()) {
             const uint32_t slot = slots.at;
             if (ok) ok = warp_wait(&ms->d_full[slot], slots.phase & 1, abort, p);
             if (ok && mine > 0) {
@@ -330,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv,
                        const __grid_constant__ CUtensorMap tmap_page, WeightsParams p) {
   constexpr int kRowBytes = kFp8 ? 64 : 128;             // a row's bytes in one 64-column piece
-  constexpr int kStageBytes = kKeys * kRowBytes;
+  constexpr int kPieceBytes = kKeys * kRowBytes;
+  constexpr int kPer = pieces_per_stage(kFp8);
+  constexpr int kStageBytes = kPer * kPieceBytes;
   constexpr int kHalf = kPage * kRowBytes;               // one page of a piece
   constexpr uint32_t kSwizzle = kFp8 ? ptx::kSwizzle64B : ptx::kSwizzle128B;
   constexpr uint32_t kSbo = 8 * kRowBytes;
@@ -347,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     ms->abort = 0;
     for (int i = 0; i < p.stages; ++i) {
-      ptx::mbar_init(&ms->kv_full[i], 1);
+      ptx::mbar_init(&ms->kv_full[i], 2);  // a producer for each of the two pages
       ptx::mbar_init(&ms->kv_empty[i], 1);
     }
     for (int i = 0; i < kPieces; ++i) {
@@ -358,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ms->d_full[i], 1);
       ptx::mbar_init(&ms->d_empty[i], 8);
     }
-    for (int i = 0; i < kIssuers; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
+    ptx::mbar_init(&ms->mma_done, 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmap_q);
     ptx::prefetch_tmap(&tmap_kv);
@@ -375,11 +372,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int b, t0, t1;
   PlanRequest req;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ loads
+    // Warp 0 loads the first page of each tile and Q, warp 2 the second page: a copy takes its
+    // issuer ~150 cycles, and a tile has 18.
+    const int second = warp >> 1;
     if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
-    Ring ring(p.stages, 0);
-    uint32_t fill = 0, qfill = 0;       // pieces and Q groups loaded so far
+    Ring ring(p.stages);
+    uint32_t qfill = 0;  // Q groups loaded so far
     bool ok = true;
     while (ok && walk.next(p, b, req, t0, t1)) {
       const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
@@ -387,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
       const int npages = (req.ctx + kPage - 1) / kPage;
       const int32_t* ids = p.page_table + (size_t)b * p.pt_stride;
-      auto load_ids = [&](int tile) {
-        const int pg = 2 * tile + lane;
-        int id = pg < min(npages, 2 * t1) && lane < 2 * sub ? ids[pg] : 0;
+      auto load_ids = [&](int tile) {  // lane l: this producer's page of tile `tile` + l
+        const int pg = 2 * (tile + lane) + second;
+        int id = lane < sub && tile + lane < t1 && pg < npages ? ids[pg] : 0;
         if (id < 0 || id >= p.num_pages) {
           report(p.status, MLA_DEVICE_BAD_PAGE);
           id = 0;
@@ -403,23 +403,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; ok && g < groups; ++g) {
           const bool new_q = groups > 1 || s0 == t0;
           for (int t = s0; ok && t < s1; ++t) {
-            const int pg = 2 * (t - s0);
-            const bool two = 2 * t + 1 < npages;
-            const int id0 = __shfl_sync(0xffffffffu, cur, pg), id1 = __shfl_sync(0xffffffffu, cur, pg + 1);
-            // ask L2 for whole pages of the next tile that HBM has to deliver
-            const int tn = g == 0 && t + 1 < s1 ? t + 1 : g == groups - 1 && t + 1 == s1 ? s1 : -1;
-            const int pn = t + 1 < s1 ? pg + 2 : 0;
-            const int n0 = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur, pn & 31) : __shfl_sync(0xffffffffu, nxt, 0);
-            const int n1 = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur, (pn + 1) & 31) : __shfl_sync(0xffffffffu, nxt, 1);
-            if (lane == 0 && tn >= 0 && tn < t1) {
-              ptx::tma_prefetch_l2_3d(&tmap_page, 0, n0 * kPage, 0);
-              if (2 * tn + 1 < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, n1 * kPage, 0);
-            }
-            for (int c = 0; ok && c < kPieces; ++c, ++fill) {
-              if (new_q && t == s0) {
+            const bool there = 2 * t + second < npages;
+            const int id = __shfl_sync(0xffffffffu, cur, t - s0);
+            // ask L2 for the whole page of the next tile that HBM has to deliver
+            const int tn = g == 0 && t + 1 < s1 ? t + 1 : g == groups - 1 && t + 1 == s1 ? s1 : t1;
+            const int id_n = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur, (t - s0 + 1) & 31) : __shfl_sync(0xffffffffu, nxt, 0);
+            if (tn < t1 && 2 * tn + second < npages && ptx::elect_one())
+              ptx::tma_prefetch_l2_3d(&tmap_page, 0, id_n * kPage, 0);
+            for (int c0 = 0; ok && c0 < kPieces; c0 += kPer) {
+              for (int c = c0; !second && new_q && t == s0 && c < c0 + kPer; ++c) {
                 if (qfill > 0) ok = warp_wait(&ms->q_empty[c], (qfill - 1) & 1, abort, p);
                 if (!ok) break;
-                if (lane == 0) {
+                if (ptx::elect_one()) {
                   const int row = req.tok0 * p.H + g * n;
                   ptx::mbar_arrive_expect_tx(&ms->q_full[c], q_piece);
                   ptx::tma_load_3d(sQ + c * q_piece, &tmap_q, &ms->q_full[c], 0, row, c);
@@ -427,17 +422,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
               }
-              const uint32_t st = ring.at;
-              if (ring.phase > 0) ok = warp_wait(&ms->kv_empty[st], (ring.phase - 1) & 1, abort, p);
+              if (ok && ring.phase > 0) ok = warp_wait(&ms->kv_empty[ring.at], (ring.phase - 1) & 1, abort, p);
               if (!ok) break;
-              ring.step(1);
-              if (lane == 0) {
-                uint8_t* dst = sK + st * kStageBytes;
-                ptx::mbar_arrive_expect_tx(&ms->kv_full[st], two ? 2 * kHalf : kHalf);
-                ptx::tma_load_3d(dst, &tmap_kv, &ms->kv_full[st], 0, id0 * kPage, c);
-                if (two) ptx::tma_load_3d(dst + kHalf, &tmap_kv, &ms->kv_full[st], 0, id1 * kPage, c);
+              if (ptx::elect_one()) {
+                if (there) {
+                  ptx::mbar_arrive_expect_tx(&ms->kv_full[ring.at], kPer * kHalf);
+#pragma unroll
+                  for (int j = 0; j < kPer; ++j)
+                    ptx::tma_load_3d(sK + ring.at * kStageBytes + j * kPieceBytes + second * kHalf, &tmap_kv,
+                                     &ms->kv_full[ring.at], 0, id * kPage, c0 + j);
+                } else {
+                  ptx::mbar_arrive(&ms->kv_full[ring.at]);
+                }
               }
               __syncwarp();
+              ring.step();
             }
           }
           if (new_q) ++qfill;
@@ -445,37 +444,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur = nxt;
       }
     }
-    // every copy must have landed before the CTA may exit: the last ones of the ring, and of
-    // the Q pieces (a piece that the loop gave up on has none in flight)
+    // After an abort every copy must have landed before the CTA may exit: the ring's last ones
+    // and the Q pieces'. A phase that the other producer never completes, or that is not open,
+    // ends by the shorter limit.
     if (*abort && lane == 0) {
-      for (uint32_t f = fill > (uint32_t)p.stages ? fill - p.stages : 0; f < fill; ++f) {
-        const long long t0c = clock64();
-        while (!ptx::mbar_try_wait(&ms->kv_full[f % p.stages], (f / p.stages) & 1) && clock64() - t0c < p.wait_budget) {
-        }
-      }
-      for (int c = 0; c < kPieces; ++c)
+      for (int i = 0; i < p.stages + kPieces; ++i)
         for (uint32_t par = 0; par < 2; ++par) {
+          uint64_t* bar = i < p.stages ? &ms->kv_full[i] : &ms->q_full[i - p.stages];
           const long long t0c = clock64();
-          while (!ptx::mbar_try_wait(&ms->q_full[c], par) && clock64() - t0c < kWaitBudgetTest) {
+          while (!ptx::mbar_try_wait(bar, par) && clock64() - t0c < kWaitBudgetTest) {
           }
         }
     }
     __syncwarp();
-  } else if (warp <= Parts<kFp8>::kCount) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    // Warp 1 + i issues part i of every tile into an accumulator that no other thread writes.
-    // bf16: a part is pieces i, i + 3, i + 6, so that neighbouring pieces have different issuers
-    // and all three work at once. e4m3: pieces 0-4 and 5-8, so that with up to 128 rows, whose
-    // 2 x 256 columns leave two accumulators, one is read while the other is filled; a product
-    // of 256 columns takes longer than its issue anyway.
-    const int mi = warp - 1;
-    const int count = kFp8 ? 5 - mi : 3;  // pieces of this part
-    auto piece = [&](int i) { return kFp8 ? 5 * mi + i : mi + 3 * i; };
     const uint32_t sq = ptx::smem_addr(sQ), sk = ptx::smem_addr(sK);
     const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kKeys, 2 * n, 0, 0) : ptx::idesc_bf16(kKeys, n, 0, 0);
     const uint32_t slot_cols = kFp8 ? 2 * n : n;
-    const bool leader = ptx::elect_one();
-    Ring ring(p.stages, piece(0)), slots(p.slots, mi);
+    Ring ring(p.stages), slots(p.slots);
     uint32_t qphase = 0;
     bool ok = true, issued = false;
     while (ok && walk.next(p, b, req, t0, t1)) {
@@ -487,40 +474,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; ok && g < groups; ++g) {
           const bool new_q = groups > 1 || s0 == t0, last_q = groups > 1 || s1 == t1;
           for (int t = s0; ok && t < s1; ++t) {
-            if (slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
-            const uint32_t d = tmem + slots.at * slot_cols;
-            for (int i = 0; i < count; ++i) {
-              const int c = piece(i);
-              if (ok && new_q && t == s0) ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
+            for (int c0 = 0; ok && c0 < kPieces; c0 += kPer) {
+              const bool first = c0 % kPartPieces == 0, last = (c0 + kPer) % kPartPieces == 0;
+              if (first && slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
+              for (int c = c0; ok && new_q && t == s0 && c < c0 + kPer; ++c)
+                ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
               if (ok) ok = warp_wait(&ms->kv_full[ring.at], ring.phase & 1, abort, p);
               if (!ok) break;
               ptx::tc_fence_after();
-              const uint32_t a0 = sk + ring.at * kStageBytes, b0 = sq + c * q_piece;
-              const uint64_t ad = ptx::smem_desc(a0, 16, kSbo, kSwizzle), bd = ptx::smem_desc(b0, 16, kSbo, kSwizzle);
-              if (leader) {
+              const uint32_t d = tmem + slots.at * slot_cols;
+              const uint64_t ad = ptx::smem_desc(sk + ring.at * kStageBytes, 16, kSbo, kSwizzle);
+              const uint64_t bd = ptx::smem_desc(sq + c0 * q_piece, 16, kSbo, kSwizzle);
+              if (ptx::elect_one()) {
 #pragma unroll
-                for (int k = 0; k < kRowBytes / 32; ++k) {  // 32 bytes on: 2 in the address field's units
-                  if constexpr (kFp8)
-                    ptx::mma_e4m3_ss(d, ad + 2 * k, bd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
-                  else
-                    ptx::mma_bf16_ss(d, ad + 2 * k, bd + 2 * k, idesc, (i | k) != 0 ? 1u : 0u);
+                for (int j = 0; j < kPer; ++j) {
+#pragma unroll
+                  for (int k = 0; k < kRowBytes / 32; ++k) {  // the address field counts 16 bytes
+                    const uint64_t a = ad + j * (kPieceBytes / 16) + 2 * k, q = bd + j * (q_piece / 16) + 2 * k;
+                    if constexpr (kFp8)
+                      ptx::mma_e4m3_ss(d, a, q, idesc, first && (j | k) == 0 ? 0u : 1u);
+                    else
+                      ptx::mma_bf16_ss(d, a, q, idesc, first && (j | k) == 0 ? 0u : 1u);
+                  }
                 }
                 ptx::mma_commit(&ms->kv_empty[ring.at]);
-                if (last_q && t == s1 - 1) ptx::mma_commit(&ms->q_empty[c]);
-                if (i == count - 1) ptx::mma_commit(&ms->d_full[slots.at]);
+                if (last_q && t == s1 - 1)
+                  for (int j = 0; j < kPer; ++j) ptx::mma_commit(&ms->q_empty[c0 + j]);
+                if (last) ptx::mma_commit(&ms->d_full[slots.at]);
               }
               __syncwarp();
-              ring.step(!kFp8 ? 3 : i < count - 1 ? 1 : kPieces - count + 1);
+              ring.step();
+              if (last) slots.step();
               issued = true;
             }
-            slots.step(Parts<kFp8>::kCount);
           }
           if (new_q) ++qphase;
         }
       }
     }
-    // every product must retire before tensor memory is released
-    if (issued && leader) drain_mmas(&ms->mma_done[mi], p.wait_budget);
+    // every product must retire before tensor memory is released (the same lane issued them all)
+    if (issued && ptx::elect_one()) drain_mmas(&ms->mma_done, p.wait_budget);
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ weights
@@ -676,12 +669,11 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   int sms = 0;
   cudaError_t ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(ce));
-  const int stage = fp8 ? 8192 : 16384, tile_bytes = kPieces * stage;
+  const int piece = fp8 ? 8192 : 16384, tile_bytes = kPieces * piece;
   const int fixed = 1024 + kMiscBytes + kPieces * most_rows * 128;
-  const int unit = fp8 ? Parts<true>::kStageUnit : Parts<false>::kStageUnit;
-  const int parts = fp8 ? Parts<true>::kCount : Parts<false>::kCount;
-  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / stage) / unit * unit;
-  const int smem = fixed + stages * stage;
+  const int per = pieces_per_stage(fp8);
+  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / (per * piece));
+  const int smem = fixed + stages * per * piece;
   auto fn = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
   ce = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(ce));
@@ -713,7 +705,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   prm.scale_log2 = sm_scale * (fp8 && !kv_scales ? kv_scale : 1.f) * 1.4426950408889634f;
   prm.rows_n = most_rows;
   prm.stages = stages;
-  prm.slots = std::min(kMaxSlots, 512 / (fp8 ? 2 * most_rows : most_rows)) / parts * parts;
+  prm.slots = std::min(kMaxSlots, 512 / (fp8 ? 2 * most_rows : most_rows));
   // tiles that all CTAs together keep in L2 while the groups pass over them
   prm.sub_tiles = std::max(1, std::min<int>(kMaxSubSums, (int)((80LL << 20) / ((long long)tile_bytes * grid))));
   prm.status = status_dev;
