@@ -189,6 +189,27 @@ __device__ __forceinline__ int counted_rows(const WeightsParams& p, int b, int q
   return c * p.H;
 }
 
+// Two fp32 operations by one instruction.
+__device__ __forceinline__ uint64_t pack2(float2 v) { return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x); }
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+  return unpack2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+  return unpack2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
+  return unpack2(r);
+}
+
 // The epilogue warpgroups (wg 0 and 1, warps of quadrant qd): rows [16 NC wg, 16 NC (wg + 1))
 // of each group, N = 32 NC. A thread owns the key of its tensor-memory lane. One warpgroup
 // hands its half of a tile's sums to the other, in turns.
@@ -255,54 +276,56 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
             if (ok && mine > 0) {
               ptx::tc_fence_after();
               const uint32_t acc = acc0 + slot * kSlotCols;
+              // e4m3: up to 32 rows' hi and lo columns in flight; bf16: all rows
+              constexpr int kStep = kFp8 ? (NC < 2 ? NC : 2) : NC;
 #pragma unroll
-              for (int h = 0; h < (kFp8 ? 2 : 1); ++h) {
-                float y[kCols];
+              for (int c0 = 0; c0 < NC; c0 += kStep) {
+                float y[16 * kStep], z[16 * kStep];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) ptx::tmem_ld16(acc + h * n + 16 * c, y + 16 * c);
+                for (int c = 0; c < kStep; ++c) {
+                  if (c0 + c >= NC) break;
+                  ptx::tmem_ld16(acc + 16 * (c0 + c), y + 16 * c);
+                  if (kFp8) ptx::tmem_ld16(acc + n + 16 * (c0 + c), z + 16 * c);
+                }
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) x[j] = u == 0 && h == 0 ? y[j] : x[j] + y[j];
+                for (int j = 0; j < 16 * kStep; j += 2) {
+                  if (16 * c0 + j >= kCols) break;
+                  float2 v = make_float2(y[j], y[j + 1]);
+                  if (kFp8) v = add2(v, make_float2(z[j], z[j + 1]));
+                  if (u > 0) v = add2(v, make_float2(x[16 * c0 + j], x[16 * c0 + j + 1]));
+                  x[16 * c0 + j] = v.x;
+                  x[16 * c0 + j + 1] = v.y;
+                }
               }
               ptx::tc_fence_before();
             }
             __syncwarp();
             if (ok && lane == 0) ptx::mbar_arrive(&ms->d_empty[slot]);
           }
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           if (ok && mine > 0) {
             const bool all = (t + 1) * kKeys <= lim_min;  // every row sees every key of the tile
+            const float2 ks2 = make_float2(ks, ks);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
               if (16 * c >= mine) break;
-              if constexpr (kFp8) {
+              const bool whole = all && 16 * c + 16 <= mine;
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 r = *reinterpret_cast<const float4*>(rscale + 16 * c + j);
-                  x[16 * c + j] *= r.x;
-                  x[16 * c + j + 1] *= r.y;
-                  x[16 * c + j + 2] *= r.z;
-                  x[16 * c + j + 3] *= r.w;
+              for (int j = 16 * c; j < 16 * c + 16; j += 2) {
+                float2 v = make_float2(x[j], x[j + 1]);
+                if constexpr (kFp8) v = mul2(v, *reinterpret_cast<const float2*>(rscale + j));
+                v = fma2(v, ks2, *reinterpret_cast<const float2*>(nlse + j));
+                float2 e = make_float2(ex2(v.x), ex2(v.y));
+                if (!whole) {  // a row past the group, or one that does not see this key, holds anything
+                  e.x = key < lim[j] ? e.x : 0.f;
+                  e.y = key < lim[j + 1] ? e.y : 0.f;
                 }
-              }
-              if (all && 16 * c + 16 <= mine) {
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 l = *reinterpret_cast<const float4*>(nlse + 16 * c + j);
-                  s[0] += ex2(fmaf(x[16 * c + j], ks, l.x));
-                  s[1] += ex2(fmaf(x[16 * c + j + 1], ks, l.y));
-                  s[2] += ex2(fmaf(x[16 * c + j + 2], ks, l.z));
-                  s[3] += ex2(fmaf(x[16 * c + j + 3], ks, l.w));
-                }
-              } else {
-                // a row past the group, or one that does not see this key, holds anything
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  s[j & 3] += key < lim[16 * c + j] ? ex2(fmaf(x[16 * c + j], ks, nlse[16 * c + j])) : 0.f;
+                s[(j >> 1) & 1] = add2(s[(j >> 1) & 1], e);
               }
             }
           }
-          float w = (s[0] + s[1]) + (s[2] + s[3]);
+          float w = (s[0].x + s[1].x) + (s[0].y + s[1].y);
           if (!writes) ms->half[tiles & 1][key_in] = w;
           ptx::bar_sync(3, 256);  // alternate buffers: the next tile's barrier closes this one's
           if (writes) {
