@@ -283,7 +283,7 @@ int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* 
  *   weights       fp32 [batch, weights_stride]
  *   seq_lens      device int32 [batch]; a length outside [0, max_seq] reports
  *                 MLA_DEVICE_PLAN_MISMATCH and keeps nothing
- *   max_seq       host: at least the longest length (sizes the launch)
+ *   max_seq       host: at least the longest length (sizes the launch); at most 2^21
  *   kv_dtype, kv_cache, kv_scales, page_table, num_pages   the cache; kv_scales NULL for a
  *                 bf16 cache or an e4m3 cache with one scale
  *   ..._dst       the cache that receives the rows, its scales and page table. It may be the

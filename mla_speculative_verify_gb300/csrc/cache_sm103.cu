@@ -29,7 +29,6 @@ int block_log2_of(int block_tokens);  // defined with the plan
 
 namespace {
 
-constexpr int kThreads = 256;  // append and gather: one page of 64 rows per CTA
 constexpr int kScaleExpMin = -60, kScaleExpMax = 60;
 
 __device__ __forceinline__ void report(int32_t* status, int bits) {
@@ -51,18 +50,35 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// Four e4m3 codes times `ratio`, rounded to e4m3 again.
-__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
-  float f[4];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> (16 * k)), __NV_E4M3);
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    f[2 * k] = v.x * ratio;
-    f[2 * k + 1] = v.y * ratio;
+// A change of scale: codes are multiplied by `ratio` and rounded to e4m3 again. down = k where
+// the ratio is 2^-k, k in [1, 14]: the exponent field of a code whose result is a normal number
+// just drops by k.
+struct Rescale {
+  float ratio;
+  int down;
+  __device__ __forceinline__ explicit Rescale(float r) : ratio(r), down(0) {
+    const uint32_t u = __float_as_uint(r);
+    const int k = 127 - (int)(u >> 23);
+    if ((u & 0x7FFFFFu) == 0 && k >= 1 && k <= 14) down = k;
   }
-  return e4m3x4(f[0], f[1], f[2], f[3]);
-}
+  __device__ __forceinline__ uint32_t operator()(uint32_t codes) const {
+    if (down > 0) {
+      // bit 7 of each byte of `fits`: magnitude >= 8 (k + 1), and of `nan`: magnitude 0x7F
+      const uint32_t mag = codes & 0x7F7F7F7Fu;
+      const uint32_t fits = mag + 0x01010101u * (0x80 - 8 * (down + 1)), nan = mag + 0x01010101u;
+      if ((fits & ~nan & 0x80808080u) == 0x80808080u) return codes - 0x08080808u * down;
+    }
+    float f[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> (16 * k)), __NV_E4M3);
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      f[2 * k] = v.x * ratio;
+      f[2 * k + 1] = v.y * ratio;
+    }
+    return e4m3x4(f[0], f[1], f[2], f[3]);
+  }
+};
 
 // ------------------------------------------------------------------ append
 struct AppendArgs {
@@ -79,9 +95,11 @@ struct AppendArgs {
 
 // One CTA per page that a request's new rows reach (blockIdx = page within those, request).
 // Eight lanes hold a row (nine 16-byte pieces each, 128 contiguous bytes of a row per load),
-// a warp four rows, so the page's rows are read once, all loads in flight together, and stay
-// in registers between the maximum and the rounding.
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+// so the page's rows are read once, all loads in flight together, and stay in registers
+// between the maximum and the rounding. The rows' loads do not wait for the page's id.
+constexpr int kAppendThreads = 512;
+
+__global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a) {
   __shared__ float row_max[kPage], scale[kPage], ratio[kPage], half_max[2];
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = a.cu[b], n = a.cu[b + 1] - r0, end = a.ends[b];
@@ -94,66 +112,56 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
   const int pg = start / kPage + blockIdx.x;
   if ((long long)pg * kPage >= end) return;
   const int page = a.page_table[(size_t)b * a.pt_stride + pg];
+  const int lo = max(start - pg * kPage, 0), hi = min(end - pg * kPage, kPage);  // new rows of the page
+  const int sub = lane & 7, r = tid >> 3;
+  const bool live = r >= lo && r < hi;
+  uint4 v[9];
+  const uint4* src = a.rows + (size_t)(live ? r0 + (pg * kPage + r - start) : 0) * 72 + sub;
+#pragma unroll
+  for (int j = 0; j < 9; ++j) v[j] = live ? __ldcs(src + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
   if (page < 0 || page >= a.num_pages) {
     if (tid == 0) report(a.status, MLA_DEVICE_BAD_PAGE);
     return;
   }
-  const int lo = max(start - pg * kPage, 0), hi = min(end - pg * kPage, kPage);  // new rows of the page
-  const int spb_log2 = 6 - a.block_log2;
-  float* page_scales = a.scales + ((size_t)page << spb_log2);
+  float* page_scales = a.scales + ((size_t)page << (6 - a.block_log2));
   // a block whose first row is older than the new ones keeps what it holds
   const int blk = tid >> a.block_log2, blk_row0 = blk << a.block_log2;
   float s_old = 0.f;
   if (tid < kPage && blk_row0 < lo) s_old = page_scales[blk];
-
-  const int sub = lane & 7, row_in = warp * 4 + (lane >> 3);
-  uint4 v[2][9];
+  // the largest magnitude from the bits (bf16 magnitudes order as integers); infinities and
+  // NaN are left out, in a second pass that only rows which hold some take
+  uint32_t m2 = 0;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = 32 * h + row_in;
-    const bool live = r >= lo && r < hi;
-    const uint4* src = a.rows + (size_t)(live ? r0 + (pg * kPage + r - start) : 0) * 72 + sub;
-#pragma unroll
-    for (int j = 0; j < 9; ++j) v[h][j] = live ? __ldcs(src + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+  for (int j = 0; j < 9; ++j) {
+    m2 = __vmaxu2(m2, __vmaxu2(v[j].x & 0x7FFF7FFFu, v[j].y & 0x7FFF7FFFu));
+    m2 = __vmaxu2(m2, __vmaxu2(v[j].z & 0x7FFF7FFFu, v[j].w & 0x7FFF7FFFu));
   }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    // the largest magnitude from the bits (bf16 magnitudes order as integers); infinities
-    // and NaN are left out, in a second pass that only rows which hold some take
-    uint32_t m = 0;
+  uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+  if (top >= 0x7F80u) {
+    top = 0;
 #pragma unroll
     for (int j = 0; j < 9; ++j) {
-      m = __vmaxu2(m, __vmaxu2(v[h][j].x & 0x7FFF7FFFu, v[h][j].y & 0x7FFF7FFFu));
-      m = __vmaxu2(m, __vmaxu2(v[h][j].z & 0x7FFF7FFFu, v[h][j].w & 0x7FFF7FFFu));
-    }
-    uint32_t top = max(m & 0xFFFFu, m >> 16);
-    if (top >= 0x7F80u) {
-      top = 0;
+      const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-      for (int j = 0; j < 9; ++j) {
-        const uint32_t w[4] = {v[h][j].x, v[h][j].y, v[h][j].z, v[h][j].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t x = w[k] & 0x7FFFu, y = (w[k] >> 16) & 0x7FFFu;
-          if (x < 0x7F80u) top = max(top, x);
-          if (y < 0x7F80u) top = max(top, y);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t x = w[k] & 0x7FFFu, y = (w[k] >> 16) & 0x7FFFu;
+        if (x < 0x7F80u) top = max(top, x);
+        if (y < 0x7F80u) top = max(top, y);
       }
     }
+  }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (sub == 0) row_max[32 * h + row_in] = __uint_as_float(top << 16);
-  }
+  for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (sub == 0) row_max[r] = __uint_as_float(top << 16);
   __syncthreads();
-  float m = 0.f;
   if (tid < kPage) {
-    m = row_max[tid];
+    float m = row_max[tid];
     for (int o = 1; o < min(1 << a.block_log2, 32); o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) half_max[warp] = m;
-  }
-  __syncthreads();
-  if (tid < kPage) {
-    if (a.block_log2 == 6) m = fmaxf(half_max[0], half_max[1]);
+    if (a.block_log2 == 6) {
+      if (lane == 0) half_max[warp] = m;
+      ptx::bar_sync(1, kPage);
+      m = fmaxf(half_max[0], half_max[1]);
+    }
     const float s = fmaxf(scale_for(m), s_old);
     scale[tid] = s;
     ratio[tid] = s_old / s;
@@ -161,41 +169,37 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     if (tid == blk_row0 && blk_row0 < hi && blk_row0 + (1 << a.block_log2) > lo) page_scales[blk] = s;
   }
   __syncthreads();
+  uint2* dst = reinterpret_cast<uint2*>(a.codes + ((size_t)page * kPage + r) * kDqk) + sub;
+  if (live) {
+    const float s = scale[r];
+    // a power of two divides exactly through its reciprocal; a block that kept another
+    // writer's scale divides
+    const bool two = (__float_as_uint(s) & 0x7FFFFFu) == 0 && s >= 0x1p-120f && s <= 0x1p120f;
+    const float inv = two ? 1.f / s : 0.f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = 32 * h + row_in;
-    uint2* dst = reinterpret_cast<uint2*>(a.codes + ((size_t)page * kPage + r) * kDqk) + sub;
-    if (r >= lo && r < hi) {
-      const float s = scale[r];
-      // a power of two divides exactly through its reciprocal; a block that kept another
-      // writer's scale divides
-      const bool two = (__float_as_uint(s) & 0x7FFFFFu) == 0 && s >= 0x1p-120f && s <= 0x1p120f;
-      const float inv = two ? 1.f / s : 0.f;
+    for (int j = 0; j < 9; ++j) {
+      const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      float f[8];
 #pragma unroll
-      for (int j = 0; j < 9; ++j) {
-        const uint32_t w[4] = {v[h][j].x, v[h][j].y, v[h][j].z, v[h][j].w};
-        float f[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[2 * k] = __uint_as_float(w[k] << 16);
-          f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        }
-        if (two) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] *= inv;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = __fdiv_rn(f[k], s);
-        }
-        dst[8 * j] = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+      for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
       }
-    } else if (r < lo && (r >> a.block_log2) == (lo >> a.block_log2) && ratio[r] != 1.f) {
-      const float q = ratio[r];
+      if (two) {
 #pragma unroll
-      for (int j = 0; j < 9; ++j) {
-        const uint2 c = dst[8 * j];
-        dst[8 * j] = make_uint2(rescale4(c.x, q), rescale4(c.y, q));
+        for (int k = 0; k < 8; ++k) f[k] *= inv;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = __fdiv_rn(f[k], s);
       }
+      dst[8 * j] = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+    }
+  } else if (r < lo && (r >> a.block_log2) == (lo >> a.block_log2) && ratio[r] != 1.f) {
+    const Rescale to(ratio[r]);
+#pragma unroll
+    for (int j = 0; j < 9; ++j) {
+      const uint2 c = dst[8 * j];
+      dst[8 * j] = make_uint2(to(c.x), to(c.y));
     }
   }
 }
@@ -206,6 +210,7 @@ struct SelectArgs {
   long long w_stride;
   const int32_t* lens;
   int max_seq, budget, n_first, n_last;
+  int cache;  // keys of the shared-memory cache
   int32_t* kept;
   float* weights_dst;
   long long wd_stride;
@@ -215,7 +220,12 @@ struct SelectArgs {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kSelBatch = 8;  // weights a lane reads per round trip
+constexpr int kSelStep = 128;       // keys a warp takes at once; a warp's share is a multiple
+constexpr int kSelCopies = 4;       // copies of a CTA's histogram: equal weights hit one bin
+constexpr int kSelKeys = 8192;     // keys a CTA takes while the cluster may grow
+constexpr int kSelMaxCtas = 16;    // (a cluster of 16 is beyond the portable 8)
+constexpr int kSelMaxKeys = kSelMaxCtas * 32 * kSelCopies * kBins / 2;  // two mark bits a key in the histograms' place
+constexpr int kSelCache = 36864;   // weights a CTA keeps in shared memory, at most
 
 // A weight as an unsigned key of the same order; -0 counts as 0, NaN as the lowest.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -229,12 +239,17 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 // those that match the bits found so far, the cluster adds the counts (each CTA reads its
 // peers' through distributed shared memory), and each finds the same bin. Then the kept keys
 // are numbered in order: those above the threshold, and of those equal to it the first ones.
-// Warp g of the cluster owns a contiguous piece of the keys in every pass.
+// A warp owns a contiguous piece of the keys in every pass; the weights are read once and kept
+// in shared memory (what does not fit is read again, from L2). Places behind the last
+// key hold the lowest key: they come after every real one, so none is ever taken.
+//
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ uint32_t hist[3][kBins];
-  __shared__ uint32_t warp_sum[kSelWarps], found[2];
+  extern __shared__ uint32_t cache[];  // a.cache keys
+  __shared__ __align__(16) uint32_t copies[kSelCopies][kBins], hist[2][kBins];
+  __shared__ uint32_t coarse[2][kSelWarps];  // this CTA's counts of 64 bins each
+  __shared__ uint32_t part[kSelThreads], found[3];
   __shared__ uint32_t gt_of[kSelWarps], eq_of[kSelWarps], totals[2];
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
@@ -266,135 +281,196 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
     if (wd) wd[a.budget - a.n_last + r] = w[n - a.n_last + r];
   }
   if (k == 0) return;  // the whole cluster again
-  const int per = ((m + ctas * kSelWarps - 1) / (ctas * kSelWarps) + 31) / 32 * 32;
-  const long long p0 = (long long)(rank * kSelWarps + warp) * per;
-  const int i0 = (int)min((long long)m, p0), i1 = (int)min((long long)m, p0 + per);  // this warp's keys
+  const int per = ((m + ctas * kSelWarps - 1) / (ctas * kSelWarps) + kSelStep - 1) / kSelStep * kSelStep;
+  const long long i0 = ((long long)rank * kSelWarps + warp) * per;  // this warp's first key
+  const int c0 = warp * per;                                          // its place in the CTA
   const float* wm = w + lo;
-  for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0u;
+  for (int i = tid; i < kSelCopies * kBins; i += kSelThreads) (&copies[0][0])[i] = 0u;
   __syncthreads();
+  // key i + lane of the warp is there while i < left; the first `cached` are kept
+  const int left = (int)min((long long)per, m - i0) - lane;
+  const int cached = max(0, min(per, a.cache - c0)) / kSelStep * kSelStep;
+  const float* wl = wm + i0 + lane;
+  uint32_t* cl = cache + c0 + lane;
+  // the weights that are kept come in by asynchronous copies, all of them in flight together,
+  // and become keys in place
+  for (int i = 0; i < min(cached, left); i += 32)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_addr(cl + i)), "l"(wl + i) : "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  for (int i = 0; i < cached; i += 32) cl[i] = i < left ? order_key(__uint_as_float(cl[i])) : 0u;
+  // body(keys i + lane, i + lane + 32, .., i) for every step of the warp's keys
+  auto sweep = [&](auto body) {
+    int i = 0;
+    uint32_t key[4];
+#pragma unroll 2
+    for (; i < cached; i += kSelStep) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) key[u] = cl[i + 32 * u];
+      body(key, i);
+    }
+    for (; i < per; i += 4 * kSelStep) {
+      float x[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) x[u] = i + 32 * u < left ? wl[i + 32 * u] : 0.f;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if (i + h * kSelStep >= per) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) key[u] = i + 32 * (4 * h + u) < left ? order_key(x[4 * h + u]) : 0u;
+        body(key, i + h * kSelStep);
+      }
+    }
+  };
 
   uint32_t prefix = 0, want = (uint32_t)k;  // bits found so far; rank within the keys that match them
+  uint32_t* mine = copies[lane % kSelCopies];
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int above = pass == 0 ? 32 : pass == 1 ? 21 : 10;  // the bits above these are found
+    const int above = pass == 1 ? 21 : 10;  // the bits from this one up are found (pass 0: none)
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    for (int i = i0 + lane; i < i1; i += 32 * kSelBatch) {
-      float x[kSelBatch];
+    sweep([&](const uint32_t (&key)[4], int) {
 #pragma unroll
-      for (int u = 0; u < kSelBatch; ++u) x[u] = i + 32 * u < i1 ? wm[i + 32 * u] : 0.f;
+      for (int u = 0; u < 4; ++u)
+        if (pass == 0 || (key[u] >> above) == prefix) atomicAdd(&mine[(key[u] >> shift) & mask], 1u);
+    });
+    __syncthreads();
+    {
+      uint2 sum = make_uint2(0u, 0u);
 #pragma unroll
-      for (int u = 0; u < kSelBatch; ++u) {
-        const uint32_t key = order_key(x[u]);
-        if (i + 32 * u < i1 && (pass == 0 || (key >> (above & 31)) == prefix)) atomicAdd(&hist[pass][(key >> shift) & mask], 1u);
+      for (int c = 0; c < kSelCopies; ++c) {
+        uint2* h = reinterpret_cast<uint2*>(&copies[c][2 * tid]);
+        sum.x += h->x;
+        sum.y += h->y;
+        *h = make_uint2(0u, 0u);
       }
+      // (two buffers: a peer may still read the last pass's)
+      *reinterpret_cast<uint2*>(&hist[pass & 1][2 * tid]) = sum;
+      uint32_t s64 = sum.x + sum.y;  // a warp holds 64 bins
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s64 += __shfl_xor_sync(0xffffffffu, s64, o);
+      if (lane == 0) coarse[pass & 1][warp] = s64;
     }
     cluster.sync();
-    // bins from the top, two per thread
-    const int hb = kBins - 1 - 2 * tid;
-    uint32_t c0 = 0, c1 = 0;
-    for (int r = 0; r < ctas; ++r) {
-      const uint32_t* h = cluster.map_shared_rank(&hist[pass][0], r);
-      const uint2 c = *reinterpret_cast<const uint2*>(h + hb - 1);
-      c0 += c.y;
-      c1 += c.x;
-    }
-    uint32_t incl = c0 + c1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
+    // Coarse to fine, so that few words cross the cluster: first the 64 bins that hold the
+    // wanted rank, by the counts of 64 bins each, then the one among them. Warp r reads CTA r's.
+    part[tid] = warp < ctas ? cluster.map_shared_rank(&coarse[pass & 1][0], warp)[kSelWarps - 1 - lane] : 0u;
     __syncthreads();
-    if (warp == 0) {
-      uint32_t s = warp_sum[lane];
+    if (warp == 0) {  // lane l: bins 64 (31 - l) ..
+      uint32_t c = 0;
+      for (int r = 0; r < ctas; ++r) c += part[32 * r + lane];
+      uint32_t incl = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += t;
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
       }
-      warp_sum[lane] = s;
+      if (incl - c < want && incl >= want) {
+        found[0] = (uint32_t)(kSelWarps - 1 - lane);
+        found[1] = want - (incl - c);
+      }
     }
     __syncthreads();
-    const uint32_t before = (warp ? warp_sum[warp - 1] : 0u) + incl - c0 - c1;
-    if (before < want && before + c0 >= want) {
-      found[0] = (uint32_t)hb;
-      found[1] = want - before;
-    } else if (before + c0 < want && before + c0 + c1 >= want) {
-      found[0] = (uint32_t)(hb - 1);
-      found[1] = want - before - c0;
-    }
-    __syncthreads();
-    prefix = pass == 0 ? found[0] : (prefix << (pass == 1 ? 11 : 10)) | found[0];
+    const uint32_t c64 = found[0];
     want = found[1];
+    part[tid] = (tid >> 6) < ctas ? cluster.map_shared_rank(&hist[pass & 1][0], tid >> 6)[64 * c64 + 63 - (tid & 63)] : 0u;
     __syncthreads();
-  }
-  // prefix is the threshold's key; `want` of the keys equal to it stay
-  uint32_t gt = 0, eq = 0;
-  for (int i = i0 + lane; i < i1; i += 32 * kSelBatch) {
-    float x[kSelBatch];
+    if (warp == 0) {  // lane l: bins 63 - 2 l and 62 - 2 l of those
+      uint32_t n0 = 0, n1 = 0;
+      for (int r = 0; r < ctas; ++r) {
+        n0 += part[64 * r + 2 * lane];
+        n1 += part[64 * r + 2 * lane + 1];
+      }
+      uint32_t incl = n0 + n1;
 #pragma unroll
-    for (int u = 0; u < kSelBatch; ++u) x[u] = i + 32 * u < i1 ? wm[i + 32 * u] : 0.f;
-#pragma unroll
-    for (int u = 0; u < kSelBatch; ++u) {
-      const uint32_t key = order_key(x[u]);
-      gt += i + 32 * u < i1 && key > prefix;
-      eq += i + 32 * u < i1 && key == prefix;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const uint32_t before = incl - n0 - n1;
+      if (before < want && before + n0 >= want) {
+        found[1] = 64 * c64 + 63 - 2 * lane;
+        found[2] = want - before;
+      } else if (before + n0 < want && incl >= want) {
+        found[1] = 64 * c64 + 62 - 2 * lane;
+        found[2] = want - before - n0;
+      }
     }
+    __syncthreads();
+    prefix = pass == 0 ? found[1] : (prefix << (pass == 1 ? 11 : 10)) | found[1];
+    want = found[2];
   }
+  // prefix is the threshold's key; `want` of the keys equal to it stay. One more sweep notes
+  // which keys are above it and which equal it, a bit each (in the histograms' place).
+  uint2* marks = reinterpret_cast<uint2*>(&copies[0][0]) + c0 / 32;
+  uint32_t gt = 0, eq = 0;
+  sweep([&](const uint32_t (&key)[4], int i) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, o);
-    eq += __shfl_xor_sync(0xffffffffu, eq, o);
-  }
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t above = __ballot_sync(0xffffffffu, key[u] > prefix);
+      const uint32_t equal = __ballot_sync(0xffffffffu, key[u] == prefix);
+      gt += __popc(above);
+      eq += __popc(equal);
+      if (lane == u) marks[i / 32 + u] = make_uint2(above, equal);
+    }
+  });
   if (lane == 0) {
     gt_of[warp] = gt;
     eq_of[warp] = eq;
   }
   __syncthreads();
+  // what the warps before this one hold, and (for the peers) what the CTA holds
+  gt = gt_of[lane];
+  eq = eq_of[lane];
+  uint32_t gt_before = lane < warp ? gt : 0u, eq_before = lane < warp ? eq : 0u;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    gt += __shfl_xor_sync(0xffffffffu, gt, o);
+    eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    gt_before += __shfl_xor_sync(0xffffffffu, gt_before, o);
+    eq_before += __shfl_xor_sync(0xffffffffu, eq_before, o);
+  }
   if (tid == 0) {
-    uint32_t g = 0, e = 0;
-    for (int i = 0; i < kSelWarps; ++i) {
-      const uint32_t gi = gt_of[i], ei = eq_of[i];
-      gt_of[i] = g;
-      eq_of[i] = e;
-      g += gi;
-      e += ei;
-    }
-    totals[0] = g;
-    totals[1] = e;
+    totals[0] = gt;
+    totals[1] = eq;
   }
   cluster.sync();
-  gt = gt_of[warp];
-  eq = eq_of[warp];
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t* t = cluster.map_shared_rank(&totals[0], r);
-    gt += t[0];
-    eq += t[1];
+  gt = lane < rank ? cluster.map_shared_rank(&totals[0], lane)[0] : 0u;
+  eq = lane < rank ? cluster.map_shared_rank(&totals[0], lane)[1] : 0u;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {  // (up to 16 CTAs)
+    gt += __shfl_xor_sync(0xffffffffu, gt, o);
+    eq += __shfl_xor_sync(0xffffffffu, eq, o);
   }
+  gt = __shfl_sync(0xffffffffu, gt, 0) + gt_before;
+  eq = __shfl_sync(0xffffffffu, eq, 0) + eq_before;
+  ptx::cluster_arrive();  // this CTA has read its peers' counts
   const uint32_t below = (1u << lane) - 1u;
-  for (int i = i0; i < i1; i += 32 * kSelBatch) {
-    float x[kSelBatch];
+  gt += (uint32_t)a.n_first;
+  const int first = lo + (int)i0 + lane;
+  for (int i = 0; i < per; i += kSelStep) {
+    uint2 mark[4];
+    float x[4];
+    uint32_t pos[4];
 #pragma unroll
-    for (int u = 0; u < kSelBatch; ++u) x[u] = i + 32 * u + lane < i1 ? wm[i + 32 * u + lane] : 0.f;
+    for (int u = 0; u < 4; ++u) mark[u] = marks[i / 32 + u];
 #pragma unroll
-    for (int u = 0; u < kSelBatch; ++u) {
-      const int j = i + 32 * u + lane;
-      const uint32_t key = order_key(x[u]);
-      const uint32_t bg = __ballot_sync(0xffffffffu, j < i1 && key > prefix);
-      const uint32_t be = __ballot_sync(0xffffffffu, j < i1 && key == prefix);
-      const uint32_t e = eq + __popc(be & below);
-      if (((bg >> lane) & 1u) || (((be >> lane) & 1u) && e < want)) {
-        const uint32_t pos = (uint32_t)a.n_first + gt + __popc(bg & below) + min(e, want);
-        kept[pos] = lo + j;
-        if (wd) wd[pos] = x[u];
-      }
-      gt += __popc(bg);
-      eq += __popc(be);
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t e = eq + __popc(mark[u].y & below);
+      const bool keep = ((mark[u].x >> lane) & 1u) || (((mark[u].y >> lane) & 1u) && e < want);
+      pos[u] = keep ? gt + __popc(mark[u].x & below) + min(e, want) : ~0u;
+      gt += __popc(mark[u].x);
+      eq += __popc(mark[u].y);
+      x[u] = keep && wd ? wl[i + 32 * u] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (pos[u] == ~0u) continue;
+      kept[pos[u]] = first + i + 32 * u;
+      if (wd) wd[pos[u]] = x[u];
     }
   }
-  cluster.sync();  // no CTA leaves while a peer may still read its counts
+  ptx::cluster_wait();  // no CTA leaves while a peer may still read its counts
 }
 
 // ------------------------------------------------------------------ eviction: moving the rows
@@ -410,34 +486,47 @@ struct GatherArgs {
   const int32_t* pt_src;
   const int32_t* pt_dst;
   int pt_src_stride, pt_dst_stride, pages_src, pages_dst;
+  int pages, batch;  // pages of the longest result, requests
   int32_t* status;
 };
 
-// One CTA per new page. P = 16-byte pieces of a row (72: bf16, 36: e4m3), held by P / 9 lanes
-// with nine pieces each; the page's rows are loaded before any is stored. For a block-scaled
-// cache the new block takes the largest scale of its rows and codes from a block with a
-// smaller one are rounded to it.
+// CTAs that take new pages in turn (page i of the list: request i / pages, its page i % pages).
+// P = 16-byte pieces of a row (72: bf16, 36: e4m3), held by P / 9 lanes with nine pieces each.
+// To find a row takes five loads one after the other (new length, new page, index, old page,
+// scale: ~3 us), so two warps of their own look up the next page's rows while the other eight
+// move this one's: 302 MB of e4m3 rows in 64 us without them. For a block-scaled cache the new
+// block takes the largest scale of its rows and codes from a block with a smaller one are
+// rounded to it.
+constexpr int kMoveThreads = 256, kGatherThreads = kMoveThreads + kPage;
+
 template <int P, bool kScaled>
-__global__ void __launch_bounds__(kThreads) evict_gather_kernel(GatherArgs a) {
-  constexpr int kLanes = P / 9;                        // 8 or 4 lanes to a row
-  constexpr int kPasses = kPage * kLanes / kThreads;   // 2 or 1
-  __shared__ long long src_row[kPage];
-  __shared__ float scale[kPage], ratio[kPage], half_max[2];
+__global__ void __launch_bounds__(kGatherThreads, 3) evict_gather_kernel(GatherArgs a) {
+  constexpr int kLanes = P / 9;                           // 8 or 4 lanes to a row
+  constexpr int kRowsPass = kMoveThreads / kLanes;        // 32 or 64 rows at a time
+  __shared__ long long src_row[2][kPage];                 // per row of a page: its old row, or -1
+  __shared__ float ratio[2][kPage], half_max[2];
+  __shared__ int dst_page[2], dst_rows[2];
   ptx::pdl_wait_primary();
-  const int b = blockIdx.y, pg = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = a.lens_dst[b];
-  const int rows = min(kPage, n - pg * kPage);
-  if (rows <= 0) return;
-  const int page = a.pt_dst[(size_t)b * a.pt_dst_stride + pg];
-  if (page < 0 || page >= a.pages_dst) {
-    if (tid == 0) report(a.status, MLA_DEVICE_BAD_PAGE);
-    return;
-  }
-  float s = 0.f;
-  if (tid < kPage) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const long long items = (long long)a.pages * a.batch;
+
+  // the index warps: page `item` of the list into buffer `k`
+  auto look_up = [&](long long item, int k) {
+    const int i = tid - kMoveThreads;  // row of the page
+    const int b = (int)(item / a.pages), pg = (int)(item % a.pages);
+    int rows = min(kPage, a.lens_dst[b] - pg * kPage);
+    int page = -1;
+    if (rows > 0) {
+      page = a.pt_dst[(size_t)b * a.pt_dst_stride + pg];
+      if (page < 0 || page >= a.pages_dst) {
+        if (i == 0) report(a.status, MLA_DEVICE_BAD_PAGE);
+        rows = 0;
+      }
+    }
     long long row = -1;
-    if (tid < rows) {
-      const int j = a.kept[(size_t)b * a.budget + pg * kPage + tid];
+    float s = 0.f;
+    if (i < rows) {
+      const int j = a.kept[(size_t)b * a.budget + pg * kPage + i];
       const int p = a.pt_src[(size_t)b * a.pt_src_stride + j / kPage];
       if (p >= 0 && p < a.pages_src) {
         row = (long long)p * kPage + j % kPage;
@@ -446,48 +535,54 @@ __global__ void __launch_bounds__(kThreads) evict_gather_kernel(GatherArgs a) {
         report(a.status, MLA_DEVICE_BAD_PAGE);
       }
     }
-    src_row[tid] = row;
+    src_row[k][i] = row;
+    if (i == 0) {
+      dst_page[k] = page;
+      dst_rows[k] = rows;
+    }
     if constexpr (kScaled) {
       float m = s;
       for (int o = 1; o < min(1 << a.block_log2, 32); o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      scale[tid] = m;
-      if (lane == 0) half_max[warp] = m;
+      if (a.block_log2 == 6) {
+        if (lane == 0) half_max[i >> 5] = m;
+        ptx::bar_sync(1, kPage);
+        m = fmaxf(half_max[0], half_max[1]);
+        ptx::bar_sync(1, kPage);
+      }
+      ratio[k][i] = m > 0.f ? s / m : 1.f;
+      const int blk = i >> a.block_log2;
+      if (i == blk << a.block_log2 && i < rows) a.scales_dst[((size_t)page << (6 - a.block_log2)) + blk] = m;
     }
-  }
+  };
+
+  if (tid >= kMoveThreads && blockIdx.x < items) look_up(blockIdx.x, 0);
   __syncthreads();
-  const int sub = tid % kLanes, row_in = tid / kLanes;
-  uint4 v[kPasses][9];
+  int k = 0;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x, k ^= 1) {
+    if (tid >= kMoveThreads) {
+      if (item + gridDim.x < items) look_up(item + gridDim.x, k ^ 1);
+    } else {
+      const int rows = dst_rows[k], page = dst_page[k];
+      const int sub = tid % kLanes;
 #pragma unroll
-  for (int h = 0; h < kPasses; ++h) {
-    const long long row = src_row[h * (kThreads / kLanes) + row_in];
-    const uint4* src = a.src + (row < 0 ? 0 : row) * P + sub;
+      for (int r = tid / kLanes; r < kPage; r += kRowsPass) {
+        const long long row = r < rows ? src_row[k][r] : -1;
+        if (row < 0) continue;
+        const uint4* src = a.src + row * P + sub;
+        uint4* dst = a.dst + ((size_t)page * kPage + r) * P + sub;
+        uint4 v[9];
 #pragma unroll
-    for (int j = 0; j < 9; ++j) v[h][j] = row < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldcs(src + kLanes * j);
-  }
-  if constexpr (kScaled) {
-    if (tid < kPage) {
-      const float m = a.block_log2 == 6 ? fmaxf(half_max[0], half_max[1]) : scale[tid];
-      ratio[tid] = m > 0.f ? s / m : 1.f;
-      const int blk = tid >> a.block_log2;
-      if (tid == blk << a.block_log2 && tid < rows) a.scales_dst[((size_t)page << (6 - a.block_log2)) + blk] = m;
-    }
-    __syncthreads();
-  }
+        for (int j = 0; j < 9; ++j) v[j] = __ldcs(src + kLanes * j);
+        if (kScaled && ratio[k][r] != 1.f) {
+          const Rescale to(ratio[k][r]);
 #pragma unroll
-  for (int h = 0; h < kPasses; ++h) {
-    const int r = h * (kThreads / kLanes) + row_in;
-    if (src_row[r] < 0) continue;
-    uint4* dst = a.dst + ((size_t)page * kPage + r) * P + sub;
-    if (kScaled && ratio[r] != 1.f) {
-      const float q = ratio[r];
+          for (int j = 0; j < 9; ++j) v[j] = make_uint4(to(v[j].x), to(v[j].y), to(v[j].z), to(v[j].w));
+        }
 #pragma unroll
-      for (int j = 0; j < 9; ++j) {
-        const uint4 c = v[h][j];
-        v[h][j] = make_uint4(rescale4(c.x, q), rescale4(c.y, q), rescale4(c.z, q), rescale4(c.w, q));
+        for (int j = 0; j < 9; ++j) dst[kLanes * j] = v[j];
       }
     }
-#pragma unroll
-    for (int j = 0; j < 9; ++j) dst[kLanes * j] = v[h][j];
+    __syncthreads();
   }
 }
 
@@ -526,7 +621,7 @@ extern "C" int mla_cache_append(const void* rows, int total_rows, const int32_t*
                      seq_lens, cu_new, (uint8_t*)kv_cache, kv_scales, status_dev};
   // max_new rows touch at most this many pages, wherever in a page they start
   const unsigned pages = (unsigned)(((long long)max_new + kPage - 2) / kPage + 1);
-  append_kernel<<<dim3(pages, (unsigned)batch), kThreads, 0, (cudaStream_t)stream>>>(a);
+  append_kernel<<<dim3(pages, (unsigned)batch), kAppendThreads, 0, (cudaStream_t)stream>>>(a);
   const cudaError_t ce = cudaGetLastError();
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "append kernel launch: %s", cudaGetErrorString(ce));
   return MLA_OK;
@@ -541,8 +636,9 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
                                int32_t* status_dev, void* stream) {
   clear_error();
   if (batch < 1 || batch > 65535) return set_error(MLA_ERR_INVALID_ARG, "batch must be in [1, 65535] (got %d)", batch);
-  if (max_seq < 0 || max_seq > 1 << 30)
-    return set_error(MLA_ERR_INVALID_ARG, "max_seq must be in [0, 2^30] (got %d)", max_seq);
+  if (max_seq < 0) return set_error(MLA_ERR_INVALID_ARG, "max_seq must be >= 0 (got %d)", max_seq);
+  if (max_seq > kSelMaxKeys)
+    return set_error(MLA_ERR_UNSUPPORTED, "max_seq must be at most %d (got %d)", kSelMaxKeys, max_seq);
   if (budget < 1 || n_first < 0 || n_last < 0 || (long long)n_first + n_last > budget)
     return set_error(MLA_ERR_INVALID_ARG, "need budget >= 1 and n_first + n_last <= budget (got %d, %d and %d)", budget,
                      n_first, n_last);
@@ -573,16 +669,26 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   int dev = 0;
   const int rc = current_device_ready(&dev);
   if (rc != MLA_OK) return rc;
+  int sms = 0;
+  cudaError_t ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(ce));
 
-  const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last,
-                     kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
-  // CTAs per request: one for every 16384 keys, up to a portable cluster of 8
+  // CTAs per request: one for every 8192 keys, up to a cluster of 16
   int ctas = 1;
-  while (ctas < 8 && (long long)ctas * 16384 < max_seq) ctas *= 2;
+  while (ctas < kSelMaxCtas && (long long)ctas * kSelKeys < max_seq) ctas *= 2;
+  const int warp_keys = (max_seq / (ctas * kSelWarps) + kSelStep) / kSelStep * kSelStep;  // at most
+  const int cache = std::min(kSelCache, kSelWarps * warp_keys);
+  const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last, cache,
+                     kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
+  ce = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSelCache);
+  if (ce == cudaSuccess && ctas > 8)
+    ce = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(ce));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((unsigned)ctas, (unsigned)batch, 1);
   cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.dynamicSmemBytes = 4 * (size_t)cache;
   cfg.stream = (cudaStream_t)stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
@@ -590,15 +696,16 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t ce = cudaLaunchKernelEx(&cfg, evict_select_kernel, s);
+  ce = cudaLaunchKernelEx(&cfg, evict_select_kernel, s);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction select kernel launch: %s", cudaGetErrorString(ce));
   if (pages_dst == 0) return MLA_OK;
 
   const GatherArgs g{kept, seq_lens_dst, budget, max_seq, (const uint4*)kv_cache, (uint4*)kv_cache_dst, kv_scales,
                      kv_scales_dst, bl, page_table, page_table_dst, page_table_stride, page_table_dst_stride, num_pages,
-                     num_pages_dst, status_dev};
-  cfg.gridDim = dim3((unsigned)pages_dst, (unsigned)batch, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+                     num_pages_dst, (int)pages_dst, batch, status_dev};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(pages_dst * batch, 3LL * sms), 1, 1);
+  cfg.blockDim = dim3(kGatherThreads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   auto fn = kv_dtype == MLA_KV_BF16 ? evict_gather_kernel<72, false>
