@@ -94,7 +94,11 @@ constexpr int kOffKv = kOffQ + kQBytes;
 constexpr int kOffPt = kOffKv + kKvBytes;
 constexpr int kOffMisc = kOffPt + 2 * kPtBytes;
 constexpr int kMiscBytes = 4096;
+constexpr int kOffScales = kOffMisc + kMiscBytes;  // block-scaled cache: a float4 per key of each of four stages
+constexpr int kScalesBytes = 4 * kTileKeys * 16;
 constexpr int kSmemBytes = kOffMisc + kMiscBytes + 1024;  // + alignment slack
+constexpr int kSmemBytesScaled = kSmemBytes + kScalesBytes;
+static_assert(kSmemBytesScaled <= 232448, "exceeds the 227 KB per-CTA shared memory");
 static_assert(kSmemBytes <= 232448, "exceeds the 227 KB per-CTA shared memory");
 static_assert(kOffKv % 1024 == 0 && kOffPt % 1024 == 0 && kOffMisc % 1024 == 0, "1024-byte swizzle atoms");
 
@@ -225,6 +229,7 @@ struct SoftmaxArgs {
   uint32_t tmem, skv, spt;
   int qd, grp, lane, sidx, nmma, b, nrows, qrow0, kv_begin, kv_end, ntiles, part_row0, ctx, qlen, tok0;
   volatile int* abort;
+  const float4* scales;  // block-scaled cache: (v, log2 v, 1 / v) of each key, by stage
 };
 
 // Softmax warps for a tile of 16 NCH packed rows. Warp (qd, grp) owns the 16 key rows of
@@ -239,8 +244,10 @@ struct SoftmaxArgs {
 // the products run on the raw codes. With s_j the score and v_j the scale of key j, the
 // softmax works on s_j + log2 v_j: P'_j = 2^(s_j + log2 v_j - ref) is what the code of key j
 // is weighted with in O^T, and l adds P'_j / v_j, so out = O / l and the reference follows
-// the terms that O is made of, however far the blocks' scales lie apart. Each thread needs
-// the scales of its two keys; they are read a tile ahead, their page id two tiles ahead.
+// the terms that O is made of, however far the blocks' scales lie apart. The producer warp
+// reads a page's scales one page ahead and leaves (v, log2 v, 1 / v) of each key beside the
+// page: looked up by every softmax thread for its two keys they cost the busiest role ~100
+// instructions a tile (1M keys q=8 301 us). Pairs of columns share fp32 instructions.
 template <int NCH, bool kFp8, bool kScaled>
 __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params& p) {
   constexpr int NC = 4 * NCH;
@@ -362,38 +369,9 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
     }
   };
   const float scale = p.score_scale_log2;
-  // kScaled: the block scales of this thread's two keys in the next tile, and the page after it
-  float sc_next[2] = {1.f, 1.f};
-  int page_after = 0;
-  auto page_of = [&](int t) {
-    const int pid = t < a.ntiles ? p.page_table[(size_t)a.b * p.pt_stride + a.kv_begin / kPage + t] : 0;
-    return pid >= 0 && pid < p.num_pages ? pid : 0;
-  };
-  auto load_scales = [&](int t, int page) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int kr = kr0 + 8 * k;
-      const bool live = a.kv_begin + t * kTileKeys + kr < a.kv_end;  // past the range a scale may be anything
-      sc_next[k] = live ? p.kv_scales[((size_t)page * kPage + kr) >> p.block_log2] : 1.f;
-    }
-  };
-  if constexpr (kScaled) {
-    load_scales(0, page_of(0));
-    page_after = page_of(1);
-  }
   for (int t = 0; !stop && t < a.ntiles; ++t) {
     const int sb = t & 1;
-    float ks[2], lks[2], inv_ks[2];
-    if constexpr (kScaled) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        ks[k] = sc_next[k] < 0x1p-60f ? 0x1p-60f : sc_next[k];  // a block of zeros may have the scale 0
-        lks[k] = lg2(ks[k]);
-        inv_ks[k] = 1.f / ks[k];
-      }
-      load_scales(t + 1, page_after);
-      page_after = page_of(t + 2);
-    }
+    float inv_ks[2];  // kScaled: 1 / v of this thread's two keys
     float x[NC];
     bool need = false;
     bool unmasked = false;  // this tile: every key visible to every row
@@ -413,8 +391,17 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
       }
       if constexpr (kFp8) {
         ptx::tmem_ld_wait();
+        if constexpr (kScaled) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) x[i] += s1[i];
+          for (int i = 0; i < NC; i += 2) {
+            const float2 v = ptx::add2(make_float2(x[i], x[i + 1]), make_float2(s1[i], s1[i + 1]));
+            x[i] = v.x;
+            x[i + 1] = v.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NC; ++i) x[i] += s1[i];
+        }
       } else {
         float s2[NC];
 #pragma unroll
@@ -429,6 +416,24 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
       const int key0 = a.kv_begin + t * kTileKeys + kr0;  // and key0 + 8
       const int tile_last = a.kv_begin + t * kTileKeys + kTileKeys - 1;
       unmasked = tile_last < a.kv_end && tile_last < lim_min;  // tile-uniform fast path
+      if constexpr (kScaled) {
+        // (the S^T warp's own arrival on s_full passes on what it saw on kv_full: a wait for
+        // kv_full here took 10 us of 279 over 1M keys)
+        const float4* sc = a.scales + (t % G::kStages) * kTileKeys + kr0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float4 q = sc[8 * k];
+          inv_ks[k] = q.z;
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            const int e = 4 * c + 2 * k;
+            float2 v = ptx::mul2(make_float2(x[e], x[e + 1]), make_float2(csr[2 * c], csr[2 * c + 1]));
+            v = ptx::fma2(v, make_float2(q.x, q.x), make_float2(q.y, q.y));
+            x[e] = v.x;
+            x[e + 1] = v.y;
+          }
+        }
+      }
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         const int n0 = 16 * c + cp;
@@ -441,8 +446,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float v = x[4 * c + j] * csv[j];
-          if constexpr (kScaled) v = fmaf(v, ks[j >> 1], lks[j >> 1]);
+          float v = kScaled ? x[4 * c + j] : x[4 * c + j] * csv[j];
           const int key = key0 + 8 * (j >> 1);
           if (!unmasked) v = (key < a.kv_end && key < ms->lim[n0 + (j & 1)]) ? v : -INFINITY;
           x[4 * c + j] = v;
@@ -513,7 +517,14 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
       for (int c = 0; c < NCH; ++c) {
         float rrv[4];
         ref4(c, rrv);
-        if (unmasked) {  // no masked score (a reference may still be -inf: then a move follows)
+        if (kScaled && unmasked) {
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const float2 v = ptx::add2(make_float2(x[4 * c + j], x[4 * c + j + 1]), make_float2(-rrv[j], -rrv[j + 1]));
+            pv[4 * c + j] = ex2(v.x);
+            pv[4 * c + j + 1] = ex2(v.y);
+          }
+        } else if (unmasked) {  // no masked score (a reference may still be -inf: then a move follows)
 #pragma unroll
           for (int j = 0; j < 4; ++j) pv[4 * c + j] = ex2(x[4 * c + j] - rrv[j]);
         } else {
@@ -580,11 +591,17 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
       }
       if (!fail) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          if constexpr (kScaled)
-            l_acc[i] = fmaf(pv[i], inv_ks[(i >> 1) & 1], l_acc[i]);
-          else
+        for (int i = 0; i < NC; i += 2) {
+          if constexpr (kScaled) {
+            const float inv = inv_ks[(i >> 1) & 1];
+            const float2 l = ptx::fma2(make_float2(pv[i], pv[i + 1]), make_float2(inv, inv),
+                                       make_float2(l_acc[i], l_acc[i + 1]));
+            l_acc[i] = l.x;
+            l_acc[i + 1] = l.y;
+          } else {
             l_acc[i] += pv[i];
+            l_acc[i + 1] += pv[i + 1];
+          }
         }
         store_p();
         __syncwarp();
@@ -724,7 +741,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
       ptx::mbar_init(&ms->kv_empty[i], kOtIssuers);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ms->s_full[i], kFp8 ? 1 : Roles<kFp8>::kSWarps);  // the S^T warp(s) of a tile
+      ptx::mbar_init(&ms->s_full[i], kScaled ? 2 : kFp8 ? 1 : Roles<kFp8>::kSWarps);  // the S^T warp(s) of a tile
       ptx::mbar_init(&ms->s_empty[i], kSoftmaxWarps);
       ptx::mbar_init(&ms->pt_empty[i], kOtIssuers);
       ptx::mbar_init(&ms->p_full[i], kSoftmaxWarps);
@@ -812,6 +829,17 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
       const uint64_t pol = ptx::policy_evict_first();
       pid_cur = checked(pid_cur, lane);
       pid_next = checked(pid_next, 32 + lane);
+      // kScaled: the scales of keys 2 lane and 2 lane + 1 of the next page to copy
+      float sc[2] = {1.f, 1.f};
+      auto load_scales = [&](int t, int page) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int key = 2 * lane + k;
+          const bool live = kv_begin + t * kTileKeys + key < kv_end;  // past the range a scale may be anything
+          sc[k] = live ? p.kv_scales[((size_t)page * kPage + key) >> p.block_log2] : 1.f;
+        }
+      };
+      if (kScaled) load_scales(0, __shfl_sync(0xffffffffu, pid_cur, 0));
       for (int t0 = 0; t0 < ntiles && !*abort; t0 += 32) {
         const int cnt = min(32, ntiles - t0);
         for (int i = 0; i < cnt; ++i) {
@@ -826,6 +854,18 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
           if (kFp8 && t >= S) ok = producer_ot(t - S) != 0;
           if (ok && t >= S) ok = warp_wait(&ms->kv_empty[slot], ((t - S) / S) & 1, abort, p);
           if (!ok) break;
+          if constexpr (kScaled) {
+            // (the softmax has read the slot's old scales: kv_empty follows from its P)
+            float4* dst = reinterpret_cast<float4*>(smem + kOffScales) + slot * kTileKeys + 2 * lane;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float v = sc[k] < 0x1p-60f ? 0x1p-60f : sc[k];  // a block of zeros may have the scale 0
+              dst[k] = make_float4(v, lg2(v), 1.f / v, 0.f);
+            }
+            const int page_n = __shfl_sync(0xffffffffu, i + 1 < 32 ? pid_cur : pid_next, (i + 1) & 31);
+            if (t + 1 < ntiles) load_scales(t + 1, page_n);
+            __syncwarp();
+          }
           if (lane == 0 && !(blockIdx.x == 0 && t == p.skip_copy)) {
             ptx::mbar_arrive_expect_tx(&ms->kv_full[slot], G::kSlot);
             if (read_once)
@@ -901,6 +941,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
         if (!ok) break;
         ptx::tc_fence_after();
         if (lane == 0) {
+          if (kScaled) ptx::mbar_arrive(&ms->s_full[t & 1]);  // with the products' own: the page's scales are there
           const uint32_t a0 = skv + (t % S) * G::kSlot;
           if constexpr (kFp8) {
             // S^T(t) = K . [Q_hi | Q_lo]^T into buffer t % 2: all 18 K-steps (32 columns each)
@@ -961,7 +1002,8 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
     constexpr int kMma = Roles<kFp8>::kMmaWarps;
     const SoftmaxArgs a{ms, sQ, sKv, sPt, tmem, ptx::smem_addr(sKv), ptx::smem_addr(sPt), warp & 3,
                         (warp - 1 - kMma) >> 2, lane, tid - 32 * (kMma + 1), nmma, b, nrows, qrow0,
-                        kv_begin, kv_end, ntiles, part_row0, ctx, qlen, tok0, abort};
+                        kv_begin, kv_end, ntiles, part_row0, ctx, qlen, tok0, abort,
+                        reinterpret_cast<const float4*>(smem + kOffScales)};
     bool issued_ot;
     if (nch == 1)
       issued_ot = softmax_role<1, kFp8, kScaled>(a, p);
@@ -1193,7 +1235,7 @@ static int prepare_device(int dev) {
                      d.minor);
   if (!d.attrs_set) {
     for (auto fn : {fold_decode_kernel<false, false>, fold_decode_kernel<true, false>, fold_decode_kernel<true, true>}) {
-      const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesScaled);
       if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
     }
     d.attrs_set = true;
@@ -1297,7 +1339,7 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
     if (rc != MLA_OK) return rc;
   } else {
     if (kv_scales)
-      fold_decode_kernel<true, true><<<h->n_units, Roles<true>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
+      fold_decode_kernel<true, true><<<h->n_units, Roles<true>::kThreads, kSmemBytesScaled, st>>>(tq, tkv, prm);
     else if (fp8)
       fold_decode_kernel<true, false><<<h->n_units, Roles<true>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
     else

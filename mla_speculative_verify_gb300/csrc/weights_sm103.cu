@@ -189,27 +189,6 @@ __device__ __forceinline__ int counted_rows(const WeightsParams& p, int b, int q
   return c * p.H;
 }
 
-// Two fp32 operations by one instruction.
-__device__ __forceinline__ uint64_t pack2(float2 v) { return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x); }
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
-  return unpack2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
-  return unpack2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
-  return unpack2(r);
-}
-
 // The epilogue warpgroups (wg 0 and 1, warps of quadrant qd): rows [16 NC wg, 16 NC (wg + 1))
 // of each group, N = 32 NC. A thread owns the key of its tensor-memory lane. One warpgroup
 // hands its half of a tile's sums to the other, in turns.
@@ -292,8 +271,8 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
                 for (int j = 0; j < 16 * kStep; j += 2) {
                   if (16 * c0 + j >= kCols) break;
                   float2 v = make_float2(y[j], y[j + 1]);
-                  if (kFp8) v = add2(v, make_float2(z[j], z[j + 1]));
-                  if (u > 0) v = add2(v, make_float2(x[16 * c0 + j], x[16 * c0 + j + 1]));
+                  if (kFp8) v = ptx::add2(v, make_float2(z[j], z[j + 1]));
+                  if (u > 0) v = ptx::add2(v, make_float2(x[16 * c0 + j], x[16 * c0 + j + 1]));
                   x[16 * c0 + j] = v.x;
                   x[16 * c0 + j + 1] = v.y;
                 }
@@ -314,14 +293,14 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
 #pragma unroll
               for (int j = 16 * c; j < 16 * c + 16; j += 2) {
                 float2 v = make_float2(x[j], x[j + 1]);
-                if constexpr (kFp8) v = mul2(v, *reinterpret_cast<const float2*>(rscale + j));
-                v = fma2(v, ks2, *reinterpret_cast<const float2*>(nlse + j));
+                if constexpr (kFp8) v = ptx::mul2(v, *reinterpret_cast<const float2*>(rscale + j));
+                v = ptx::fma2(v, ks2, *reinterpret_cast<const float2*>(nlse + j));
                 float2 e = make_float2(ex2(v.x), ex2(v.y));
                 if (!whole) {  // a row past the group, or one that does not see this key, holds anything
                   e.x = key < lim[j] ? e.x : 0.f;
                   e.y = key < lim[j + 1] ? e.y : 0.f;
                 }
-                s[(j >> 1) & 1] = add2(s[(j >> 1) & 1], e);
+                s[(j >> 1) & 1] = ptx::add2(s[(j >> 1) & 1], e);
               }
             }
           }
