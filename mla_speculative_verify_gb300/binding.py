@@ -185,16 +185,11 @@ def run_static_ws(plan_dev_ptr: int, plan_host: np.ndarray, q_ptr: int, kv_ptr: 
     check(rc, lib)
 
 
-def run_scaled(plan_dev_ptr: int, plan_host: np.ndarray, q_ptr: int, kv_ptr: int, scales_ptr: int, block_tokens: int,
-               page_table_ptr: int, page_table_stride: int, num_pages: int, seq_lens_ptr: int, q_lens_ptr: int,
-               sm_scale: float, out_ptr: int, lse_ptr: int | None, workspace_ptr: int | None, workspace_bytes: int,
-               status_ptr: int | None, stream_handle: int) -> None:
-    """mla_decode_run_scaled: the decode over an e4m3 cache with a scale for each block of tokens."""
-    lib = load()
-    check(lib.mla_decode_run_scaled(plan_dev_ptr, plan_host.ctypes.data_as(_P), plan_host.nbytes, q_ptr, kv_ptr,
-                                    scales_ptr, block_tokens, page_table_ptr, page_table_stride, num_pages,
-                                    seq_lens_ptr, q_lens_ptr, sm_scale, out_ptr, lse_ptr, workspace_ptr,
-                                    workspace_bytes, status_ptr, stream_handle), lib)
+def run_scaled(*args) -> None:
+    """mla_decode_run_scaled, arguments as in the header (pointers as ints): the decode over an
+    e4m3 cache with a scale for each block of tokens."""
+    lib = _lib or load()
+    check(lib.mla_decode_run_scaled(*args), lib)
 
 
 def key_weights_workspace(plan_host: np.ndarray) -> int:
@@ -205,28 +200,22 @@ def key_weights_workspace(plan_host: np.ndarray) -> int:
     return int(n.value)
 
 
-def key_weights(plan_dev_ptr: int, plan_host: np.ndarray, q_ptr: int, kv_ptr: int, scales_ptr: int | None,
-                block_tokens: int, page_table_ptr: int, page_table_stride: int, num_pages: int, lse_ptr: int,
-                counted_ptr: int | None, sm_scale: float, kv_scale: float, decay: float, weights_ptr: int,
-                weights_stride: int, workspace_ptr: int | None, workspace_bytes: int, status_ptr: int | None,
-                stream_handle: int) -> None:
-    """mla_key_weights: accumulate the attention weight of every cached key."""
-    lib = load()
-    check(lib.mla_key_weights(plan_dev_ptr, plan_host.ctypes.data_as(_P), plan_host.nbytes, q_ptr, kv_ptr, scales_ptr,
-                              block_tokens, page_table_ptr, page_table_stride, num_pages, lse_ptr, counted_ptr,
-                              sm_scale, kv_scale, decay, weights_ptr, weights_stride, workspace_ptr, workspace_bytes,
-                              status_ptr, stream_handle), lib)
+def key_weights(*args) -> None:
+    """mla_key_weights, arguments as in the header (pointers as ints): accumulate the attention
+    weight of every cached key."""
+    lib = _lib or load()
+    check(lib.mla_key_weights(*args), lib)
 
 
 def cache_append(*args) -> None:
-    """mla_cache_append, arguments as in the header (device pointers as ints)."""
-    lib = load()
+    """mla_cache_append, arguments as in the header (pointers as ints)."""
+    lib = _lib or load()
     check(lib.mla_cache_append(*args), lib)
 
 
 def cache_evict(*args) -> None:
-    """mla_cache_evict, arguments as in the header (device pointers as ints)."""
-    lib = load()
+    """mla_cache_evict, arguments as in the header (pointers as ints)."""
+    lib = _lib or load()
     check(lib.mla_cache_evict(*args), lib)
 
 

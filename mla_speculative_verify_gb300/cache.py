@@ -10,51 +10,70 @@ graph. Device-side faults (lengths that do not fit, pages out of range) are OR-e
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import binding
 
 PAGE_SIZE = 64
 D_QK = 576
-_NO_GUARD = contextlib.nullcontext()
+ROW = (PAGE_SIZE, D_QK)
+E4M3 = (torch.uint8, torch.float8_e4m3fn)  # a cache of e4m3 codes comes as either
 
 
-def device_guard(device: torch.device):
-    """Makes ``device`` current for a library call, which launches on the current device."""
-    return _NO_GUARD if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def stream_handle(index: int, stream: torch.cuda.Stream | None) -> int:
+    """The cudaStream_t of ``stream``, or of torch's current stream of device ``index``."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def check_tensor(name: str, t: torch.Tensor, dtype, shape, device) -> None:
-    """A contiguous tensor of this dtype (or one of these), shape (None: any) and device."""
-    ok = t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype
-    if not ok or t.dim() != len(shape) or any(w is not None and w != s for w, s in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be {dtype} {['any' if s is None else s for s in shape]}, got {t.dtype} {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, the device of the call's tensors")
+def on_device(index: int, call, *args) -> None:
+    """A library call, which launches on the current device, with device ``index`` current."""
+    if torch.cuda.current_device() == index:
+        call(*args)
+    else:
+        with torch.cuda.device(index):
+            call(*args)
 
 
-def check_scales(name: str, scales: torch.Tensor, pages: int, device) -> int:
+def check_tensor(name: str, t: torch.Tensor, dtype, shape, index: int) -> None:
+    """A contiguous tensor of this dtype (or one of these) and shape on CUDA device ``index``. (A
+    call checks up to a dozen tensors, so the case that all is well is one test.)"""
+    if (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and t.shape == shape \
+            and t.get_device() == index and t.is_contiguous():
+        return
+    if t.shape != shape or not (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, the device of the call's tensors")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def check_scales(name: str, scales: torch.Tensor, pages: int, index: int) -> int:
     """Scales [pages, 64 / block_tokens] of a cache; returns block_tokens."""
-    check_tensor(name, scales, torch.float32, (pages, None), device)
-    per_page = scales.shape[1]
-    if per_page < 1 or per_page > PAGE_SIZE or PAGE_SIZE % per_page:
-        raise ValueError(f"{name} must hold 1, 2, 4, .. 64 scales a page, got {per_page}")
+    check_tensor(name, scales, torch.float32, (pages, *scales.shape[1:2]), index)
+    per_page = scales.shape[1] if scales.dim() == 2 else 0
+    if per_page < 1 or PAGE_SIZE % per_page:
+        raise ValueError(f"{name} must hold 1, 2, 4, .. 64 scales a page, got {list(scales.shape)}")
     return PAGE_SIZE // per_page
 
 
-def check_status(status: torch.Tensor | None, device) -> None:
-    if status is not None:
-        check_tensor("status", status, torch.int32, (1,), device)
+def check_table(name: str, table: torch.Tensor, batch: int, index: int) -> int:
+    """A page table [batch, stride] int32; returns its stride."""
+    if table.dim() != 2:
+        raise ValueError(f"{name} must be int32 [batch, stride], got {list(table.shape)}")
+    stride = table.shape[1]
+    check_tensor(name, table, torch.int32, (batch, stride), index)
+    return stride
 
 
-def _cuda_device(t: torch.Tensor) -> torch.device:
-    if not t.is_cuda:
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _cuda_index(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("the cache operators run on CUDA tensors")
-    return t.device
+    return index
 
 
 def append(rows: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
@@ -67,20 +86,20 @@ def append(rows: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, page_t
     tokens: its length with them is seq_lens[b] (int32, device). ``max_new`` is at least the
     largest number of new rows of a request.
     """
-    device = _cuda_device(rows)
-    check_tensor("rows", rows, torch.bfloat16, (None, D_QK), device)
-    check_tensor("codes", codes, (torch.uint8, torch.float8_e4m3fn), (None, PAGE_SIZE, D_QK), device)
-    block = check_scales("scales", scales, codes.shape[0], device)
-    check_tensor("page_table", page_table, torch.int32, (None, None), device)
-    batch = page_table.shape[0]
-    check_tensor("seq_lens", seq_lens, torch.int32, (batch,), device)
-    check_tensor("cu_new", cu_new, torch.int32, (batch + 1,), device)
-    check_status(status, device)
-    st = stream if stream is not None else torch.cuda.current_stream(device)
-    with device_guard(device):
-        binding.cache_append(rows.data_ptr(), rows.shape[0], cu_new.data_ptr(), seq_lens.data_ptr(), batch, max_new,
-                             codes.data_ptr(), scales.data_ptr(), block, page_table.data_ptr(), page_table.shape[1],
-                             codes.shape[0], None if status is None else status.data_ptr(), st.cuda_stream)
+    index = _cuda_index(rows)
+    check_tensor("rows", rows, torch.bfloat16, rows.shape[:1] + (D_QK,), index)
+    pages = codes.shape[0] if codes.dim() else 0
+    check_tensor("codes", codes, E4M3, (pages, *ROW), index)
+    block = check_scales("scales", scales, pages, index)
+    batch = page_table.shape[0] if page_table.dim() else 0
+    stride = check_table("page_table", page_table, batch, index)
+    check_tensor("seq_lens", seq_lens, torch.int32, (batch,), index)
+    check_tensor("cu_new", cu_new, torch.int32, (batch + 1,), index)
+    if status is not None:
+        check_tensor("status", status, torch.int32, (1,), index)
+    on_device(index, binding.cache_append, rows.data_ptr(), rows.shape[0], cu_new.data_ptr(), seq_lens.data_ptr(), batch,
+              max_new, codes.data_ptr(), scales.data_ptr(), block, page_table.data_ptr(), stride, pages, _ptr(status),
+              stream_handle(index, stream))
 
 
 def evict(weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, n_first: int, n_last: int, kv: torch.Tensor,
@@ -98,41 +117,38 @@ def evict(weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, n_first: i
     ``kv_dst`` may be ``kv`` itself; the new pages must not be among the old ones. ``max_seq``
     (default: what ``weights`` and ``page_table`` have room for) is at least the longest length.
     """
-    device = _cuda_device(weights)
-    check_tensor("weights", weights, torch.float32, (None, None), device)
-    batch = weights.shape[0]
-    if kv.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
-        raise ValueError("kv must be bf16, or e4m3 codes as uint8 or float8_e4m3fn")
+    index = _cuda_index(weights)
+    if weights.dim() != 2:
+        raise ValueError(f"weights must be fp32 [batch, stride], got {list(weights.shape)}")
+    batch, w_stride = weights.shape
+    check_tensor("weights", weights, torch.float32, (batch, w_stride), index)
     bf16 = kv.dtype == torch.bfloat16
-    check_tensor("kv", kv, kv.dtype, (None, PAGE_SIZE, D_QK), device)
-    check_tensor("kv_dst", kv_dst, torch.bfloat16 if bf16 else (torch.uint8, torch.float8_e4m3fn),
-                 (None, PAGE_SIZE, D_QK), device)
-    if (scales is None) != (scales_dst is None):
-        raise ValueError("scales and scales_dst must both be given, or neither")
+    kind = torch.bfloat16 if bf16 else E4M3
+    pages, pages_dst = kv.shape[0] if kv.dim() else 0, kv_dst.shape[0] if kv_dst.dim() else 0
+    check_tensor("kv", kv, kind, (pages, *ROW), index)
+    check_tensor("kv_dst", kv_dst, kind, (pages_dst, *ROW), index)
     block = 0
-    if scales is not None:
-        block = check_scales("scales", scales, kv.shape[0], device)
-        if check_scales("scales_dst", scales_dst, kv_dst.shape[0], device) != block:
+    if scales is not None and scales_dst is not None:
+        block = check_scales("scales", scales, pages, index)
+        if check_scales("scales_dst", scales_dst, pages_dst, index) != block:
             raise ValueError("scales and scales_dst must have the same block_tokens")
-    check_tensor("page_table", page_table, torch.int32, (batch, None), device)
-    check_tensor("page_table_dst", page_table_dst, torch.int32, (batch, None), device)
-    check_tensor("seq_lens", seq_lens, torch.int32, (batch,), device)
-    check_tensor("seq_lens_dst", seq_lens_dst, torch.int32, (batch,), device)
-    check_tensor("kept", kept, torch.int32, (batch, budget), device)
+    elif scales is not None or scales_dst is not None:
+        raise ValueError("scales and scales_dst must both be given, or neither")
+    stride = check_table("page_table", page_table, batch, index)
+    stride_dst = check_table("page_table_dst", page_table_dst, batch, index)
+    check_tensor("seq_lens", seq_lens, torch.int32, (batch,), index)
+    check_tensor("seq_lens_dst", seq_lens_dst, torch.int32, (batch,), index)
+    check_tensor("kept", kept, torch.int32, (batch, budget), index)
+    wd_stride = 0
     if weights_dst is not None:
-        check_tensor("weights_dst", weights_dst, torch.float32, (batch, None), device)
-    check_status(status, device)
+        wd_stride = weights_dst.shape[1] if weights_dst.dim() == 2 else 0
+        check_tensor("weights_dst", weights_dst, torch.float32, (batch, wd_stride), index)
+    if status is not None:
+        check_tensor("status", status, torch.int32, (1,), index)
     if max_seq is None:
-        max_seq = min(weights.shape[1], PAGE_SIZE * page_table.shape[1])
-    st = stream if stream is not None else torch.cuda.current_stream(device)
-    with device_guard(device):
-        binding.cache_evict(weights.data_ptr(), weights.shape[1], seq_lens.data_ptr(), batch,
-                            max_seq, budget, n_first, n_last,
-                            binding.MLA_KV_BF16 if bf16 else binding.MLA_KV_FP8_E4M3, kv.data_ptr(),
-                            None if scales is None else scales.data_ptr(), block, page_table.data_ptr(),
-                            page_table.shape[1], kv.shape[0], kv_dst.data_ptr(),
-                            None if scales_dst is None else scales_dst.data_ptr(), page_table_dst.data_ptr(),
-                            page_table_dst.shape[1], kv_dst.shape[0], kept.data_ptr(), seq_lens_dst.data_ptr(),
-                            None if weights_dst is None else weights_dst.data_ptr(),
-                            0 if weights_dst is None else weights_dst.shape[1],
-                            None if status is None else status.data_ptr(), st.cuda_stream)
+        max_seq = min(w_stride, PAGE_SIZE * stride)
+    on_device(index, binding.cache_evict, weights.data_ptr(), w_stride, seq_lens.data_ptr(), batch, max_seq, budget,
+              n_first, n_last, binding.MLA_KV_BF16 if bf16 else binding.MLA_KV_FP8_E4M3, kv.data_ptr(), _ptr(scales),
+              block, page_table.data_ptr(), stride, pages, kv_dst.data_ptr(), _ptr(scales_dst),
+              page_table_dst.data_ptr(), stride_dst, pages_dst, kept.data_ptr(), seq_lens_dst.data_ptr(),
+              _ptr(weights_dst), wd_stride, _ptr(status), stream_handle(index, stream))

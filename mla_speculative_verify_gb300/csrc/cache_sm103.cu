@@ -24,7 +24,7 @@
 
 namespace mla {
 
-int current_device_ready(int* dev);   // defined next to the decode kernel
+int current_device_ready(int* sms);   // defined next to the decode kernel
 int block_log2_of(int block_tokens);  // defined with the plan
 
 namespace {
@@ -590,6 +590,13 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 }  // namespace
+
+cudaError_t set_cache_kernel_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSelCache);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
+}
+
 }  // namespace mla
 
 using namespace mla;
@@ -614,8 +621,8 @@ extern "C" int mla_cache_append(const void* rows, int total_rows, const int32_t*
     return set_error(MLA_ERR_INVALID_ARG, "rows and kv_cache must be 16-byte aligned");
   if (!aligned4(cu_new) || !aligned4(seq_lens) || !aligned4(kv_scales) || !aligned4(page_table) || !aligned4(status_dev))
     return set_error(MLA_ERR_INVALID_ARG, "cu_new, seq_lens, kv_scales, page_table and status_dev must be 4-byte aligned");
-  int dev = 0;
-  const int rc = current_device_ready(&dev);
+  int sms = 0;
+  const int rc = current_device_ready(&sms);
   if (rc != MLA_OK) return rc;
   const AppendArgs a{(const uint4*)rows, total_rows, page_table, page_table_stride, num_pages, max_new, bl,
                      seq_lens, cu_new, (uint8_t*)kv_cache, kv_scales, status_dev};
@@ -666,12 +673,9 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   if (weights_stride < max_seq || (weights_dst && weights_dst_stride < most))
     return set_error(MLA_ERR_INVALID_ARG, "weights_stride %lld or weights_dst_stride %lld is smaller than a row",
                      weights_stride, weights_dst_stride);
-  int dev = 0;
-  const int rc = current_device_ready(&dev);
-  if (rc != MLA_OK) return rc;
   int sms = 0;
-  cudaError_t ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(ce));
+  const int rc = current_device_ready(&sms);
+  if (rc != MLA_OK) return rc;
 
   // CTAs per request: one for every 8192 keys, up to a cluster of 16
   int ctas = 1;
@@ -680,10 +684,6 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   const int cache = std::min(kSelCache, kSelWarps * warp_keys);
   const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last, cache,
                      kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
-  ce = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSelCache);
-  if (ce == cudaSuccess && ctas > 8)
-    ce = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(ce));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((unsigned)ctas, (unsigned)batch, 1);
@@ -696,7 +696,7 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  ce = cudaLaunchKernelEx(&cfg, evict_select_kernel, s);
+  cudaError_t ce = cudaLaunchKernelEx(&cfg, evict_select_kernel, s);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction select kernel launch: %s", cudaGetErrorString(ce));
   if (pages_dst == 0) return MLA_OK;
 

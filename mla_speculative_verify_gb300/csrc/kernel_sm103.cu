@@ -1215,10 +1215,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 struct DeviceInfo {
   bool checked = false, ok = false, attrs_set = false;
-  int major = 0, minor = 0;
+  int major = 0, minor = 0, sms = 0;
 };
 static DeviceInfo g_dev[64];
 static std::mutex g_dev_mu;
+
+cudaError_t set_weights_kernel_attributes();  // defined next to those kernels
+cudaError_t set_cache_kernel_attributes();
 
 static int prepare_device(int dev) {
   if (dev < 0 || dev >= 64) return set_error(MLA_ERR_CUDA, "device ordinal %d out of range", dev);
@@ -1227,6 +1230,7 @@ static int prepare_device(int dev) {
   if (!d.checked) {
     cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev);
+    cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
     d.ok = (d.major == 10 && d.minor == 3);
     d.checked = true;
   }
@@ -1238,16 +1242,23 @@ static int prepare_device(int dev) {
       const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesScaled);
       if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
     }
+    cudaError_t e = set_weights_kernel_attributes();
+    if (e == cudaSuccess) e = set_cache_kernel_attributes();
+    if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
     d.attrs_set = true;
   }
   return MLA_OK;
 }
 
-// The current device, checked to be one this library runs on (for the other entry points).
-int current_device_ready(int* dev) {
-  const cudaError_t ce = cudaGetDevice(dev);
+// The current device, checked to be one this library runs on, and its SMs (for the other entry
+// points).
+int current_device_ready(int* sms) {
+  int dev = 0;
+  const cudaError_t ce = cudaGetDevice(&dev);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(ce));
-  return prepare_device(*dev);
+  const int rc = prepare_device(dev);
+  if (rc == MLA_OK) *sms = g_dev[dev].sms;
+  return rc;
 }
 
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }

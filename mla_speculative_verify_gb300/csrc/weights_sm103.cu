@@ -53,7 +53,7 @@
 
 namespace mla {
 
-int current_device_ready(int* dev);                         // defined next to the decode kernel
+int current_device_ready(int* sms);                         // defined next to the decode kernel
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();     // defined next to the decode kernel
 int block_log2_of(int block_tokens);                        // defined with the plan
 int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out);
@@ -605,6 +605,14 @@ CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const v
 }
 
 }  // namespace
+
+cudaError_t set_weights_kernel_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(key_weights_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
+  return e;
+}
+
 }  // namespace mla
 
 using namespace mla;
@@ -665,20 +673,15 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
     return set_error(MLA_ERR_BUFFER, "workspace needs %zu bytes (got %zu)", need, workspace ? workspace_bytes : (size_t)0);
   if (need > 0 && ((uintptr_t)workspace & 255u)) return set_error(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
 
-  int dev = 0;
-  rc = current_device_ready(&dev);
-  if (rc != MLA_OK) return rc;
   int sms = 0;
-  cudaError_t ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaDeviceGetAttribute: %s", cudaGetErrorString(ce));
+  rc = current_device_ready(&sms);
+  if (rc != MLA_OK) return rc;
   const int piece = fp8 ? 8192 : 16384, tile_bytes = kPieces * piece;
   const int fixed = 1024 + kMiscBytes + kPieces * most_rows * 128;
   const int per = pieces_per_stage(fp8);
   const int stages = std::min(kMaxStages, (kSmemCap - fixed) / (per * piece));
   const int smem = fixed + stages * per * piece;
   auto fn = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
-  ce = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
-  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(ce));
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return set_error(MLA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
 
@@ -726,7 +729,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   if (fp8) {
     q_split_kernel<<<(prm.total_rows + kSplitWarps - 1) / kSplitWarps, 32 * kSplitWarps, 0, st>>>(
         (const uint4*)q, prm.total_rows, (uint8_t*)workspace, const_cast<float*>(prm.q_scale));
-    ce = cudaGetLastError();
+    const cudaError_t ce = cudaGetLastError();
     if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "Q split kernel launch: %s", cudaGetErrorString(ce));
   }
   cudaLaunchConfig_t cfg = {};
@@ -739,7 +742,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = fp8 ? 1 : 0;
-  ce = cudaLaunchKernelEx(&cfg, fn, tq, tkv, tpage, prm);
+  const cudaError_t ce = cudaLaunchKernelEx(&cfg, fn, tq, tkv, tpage, prm);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "key weights kernel launch: %s", cudaGetErrorString(ce));
   return MLA_OK;
 }

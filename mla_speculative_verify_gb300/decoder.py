@@ -14,7 +14,7 @@ import numpy as np
 import torch
 
 from . import binding
-from .cache import check_scales, check_status, check_tensor, device_guard
+from .cache import E4M3, check_scales, check_table, check_tensor, on_device, stream_handle
 
 KV_DTYPES = {"bf16": binding.MLA_KV_BF16, "fp8": binding.MLA_KV_FP8_E4M3}
 SM_SCALE = 1.0 / math.sqrt(192.0)
@@ -49,6 +49,7 @@ class VerifyDecoder:
         self.plan_host, self.workspace_bytes = binding.plan(self.seq_lens, self.q_lens, self.num_heads,
                                                             KV_DTYPES[kv_dtype], self.num_sms, options)
         self.info = binding.plan_info(self.plan_host)
+        self._plan_host_ptr = self.plan_host.ctypes.data
         self.weights_workspace_bytes = binding.key_weights_workspace(self.plan_host)
         # the plan runs on clusters of two CTAs (PlanHeader.cta_pair, the int32 at byte 64)
         self.cta_pair = bool(int(self.plan_host[64:68].view(np.int32)[0]))
@@ -86,19 +87,20 @@ class VerifyDecoder:
         for t in (q, kv_cache, out, page_table, lse, status):
             if t is not None and t.device != self.device:
                 raise ValueError("all tensors must be on the decoder's device")
-        st = stream if stream is not None else torch.cuda.current_stream(self.device)
         if kv_scales is not None:
             if self.kv_dtype != "fp8":
                 raise ValueError("block scales belong to an fp8 cache")
-            block = check_scales("kv_scales", kv_scales, rows // 64, self.device)
-            with device_guard(self.device):
-                binding.run_scaled(self.plan_dev.data_ptr(), self.plan_host, q.data_ptr(), kv_cache.data_ptr(),
-                                   kv_scales.data_ptr(), block, page_table.data_ptr(), page_table.shape[1], rows // 64,
-                                   (seq_lens_dev if seq_lens_dev is not None else self.seq_lens_dev).data_ptr(),
-                                   (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(),
-                                   sm_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
-                                   _ptr(status), st.cuda_stream)
+            index = self.device.index
+            block = check_scales("kv_scales", kv_scales, rows // 64, index)
+            on_device(index, binding.run_scaled, self.plan_dev.data_ptr(), self._plan_host_ptr, self.plan_host.nbytes,
+                      q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block, page_table.data_ptr(),
+                      page_table.shape[1], rows // 64,
+                      (seq_lens_dev if seq_lens_dev is not None else self.seq_lens_dev).data_ptr(),
+                      (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(),
+                      sm_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
+                      _ptr(status), stream_handle(index, stream))
             return
+        st = stream if stream is not None else torch.cuda.current_stream(self.device)
         binding.run(self.plan_dev.data_ptr(), self.plan_host, q.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
                     page_table.shape[1], rows // 64,
                     (seq_lens_dev if seq_lens_dev is not None else self.seq_lens_dev).data_ptr(),
@@ -115,31 +117,31 @@ class VerifyDecoder:
         ``lse`` that ``run`` wrote. ``counted`` [batch] int32: only the first so many verify
         tokens of a request count (the accepted ones). Its scratch comes from torch's allocator,
         call by call, so calls on several streams or captured in several graphs share none."""
-        H, batch, dev = self.num_heads, self.seq_lens.shape[0], self.device
-        if dev.type != "cuda":
+        if self.device.type != "cuda":
             raise ValueError("key_weights runs on a CUDA device")
-        check_tensor("q", q, torch.bfloat16, (self.total_q, H, 576), dev)
-        check_tensor("kv_cache", kv_cache,
-                     torch.bfloat16 if self.kv_dtype == "bf16" else (torch.uint8, torch.float8_e4m3fn),
-                     (None,) * (kv_cache.dim() - 1) + (576,), dev)
-        rows = kv_cache.numel() // 576
-        if rows % 64:
-            raise ValueError("kv_cache must hold whole 64-row pages")
-        block = 0 if kv_scales is None else check_scales("kv_scales", kv_scales, rows // 64, dev)
-        check_tensor("page_table", page_table, torch.int32, (batch, None), dev)
-        check_tensor("lse", lse, torch.float32, (self.total_q, H), dev)
-        check_tensor("weights", weights, torch.float32, (batch, None), dev)
+        H, batch, index = self.num_heads, self.seq_lens.shape[0], self.device.index
+        check_tensor("q", q, torch.bfloat16, (self.total_q, H, 576), index)
+        if kv_cache.shape[-1:] != (576,) or kv_cache.numel() % (64 * 576):
+            raise ValueError("kv_cache must hold whole 64-row pages [..., 576]")
+        pages = kv_cache.numel() // (64 * 576)
+        check_tensor("kv_cache", kv_cache, torch.bfloat16 if self.kv_dtype == "bf16" else E4M3, kv_cache.shape, index)
+        block = 0 if kv_scales is None else check_scales("kv_scales", kv_scales, pages, index)
+        stride = check_table("page_table", page_table, batch, index)
+        check_tensor("lse", lse, torch.float32, (self.total_q, H), index)
+        w_stride = weights.shape[1] if weights.dim() == 2 else 0
+        check_tensor("weights", weights, torch.float32, (batch, w_stride), index)
         if counted is not None:
-            check_tensor("counted", counted, torch.int32, (batch,), dev)
-        check_status(status, dev)
-        st = stream if stream is not None else torch.cuda.current_stream(dev)
-        need = self.weights_workspace_bytes
-        with device_guard(dev):
-            scratch = None
-            if need:
-                with torch.cuda.stream(st):
-                    scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-            binding.key_weights(self.plan_dev.data_ptr(), self.plan_host, q.data_ptr(), kv_cache.data_ptr(),
-                                _ptr(kv_scales), block, page_table.data_ptr(), page_table.shape[1], rows // 64,
-                                lse.data_ptr(), _ptr(counted), sm_scale, kv_scale, decay, weights.data_ptr(),
-                                weights.shape[1], _ptr(scratch), need, _ptr(status), st.cuda_stream)
+            check_tensor("counted", counted, torch.int32, (batch,), index)
+        if status is not None:
+            check_tensor("status", status, torch.int32, (1,), index)
+        need, scratch = self.weights_workspace_bytes, None
+        if need:
+            if stream is None:
+                scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+            else:
+                with torch.cuda.stream(stream):
+                    scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+        on_device(index, binding.key_weights, self.plan_dev.data_ptr(), self._plan_host_ptr, self.plan_host.nbytes,
+                  q.data_ptr(), kv_cache.data_ptr(), _ptr(kv_scales), block, page_table.data_ptr(), stride, pages,
+                  lse.data_ptr(), _ptr(counted), sm_scale, kv_scale, decay, weights.data_ptr(), w_stride, _ptr(scratch),
+                  need, _ptr(status), stream_handle(index, stream))
