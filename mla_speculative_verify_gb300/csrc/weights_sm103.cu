@@ -26,15 +26,13 @@
 //
 // The tensor cores cut the bits below an accumulator's last one at every step, always towards
 // zero, so a score of 36 steps in one accumulator is off by ~2^-20 of itself: 1.9e-5 in the
-// weights of a million keys with scores of 20 and more. The columns are therefore summed in
-// parts (three for bf16, two for e4m3, whose steps are half as many), each in an accumulator
-// that starts at zero, and the parts are added in fp32 registers, rounded: 6.8e-6 there. A part
-// has an issuing warp of its own, since one thread issues a product only every ~100 cycles. The
-// accumulators form a ring, so the next tile's products run while this one's are read.
+// weights of a million keys with scores of 20 and more. Each tile's columns are therefore summed
+// in three parts of three pieces, each in an accumulator that starts at zero, and the parts are
+// added in fp32 registers, rounded: 6.8e-6 there. While one part is read the next is computed.
 //
-// Warp roles (one CTA per SM): warp 0 loads (TMA), warps 1-3 (e4m3: 1-2) issue the products, a part each,
-// warps 4-7 and 8-11 take the scores out, each half of the rows. All of them walk the same work list (Walk).
-// Waits are bounded as in the decode kernel.
+// Warp roles (one CTA per SM): warps 0-3 load (TMA) and issue the products (Roles), warps 4-7
+// and 8-11 take the scores out, each half of the rows. All of them walk the same work list
+// (Walk). Waits are bounded as in the decode kernel.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -66,12 +64,23 @@ constexpr int kMaxRows = 128;       // rows of a group
 constexpr int kMaxStages = 16;
 constexpr int kParts = 3;           // parts of a score's 576 columns, three pieces each
 constexpr int kPartPieces = kPieces / kParts;
-constexpr int kMaxSlots = 8;        // accumulators of the ring
-// Pieces that share a stage of the ring. The issuer's waits and commits cost it ~300 cycles a
-// stage, more than the products of an e4m3 piece take, so three of those go together (batch
-// of 128 heads 207 -> 179 us). bf16 pieces are twice as large: two stages of three would be all
-// that fits, and the copies stall (a million keys 202 -> 208 us).
-__host__ __device__ constexpr int pieces_per_stage(bool fp8) { return fp8 ? 3 : 1; }
+constexpr int kMaxSlots = 6;        // accumulators, taken in turns by the parts
+// What the four control warps do. The e4m3 products of a tile take less time than one thread
+// needs to issue them (~125 cycles each, and ~300 for a stage's waits and commits), so each
+// part has an issuer and its three pieces share a stage; one warp loads. bf16 tiles are twice
+// as large and bound by the copies: one issuer, a loading warp for each of a tile's two pages,
+// and stages of one piece, since two of three would be all that fits (a million keys 202 -> 208
+// us).
+template <bool kFp8>
+struct Roles {
+  static constexpr int kPer = kFp8 ? kPartPieces : 1;  // pieces of a stage
+  static constexpr int kLoaders = kFp8 ? 1 : 2;        // warps 0 and (bf16) 2
+  static constexpr int kIssuers = kFp8 ? 3 : 1;        // warps 1 ..
+  // An issuer waits for a stage's or an accumulator's next phase, which says nothing while the
+  // phase before it is open; so with several issuers each of them belongs to one issuer: their
+  // number is a multiple of this.
+  static constexpr int kRingUnit = kFp8 ? kParts : 1;
+};
 constexpr int kMaxSub = 16;         // tiles of one sub-range: 32 page ids, one per lane
 constexpr int kMaxSubSums = 8;      // of those when sums wait in shared memory (G > 1)
 constexpr int kThreads = 384;
@@ -80,7 +89,7 @@ constexpr int kSmemCap = 232448;    // 227 KB per CTA
 struct WeightsMisc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[kPieces], q_empty[kPieces];
-  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done;
+  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done[kParts];
   uint32_t tmem_base;
   int abort;
   alignas(16) float nlse[kMaxRows];    // -lse * log2(e) of the current group's rows
@@ -103,9 +112,8 @@ struct WeightsParams {
   long long w_stride;
   float decay, scale_log2;
   int rows_n;              // MMA rows of every group (multiple of 32)
-  int slots;               // accumulators in the ring
   int total_rows;
-  int stages, sub_tiles;
+  int stages, slots, sub_tiles;
   long long total_work;    // sum over requests of tiles * groups
   int32_t* status;
   long long wait_budget;
@@ -196,7 +204,6 @@ template <int NC, bool kFp8>
 __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc* ms, Walk& walk, uint32_t tmem, int wg,
                                              int qd, int lane) {
   constexpr int kCols = 16 * NC, n = 32 * NC;
-  constexpr uint32_t kSlotCols = kFp8 ? 2 * n : n;
   const int key_in = 32 * qd + lane, col0 = kCols * wg;
   const uint32_t acc0 = tmem + col0 + ((uint32_t)(32 * qd) << 16);
   const float* nlse = ms->nlse + col0;
@@ -254,28 +261,16 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
             if (ok) ok = warp_wait(&ms->d_full[slot], slots.phase & 1, abort, p);
             if (ok && mine > 0) {
               ptx::tc_fence_after();
-              const uint32_t acc = acc0 + slot * kSlotCols;
-              // e4m3: up to 32 rows' hi and lo columns in flight; bf16: all rows
-              constexpr int kStep = kFp8 ? (NC < 2 ? NC : 2) : NC;
+              float y[kCols];
 #pragma unroll
-              for (int c0 = 0; c0 < NC; c0 += kStep) {
-                float y[16 * kStep], z[16 * kStep];
+              for (int c = 0; c < NC; ++c) ptx::tmem_ld16(acc0 + slot * n + 16 * c, y + 16 * c);
+              ptx::tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < kStep; ++c) {
-                  if (c0 + c >= NC) break;
-                  ptx::tmem_ld16(acc + 16 * (c0 + c), y + 16 * c);
-                  if (kFp8) ptx::tmem_ld16(acc + n + 16 * (c0 + c), z + 16 * c);
-                }
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16 * kStep; j += 2) {
-                  if (16 * c0 + j >= kCols) break;
-                  float2 v = make_float2(y[j], y[j + 1]);
-                  if (kFp8) v = ptx::add2(v, make_float2(z[j], z[j + 1]));
-                  if (u > 0) v = ptx::add2(v, make_float2(x[16 * c0 + j], x[16 * c0 + j + 1]));
-                  x[16 * c0 + j] = v.x;
-                  x[16 * c0 + j + 1] = v.y;
-                }
+              for (int j = 0; j < kCols; j += 2) {
+                float2 v = make_float2(y[j], y[j + 1]);
+                if (u > 0) v = ptx::add2(v, make_float2(x[j], x[j + 1]));
+                x[j] = v.x;
+                x[j + 1] = v.y;
               }
               ptx::tc_fence_before();
             }
@@ -328,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmap_page, WeightsParams p) {
   constexpr int kRowBytes = kFp8 ? 64 : 128;             // a row's bytes in one 64-column piece
   constexpr int kPieceBytes = kKeys * kRowBytes;
-  constexpr int kPer = pieces_per_stage(kFp8);
+  using R = Roles<kFp8>;
+  constexpr int kPer = R::kPer;
   constexpr int kStageBytes = kPer * kPieceBytes;
   constexpr int kHalf = kPage * kRowBytes;               // one page of a piece
   constexpr uint32_t kSwizzle = kFp8 ? ptx::kSwizzle64B : ptx::kSwizzle128B;
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     ms->abort = 0;
     for (int i = 0; i < p.stages; ++i) {
-      ptx::mbar_init(&ms->kv_full[i], 2);  // a producer for each of the two pages
+      ptx::mbar_init(&ms->kv_full[i], Roles<kFp8>::kLoaders);
       ptx::mbar_init(&ms->kv_empty[i], 1);
     }
     for (int i = 0; i < kPieces; ++i) {
@@ -357,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ms->d_full[i], 1);
       ptx::mbar_init(&ms->d_empty[i], 8);
     }
-    ptx::mbar_init(&ms->mma_done, 1);
+    for (int i = 0; i < kParts; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmap_q);
     ptx::prefetch_tmap(&tmap_kv);
@@ -374,11 +370,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int b, t0, t1;
   PlanRequest req;
 
-  if (warp == 0 || warp == 2) {
+  if (warp == 0 || (R::kLoaders == 2 && warp == 2)) {
     // ------------------------------------------------------------ loads
-    // Warp 0 loads the first page of each tile and Q, warp 2 the second page: a copy takes its
-    // issuer ~150 cycles, and a tile has 18.
-    const int second = warp >> 1;
+    // Warp 0 loads Q and each tile's first page; the second page warp 2, or with one loader
+    // warp 0 too. Lane l holds the page ids of the two pages (or of this warp's) of tile l.
+    constexpr bool kBoth = R::kLoaders == 1;
+    const int second = warp == 2;
     if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
     Ring ring(p.stages);
     uint32_t qfill = 0;  // Q groups loaded so far
@@ -389,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
       const int npages = (req.ctx + kPage - 1) / kPage;
       const int32_t* ids = p.page_table + (size_t)b * p.pt_stride;
-      auto load_ids = [&](int tile) {  // lane l: this producer's page of tile `tile` + l
-        const int pg = 2 * (tile + lane) + second;
+      auto load_ids = [&](int tile, int which) {  // lane l: page `which` of tile `tile` + l
+        const int pg = 2 * (tile + lane) + which;
         int id = lane < sub && tile + lane < t1 && pg < npages ? ids[pg] : 0;
         if (id < 0 || id >= p.num_pages) {
           report(p.status, MLA_DEVICE_BAD_PAGE);
@@ -398,20 +395,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return id;
       };
-      int cur = load_ids(t0);
+      int cur = load_ids(t0, second), cur1 = kBoth ? load_ids(t0, 1) : 0;
       for (int s0 = t0; ok && s0 < t1; s0 += sub) {
         const int s1 = min(t1, s0 + sub);
-        const int nxt = s1 < t1 ? load_ids(s1) : 0;
+        const int nxt = s1 < t1 ? load_ids(s1, second) : 0, nxt1 = kBoth && s1 < t1 ? load_ids(s1, 1) : 0;
         for (int g = 0; ok && g < groups; ++g) {
           const bool new_q = groups > 1 || s0 == t0;
           for (int t = s0; ok && t < s1; ++t) {
             const bool there = 2 * t + second < npages;
-            const int id = __shfl_sync(0xffffffffu, cur, t - s0);
+            const bool there1 = kBoth && 2 * t + 1 < npages;
+            const int id = __shfl_sync(0xffffffffu, cur, t - s0), id1 = __shfl_sync(0xffffffffu, cur1, t - s0);
             // ask L2 for the whole page of the next tile that HBM has to deliver
             const int tn = g == 0 && t + 1 < s1 ? t + 1 : g == groups - 1 && t + 1 == s1 ? s1 : t1;
             const int id_n = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur, (t - s0 + 1) & 31) : __shfl_sync(0xffffffffu, nxt, 0);
-            if (tn < t1 && 2 * tn + second < npages && ptx::elect_one())
-              ptx::tma_prefetch_l2_3d(&tmap_page, 0, id_n * kPage, 0);
+            const int id_n1 = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur1, (t - s0 + 1) & 31) : __shfl_sync(0xffffffffu, nxt1, 0);
+            if (tn < t1 && ptx::elect_one()) {
+              if (2 * tn + second < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, id_n * kPage, 0);
+              if (kBoth && 2 * tn + 1 < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, id_n1 * kPage, 0);
+            }
             for (int c0 = 0; ok && c0 < kPieces; c0 += kPer) {
               for (int c = c0; !second && new_q && t == s0 && c < c0 + kPer; ++c) {
                 if (qfill > 0) ok = warp_wait(&ms->q_empty[c], (qfill - 1) & 1, abort, p);
@@ -427,12 +428,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (ok && ring.phase > 0) ok = warp_wait(&ms->kv_empty[ring.at], (ring.phase - 1) & 1, abort, p);
               if (!ok) break;
               if (ptx::elect_one()) {
+                uint8_t* dst = sK + ring.at * kStageBytes + second * kHalf;
                 if (there) {
-                  ptx::mbar_arrive_expect_tx(&ms->kv_full[ring.at], kPer * kHalf);
+                  ptx::mbar_arrive_expect_tx(&ms->kv_full[ring.at], (there1 ? 2 : 1) * kPer * kHalf);
 #pragma unroll
-                  for (int j = 0; j < kPer; ++j)
-                    ptx::tma_load_3d(sK + ring.at * kStageBytes + j * kPieceBytes + second * kHalf, &tmap_kv,
-                                     &ms->kv_full[ring.at], 0, id * kPage, c0 + j);
+                  for (int j = 0; j < kPer; ++j) {
+                    ptx::tma_load_3d(dst + j * kPieceBytes, &tmap_kv, &ms->kv_full[ring.at], 0, id * kPage, c0 + j);
+                    if (there1)
+                      ptx::tma_load_3d(dst + j * kPieceBytes + kHalf, &tmap_kv, &ms->kv_full[ring.at], 0, id1 * kPage, c0 + j);
+                  }
                 } else {
                   ptx::mbar_arrive(&ms->kv_full[ring.at]);
                 }
@@ -444,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (new_q) ++qfill;
         }
         cur = nxt;
+        cur1 = nxt1;
       }
     }
     // After an abort every copy must have landed before the CTA may exit: the ring's last ones
@@ -459,12 +464,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= R::kIssuers) {
     // ------------------------------------------------------------ products
+    // With three issuers warp 1 + u issues part u of every tile, else warp 1 all of them. Each
+    // accumulator is written by one thread in order, so the sums repeat.
     const uint32_t sq = ptx::smem_addr(sQ), sk = ptx::smem_addr(sK);
-    const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kKeys, 2 * n, 0, 0) : ptx::idesc_bf16(kKeys, n, 0, 0);
-    const uint32_t slot_cols = kFp8 ? 2 * n : n;
+    const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kKeys, n, 0, 0) : ptx::idesc_bf16(kKeys, n, 0, 0);
+    const int u0 = R::kIssuers == 1 ? 0 : warp - 1, u1 = R::kIssuers == 1 ? kParts : warp;
     Ring ring(p.stages), slots(p.slots);
+    for (int i = 0; i < u0; ++i) {
+      ring.step();
+      slots.step();
+    }
     uint32_t qphase = 0;
     bool ok = true, issued = false;
     while (ok && walk.next(p, b, req, t0, t1)) {
@@ -476,38 +487,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; ok && g < groups; ++g) {
           const bool new_q = groups > 1 || s0 == t0, last_q = groups > 1 || s1 == t1;
           for (int t = s0; ok && t < s1; ++t) {
-            for (int c0 = 0; ok && c0 < kPieces; c0 += kPer) {
-              const bool first = c0 % kPartPieces == 0, last = (c0 + kPer) % kPartPieces == 0;
-              if (first && slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
-              for (int c = c0; ok && new_q && t == s0 && c < c0 + kPer; ++c)
-                ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
-              if (ok) ok = warp_wait(&ms->kv_full[ring.at], ring.phase & 1, abort, p);
-              if (!ok) break;
-              ptx::tc_fence_after();
-              const uint32_t d = tmem + slots.at * slot_cols;
-              const uint64_t ad = ptx::smem_desc(sk + ring.at * kStageBytes, 16, kSbo, kSwizzle);
-              const uint64_t bd = ptx::smem_desc(sq + c0 * q_piece, 16, kSbo, kSwizzle);
-              if (ptx::elect_one()) {
+            for (int u = u0; ok && u < u1; ++u) {
+              // what the accumulator held has been read
+              if (slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
+              const uint32_t d = tmem + slots.at * n;
+              for (int c0 = kPartPieces * u; ok && c0 < kPartPieces * (u + 1); c0 += kPer) {
+                const bool first = c0 == kPartPieces * u, last = c0 + kPer == kPartPieces * (u + 1);
+                for (int c = c0; ok && new_q && t == s0 && c < c0 + kPer; ++c)
+                  ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
+                if (ok) ok = warp_wait(&ms->kv_full[ring.at], ring.phase & 1, abort, p);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t ad = ptx::smem_desc(sk + ring.at * kStageBytes, 16, kSbo, kSwizzle);
+                const uint64_t bd = ptx::smem_desc(sq + c0 * q_piece, 16, kSbo, kSwizzle);
+                if (ptx::elect_one()) {
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
+                  for (int j = 0; j < kPer; ++j) {
 #pragma unroll
-                  for (int k = 0; k < kRowBytes / 32; ++k) {  // the address field counts 16 bytes
-                    const uint64_t a = ad + j * (kPieceBytes / 16) + 2 * k, q = bd + j * (q_piece / 16) + 2 * k;
-                    if constexpr (kFp8)
-                      ptx::mma_e4m3_ss(d, a, q, idesc, first && (j | k) == 0 ? 0u : 1u);
-                    else
-                      ptx::mma_bf16_ss(d, a, q, idesc, first && (j | k) == 0 ? 0u : 1u);
+                    for (int k = 0; k < kRowBytes / 32; ++k) {  // the address field counts 16 bytes
+                      const uint64_t a = ad + j * (kPieceBytes / 16) + 2 * k, q = bd + j * (q_piece / 16) + 2 * k;
+                      if constexpr (kFp8) {
+                        ptx::mma_e4m3_ss(d, a, q, idesc, first && (j | k) == 0 ? 0u : 1u);
+                        ptx::mma_e4m3_ss(d, a, q + n * 64 / 16, idesc, 1u);
+                      } else
+                        ptx::mma_bf16_ss(d, a, q, idesc, first && (j | k) == 0 ? 0u : 1u);
+                    }
                   }
+                  ptx::mma_commit(&ms->kv_empty[ring.at]);
+                  if (last_q && t == s1 - 1)
+                    for (int j = 0; j < kPer; ++j) ptx::mma_commit(&ms->q_empty[c0 + j]);
+                  if (last) ptx::mma_commit(&ms->d_full[slots.at]);
                 }
-                ptx::mma_commit(&ms->kv_empty[ring.at]);
-                if (last_q && t == s1 - 1)
-                  for (int j = 0; j < kPer; ++j) ptx::mma_commit(&ms->q_empty[c0 + j]);
-                if (last) ptx::mma_commit(&ms->d_full[slots.at]);
+                __syncwarp();
+                for (int i = 0; i < R::kIssuers; ++i) ring.step();  // the other issuers' stages
+                issued = true;
               }
-              __syncwarp();
-              ring.step();
-              if (last) slots.step();
-              issued = true;
+              for (int i = 0; i < R::kIssuers; ++i) slots.step();
             }
           }
           if (new_q) ++qphase;
@@ -515,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // every product must retire before tensor memory is released (the same lane issued them all)
-    if (issued && ptx::elect_one()) drain_mmas(&ms->mma_done, p.wait_budget);
+    if (issued && ptx::elect_one()) drain_mmas(&ms->mma_done[warp - 1], p.wait_budget);
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ weights
@@ -678,8 +693,9 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   if (rc != MLA_OK) return rc;
   const int piece = fp8 ? 8192 : 16384, tile_bytes = kPieces * piece;
   const int fixed = 1024 + kMiscBytes + kPieces * most_rows * 128;
-  const int per = pieces_per_stage(fp8);
-  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / (per * piece));
+  const int per = fp8 ? Roles<true>::kPer : Roles<false>::kPer;
+  const int unit = fp8 ? Roles<true>::kRingUnit : Roles<false>::kRingUnit;
+  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / (per * piece)) / unit * unit;
   const int smem = fixed + stages * per * piece;
   auto fn = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -710,7 +726,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   prm.scale_log2 = sm_scale * (fp8 && !kv_scales ? kv_scale : 1.f) * 1.4426950408889634f;
   prm.rows_n = most_rows;
   prm.stages = stages;
-  prm.slots = std::min(kMaxSlots, 512 / (fp8 ? 2 * most_rows : most_rows));
+  prm.slots = std::min(kMaxSlots, 512 / most_rows) / unit * unit;
   // tiles that all CTAs together keep in L2 while the groups pass over them
   prm.sub_tiles = std::max(1, std::min<int>(kMaxSubSums, (int)((80LL << 20) / ((long long)tile_bytes * grid))));
   prm.status = status_dev;
