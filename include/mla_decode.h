@@ -291,7 +291,8 @@ int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* 
  *                 call reads, nor be named twice
  *   kept          int32 [batch, budget]: the kept indices in order, then -1
  *   seq_lens_dst  int32 [batch]: the new lengths
- *   weights_dst   NULL, or fp32 [batch, weights_dst_stride]: the kept keys' weights in order
+ *   weights_dst   NULL, or fp32 [batch, weights_dst_stride]: the kept keys' weights in order (a
+ *                 -0 may come back as 0, a NaN as another NaN)
  *
  * A new block's scale is the largest among its rows' old ones; codes of a row from a block
  * with another scale are multiplied by old / new and rounded. Rows of the new pages behind the

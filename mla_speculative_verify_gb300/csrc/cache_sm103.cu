@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "decode_common.cuh"
 #include "mla_decode.h"
 #include "plan_format.h"
 #include "ptx.cuh"
@@ -30,10 +31,6 @@ int block_log2_of(int block_tokens);  // defined with the plan
 namespace {
 
 constexpr int kScaleExpMin = -60, kScaleExpMax = 60;
-
-__device__ __forceinline__ void report(int32_t* status, int bits) {
-  if (status) atomicOr(status, bits);
-}
 
 // The least 2^e, e in [-60, 60], with amax <= 448 * 2^e, from amax's bits: 448 = 1.75 * 2^8, so
 // e is amax's own exponent - 8, one more if its mantissa is above 1.75.
@@ -210,7 +207,7 @@ struct SelectArgs {
   long long w_stride;
   const int32_t* lens;
   int max_seq, budget, n_first, n_last;
-  int cache;  // keys of the shared-memory cache
+  int cache;  // keys a warp keeps in shared memory
   int32_t* kept;
   float* weights_dst;
   long long wd_stride;
@@ -225,13 +222,18 @@ constexpr int kSelCopies = 4;       // copies of a CTA's histogram: equal weight
 constexpr int kSelKeys = 8192;     // keys a CTA takes while the cluster may grow
 constexpr int kSelMaxCtas = 16;    // (a cluster of 16 is beyond the portable 8)
 constexpr int kSelMaxKeys = kSelMaxCtas * 32 * kSelCopies * kBins / 2;  // two mark bits a key in the histograms' place
-constexpr int kSelCache = 36864;   // weights a CTA keeps in shared memory, at most
+constexpr int kSelCache = 1280;    // keys a warp keeps in shared memory, at most
+constexpr int kSelCacheBytes = 4 * 32 * (kSelCache + 4);
 
 // A weight as an unsigned key of the same order; -0 counts as 0, NaN as the lowest.
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float weight_of(uint32_t key) {
+  return key == 0u ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
 // One cluster of CTAs per request (blockIdx.y). The k-th largest key of the middle is found
@@ -243,16 +245,24 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 // in shared memory (what does not fit is read again, from L2). Places behind the last
 // key hold the lowest key: they come after every real one, so none is ever taken.
 //
+template <bool kOne>  // one CTA per request
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  extern __shared__ uint32_t cache[];  // a.cache keys
+  extern __shared__ __align__(16) uint32_t cache[];  // per warp a.cache keys, and 4 places more
+  __shared__ uint64_t loaded[kSelWarps];
   __shared__ __align__(16) uint32_t copies[kSelCopies][kBins], hist[2][kBins];
   __shared__ uint32_t coarse[2][kSelWarps];  // this CTA's counts of 64 bins each
-  __shared__ uint32_t part[kSelThreads], found[3];
+  __shared__ uint32_t part[2][kSelThreads];  // words read from the peers
   __shared__ uint32_t gt_of[kSelWarps], eq_of[kSelWarps], totals[2];
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int rank = kOne ? 0 : (int)cluster.block_rank(), ctas = kOne ? 1 : (int)cluster.num_blocks();
+  auto sync_all = [&] {
+    if (kOne)
+      __syncthreads();
+    else
+      cluster.sync();
+  };
   const int n = a.lens[b];
   const float* w = a.weights + (size_t)b * a.w_stride;
   int32_t* kept = a.kept + (size_t)b * a.budget;
@@ -283,21 +293,41 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
   if (k == 0) return;  // the whole cluster again
   const int per = ((m + ctas * kSelWarps - 1) / (ctas * kSelWarps) + kSelStep - 1) / kSelStep * kSelStep;
   const long long i0 = ((long long)rank * kSelWarps + warp) * per;  // this warp's first key
-  const int c0 = warp * per;                                          // its place in the CTA
   const float* wm = w + lo;
+  // key i + lane of the warp is there while i < left; the first `cached` are kept
+  const int left = (int)max(-32ll, min((long long)per, m - i0)) - lane;
+  const int cached = min(per, a.cache);
+  const float* wl = wm + i0 + lane;
+  // The weights that are kept come in by one bulk copy for each warp, which wants 16-byte
+  // boundaries: they lie in shared memory as they do in their 16 bytes of global memory, and up
+  // to three before the first boundary and after the last come in by themselves.
+  const int count = max(0, min(cached, left + lane));
+  const int off = (int)(((uintptr_t)(wm + i0) >> 2) & 3);
+  uint32_t* cw = cache + warp * (a.cache + 4) + off;
+  uint32_t* cl = cw + lane;
+  const int head = min(count, (4 - off) & 3), body_words = (count - head) & ~3, rest = count - head - body_words;
+  if (lane == 0) {
+    ptx::mbar_init(&loaded[warp], 1);
+    ptx::fence_mbar_init();
+    if (body_words > 0) {
+      ptx::mbar_arrive_expect_tx(&loaded[warp], 4 * body_words);
+      ptx::bulk_load(cw + head, wm + i0 + head, 4 * body_words, &loaded[warp]);
+    }
+  }
+  if (lane < head) cw[lane] = __float_as_uint(wm[i0 + lane]);
+  if (lane < rest) cw[head + body_words + lane] = __float_as_uint(wm[i0 + head + body_words + lane]);
   for (int i = tid; i < kSelCopies * kBins; i += kSelThreads) (&copies[0][0])[i] = 0u;
   __syncthreads();
-  // key i + lane of the warp is there while i < left; the first `cached` are kept
-  const int left = (int)min((long long)per, m - i0) - lane;
-  const int cached = max(0, min(per, a.cache - c0)) / kSelStep * kSelStep;
-  const float* wl = wm + i0 + lane;
-  uint32_t* cl = cache + c0 + lane;
-  // the weights that are kept come in by asynchronous copies, all of them in flight together,
-  // and become keys in place
-  for (int i = 0; i < min(cached, left); i += 32)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_addr(cl + i)), "l"(wl + i) : "memory");
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  for (int i = 0; i < cached; i += 32) cl[i] = i < left ? order_key(__uint_as_float(cl[i])) : 0u;
+  if (body_words > 0) {
+    const long long t0 = clock64();
+    while (!ptx::mbar_try_wait(&loaded[warp], 0)) {
+      if (clock64() - t0 > kWaitBudget) {
+        report(a.status, MLA_DEVICE_WAIT_TIMEOUT);
+        break;
+      }
+    }
+  }
+  __syncwarp();
   // body(keys i + lane, i + lane + 32, .., i) for every step of the warp's keys
   auto sweep = [&](auto body) {
     int i = 0;
@@ -329,6 +359,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int above = pass == 1 ? 21 : 10;  // the bits from this one up are found (pass 0: none)
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    if (pass == 0)  // (the copied weights become keys as they are counted)
+#pragma unroll 4
+      for (int i = 0; i < cached; i += 32) cl[i] = i < left ? order_key(__uint_as_float(cl[i])) : 0u;
     sweep([&](const uint32_t (&key)[4], int) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -351,69 +384,76 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
       for (int o = 16; o > 0; o >>= 1) s64 += __shfl_xor_sync(0xffffffffu, s64, o);
       if (lane == 0) coarse[pass & 1][warp] = s64;
     }
-    cluster.sync();
+    sync_all();
     // Coarse to fine, so that few words cross the cluster: first the 64 bins that hold the
-    // wanted rank, by the counts of 64 bins each, then the one among them. Warp r reads CTA r's.
-    part[tid] = warp < ctas ? cluster.map_shared_rank(&coarse[pass & 1][0], warp)[kSelWarps - 1 - lane] : 0u;
-    __syncthreads();
-    if (warp == 0) {  // lane l: bins 64 (31 - l) ..
-      uint32_t c = 0;
-      for (int r = 0; r < ctas; ++r) c += part[32 * r + lane];
-      uint32_t incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      if (incl - c < want && incl >= want) {
-        found[0] = (uint32_t)(kSelWarps - 1 - lane);
-        found[1] = want - (incl - c);
-      }
+    // wanted rank, by the counts of 64 bins each, then the one among them. Warp r reads CTA r's;
+    // then every warp finds the same.
+    if (!kOne) {
+      part[0][tid] = warp < ctas ? cluster.map_shared_rank(&coarse[pass & 1][0], warp)[lane] : 0u;
+      __syncthreads();
     }
-    __syncthreads();
-    const uint32_t c64 = found[0];
-    want = found[1];
-    part[tid] = (tid >> 6) < ctas ? cluster.map_shared_rank(&hist[pass & 1][0], tid >> 6)[64 * c64 + 63 - (tid & 63)] : 0u;
-    __syncthreads();
-    if (warp == 0) {  // lane l: bins 63 - 2 l and 62 - 2 l of those
-      uint32_t n0 = 0, n1 = 0;
-      for (int r = 0; r < ctas; ++r) {
-        n0 += part[64 * r + 2 * lane];
-        n1 += part[64 * r + 2 * lane + 1];
-      }
-      uint32_t incl = n0 + n1;
+    uint32_t n0 = 0, n1 = 0;  // lane l: the counts of bins 64 (31 - l) ..
+    if (kOne)
+      n0 = coarse[pass & 1][kSelWarps - 1 - lane];
+    else
+      for (int r = 0; r < ctas; ++r) n0 += part[0][32 * r + kSelWarps - 1 - lane];
+    uint32_t incl = n0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      const uint32_t before = incl - n0 - n1;
-      if (before < want && before + n0 >= want) {
-        found[1] = 64 * c64 + 63 - 2 * lane;
-        found[2] = want - before;
-      } else if (before + n0 < want && incl >= want) {
-        found[1] = 64 * c64 + 62 - 2 * lane;
-        found[2] = want - before - n0;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
     }
-    __syncthreads();
-    prefix = pass == 0 ? found[1] : (prefix << (pass == 1 ? 11 : 10)) | found[1];
-    want = found[2];
+    int at = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;  // (there is one: want is a rank)
+    want -= __shfl_sync(0xffffffffu, incl - n0, at);
+    const uint32_t base = 64 * (kSelWarps - 1 - at);
+    if (!kOne) {
+      part[1][tid] = (tid >> 6) < ctas ? cluster.map_shared_rank(&hist[pass & 1][0], tid >> 6)[base + (tid & 63)] : 0u;
+      __syncthreads();
+    }
+    n0 = n1 = 0;  // lane l: bins 63 - 2 l and 62 - 2 l of those
+    for (int r = 0; r < ctas; ++r) {
+      const uint2 c = *reinterpret_cast<const uint2*>(kOne ? &hist[pass & 1][base + 62 - 2 * lane] : &part[1][64 * r + 62 - 2 * lane]);
+      n0 += c.y;
+      n1 += c.x;
+    }
+    incl = n0 + n1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    at = __ffs(__ballot_sync(0xffffffffu, incl >= want)) - 1;
+    const uint32_t before = __shfl_sync(0xffffffffu, incl - n0 - n1, at), upper = __shfl_sync(0xffffffffu, n0, at);
+    const bool second = before + upper < want;
+    const uint32_t bin = base + 63 - 2 * at - (second ? 1 : 0);
+    prefix = pass == 0 ? bin : (prefix << (pass == 1 ? 11 : 10)) | bin;
+    want -= before + (second ? upper : 0u);
   }
   // prefix is the threshold's key; `want` of the keys equal to it stay. One more sweep notes
-  // which keys are above it and which equal it, a bit each (in the histograms' place).
-  uint2* marks = reinterpret_cast<uint2*>(&copies[0][0]) + c0 / 32;
-  uint32_t gt = 0, eq = 0;
+  // which keys are above it and which equal it, a bit each (in the histograms' place). Bits are
+  // then counted a word to a lane: counted a word to a warp, at four per clock, they took two
+  // thirds of the time of this and of the writing (1M keys 54 us).
+  const int words = per / 32;
+  uint2* marks = reinterpret_cast<uint2*>(&copies[0][0]) + warp * words;
   sweep([&](const uint32_t (&key)[4], int i) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t above = __ballot_sync(0xffffffffu, key[u] > prefix);
       const uint32_t equal = __ballot_sync(0xffffffffu, key[u] == prefix);
-      gt += __popc(above);
-      eq += __popc(equal);
       if (lane == u) marks[i / 32 + u] = make_uint2(above, equal);
     }
   });
+  __syncwarp();
+  uint32_t gt = 0, eq = 0;
+  for (int j = lane; j < words; j += 32) {
+    gt += __popc(marks[j].x);
+    eq += __popc(marks[j].y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    gt += __shfl_xor_sync(0xffffffffu, gt, o);
+    eq += __shfl_xor_sync(0xffffffffu, eq, o);
+  }
   if (lane == 0) {
     gt_of[warp] = gt;
     eq_of[warp] = eq;
@@ -430,47 +470,81 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
     gt_before += __shfl_xor_sync(0xffffffffu, gt_before, o);
     eq_before += __shfl_xor_sync(0xffffffffu, eq_before, o);
   }
-  if (tid == 0) {
-    totals[0] = gt;
-    totals[1] = eq;
-  }
-  cluster.sync();
-  gt = lane < rank ? cluster.map_shared_rank(&totals[0], lane)[0] : 0u;
-  eq = lane < rank ? cluster.map_shared_rank(&totals[0], lane)[1] : 0u;
+  if (!kOne) {
+    if (tid == 0) {
+      totals[0] = gt;
+      totals[1] = eq;
+    }
+    cluster.sync();
+    gt = lane < rank ? cluster.map_shared_rank(&totals[0], lane)[0] : 0u;
+    eq = lane < rank ? cluster.map_shared_rank(&totals[0], lane)[1] : 0u;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {  // (up to 16 CTAs)
-    gt += __shfl_xor_sync(0xffffffffu, gt, o);
-    eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      gt += __shfl_xor_sync(0xffffffffu, gt, o);
+      eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    }
+    ptx::cluster_arrive();  // this CTA has read its peers' counts
+    gt_before += gt;
+    eq_before += eq;
   }
-  gt = __shfl_sync(0xffffffffu, gt, 0) + gt_before;
-  eq = __shfl_sync(0xffffffffu, eq, 0) + eq_before;
-  ptx::cluster_arrive();  // this CTA has read its peers' counts
+  gt = gt_before;
+  eq = eq_before;
+  // lane's words: which keys stay, and how many stay before them
+  gt += (uint32_t)a.n_first + min(eq, want);  // (kept keys before this warp's)
+  for (int j0 = 0; j0 < words; j0 += 32) {
+    const int j = j0 + lane;
+    uint2 mark = j < words ? marks[j] : make_uint2(0u, 0u);
+    const uint32_t ties = __popc(mark.y);
+    uint32_t incl = ties;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const uint32_t before = eq + incl - ties;
+    uint32_t room = want > before ? want - before : 0u;  // ties that still stay
+    if (room < ties) {  // the lowest `room` of them
+      uint32_t rest = mark.y;
+      for (; room > 0; --room) rest &= rest - 1;
+      mark.y &= ~rest;
+    }
+    eq += __shfl_sync(0xffffffffu, incl, 31);
+    const uint32_t stay = mark.x | mark.y, n_stay = __popc(stay);
+    incl = n_stay;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (j < words) marks[j] = make_uint2(stay, gt + incl - n_stay);
+    gt += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __syncwarp();
   const uint32_t below = (1u << lane) - 1u;
-  gt += (uint32_t)a.n_first;
   const int first = lo + (int)i0 + lane;
-  for (int i = 0; i < per; i += kSelStep) {
-    uint2 mark[4];
-    float x[4];
-    uint32_t pos[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) mark[u] = marks[i / 32 + u];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t e = eq + __popc(mark[u].y & below);
-      const bool keep = ((mark[u].x >> lane) & 1u) || (((mark[u].y >> lane) & 1u) && e < want);
-      pos[u] = keep ? gt + __popc(mark[u].x & below) + min(e, want) : ~0u;
-      gt += __popc(mark[u].x);
-      eq += __popc(mark[u].y);
-      x[u] = keep && wd ? wl[i + 32 * u] : 0.f;
+#pragma unroll 4
+  for (int j = 0; j < words; ++j) {
+    const uint2 mark = marks[j];
+    if ((mark.x >> lane) & 1u) kept[mark.y + __popc(mark.x & below)] = first + 32 * j;
+  }
+  if (wd) {
+#pragma unroll 4
+    for (int j = 0; j < cached / 32; ++j) {
+      const uint2 mark = marks[j];
+      if ((mark.x >> lane) & 1u) wd[mark.y + __popc(mark.x & below)] = weight_of(cl[32 * j]);
     }
+    for (int j = cached / 32; j < words; j += 4) {  // (a multiple of four words)
+      float x[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (pos[u] == ~0u) continue;
-      kept[pos[u]] = first + i + 32 * u;
-      if (wd) wd[pos[u]] = x[u];
+      for (int u = 0; u < 4; ++u) x[u] = (marks[j + u].x >> lane) & 1u ? wl[32 * (j + u)] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint2 mark = marks[j + u];
+        if ((mark.x >> lane) & 1u) wd[mark.y + __popc(mark.x & below)] = x[u];
+      }
     }
   }
-  ptx::cluster_wait();  // no CTA leaves while a peer may still read its counts
+  if (!kOne) ptx::cluster_wait();  // no CTA leaves while a peer may still read its counts
 }
 
 // ------------------------------------------------------------------ eviction: moving the rows
@@ -592,8 +666,11 @@ bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 }  // namespace
 
 cudaError_t set_cache_kernel_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kSelCache);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCacheBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCacheBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
 }
 
@@ -681,14 +758,14 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   int ctas = 1;
   while (ctas < kSelMaxCtas && (long long)ctas * kSelKeys < max_seq) ctas *= 2;
   const int warp_keys = (max_seq / (ctas * kSelWarps) + kSelStep) / kSelStep * kSelStep;  // at most
-  const int cache = std::min(kSelCache, kSelWarps * warp_keys);
+  const int cache = std::min(kSelCache, warp_keys);
   const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last, cache,
                      kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = dim3((unsigned)ctas, (unsigned)batch, 1);
   cfg.blockDim = dim3(kSelThreads, 1, 1);
-  cfg.dynamicSmemBytes = 4 * (size_t)cache;
+  cfg.dynamicSmemBytes = 4 * (size_t)kSelWarps * (cache + 4);
   cfg.stream = (cudaStream_t)stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
@@ -696,7 +773,7 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t ce = cudaLaunchKernelEx(&cfg, evict_select_kernel, s);
+  cudaError_t ce = cudaLaunchKernelEx(&cfg, ctas == 1 ? evict_select_kernel<true> : evict_select_kernel<false>, s);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction select kernel launch: %s", cudaGetErrorString(ce));
   if (pages_dst == 0) return MLA_OK;
 
