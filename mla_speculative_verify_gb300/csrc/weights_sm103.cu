@@ -27,8 +27,9 @@
 // The tensor cores cut the bits below an accumulator's last one at every step, always towards
 // zero, so a score of 36 steps in one accumulator is off by ~2^-20 of itself: 1.9e-5 in the
 // weights of a million keys with scores of 20 and more. Each tile's columns are therefore summed
-// in three parts of three pieces, each in an accumulator that starts at zero, and the parts are
-// added in fp32 registers, rounded: 6.8e-6 there. While one part is read the next is computed.
+// in parts (bf16: nine of 64 columns, e4m3: three of 192), each in an accumulator that starts at
+// zero, and the parts are added in fp32 registers, rounded. The accumulators are taken in turns,
+// so one part is read while the next are computed.
 //
 // Warp roles (one CTA per SM): warps 0-3 load (TMA) and issue the products (Roles), warps 4-7
 // and 8-11 take the scores out, each half of the rows. All of them walk the same work list
@@ -62,18 +63,17 @@ constexpr int kKeys = 128;          // keys per tile (two pages)
 constexpr int kPieces = 9;          // 576 = 9 x 64 columns
 constexpr int kMaxRows = 128;       // rows of a group
 constexpr int kMaxStages = 16;
-constexpr int kParts = 3;           // parts of a score's 576 columns, three pieces each
-constexpr int kPartPieces = kPieces / kParts;
 constexpr int kMaxSlots = 6;        // accumulators, taken in turns by the parts
-// What the four control warps do. The e4m3 products of a tile take less time than one thread
-// needs to issue them (~125 cycles each, and ~300 for a stage's waits and commits), so each
-// part has an issuer and its three pieces share a stage; one warp loads. bf16 tiles are twice
-// as large and bound by the copies: one issuer, a loading warp for each of a tile's two pages,
-// and stages of one piece, since two of three would be all that fits (a million keys 202 -> 208
+// The parts of a tile and what the four control warps do. The e4m3 products of a tile take less
+// time than one thread needs to issue them (~125 cycles each, and ~300 for a stage's waits and
+// commits), so three pieces make a part, each part has an issuer, and one warp loads. bf16 tiles
+// are twice as large and bound by the copies: one issuer, a loading warp for each of a tile's two
+// pages, and parts of one piece (a stage of three would fit only twice: a million keys 202 -> 208
 // us).
 template <bool kFp8>
 struct Roles {
-  static constexpr int kPer = kFp8 ? kPartPieces : 1;  // pieces of a stage
+  static constexpr int kParts = kFp8 ? 3 : 9;          // parts of a score's 576 columns
+  static constexpr int kPer = kPieces / kParts;        // pieces of a part, which is a stage of the ring
   static constexpr int kLoaders = kFp8 ? 1 : 2;        // warps 0 and (bf16) 2
   static constexpr int kIssuers = kFp8 ? 3 : 1;        // warps 1 ..
   // An issuer waits for a stage's or an accumulator's next phase, which says nothing while the
@@ -89,10 +89,10 @@ constexpr int kSmemCap = 232448;    // 227 KB per CTA
 struct WeightsMisc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[kPieces], q_empty[kPieces];
-  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done[kParts];
+  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done[3];
   uint32_t tmem_base;
   int abort;
-  alignas(16) float nlse[kMaxRows];    // -lse * log2(e) of the current group's rows
+  alignas(16) float nlse[kMaxRows];    // -lse of the current group's rows
   alignas(16) float rscale[kMaxRows];  // e4m3: each row's part of its scores' scale
   alignas(16) int lim[kMaxRows];       // keys that each row sees
   float half[2][kKeys];                // one warpgroup's sums of a tile, for the other
@@ -110,7 +110,7 @@ struct WeightsParams {
   const float* q_scale;    // e4m3: per row, undoes its power of two
   float* weights;
   long long w_stride;
-  float decay, scale_log2;
+  float decay, sm_scale, kv_scale;
   int rows_n;              // MMA rows of every group (multiple of 32)
   int total_rows;
   int stages, slots, sub_tiles;
@@ -237,8 +237,8 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
           if (key_in < kCols) {
             const bool live = key_in < mine;
             const float l = live ? p.lse[row0 + key_in] : INFINITY;
-            ms->nlse[col0 + key_in] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;  // a row that saw nothing adds nothing
-            if (kFp8) ms->rscale[col0 + key_in] = live ? p.scale_log2 * p.q_scale[row0 + key_in] : 0.f;
+            ms->nlse[col0 + key_in] = l == -INFINITY ? -INFINITY : -l;  // a row that saw nothing adds nothing
+            if (kFp8) ms->rscale[col0 + key_in] = live ? p.sm_scale * p.q_scale[row0 + key_in] : 0.f;
             ms->lim[col0 + key_in] = live ? req.ctx - req.q + (g * n + col0 + key_in) / p.H + 1 : 0;
           }
           ptx::bar_sync(1 + wg, 128);
@@ -247,7 +247,7 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
         for (int t = s0; t < s1; ++t, ++tiles) {
           const int key = t * kKeys + key_in;
           const bool live = key < req.ctx, writes = ((t - s0) & 1) == wg;
-          float old = 0.f, ks = kFp8 ? 1.f : p.scale_log2;  // the key's part of its scores' scale
+          float old = 0.f, ks = kFp8 ? p.kv_scale : p.sm_scale;  // the key's part of its scores' scale
           if (writes && g == groups - 1 && live && p.decay != 0.f) old = wrow[key] * p.decay;
           if (kFp8 && p.kv_scales && live) {
             int id = ids[key / kPage];
@@ -256,7 +256,9 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
           }
           float x[kCols];
 #pragma unroll
-          for (int u = 0; u < kParts; ++u, slots.step()) {
+          for (int j = 0; j < kCols; ++j) x[j] = 0.f;
+#pragma unroll (kFp8 ? Roles<kFp8>::kParts : 1)
+          for (int u = 0; u < Roles<kFp8>::kParts; ++u, slots.step()) {
             const uint32_t slot = slots.at;
             if (ok) ok = warp_wait(&ms->d_full[slot], slots.phase & 1, abort, p);
             if (ok && mine > 0) {
@@ -268,7 +270,7 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
 #pragma unroll
               for (int j = 0; j < kCols; j += 2) {
                 float2 v = make_float2(y[j], y[j + 1]);
-                if (u > 0) v = ptx::add2(v, make_float2(x[j], x[j + 1]));
+                if (!kFp8 || u > 0) v = ptx::add2(v, make_float2(x[j], x[j + 1]));
                 x[j] = v.x;
                 x[j + 1] = v.y;
               }
@@ -289,7 +291,10 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
               for (int j = 16 * c; j < 16 * c + 16; j += 2) {
                 float2 v = make_float2(x[j], x[j + 1]);
                 if constexpr (kFp8) v = ptx::mul2(v, *reinterpret_cast<const float2*>(rscale + j));
+                // score - lse is rounded once, at its own size, before it goes to base 2: a score
+                // and an lse of 40 rounded apart would each put 2e-6 into the weight
                 v = ptx::fma2(v, ks2, *reinterpret_cast<const float2*>(nlse + j));
+                v = ptx::mul2(v, make_float2(1.4426950408889634f, 1.4426950408889634f));
                 float2 e = make_float2(ex2(v.x), ex2(v.y));
                 if (!whole) {  // a row past the group, or one that does not see this key, holds anything
                   e.x = key < lim[j] ? e.x : 0.f;
@@ -353,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ms->d_full[i], 1);
       ptx::mbar_init(&ms->d_empty[i], 8);
     }
-    for (int i = 0; i < kParts; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
+    for (int i = 0; i < 3; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmap_q);
     ptx::prefetch_tmap(&tmap_kv);
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // accumulator is written by one thread in order, so the sums repeat.
     const uint32_t sq = ptx::smem_addr(sQ), sk = ptx::smem_addr(sK);
     const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kKeys, n, 0, 0) : ptx::idesc_bf16(kKeys, n, 0, 0);
-    const int u0 = R::kIssuers == 1 ? 0 : warp - 1, u1 = R::kIssuers == 1 ? kParts : warp;
+    const int u0 = R::kIssuers == 1 ? 0 : warp - 1, u1 = R::kIssuers == 1 ? R::kParts : warp;
     Ring ring(p.stages), slots(p.slots);
     for (int i = 0; i < u0; ++i) {
       ring.step();
@@ -490,39 +495,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = u0; ok && u < u1; ++u) {
               // what the accumulator held has been read
               if (slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
+              const int c0 = kPer * u;
+              for (int c = c0; ok && new_q && t == s0 && c < c0 + kPer; ++c)
+                ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
+              if (ok) ok = warp_wait(&ms->kv_full[ring.at], ring.phase & 1, abort, p);
+              if (!ok) break;
+              ptx::tc_fence_after();
               const uint32_t d = tmem + slots.at * n;
-              for (int c0 = kPartPieces * u; ok && c0 < kPartPieces * (u + 1); c0 += kPer) {
-                const bool first = c0 == kPartPieces * u, last = c0 + kPer == kPartPieces * (u + 1);
-                for (int c = c0; ok && new_q && t == s0 && c < c0 + kPer; ++c)
-                  ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
-                if (ok) ok = warp_wait(&ms->kv_full[ring.at], ring.phase & 1, abort, p);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint64_t ad = ptx::smem_desc(sk + ring.at * kStageBytes, 16, kSbo, kSwizzle);
-                const uint64_t bd = ptx::smem_desc(sq + c0 * q_piece, 16, kSbo, kSwizzle);
-                if (ptx::elect_one()) {
+              const uint64_t ad = ptx::smem_desc(sk + ring.at * kStageBytes, 16, kSbo, kSwizzle);
+              const uint64_t bd = ptx::smem_desc(sq + c0 * q_piece, 16, kSbo, kSwizzle);
+              if (ptx::elect_one()) {
 #pragma unroll
-                  for (int j = 0; j < kPer; ++j) {
+                for (int j = 0; j < kPer; ++j) {
 #pragma unroll
-                    for (int k = 0; k < kRowBytes / 32; ++k) {  // the address field counts 16 bytes
-                      const uint64_t a = ad + j * (kPieceBytes / 16) + 2 * k, q = bd + j * (q_piece / 16) + 2 * k;
-                      if constexpr (kFp8) {
-                        ptx::mma_e4m3_ss(d, a, q, idesc, first && (j | k) == 0 ? 0u : 1u);
-                        ptx::mma_e4m3_ss(d, a, q + n * 64 / 16, idesc, 1u);
-                      } else
-                        ptx::mma_bf16_ss(d, a, q, idesc, first && (j | k) == 0 ? 0u : 1u);
+                  for (int k = 0; k < kRowBytes / 32; ++k) {  // the address field counts 16 bytes
+                    const uint64_t a = ad + j * (kPieceBytes / 16) + 2 * k, q = bd + j * (q_piece / 16) + 2 * k;
+                    const uint32_t add = (j | k) == 0 ? 0u : 1u;
+                    if constexpr (kFp8) {
+                      ptx::mma_e4m3_ss(d, a, q, idesc, add);
+                      ptx::mma_e4m3_ss(d, a, q + n * 64 / 16, idesc, 1u);
+                    } else {
+                      ptx::mma_bf16_ss(d, a, q, idesc, add);
                     }
                   }
-                  ptx::mma_commit(&ms->kv_empty[ring.at]);
-                  if (last_q && t == s1 - 1)
-                    for (int j = 0; j < kPer; ++j) ptx::mma_commit(&ms->q_empty[c0 + j]);
-                  if (last) ptx::mma_commit(&ms->d_full[slots.at]);
                 }
-                __syncwarp();
-                for (int i = 0; i < R::kIssuers; ++i) ring.step();  // the other issuers' stages
-                issued = true;
+                ptx::mma_commit(&ms->kv_empty[ring.at]);
+                if (last_q && t == s1 - 1)
+                  for (int j = 0; j < kPer; ++j) ptx::mma_commit(&ms->q_empty[c0 + j]);
+                ptx::mma_commit(&ms->d_full[slots.at]);
               }
-              for (int i = 0; i < R::kIssuers; ++i) slots.step();
+              __syncwarp();
+              issued = true;
+              for (int i = 0; i < R::kIssuers; ++i) {  // past the other issuers' parts
+                ring.step();
+                slots.step();
+              }
             }
           }
           if (new_q) ++qphase;
@@ -723,7 +730,8 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   prm.weights = weights;
   prm.w_stride = weights_stride;
   prm.decay = decay;
-  prm.scale_log2 = sm_scale * (fp8 && !kv_scales ? kv_scale : 1.f) * 1.4426950408889634f;
+  prm.sm_scale = sm_scale;
+  prm.kv_scale = kv_scale;
   prm.rows_n = most_rows;
   prm.stages = stages;
   prm.slots = std::min(kMaxSlots, 512 / most_rows) / unit * unit;
