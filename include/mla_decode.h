@@ -293,6 +293,8 @@ int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* 
  *   seq_lens_dst  int32 [batch]: the new lengths
  *   weights_dst   NULL, or fp32 [batch, weights_dst_stride]: the kept keys' weights in order (a
  *                 -0 may come back as 0, a NaN as another NaN)
+ *   workspace     mla_cache_evict_workspace bytes for this batch and max_seq (0 unless max_seq is
+ *                 large), 256-byte aligned; calls that may overlap need one each
  *
  * A new block's scale is the largest among its rows' old ones; codes of a row from a block
  * with another scale are multiplied by old / new and rounded. Rows of the new pages behind the
@@ -304,7 +306,9 @@ int mla_cache_evict(const float* weights, long long weights_stride, const int32_
                     int block_tokens, const int32_t* page_table, int page_table_stride, int num_pages,
                     void* kv_cache_dst, float* kv_scales_dst, const int32_t* page_table_dst,
                     int page_table_dst_stride, int num_pages_dst, int32_t* kept, int32_t* seq_lens_dst,
-                    float* weights_dst, long long weights_dst_stride, int32_t* status_dev, void* stream);
+                    float* weights_dst, long long weights_dst_stride, void* workspace, size_t workspace_bytes,
+                    int32_t* status_dev, void* stream);
+int mla_cache_evict_workspace(int batch, int max_seq, size_t* workspace_bytes_out);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* mla_last_error(void);

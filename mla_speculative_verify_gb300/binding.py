@@ -70,7 +70,8 @@ SIGNATURES = {
     "mla_cache_evict": (ctypes.c_int, [_P, ctypes.c_longlong, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                        ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, ctypes.c_int, _P,
                                        ctypes.c_int, ctypes.c_int, _P, _P, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P,
-                                       ctypes.c_longlong, _P, _P]),
+                                       ctypes.c_longlong, _P, ctypes.c_size_t, _P, _P]),
+    "mla_cache_evict_workspace": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _SZP]),
     "mla_device_pair_slots": (ctypes.c_int, [ctypes.c_int, _IP]),
     "mla_last_error": (ctypes.c_char_p, []),
     "mla_version": (ctypes.c_int, []),
@@ -211,6 +212,14 @@ def cache_append(*args) -> None:
     """mla_cache_append, arguments as in the header (pointers as ints)."""
     lib = _lib or load()
     check(lib.mla_cache_append(*args), lib)
+
+
+def cache_evict_workspace(batch: int, max_seq: int) -> int:
+    """mla_cache_evict_workspace: device scratch bytes that mla_cache_evict needs."""
+    lib = _lib or load()
+    n = ctypes.c_size_t(0)
+    check(lib.mla_cache_evict_workspace(batch, max_seq, ctypes.byref(n)), lib)
+    return n.value
 
 
 def cache_evict(*args) -> None:

@@ -4,8 +4,8 @@ block-scaled e4m3 cache, ``evict`` keeps the keys with the largest accumulated w
 Both only check shapes, dtypes and devices and pass raw pointers through to
 ``mla_cache_append`` / ``mla_cache_evict``; what they compute is stated in
 include/mla_decode.h. They enqueue on ``stream`` (default: torch's current stream of the
-tensors' device), allocate nothing and do not synchronise, so they can be captured in a CUDA
-graph. Device-side faults (lengths that do not fit, pages out of range) are OR-ed into
+tensors' device) and do not synchronise, so they can be captured in a CUDA graph; what scratch
+``evict`` needs comes from torch's allocator, call by call. Device-side faults (lengths that do not fit, pages out of range) are OR-ed into
 ``status``, an int32 tensor, as ``binding.MLA_DEVICE_*`` bits.
 """
 from __future__ import annotations
@@ -32,6 +32,15 @@ def on_device(index: int, call, *args) -> None:
     else:
         with torch.cuda.device(index):
             call(*args)
+
+
+def scratch_bytes(count: int, index: int, stream: torch.cuda.Stream | None) -> torch.Tensor:
+    """Scratch for one call on ``stream`` from torch's allocator, which hands it out again only to
+    later work of that stream (or, in a capture, of that graph): no two calls share any."""
+    if stream is None:
+        return torch.empty(count, dtype=torch.uint8, device=index)
+    with torch.cuda.stream(stream):
+        return torch.empty(count, dtype=torch.uint8, device=index)
 
 
 def check_tensor(name: str, t: torch.Tensor, dtype, shape, index: int) -> None:
@@ -147,8 +156,10 @@ def evict(weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, n_first: i
         check_tensor("status", status, torch.int32, (1,), index)
     if max_seq is None:
         max_seq = min(w_stride, PAGE_SIZE * stride)
+    need = binding.cache_evict_workspace(batch, max_seq)
+    scratch = scratch_bytes(need, index, stream) if need else None
     on_device(index, binding.cache_evict, weights.data_ptr(), w_stride, seq_lens.data_ptr(), batch, max_seq, budget,
               n_first, n_last, binding.MLA_KV_BF16 if bf16 else binding.MLA_KV_FP8_E4M3, kv.data_ptr(), _ptr(scales),
               block, page_table.data_ptr(), stride, pages, kv_dst.data_ptr(), _ptr(scales_dst),
               page_table_dst.data_ptr(), stride_dst, pages_dst, kept.data_ptr(), seq_lens_dst.data_ptr(),
-              _ptr(weights_dst), wd_stride, _ptr(status), stream_handle(index, stream))
+              _ptr(weights_dst), wd_stride, _ptr(scratch), need, _ptr(status), stream_handle(index, stream))

@@ -246,7 +246,7 @@ __device__ __forceinline__ float weight_of(uint32_t key) {
 // key hold the lowest key: they come after every real one, so none is ever taken.
 //
 template <bool kOne>  // one CTA per request
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   extern __shared__ __align__(16) uint32_t cache[];  // per warp a.cache keys, and 4 places more
@@ -436,11 +436,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
   const int words = per / 32;
   uint2* marks = reinterpret_cast<uint2*>(&copies[0][0]) + warp * words;
   sweep([&](const uint32_t (&key)[4], int i) {
+    uint32_t above[4], equal[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t above = __ballot_sync(0xffffffffu, key[u] > prefix);
-      const uint32_t equal = __ballot_sync(0xffffffffu, key[u] == prefix);
-      if (lane == u) marks[i / 32 + u] = make_uint2(above, equal);
+    for (int u = 0; u < 4; ++u) above[u] = __ballot_sync(0xffffffffu, key[u] > prefix);
+    if (__any_sync(0xffffffffu, key[0] == prefix || key[1] == prefix || key[2] == prefix || key[3] == prefix)) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) equal[u] = __ballot_sync(0xffffffffu, key[u] == prefix);
+    }
+    if (lane == 0) {
+      uint4* m = reinterpret_cast<uint4*>(marks + i / 32);
+      m[0] = make_uint4(above[0], equal[0], above[1], equal[1]);
+      m[1] = make_uint4(above[2], equal[2], above[3], equal[3]);
     }
   });
   __syncwarp();
@@ -522,29 +528,215 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
   __syncwarp();
   const uint32_t below = (1u << lane) - 1u;
   const int first = lo + (int)i0 + lane;
-#pragma unroll 4
-  for (int j = 0; j < words; ++j) {
-    const uint2 mark = marks[j];
-    if ((mark.x >> lane) & 1u) kept[mark.y + __popc(mark.x & below)] = first + 32 * j;
-  }
-  if (wd) {
-#pragma unroll 4
-    for (int j = 0; j < cached / 32; ++j) {
-      const uint2 mark = marks[j];
-      if ((mark.x >> lane) & 1u) wd[mark.y + __popc(mark.x & below)] = weight_of(cl[32 * j]);
+  for (int j = 0; j < words; j += 4) {  // (a multiple of four words)
+    uint2 mark[4];
+    uint32_t pos[4];
+    float x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      mark[u] = marks[j + u];
+      pos[u] = mark[u].y + __popc(mark[u].x & below);
     }
-    for (int j = cached / 32; j < words; j += 4) {  // (a multiple of four words)
-      float x[4];
+    if (wd) {
+      if (32 * j < cached) {  // (and with it all four words)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) x[u] = (marks[j + u].x >> lane) & 1u ? wl[32 * (j + u)] : 0.f;
+        for (int u = 0; u < 4; ++u) x[u] = weight_of(cl[32 * (j + u)]);
+      } else {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint2 mark = marks[j + u];
-        if ((mark.x >> lane) & 1u) wd[mark.y + __popc(mark.x & below)] = x[u];
+        for (int u = 0; u < 4; ++u) x[u] = (mark[u].x >> lane) & 1u ? wl[32 * (j + u)] : 0.f;
       }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (!((mark[u].x >> lane) & 1u)) continue;
+      kept[pos[u]] = first + 32 * (j + u);
+      if (wd) wd[pos[u]] = x[u];
     }
   }
   if (!kOne) ptx::cluster_wait();  // no CTA leaves while a peer may still read its counts
+}
+
+// ------------------------------------------------------------------ eviction: long requests
+// The same selection spread over the whole GPU, for requests so long that a cluster's 16 CTAs
+// take longer than a few launches (the sweeps of 1M keys on 16 CTAs: 45 us). A CTA takes 4096
+// keys, eight to a thread, and every pass is a launch of its own, which sees the counts of the
+// one before:
+//   step 0..2  counts of the next 11, 11, 10 bits among the keys that match the bits found so far
+//   step 3     how many keys of each CTA's are above the threshold, and equal to it
+//   step 4     the kept keys, numbered from those counts
+constexpr int kWideThreads = 512, kWideWarps = kWideThreads / 32;
+constexpr int kWidePer = 8, kWideKeys = kWideThreads * kWidePer;
+constexpr int kWideFrom = 65536;    // keys of the longest request above which the steps are launched
+constexpr int kWideMaxChunks = kSelMaxKeys / kWideKeys;
+
+struct alignas(256) WideState {  // per request, in the workspace; zero before step 0
+  uint32_t hist[3][kBins];
+  uint2 found[3];  // bits found by step s + 1, rank among the keys that match them
+  uint2 counts[kWideMaxChunks];
+};
+
+template <int kStep>
+__global__ void __launch_bounds__(kWideThreads) evict_wide_kernel(SelectArgs a, WideState* states) {
+  __shared__ __align__(16) uint32_t copies[kStep < 3 ? kSelCopies : 1][kStep < 3 ? kBins : 1];
+  __shared__ uint32_t sums[2][kWideWarps];
+  __shared__ uint2 hit;
+  ptx::pdl_wait_primary();
+  if (kStep < 4) ptx::pdl_launch_dependents();  // the next step's CTAs come up and wait for this grid
+  const int b = blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = a.lens[b];
+  WideState& st = states[b];
+  const float* w = a.weights + (size_t)b * a.w_stride;
+  const bool bad = n < 0 || n > a.max_seq;
+  const int out = bad ? 0 : min(n, a.budget);
+  const int m = n - a.n_first - a.n_last, k = a.budget - a.n_first - a.n_last;
+  const bool all = out < a.budget || n == a.budget;  // everything stays
+  if constexpr (kStep == 4) {
+    int32_t* kept = a.kept + (size_t)b * a.budget;
+    float* wd = a.weights_dst ? a.weights_dst + (size_t)b * a.wd_stride : nullptr;
+    if (chunk == 0 && tid == 0) {
+      a.lens_dst[b] = out;
+      if (bad) report(a.status, MLA_DEVICE_PLAN_MISMATCH);
+    }
+    const int g0 = chunk * kWideThreads + tid, gs = gridDim.x * kWideThreads;
+    if (all) {
+      for (int r = g0; r < a.budget; r += gs) {
+        kept[r] = r < out ? r : -1;
+        if (wd && r < out) wd[r] = w[r];
+      }
+      return;
+    }
+    for (int r = g0; r < a.n_first; r += gs) {
+      kept[r] = r;
+      if (wd) wd[r] = w[r];
+    }
+    for (int r = g0; r < a.n_last; r += gs) {
+      kept[a.budget - a.n_last + r] = n - a.n_last + r;
+      if (wd) wd[a.budget - a.n_last + r] = w[n - a.n_last + r];
+    }
+  }
+  if (all || k == 0) return;
+  const int i0 = chunk * kWideKeys + warp * 32 * kWidePer + lane;  // this lane's keys: i0, i0 + 32, ..
+  if (chunk * kWideKeys >= m && kStep != 3) return;
+  const float* wm = w + a.n_first;
+  float x[kWidePer];
+  uint32_t key[kWidePer];
+#pragma unroll
+  for (int u = 0; u < kWidePer; ++u) x[u] = i0 + 32 * u < m ? wm[i0 + 32 * u] : 0.f;
+#pragma unroll
+  for (int u = 0; u < kWidePer; ++u) key[u] = i0 + 32 * u < m ? order_key(x[u]) : 0u;  // (behind the last: the lowest)
+  if (kStep < 3) {
+    for (int i = tid; i < kSelCopies * kBins; i += kWideThreads) (&copies[0][0])[i] = 0u;
+  }
+  uint2 known = make_uint2(0u, (uint32_t)k);  // bits found so far, rank among the keys that match them
+  if (kStep >= 1 && kStep <= 3) {
+    // the bin of the last step's counts that holds the rank: bins from the top, four to a thread
+    if (kStep >= 2) known = st.found[kStep - 2];
+    const uint4 c = *reinterpret_cast<const uint4*>(&st.hist[kStep - 1][kBins - 4 - 4 * tid]);
+    const uint32_t own = c.x + c.y + c.z + c.w;
+    uint32_t incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) sums[0][warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - own;
+    for (int i = 0; i < warp; ++i) before += sums[0][i];
+    if (before < known.y && before + own >= known.y) {
+      const uint32_t bins[4] = {c.w, c.z, c.y, c.x};
+      uint32_t rank = known.y - before;
+      int at = 0;
+      while (at < 3 && rank > bins[at]) rank -= bins[at++];
+      const uint32_t bin = (uint32_t)(kBins - 1 - 4 * tid - at);
+      hit = make_uint2(kStep == 1 ? bin : (known.x << (kStep == 2 ? 11 : 10)) | bin, rank);
+    }
+    __syncthreads();
+    known = hit;
+    if (chunk == 0 && tid == 0) st.found[kStep - 1] = known;
+  } else if (kStep == 4) {
+    known = st.found[2];
+  } else {
+    __syncthreads();
+  }
+  if constexpr (kStep < 3) {
+    constexpr int shift = kStep == 0 ? 21 : kStep == 1 ? 10 : 0;
+    constexpr int above = kStep == 1 ? 21 : 10;
+    constexpr uint32_t mask = kStep == 2 ? 1023u : 2047u;
+    uint32_t* mine = copies[lane % kSelCopies];
+#pragma unroll
+    for (int u = 0; u < kWidePer; ++u)
+      if (i0 + 32 * u < m && (kStep == 0 || (key[u] >> above) == known.x)) atomicAdd(&mine[(key[u] >> shift) & mask], 1u);
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kWideThreads) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < kSelCopies; ++j) c += copies[j][i];
+      if (c) atomicAdd(&st.hist[kStep][i], c);  // (whole numbers: the order of CTAs changes nothing)
+    }
+  } else {
+    uint32_t above[kWidePer], equal[kWidePer], gt = 0, eq = 0;
+#pragma unroll
+    for (int u = 0; u < kWidePer; ++u) {
+      above[u] = __ballot_sync(0xffffffffu, key[u] > known.x);
+      equal[u] = __ballot_sync(0xffffffffu, key[u] == known.x && i0 + 32 * u < m);
+      gt += __popc(above[u]);
+      eq += __popc(equal[u]);
+    }
+    if (lane == 0) {
+      sums[0][warp] = gt;
+      sums[1][warp] = eq;
+    }
+    if constexpr (kStep == 4) {
+      // what the CTAs before this one hold
+      uint2 c = make_uint2(0u, 0u);
+      for (int i = tid; i < chunk; i += kWideThreads) {
+        c.x += st.counts[i].x;
+        c.y += st.counts[i].y;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        c.x += __shfl_xor_sync(0xffffffffu, c.x, o);
+        c.y += __shfl_xor_sync(0xffffffffu, c.y, o);
+      }
+      __shared__ uint2 part[kWideWarps];
+      if (lane == 0) part[warp] = c;
+      __syncthreads();
+      gt = eq = 0;
+      for (int i = 0; i < kWideWarps; ++i) {
+        gt += part[i].x;
+        eq += part[i].y;
+      }
+      for (int i = 0; i < warp; ++i) {
+        gt += sums[0][i];
+        eq += sums[1][i];
+      }
+      int32_t* kept = a.kept + (size_t)b * a.budget;
+      float* wd = a.weights_dst ? a.weights_dst + (size_t)b * a.wd_stride : nullptr;
+      const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+      for (int u = 0; u < kWidePer; ++u) {
+        const uint32_t e = eq + __popc(equal[u] & below);
+        if (((above[u] >> lane) & 1u) || (((equal[u] >> lane) & 1u) && e < known.y)) {
+          const uint32_t pos = (uint32_t)a.n_first + gt + __popc(above[u] & below) + min(e, known.y);
+          kept[pos] = a.n_first + i0 + 32 * u;
+          if (wd) wd[pos] = x[u];
+        }
+        gt += __popc(above[u]);
+        eq += __popc(equal[u]);
+      }
+    } else {
+      __syncthreads();
+      if (tid == 0) {
+        uint2 c = make_uint2(0u, 0u);
+        for (int i = 0; i < kWideWarps; ++i) {
+          c.x += sums[0][i];
+          c.y += sums[1][i];
+        }
+        st.counts[chunk] = c;
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------ eviction: moving the rows
@@ -711,13 +903,29 @@ extern "C" int mla_cache_append(const void* rows, int total_rows, const int32_t*
   return MLA_OK;
 }
 
+namespace mla {
+// Long requests are selected by the five launches, others by clusters. Whole calls that keep 64
+// keys, clusters against launches: 1 x 64k keys 19 against 19 us, 8 x 64k 19 against 25, 1 x 128k
+// 23 against 19, 4 x 128k 23 against 23, 8 x 128k 37 against 27 (eight clusters of 16 do not
+// run at once), 1 x 1M 42 against 27.
+static bool wide_selection(int max_seq) { return max_seq > kWideFrom; }
+}  // namespace mla
+
+extern "C" int mla_cache_evict_workspace(int batch, int max_seq, size_t* workspace_bytes_out) {
+  clear_error();
+  if (batch < 1 || max_seq < 0 || !workspace_bytes_out)
+    return set_error(MLA_ERR_INVALID_ARG, "need batch >= 1, max_seq >= 0 and workspace_bytes_out");
+  *workspace_bytes_out = wide_selection(max_seq) ? (size_t)batch * sizeof(WideState) : 0;
+  return MLA_OK;
+}
+
 extern "C" int mla_cache_evict(const float* weights, long long weights_stride, const int32_t* seq_lens, int batch,
                                int max_seq, int budget, int n_first, int n_last, int kv_dtype, const void* kv_cache,
                                const float* kv_scales, int block_tokens, const int32_t* page_table,
                                int page_table_stride, int num_pages, void* kv_cache_dst, float* kv_scales_dst,
                                const int32_t* page_table_dst, int page_table_dst_stride, int num_pages_dst,
                                int32_t* kept, int32_t* seq_lens_dst, float* weights_dst, long long weights_dst_stride,
-                               int32_t* status_dev, void* stream) {
+                               void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
   clear_error();
   if (batch < 1 || batch > 65535) return set_error(MLA_ERR_INVALID_ARG, "batch must be in [1, 65535] (got %d)", batch);
   if (max_seq < 0) return set_error(MLA_ERR_INVALID_ARG, "max_seq must be >= 0 (got %d)", max_seq);
@@ -750,31 +958,52 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   if (weights_stride < max_seq || (weights_dst && weights_dst_stride < most))
     return set_error(MLA_ERR_INVALID_ARG, "weights_stride %lld or weights_dst_stride %lld is smaller than a row",
                      weights_stride, weights_dst_stride);
+  const bool wide = wide_selection(max_seq);
+  const size_t need = wide ? (size_t)batch * sizeof(WideState) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return set_error(MLA_ERR_BUFFER, "workspace needs %zu bytes (got %zu)", need, workspace ? workspace_bytes : (size_t)0);
+  if (need > 0 && ((uintptr_t)workspace & 255u)) return set_error(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   int sms = 0;
   const int rc = current_device_ready(&sms);
   if (rc != MLA_OK) return rc;
 
-  // CTAs per request: one for every 8192 keys, up to a cluster of 16
-  int ctas = 1;
-  while (ctas < kSelMaxCtas && (long long)ctas * kSelKeys < max_seq) ctas *= 2;
-  const int warp_keys = (max_seq / (ctas * kSelWarps) + kSelStep) / kSelStep * kSelStep;  // at most
-  const int cache = std::min(kSelCache, warp_keys);
-  const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last, cache,
-                     kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)batch, 1);
-  cfg.blockDim = dim3(kSelThreads, 1, 1);
-  cfg.dynamicSmemBytes = 4 * (size_t)kSelWarps * (cache + 4);
   cfg.stream = (cudaStream_t)stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t ce = cudaLaunchKernelEx(&cfg, ctas == 1 ? evict_select_kernel<true> : evict_select_kernel<false>, s);
-  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction select kernel launch: %s", cudaGetErrorString(ce));
+  cudaError_t ce;
+  if (wide) {
+    const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last, 0,
+                       kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
+    ce = cudaMemsetAsync(workspace, 0, need, cfg.stream);
+    cfg.gridDim = dim3((unsigned)((max_seq + kWideKeys - 1) / kWideKeys), (unsigned)batch, 1);
+    cfg.blockDim = dim3(kWideThreads, 1, 1);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    int step = 0;
+    for (auto fn : {evict_wide_kernel<0>, evict_wide_kernel<1>, evict_wide_kernel<2>, evict_wide_kernel<3>, evict_wide_kernel<4>}) {
+      cfg.numAttrs = step++ > 0 ? 1 : 0;
+      if (ce == cudaSuccess) ce = cudaLaunchKernelEx(&cfg, fn, s, (WideState*)workspace);
+    }
+  } else {
+    // CTAs per request: one for every 8192 keys, up to a cluster of 16
+    int ctas = 1;
+    while (ctas < kSelMaxCtas && (long long)ctas * kSelKeys < max_seq) ctas *= 2;
+    const int warp_keys = (max_seq / (ctas * kSelWarps) + kSelStep) / kSelStep * kSelStep;  // at most
+    const int cache = std::min(kSelCache, warp_keys);
+    const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last, cache,
+                       kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)batch, 1);
+    cfg.blockDim = dim3(kSelThreads, 1, 1);
+    cfg.dynamicSmemBytes = 4 * (size_t)kSelWarps * (cache + 4);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+    ce = cudaLaunchKernelEx(&cfg, ctas == 1 ? evict_select_kernel<true> : evict_select_kernel<false>, s);
+  }
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction selection launch: %s", cudaGetErrorString(ce));
   if (pages_dst == 0) return MLA_OK;
 
   const GatherArgs g{kept, seq_lens_dst, budget, max_seq, (const uint4*)kv_cache, (uint4*)kv_cache_dst, kv_scales,
@@ -783,6 +1012,7 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   cfg.gridDim = dim3((unsigned)std::min<long long>(pages_dst * batch, 3LL * sms), 1, 1);
   cfg.blockDim = dim3(kGatherThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   auto fn = kv_dtype == MLA_KV_BF16 ? evict_gather_kernel<72, false>

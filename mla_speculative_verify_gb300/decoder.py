@@ -14,7 +14,7 @@ import numpy as np
 import torch
 
 from . import binding
-from .cache import E4M3, check_scales, check_table, check_tensor, on_device, stream_handle
+from .cache import E4M3, check_scales, check_table, check_tensor, on_device, scratch_bytes, stream_handle
 
 KV_DTYPES = {"bf16": binding.MLA_KV_BF16, "fp8": binding.MLA_KV_FP8_E4M3}
 SM_SCALE = 1.0 / math.sqrt(192.0)
@@ -134,13 +134,8 @@ class VerifyDecoder:
             check_tensor("counted", counted, torch.int32, (batch,), index)
         if status is not None:
             check_tensor("status", status, torch.int32, (1,), index)
-        need, scratch = self.weights_workspace_bytes, None
-        if need:
-            if stream is None:
-                scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
-            else:
-                with torch.cuda.stream(stream):
-                    scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+        need = self.weights_workspace_bytes
+        scratch = scratch_bytes(need, index, stream) if need else None
         on_device(index, binding.key_weights, self.plan_dev.data_ptr(), self._plan_host_ptr, self.plan_host.nbytes,
                   q.data_ptr(), kv_cache.data_ptr(), _ptr(kv_scales), block, page_table.data_ptr(), stride, pages,
                   lse.data_ptr(), _ptr(counted), sm_scale, kv_scale, decay, weights.data_ptr(), w_stride, _ptr(scratch),

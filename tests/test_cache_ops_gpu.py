@@ -320,6 +320,16 @@ def test_evict_long(budget):
     run_evict(batch, w, budget, 4, 50)
 
 
+@pytest.mark.parametrize("budget,first,last", [(1, 0, 0), (5000, 7, 100), (90000, 0, 0), (70000, 35000, 35000)])
+def test_evict_few_long_requests(budget, first, last):
+    """Selection spread over the whole GPU: long requests, one that keeps all, an empty one."""
+    batch, w = evict_batch([100001, 3, 70000], "e4m3", 64, seed=budget)
+    run_evict(batch, w, budget, first, last)
+    w[:] = 0.5  # ties decide everything
+    w[:, 1::2] = np.nan
+    run_evict(batch, w, budget, first, last)
+
+
 def test_evict_special_weights():
     """Ties decided by index, negative weights, infinities, NaN as the lowest, -0 as 0."""
     batch, w = evict_batch([600, 600, 600, 600, 600], "bf16", 0, seed=31)

@@ -44,7 +44,7 @@ def test_append_of_nothing_is_no_call():
 EVICT = dict(weights=P, weights_stride=1000, seq_lens=P, batch=3, max_seq=900, budget=100, n_first=4, n_last=16,
              kv_dtype=binding.MLA_KV_FP8_E4M3, kv_cache=P, kv_scales=P, block_tokens=64, page_table=P, page_table_stride=15,
              num_pages=60, kv_cache_dst=P, kv_scales_dst=P, page_table_dst=P, page_table_dst_stride=2, num_pages_dst=10,
-             kept=P, seq_lens_dst=P, weights_dst=P, weights_dst_stride=100, status_dev=None, stream=None)
+             kept=P, seq_lens_dst=P, weights_dst=P, weights_dst_stride=100, workspace=None, workspace_bytes=0, status_dev=None, stream=None)
 
 
 @pytest.mark.parametrize("change,code", [
@@ -58,10 +58,19 @@ EVICT = dict(weights=P, weights_stride=1000, seq_lens=P, batch=3, max_seq=900, b
     (dict(kv_dtype=binding.MLA_KV_BF16), INVALID), (dict(weights_stride=899), INVALID), (dict(weights_dst_stride=99), INVALID),
     (dict(page_table_stride=14), INVALID), (dict(page_table_dst_stride=1), INVALID), (dict(num_pages=0), INVALID),
     (dict(num_pages_dst=0), INVALID), (dict(block_tokens=48), UNSUPPORTED),
-    (dict(max_seq=2**21 + 1, weights_stride=2**22, page_table_stride=2**16), UNSUPPORTED)])
+    (dict(max_seq=2**21 + 1, weights_stride=2**22, page_table_stride=2**16), UNSUPPORTED),
+    (dict(batch=1, max_seq=2**20, weights_stride=2**20, page_table_stride=2**14), BUFFER),
+    (dict(batch=1, max_seq=2**20, weights_stride=2**20, page_table_stride=2**14, workspace=P + 16, workspace_bytes=1 << 20), INVALID)])
 def test_evict_refusals(change, code):
     assert call("mla_cache_evict", EVICT, change) == code
     assert binding.last_error()
+
+
+def test_evict_workspace():
+    assert binding.cache_evict_workspace(32, 32768) == 0
+    assert binding.cache_evict_workspace(1, 1 << 20) > 0
+    assert binding.load().mla_cache_evict_workspace(0, 10, ctypes.byref(ctypes.c_size_t())) == INVALID
+    assert binding.load().mla_cache_evict_workspace(1, 10, None) == INVALID
 
 
 def plan(kv, seq=(900, 64), q=(4, 1)):
