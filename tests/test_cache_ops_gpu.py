@@ -59,6 +59,17 @@ def test_append(block, lens_new, pasts):
     same(s, want_s)
 
 
+def test_append_many_requests():
+    g = np.random.default_rng(6)
+    batch, codes, scales, rows, ends, cu = append_case(g.integers(0, 90, size=90), g.integers(0, 200, size=90), 8, seed=6)
+    values, want_s = ref.code_values(codes), scales.double().numpy()
+    ref.append(rows, values, want_s, batch.table, ends, cu, 8)
+    c, s, status = run_append(batch, codes, scales, rows, ends, cu)
+    assert status == 0
+    same(c.view(F8), values)
+    same(s, want_s)
+
+
 def test_append_special_values():
     """Zero rows, infinities, NaN, bf16's largest and least values, another writer's scale."""
     batch, codes, scales, rows, ends, cu = append_case([40, 24], [10, 64], 16, seed=3)
@@ -249,6 +260,104 @@ def test_key_weights_sum_to_the_rows():
     assert np.abs(total / [48, 24] - 1).max() < 1e-4
 
 
+@pytest.mark.parametrize("kind,block", [("bf16", 0), ("e4m3", 32)])
+def test_key_weights_of_many_requests(kind, block):
+    """More requests than a warp looks at together, several of them in one CTA's share and some
+    over several CTAs."""
+    g = np.random.default_rng(25)
+    seq, q = g.integers(1, 400, size=75), g.integers(1, 4, size=75)
+    q = np.minimum(seq, q)
+    batch = ref.Batch(20, seq, q, kind, block, seed=25)
+    old = g.random((75, 400)).astype(np.float32)
+    w, lse = run_weights(batch, 0.5, old)
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 0.5, old)
+    assert (np.abs(w.cpu().double().numpy() - want) <= bound + 1e-30).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "scaled"])
+@pytest.mark.parametrize("heads,q", [(4, 2), (96, 3)])
+def test_key_weights_long(kind, heads, q):
+    """330k keys: more tiles to a CTA than one look-up of page ids holds, one and three groups of
+    rows, against 64-bit torch on the GPU."""
+    n = 330001
+    pages = (n + 63) // 64
+    gen = torch.Generator(device="cuda").manual_seed(q)
+    x = torch.randn((pages, 64, D), generator=gen, device="cuda")
+    table = torch.randperm(pages, generator=gen, device="cuda").int().view(1, -1)
+    scales = None
+    if kind == "bf16":
+        kv = x.to(torch.bfloat16)
+        k = kv.double()
+    else:
+        scales = torch.exp2(torch.randint(-9, -6, (pages, 4), generator=gen, device="cuda").float())
+        kv = (x * 100).clamp(-448, 448).to(F8).view(torch.uint8)
+        k = kv.view(F8).double() * scales.double().repeat_interleave(16, 1)[:, :, None]
+    k = k[table[0].long()].view(-1, D)[:n]
+    queries = torch.randn((q, heads, D), generator=gen, device="cuda").to(torch.bfloat16)
+    d = VerifyDecoder([n], [q], heads, "bf16" if kind == "bf16" else "fp8")
+    lse, w = torch.empty((q, heads), device="cuda"), torch.zeros((1, n), device="cuda")
+    bound = torch.zeros(n, dtype=torch.float64, device="cuda")
+    want = torch.zeros(n, dtype=torch.float64, device="cuda")
+    for i in range(q):
+        rows = queries[i].double()
+        s = rows @ k[:n - q + i + 1].T * inputs.SM_SCALE
+        lse[i] = torch.logsumexp(s, 1)
+        p = torch.exp(s - lse[i].double()[:, None])
+        err = 576 * 2.0 ** -23 * (rows.abs() @ k[:n - q + i + 1].abs().T)
+        if kind != "bf16":
+            err += 2.0 ** -17 * rows.abs().amax(1, keepdim=True) * k[:n - q + i + 1].abs().sum(1)
+        want[:n - q + i + 1] += p.sum(0)
+        bound[:n - q + i + 1] += (p * (inputs.SM_SCALE * err + 2.0 ** -16)).sum(0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    d.key_weights(queries, kv, table, lse, w, kv_scales=scales, status=status)
+    assert int(status.item()) == 0
+    assert ((w[0].double() - want).abs() <= bound).all()
+
+
+def test_two_graphs_at_once():
+    """Graphs of one decoder, captured one after the other and replayed on two streams at the same
+    time, share no scratch: the key weights of an e4m3 cache, and an eviction of a long request."""
+    batch = ref.Batch(24, [3000, 900], [4, 2], "e4m3", 16, seed=26)
+    d, t, _, lse = decode(batch)
+    n = 70000
+    wide = torch.rand((1, n), device="cuda")
+    pages = (n + 63) // 64
+    kv = torch.zeros((pages + 20, 64, D), dtype=torch.uint8, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
+    outs, graphs = [], []
+    for k in range(2):
+        w = torch.zeros((2, 3000), device="cuda")
+        kept, lens = torch.zeros((1, 640), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        dst = torch.arange(pages + 10 * k, pages + 10 * (k + 1), dtype=torch.int32, device="cuda").view(1, -1)
+        q = t["q"] if k == 0 else t["q"].flip(0).contiguous()
+        weights = wide if k == 0 else wide.flip(1).contiguous()
+        keep = (w, kept, lens, dst, q, weights, torch.full((1,), n, dtype=torch.int32, device="cuda"))
+
+        def step(w=w, kept=kept, lens=lens, dst=dst, q=q, weights=weights, n_dev=keep[-1]):
+            d.key_weights(q, t["kv"], t["table"], lse, w, 0.0, kv_scales=t["scales"])
+            cache.evict(weights, n_dev, 640, 1, 2, kv, table, kv, dst, kept, lens)
+
+        step()
+        torch.cuda.synchronize()
+        outs.append((keep, w.clone(), kept.clone()))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for keep, _, _ in outs:
+        keep[0].zero_()
+        keep[1].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for keep, w, kept in outs:
+        assert torch.equal(keep[0], w) and torch.equal(keep[1], kept)
+
+
 # ------------------------------------------------------------------------------- evict
 def run_evict(batch, weights, budget, first, last, seed=0, max_seq=None, same_cache=True):
     """Evicts into free pages of the batch's own cache (or another one); compares everything."""
@@ -328,6 +437,12 @@ def test_evict_few_long_requests(budget, first, last):
     w[:] = 0.5  # ties decide everything
     w[:, 1::2] = np.nan
     run_evict(batch, w, budget, first, last)
+
+
+def test_evict_many_requests():
+    g = np.random.default_rng(8)
+    batch, w = evict_batch(g.integers(1, 500, size=90), "e4m3", 16, seed=33)
+    run_evict(batch, w, 130, 3, 30, same_cache=False)
 
 
 def test_evict_special_weights():
