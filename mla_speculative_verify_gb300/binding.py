@@ -7,6 +7,7 @@ missing the import of this module's loader fails loudly; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -214,6 +215,7 @@ def cache_append(*args) -> None:
     check(lib.mla_cache_append(*args), lib)
 
 
+@functools.lru_cache(maxsize=1024)
 def cache_evict_workspace(batch: int, max_seq: int) -> int:
     """mla_cache_evict_workspace: device scratch bytes that mla_cache_evict needs."""
     lib = _lib or load()

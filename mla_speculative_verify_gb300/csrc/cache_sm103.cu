@@ -207,7 +207,6 @@ struct SelectArgs {
   long long w_stride;
   const int32_t* lens;
   int max_seq, budget, n_first, n_last;
-  int cache;  // keys a warp keeps in shared memory
   int32_t* kept;
   float* weights_dst;
   long long wd_stride;
@@ -217,13 +216,12 @@ struct SelectArgs {
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kSelStep = 128;       // keys a warp takes at once; a warp's share is a multiple
-constexpr int kSelCopies = 4;       // copies of a CTA's histogram: equal weights hit one bin
-constexpr int kSelKeys = 8192;     // keys a CTA takes while the cluster may grow
-constexpr int kSelMaxCtas = 16;    // (a cluster of 16 is beyond the portable 8)
-constexpr int kSelMaxKeys = kSelMaxCtas * 32 * kSelCopies * kBins / 2;  // two mark bits a key in the histograms' place
-constexpr int kSelCache = 1280;    // keys a warp keeps in shared memory, at most
-constexpr int kSelCacheBytes = 4 * 32 * (kSelCache + 4);
+constexpr int kSelStep = 128;    // keys a warp takes at once; a warp's share is a multiple
+constexpr int kSelCopies = 4;    // copies of a CTA's histogram: equal weights hit one bin
+constexpr int kSelKeys = 8192;   // keys of a CTA, at most
+constexpr int kSelMaxCtas = 8;   // CTAs of a cluster, at most
+constexpr int kSelWarpKeys = kSelKeys / kSelWarps;
+constexpr int kSelCacheBytes = 4 * kSelWarps * (kSelWarpKeys + 4);
 
 // A weight as an unsigned key of the same order; -0 counts as 0, NaN as the lowest.
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -242,14 +240,14 @@ __device__ __forceinline__ float weight_of(uint32_t key) {
 // peers' through distributed shared memory), and each finds the same bin. Then the kept keys
 // are numbered in order: those above the threshold, and of those equal to it the first ones.
 // A warp owns a contiguous piece of the keys in every pass; the weights are read once and kept
-// in shared memory (what does not fit is read again, from L2). Places behind the last
-// key hold the lowest key: they come after every real one, so none is ever taken.
-//
+// in shared memory. Places behind the last key hold the lowest key: they come after every real
+// one, so none is ever taken. What bounds it is the chain of passes: 4 requests of 4k keys 9 us,
+// 32 of 32k 15 us.
 template <bool kOne>  // one CTA per request
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  extern __shared__ __align__(16) uint32_t cache[];  // per warp a.cache keys, and 4 places more
+  extern __shared__ __align__(16) uint32_t cache[];  // per warp its keys, and 4 places more
   __shared__ uint64_t loaded[kSelWarps];
   __shared__ __align__(16) uint32_t copies[kSelCopies][kBins], hist[2][kBins];
   __shared__ uint32_t coarse[2][kSelWarps];  // this CTA's counts of 64 bins each
@@ -294,16 +292,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
   const int per = ((m + ctas * kSelWarps - 1) / (ctas * kSelWarps) + kSelStep - 1) / kSelStep * kSelStep;
   const long long i0 = ((long long)rank * kSelWarps + warp) * per;  // this warp's first key
   const float* wm = w + lo;
-  // key i + lane of the warp is there while i < left; the first `cached` are kept
-  const int left = (int)max(-32ll, min((long long)per, m - i0)) - lane;
-  const int cached = min(per, a.cache);
-  const float* wl = wm + i0 + lane;
-  // The weights that are kept come in by one bulk copy for each warp, which wants 16-byte
-  // boundaries: they lie in shared memory as they do in their 16 bytes of global memory, and up
-  // to three before the first boundary and after the last come in by themselves.
-  const int count = max(0, min(cached, left + lane));
+  // The warp's weights come in by a bulk copy, which wants 16-byte boundaries: they lie in shared
+  // memory as they do in their 16 bytes of global memory, and up to three before the first
+  // boundary and after the last come in by themselves.
+  const int count = (int)max(0ll, min((long long)per, m - i0));
   const int off = (int)(((uintptr_t)(wm + i0) >> 2) & 3);
-  uint32_t* cw = cache + warp * (a.cache + 4) + off;
+  uint32_t* cw = cache + warp * (kSelWarpKeys + 4) + off;
   uint32_t* cl = cw + lane;
   const int head = min(count, (4 - off) & 3), body_words = (count - head) & ~3, rest = count - head - body_words;
   if (lane == 0) {
@@ -328,27 +322,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     }
   }
   __syncwarp();
+  for (int i = 0; i < per; i += 32) cl[i] = i + lane < count ? order_key(__uint_as_float(cl[i])) : 0u;
   // body(keys i + lane, i + lane + 32, .., i) for every step of the warp's keys
   auto sweep = [&](auto body) {
-    int i = 0;
-    uint32_t key[4];
 #pragma unroll 2
-    for (; i < cached; i += kSelStep) {
+    for (int i = 0; i < per; i += kSelStep) {
+      uint32_t key[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) key[u] = cl[i + 32 * u];
       body(key, i);
-    }
-    for (; i < per; i += 4 * kSelStep) {
-      float x[16];
-#pragma unroll
-      for (int u = 0; u < 16; ++u) x[u] = i + 32 * u < left ? wl[i + 32 * u] : 0.f;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        if (i + h * kSelStep >= per) break;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) key[u] = i + 32 * (4 * h + u) < left ? order_key(x[4 * h + u]) : 0u;
-        body(key, i + h * kSelStep);
-      }
     }
   };
 
@@ -359,9 +341,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int above = pass == 1 ? 21 : 10;  // the bits from this one up are found (pass 0: none)
     const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    if (pass == 0)  // (the copied weights become keys as they are counted)
-#pragma unroll 4
-      for (int i = 0; i < cached; i += 32) cl[i] = i < left ? order_key(__uint_as_float(cl[i])) : 0u;
     sweep([&](const uint32_t (&key)[4], int) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -431,8 +410,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
   }
   // prefix is the threshold's key; `want` of the keys equal to it stay. One more sweep notes
   // which keys are above it and which equal it, a bit each (in the histograms' place). Bits are
-  // then counted a word to a lane: counted a word to a warp, at four per clock, they took two
-  // thirds of the time of this and of the writing (1M keys 54 us).
+  // then counted a word to a lane: a word to a warp, at four counts a clock, bounded this sweep.
   const int words = per / 32;
   uint2* marks = reinterpret_cast<uint2*>(&copies[0][0]) + warp * words;
   sweep([&](const uint32_t (&key)[4], int i) {
@@ -531,26 +509,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
   for (int j = 0; j < words; j += 4) {  // (a multiple of four words)
     uint2 mark[4];
     uint32_t pos[4];
-    float x[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       mark[u] = marks[j + u];
       pos[u] = mark[u].y + __popc(mark[u].x & below);
     }
-    if (wd) {
-      if (32 * j < cached) {  // (and with it all four words)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = weight_of(cl[32 * (j + u)]);
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = (mark[u].x >> lane) & 1u ? wl[32 * (j + u)] : 0.f;
-      }
-    }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (!((mark[u].x >> lane) & 1u)) continue;
       kept[pos[u]] = first + 32 * (j + u);
-      if (wd) wd[pos[u]] = x[u];
+      if (wd) wd[pos[u]] = weight_of(cl[32 * (j + u)]);
     }
   }
   if (!kOne) ptx::cluster_wait();  // no CTA leaves while a peer may still read its counts
@@ -566,7 +534,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
 //   step 4     the kept keys, numbered from those counts
 constexpr int kWideThreads = 512, kWideWarps = kWideThreads / 32;
 constexpr int kWidePer = 8, kWideKeys = kWideThreads * kWidePer;
-constexpr int kWideFrom = 65536;    // keys of the longest request above which the steps are launched
+constexpr int kWideFrom = kSelMaxCtas * kSelKeys;  // keys of the longest request above which these are launched
+constexpr int kSelMaxKeys = 1 << 21;               // the longest request that can be asked for
 constexpr int kWideMaxChunks = kSelMaxKeys / kWideKeys;
 
 struct alignas(256) WideState {  // per request, in the workspace; zero before step 0
@@ -861,8 +830,6 @@ cudaError_t set_cache_kernel_attributes() {
   cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCacheBytes);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCacheBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
 }
 
@@ -906,8 +873,8 @@ extern "C" int mla_cache_append(const void* rows, int total_rows, const int32_t*
 namespace mla {
 // Long requests are selected by the five launches, others by clusters. Whole calls that keep 64
 // keys, clusters against launches: 1 x 64k keys 19 against 19 us, 8 x 64k 19 against 25, 1 x 128k
-// 23 against 19, 4 x 128k 23 against 23, 8 x 128k 37 against 27 (eight clusters of 16 do not
-// run at once), 1 x 1M 42 against 27.
+// 23 against 19, 4 x 128k 23 against 23, 8 x 128k 37 against 27, 1 x 1M 42 against 27 (in
+// clusters of 16, of which eight do not run at once).
 static bool wide_selection(int max_seq) { return max_seq > kWideFrom; }
 }  // namespace mla
 
@@ -972,9 +939,9 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   cfg.stream = (cudaStream_t)stream;
   cfg.attrs = attr;
   cudaError_t ce;
+  const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last,
+                     kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
   if (wide) {
-    const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last, 0,
-                       kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
     ce = cudaMemsetAsync(workspace, 0, need, cfg.stream);
     cfg.gridDim = dim3((unsigned)((max_seq + kWideKeys - 1) / kWideKeys), (unsigned)batch, 1);
     cfg.blockDim = dim3(kWideThreads, 1, 1);
@@ -986,16 +953,12 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
       if (ce == cudaSuccess) ce = cudaLaunchKernelEx(&cfg, fn, s, (WideState*)workspace);
     }
   } else {
-    // CTAs per request: one for every 8192 keys, up to a cluster of 16
+    // a cluster of CTAs per request, one for every 8192 keys
     int ctas = 1;
-    while (ctas < kSelMaxCtas && (long long)ctas * kSelKeys < max_seq) ctas *= 2;
-    const int warp_keys = (max_seq / (ctas * kSelWarps) + kSelStep) / kSelStep * kSelStep;  // at most
-    const int cache = std::min(kSelCache, warp_keys);
-    const SelectArgs s{weights, weights_stride, seq_lens, max_seq, budget, n_first, n_last, cache,
-                       kept, weights_dst, weights_dst_stride, seq_lens_dst, status_dev};
+    while (ctas * kSelKeys < max_seq) ctas *= 2;
     cfg.gridDim = dim3((unsigned)ctas, (unsigned)batch, 1);
     cfg.blockDim = dim3(kSelThreads, 1, 1);
-    cfg.dynamicSmemBytes = 4 * (size_t)kSelWarps * (cache + 4);
+    cfg.dynamicSmemBytes = kSelCacheBytes;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)ctas;
     attr[0].val.clusterDim.y = 1;
