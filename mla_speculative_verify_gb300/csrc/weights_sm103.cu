@@ -18,11 +18,15 @@
 // tiles (sub_tiles, which fit L2 over all CTAs) through all groups before it goes on, so the
 // cache leaves HBM once; the sums of those keys wait in shared memory.
 //
-// An e4m3 cache is multiplied as stored (kind::f8f6f4). q_split_kernel first writes each Q row
-// as two e4m3 parts: the row times the power of two that brings its largest entry to [128,
-// 256), rounded, and the remainder. A bf16 entry has 8 significant bits and each part carries
-// 4, so entries down to 2^-9 of the row's largest are exact; below that the error is at most
-// 2^-18 of the largest. N = 2 * rows columns then hold both parts' scores.
+// An e4m3 cache is multiplied as stored (kind::f8f6f4). q_split_kernel first writes each Q row,
+// times the power of two that brings its largest entry to [128, 256), as an e4m3 part and the
+// remainder in e5m2. A bf16 entry has 8 significant bits: the first part takes 4 and leaves at
+// most 8 units of the last of them, which e5m2's 3 bits hold, so entries down to 2^-13 of the
+// row's largest are exact; below that the error is at most 2^-20 of the largest (with both parts
+// in e4m3 it was 2^-18 from 2^-9 on: 3.7e-6 in weights that fp32 has to 1.2e-6).
+// Both parts' products go into one accumulator: side by side in 2 x rows
+// columns they took half the products, but left two accumulators and twice the columns to read
+// (170 against 134 us for 32 requests of 8k-16k keys, 128 heads).
 //
 // The tensor cores cut the bits below an accumulator's last one at every step, always towards
 // zero, so a score of 36 steps in one accumulator is off by ~2^-20 of itself: 1.9e-5 in the
@@ -31,9 +35,14 @@
 // zero, and the parts are added in fp32 registers, rounded. The accumulators are taken in turns,
 // so one part is read while the next are computed.
 //
-// Warp roles (one CTA per SM): warps 0-3 load (TMA) and issue the products (Roles), warps 4-7
-// and 8-11 take the scores out, each half of the rows. All of them walk the same work list
+// Warp roles (one CTA per SM): warp 0 loads (TMA), warps 1-3 issue the products, warps 4-7 and
+// 8-11 take the scores out, each half of the rows. All of them walk the same work list
 // (Walk). Waits are bounded as in the decode kernel.
+//
+// Measured: 96 rows over 1M bf16 keys 200 us, 6.0 TB/s, 0.89 of the measured copy rate: bound by
+// HBM, and by the slowest of 152 equal shares (CTAs end 171 to 193 us after the start). 128 to 512
+// rows over 32 x 8k-16k e4m3 keys 137 us: bound by the exponentials' warps and the products'
+// operand reads, in turns; HBM would need 38 us and the products 86.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -64,24 +73,21 @@ constexpr int kPieces = 9;          // 576 = 9 x 64 columns
 constexpr int kMaxRows = 128;       // rows of a group
 constexpr int kMaxStages = 16;
 constexpr int kMaxSlots = 6;        // accumulators, taken in turns by the parts
-// The parts of a tile and what the four control warps do. The e4m3 products of a tile take less
-// time than one thread needs to issue them (~125 cycles each, and ~300 for a stage's waits and
-// commits), so three pieces make a part, each part has an issuer, and one warp loads. bf16 tiles
-// are twice as large and bound by the copies: one issuer, a loading warp for each of a tile's two
-// pages, and parts of one piece (a stage of three would fit only twice: a million keys 202 -> 208
-// us).
+
+// The parts of a tile; a part is a stage of the ring. One thread issues a product only every ~125
+// cycles and loses ~300 to a stage's waits and commits, more than the products themselves take,
+// so three warps issue parts in turns (bf16, 768 rows: 172 us with one, 159 with three). An issuer
+// waits for a stage's or an accumulator's next phase, which says nothing while the phase before
+// it is open; so each of them belongs to one issuer: their numbers are multiples of three. e4m3
+// pieces are half as large, so three make a part (batch of 128 heads 207 -> 179 us); bf16 parts
+// of three would leave two stages (a million keys 202 -> 208 us).
+constexpr int kIssuers = 3;  // warps 1-3; warp 0 loads
 template <bool kFp8>
-struct Roles {
-  static constexpr int kParts = kFp8 ? 3 : 9;          // parts of a score's 576 columns
-  static constexpr int kPer = kPieces / kParts;        // pieces of a part, which is a stage of the ring
-  static constexpr int kLoaders = kFp8 ? 1 : 2;        // warps 0 and (bf16) 2
-  static constexpr int kIssuers = kFp8 ? 3 : 1;        // warps 1 ..
-  // An issuer waits for a stage's or an accumulator's next phase, which says nothing while the
-  // phase before it is open; so with several issuers each of them belongs to one issuer: their
-  // number is a multiple of this.
-  static constexpr int kRingUnit = kFp8 ? kParts : 1;
+struct Parts {
+  static constexpr int kCount = kFp8 ? 3 : 9;    // parts of a score's 576 columns
+  static constexpr int kPer = kPieces / kCount;  // pieces of a part
 };
-constexpr int kMaxSub = 16;         // tiles of one sub-range: 32 page ids, one per lane
+constexpr int kMaxSub = 32;         // tiles of one sub-range: a loading warp holds a page id in each lane
 constexpr int kMaxSubSums = 8;      // of those when sums wait in shared memory (G > 1)
 constexpr int kThreads = 384;
 constexpr int kSmemCap = 232448;    // 227 KB per CTA
@@ -89,7 +95,7 @@ constexpr int kSmemCap = 232448;    // 227 KB per CTA
 struct WeightsMisc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[kPieces], q_empty[kPieces];
-  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done[3];
+  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done[kIssuers];
   uint32_t tmem_base;
   int abort;
   alignas(16) float nlse[kMaxRows];    // -lse of the current group's rows
@@ -257,8 +263,8 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
           float x[kCols];
 #pragma unroll
           for (int j = 0; j < kCols; ++j) x[j] = 0.f;
-#pragma unroll (kFp8 ? Roles<kFp8>::kParts : 1)
-          for (int u = 0; u < Roles<kFp8>::kParts; ++u, slots.step()) {
+#pragma unroll (kFp8 ? Parts<kFp8>::kCount : 1)
+          for (int u = 0; u < Parts<kFp8>::kCount; ++u, slots.step()) {
             const uint32_t slot = slots.at;
             if (ok) ok = warp_wait(&ms->d_full[slot], slots.phase & 1, abort, p);
             if (ok && mine > 0) {
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmap_page, WeightsParams p) {
   constexpr int kRowBytes = kFp8 ? 64 : 128;             // a row's bytes in one 64-column piece
   constexpr int kPieceBytes = kKeys * kRowBytes;
-  using R = Roles<kFp8>;
+  using R = Parts<kFp8>;
   constexpr int kPer = R::kPer;
   constexpr int kStageBytes = kPer * kPieceBytes;
   constexpr int kHalf = kPage * kRowBytes;               // one page of a piece
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     ms->abort = 0;
     for (int i = 0; i < p.stages; ++i) {
-      ptx::mbar_init(&ms->kv_full[i], Roles<kFp8>::kLoaders);
+      ptx::mbar_init(&ms->kv_full[i], 1);
       ptx::mbar_init(&ms->kv_empty[i], 1);
     }
     for (int i = 0; i < kPieces; ++i) {
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&ms->d_full[i], 1);
       ptx::mbar_init(&ms->d_empty[i], 8);
     }
-    for (int i = 0; i < 3; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
+    for (int i = 0; i < kIssuers; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmap_q);
     ptx::prefetch_tmap(&tmap_kv);
@@ -375,12 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int b, t0, t1;
   PlanRequest req;
 
-  if (warp == 0 || (R::kLoaders == 2 && warp == 2)) {
+  if (warp == 0) {
     // ------------------------------------------------------------ loads
-    // Warp 0 loads Q and each tile's first page; the second page warp 2, or with one loader
-    // warp 0 too. Lane l holds the page ids of the two pages (or of this warp's) of tile l.
-    constexpr bool kBoth = R::kLoaders == 1;
-    const int second = warp == 2;
     if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
     Ring ring(p.stages);
     uint32_t qfill = 0;  // Q groups loaded so far
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
       const int npages = (req.ctx + kPage - 1) / kPage;
       const int32_t* ids = p.page_table + (size_t)b * p.pt_stride;
-      auto load_ids = [&](int tile, int which) {  // lane l: page `which` of tile `tile` + l
+      auto load_ids = [&](int tile, int which) {  // lane l: page `which` (0, 1) of tile `tile` + l
         const int pg = 2 * (tile + lane) + which;
         int id = lane < sub && tile + lane < t1 && pg < npages ? ids[pg] : 0;
         if (id < 0 || id >= p.num_pages) {
@@ -400,26 +402,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return id;
       };
-      int cur = load_ids(t0, second), cur1 = kBoth ? load_ids(t0, 1) : 0;
+      int cur0 = load_ids(t0, 0), cur1 = load_ids(t0, 1);
       for (int s0 = t0; ok && s0 < t1; s0 += sub) {
         const int s1 = min(t1, s0 + sub);
-        const int nxt = s1 < t1 ? load_ids(s1, second) : 0, nxt1 = kBoth && s1 < t1 ? load_ids(s1, 1) : 0;
+        const int nxt0 = s1 < t1 ? load_ids(s1, 0) : 0, nxt1 = s1 < t1 ? load_ids(s1, 1) : 0;
         for (int g = 0; ok && g < groups; ++g) {
           const bool new_q = groups > 1 || s0 == t0;
           for (int t = s0; ok && t < s1; ++t) {
-            const bool there = 2 * t + second < npages;
-            const bool there1 = kBoth && 2 * t + 1 < npages;
-            const int id = __shfl_sync(0xffffffffu, cur, t - s0), id1 = __shfl_sync(0xffffffffu, cur1, t - s0);
-            // ask L2 for the whole page of the next tile that HBM has to deliver
-            const int tn = g == 0 && t + 1 < s1 ? t + 1 : g == groups - 1 && t + 1 == s1 ? s1 : t1;
-            const int id_n = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur, (t - s0 + 1) & 31) : __shfl_sync(0xffffffffu, nxt, 0);
-            const int id_n1 = t + 1 < s1 ? __shfl_sync(0xffffffffu, cur1, (t - s0 + 1) & 31) : __shfl_sync(0xffffffffu, nxt1, 0);
+            const bool two = 2 * t + 1 < npages;  // (the last tile may have one page)
+            const int id0 = __shfl_sync(0xffffffffu, cur0, t - s0), id1 = __shfl_sync(0xffffffffu, cur1, t - s0);
+            // ask L2 for the whole pages of the next tile that HBM has to deliver
+            const bool in = t + 1 < s1;
+            const int tn = g == 0 && in ? t + 1 : g == groups - 1 && !in ? s1 : t1;
+            const int next0 = __shfl_sync(0xffffffffu, in ? cur0 : nxt0, in ? t + 1 - s0 : 0);
+            const int next1 = __shfl_sync(0xffffffffu, in ? cur1 : nxt1, in ? t + 1 - s0 : 0);
             if (tn < t1 && ptx::elect_one()) {
-              if (2 * tn + second < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, id_n * kPage, 0);
-              if (kBoth && 2 * tn + 1 < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, id_n1 * kPage, 0);
+              ptx::tma_prefetch_l2_3d(&tmap_page, 0, next0 * kPage, 0);
+              if (2 * tn + 1 < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, next1 * kPage, 0);
             }
             for (int c0 = 0; ok && c0 < kPieces; c0 += kPer) {
-              for (int c = c0; !second && new_q && t == s0 && c < c0 + kPer; ++c) {
+              for (int c = c0; new_q && t == s0 && c < c0 + kPer; ++c) {
                 if (qfill > 0) ok = warp_wait(&ms->q_empty[c], (qfill - 1) & 1, abort, p);
                 if (!ok) break;
                 if (ptx::elect_one()) {
@@ -433,17 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (ok && ring.phase > 0) ok = warp_wait(&ms->kv_empty[ring.at], (ring.phase - 1) & 1, abort, p);
               if (!ok) break;
               if (ptx::elect_one()) {
-                uint8_t* dst = sK + ring.at * kStageBytes + second * kHalf;
-                if (there) {
-                  ptx::mbar_arrive_expect_tx(&ms->kv_full[ring.at], (there1 ? 2 : 1) * kPer * kHalf);
+                uint8_t* dst = sK + ring.at * kStageBytes;
+                ptx::mbar_arrive_expect_tx(&ms->kv_full[ring.at], (two ? 2 : 1) * kPer * kHalf);
 #pragma unroll
-                  for (int j = 0; j < kPer; ++j) {
-                    ptx::tma_load_3d(dst + j * kPieceBytes, &tmap_kv, &ms->kv_full[ring.at], 0, id * kPage, c0 + j);
-                    if (there1)
-                      ptx::tma_load_3d(dst + j * kPieceBytes + kHalf, &tmap_kv, &ms->kv_full[ring.at], 0, id1 * kPage, c0 + j);
-                  }
-                } else {
-                  ptx::mbar_arrive(&ms->kv_full[ring.at]);
+                for (int j = 0; j < kPer; ++j) {
+                  ptx::tma_load_3d(dst + j * kPieceBytes, &tmap_kv, &ms->kv_full[ring.at], 0, id0 * kPage, c0 + j);
+                  if (two)
+                    ptx::tma_load_3d(dst + j * kPieceBytes + kHalf, &tmap_kv, &ms->kv_full[ring.at], 0, id1 * kPage, c0 + j);
                 }
               }
               __syncwarp();
@@ -452,13 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (new_q) ++qfill;
         }
-        cur = nxt;
+        cur0 = nxt0;
         cur1 = nxt1;
       }
     }
     // After an abort every copy must have landed before the CTA may exit: the ring's last ones
-    // and the Q pieces'. A phase that the other producer never completes, or that is not open,
-    // ends by the shorter limit.
+    // and the Q pieces'. (Of a barrier's two phases one is always over; where no copy is under
+    // way the other ends by the short limit.)
     if (*abort && lane == 0) {
       for (int i = 0; i < p.stages + kPieces; ++i)
         for (uint32_t par = 0; par < 2; ++par) {
@@ -469,13 +467,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-  } else if (warp <= R::kIssuers) {
+  } else if (warp <= kIssuers) {
     // ------------------------------------------------------------ products
-    // With three issuers warp 1 + u issues part u of every tile, else warp 1 all of them. Each
-    // accumulator is written by one thread in order, so the sums repeat.
+    // Warp 1 + i issues parts i, i + 3, .. Each accumulator is written by one thread in order,
+    // so the sums repeat.
     const uint32_t sq = ptx::smem_addr(sQ), sk = ptx::smem_addr(sK);
     const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kKeys, n, 0, 0) : ptx::idesc_bf16(kKeys, n, 0, 0);
-    const int u0 = R::kIssuers == 1 ? 0 : warp - 1, u1 = R::kIssuers == 1 ? R::kParts : warp;
+    const int u0 = warp - 1;
     Ring ring(p.stages), slots(p.slots);
     for (int i = 0; i < u0; ++i) {
       ring.step();
@@ -492,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; ok && g < groups; ++g) {
           const bool new_q = groups > 1 || s0 == t0, last_q = groups > 1 || s1 == t1;
           for (int t = s0; ok && t < s1; ++t) {
-            for (int u = u0; ok && u < u1; ++u) {
+            for (int u = u0; ok && u < R::kCount; u += kIssuers) {
               // what the accumulator held has been read
               if (slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
               const int c0 = kPer * u;
@@ -513,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t add = (j | k) == 0 ? 0u : 1u;
                     if constexpr (kFp8) {
                       ptx::mma_e4m3_ss(d, a, q, idesc, add);
-                      ptx::mma_e4m3_ss(d, a, q + n * 64 / 16, idesc, 1u);
+                      ptx::mma_e4m3_ss(d, a, q + n * 64 / 16, idesc | ptx::kB_E5M2, 1u);
                     } else {
                       ptx::mma_bf16_ss(d, a, q, idesc, add);
                     }
@@ -526,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
               issued = true;
-              for (int i = 0; i < R::kIssuers; ++i) {  // past the other issuers' parts
+              for (int i = 0; i < kIssuers; ++i) {  // past the other issuers' parts
                 ring.step();
                 slots.step();
               }
@@ -560,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Q [rows, 576] bf16 -> e4m3 parts [2][rows][576] and the factor that undoes each row's power
+// Q [rows, 576] bf16 -> its e4m3 and its e5m2 part [2][rows][576] and the factor that undoes each row's power
 // of two. One warp per row: 72 pieces of 8 entries, lane l holds pieces l, l + 32 and (l < 8) 64 + l.
 constexpr int kSplitWarps = 8;
 __global__ void __launch_bounds__(32 * kSplitWarps) q_split_kernel(const uint4* q, int rows, uint8_t* parts,
@@ -595,7 +593,7 @@ __global__ void __launch_bounds__(32 * kSplitWarps) q_split_kernel(const uint4* 
       const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, c), __NV_SATFINITE, __NV_E4M3);
       const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
       const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-      const __nv_fp8x2_storage_t r = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, c - back.y), __NV_SATFINITE, __NV_E4M3);
+      const __nv_fp8x2_storage_t r = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, c - back.y), __NV_SATFINITE, __NV_E5M2);
       hi[k >> 2] |= (uint32_t)h << (8 * (k & 3));
       lo[k >> 2] |= (uint32_t)r << (8 * (k & 3));
     }
@@ -700,9 +698,8 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   if (rc != MLA_OK) return rc;
   const int piece = fp8 ? 8192 : 16384, tile_bytes = kPieces * piece;
   const int fixed = 1024 + kMiscBytes + kPieces * most_rows * 128;
-  const int per = fp8 ? Roles<true>::kPer : Roles<false>::kPer;
-  const int unit = fp8 ? Roles<true>::kRingUnit : Roles<false>::kRingUnit;
-  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / (per * piece)) / unit * unit;
+  const int per = fp8 ? Parts<true>::kPer : Parts<false>::kPer;
+  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / (per * piece)) / kIssuers * kIssuers;
   const int smem = fixed + stages * per * piece;
   auto fn = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -734,7 +731,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   prm.kv_scale = kv_scale;
   prm.rows_n = most_rows;
   prm.stages = stages;
-  prm.slots = std::min(kMaxSlots, 512 / most_rows) / unit * unit;
+  prm.slots = std::min(kMaxSlots, 512 / most_rows) / kIssuers * kIssuers;
   // tiles that all CTAs together keep in L2 while the groups pass over them
   prm.sub_tiles = std::max(1, std::min<int>(kMaxSubSums, (int)((80LL << 20) / ((long long)tile_bytes * grid))));
   prm.status = status_dev;
