@@ -90,7 +90,8 @@ typedef struct {
                               the first work unit skip the copy of its page number
                               debug_skip_copy - 1 and shortens every bounded wait of the call to
                               ~2 ms, so the units that wait for that page report
-                              MLA_DEVICE_WAIT_TIMEOUT and stop (no fault, no hang) */
+                              MLA_DEVICE_WAIT_TIMEOUT and stop (no fault, no hang);
+                              mla_key_weights: its first CTA skips that part of its copies */
 } mla_plan_options;
 
 /*
@@ -222,7 +223,7 @@ int mla_device_pair_slots(int device, int* slots);
  * tokens gets the larger of that and its present scale; where that is larger its old codes are
  * rounded to it. Codes are round-to-nearest-even of x / scale; infinities and larger values
  * become +-448, NaN stays NaN. Rows behind a request's last token are left as they are.
- * No two requests of a call may write one page.
+ * No page may be named twice among those that a call writes.
  *
  * Requests whose lengths do not fit (more than max_new rows, more rows than tokens, more
  * pages than page_table_stride, cu_new outside rows) write nothing and report

@@ -122,7 +122,8 @@ struct WeightsParams {
   int stages, slots, sub_tiles;
   long long total_work;    // sum over requests of tiles * groups
   int32_t* status;
-  long long wait_budget;
+  long long wait_budget;  // cycles a bounded wait may take (kWaitBudget; kWaitBudgetTest in a timeout test)
+  int skip_copy;          // part of the first CTA that is never copied (timeout test), or -1
 };
 
 // This CTA's share of the work list, as every role's warps walk it. The list is request by
@@ -386,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
     Ring ring(p.stages);
     uint32_t qfill = 0;  // Q groups loaded so far
+    int fill = 0;        // parts copied so far
     bool ok = true;
     while (ok && walk.next(p, b, req, t0, t1)) {
       const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (ok && ring.phase > 0) ok = warp_wait(&ms->kv_empty[ring.at], (ring.phase - 1) & 1, abort, p);
               if (!ok) break;
-              if (ptx::elect_one()) {
+              if (!(blockIdx.x == 0 && fill == p.skip_copy) && ptx::elect_one()) {
                 uint8_t* dst = sK + ring.at * kStageBytes;
                 ptx::mbar_arrive_expect_tx(&ms->kv_full[ring.at], (two ? 2 : 1) * kPer * kHalf);
 #pragma unroll
@@ -446,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
               ring.step();
+              ++fill;
             }
           }
           if (new_q) ++qfill;
@@ -735,7 +738,8 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   // tiles that all CTAs together keep in L2 while the groups pass over them
   prm.sub_tiles = std::max(1, std::min<int>(kMaxSubSums, (int)((80LL << 20) / ((long long)tile_bytes * grid))));
   prm.status = status_dev;
-  prm.wait_budget = kWaitBudget;
+  prm.wait_budget = h->debug_skip_copy > 0 ? kWaitBudgetTest : kWaitBudget;
+  prm.skip_copy = h->debug_skip_copy - 1;
   const void* q_src = q;
   if (fp8) {
     prm.q_scale = (const float*)((uint8_t*)workspace + ((size_t)prm.total_rows * 1152 + 255) / 256 * 256);

@@ -92,6 +92,7 @@ class VerifyDecoder:
                 raise ValueError("block scales belong to an fp8 cache")
             index = self.device.index
             block = check_scales("kv_scales", kv_scales, rows // 64, index)
+            check_table("page_table", page_table, self.seq_lens.shape[0], index)
             on_device(index, binding.run_scaled, self.plan_dev.data_ptr(), self._plan_host_ptr, self.plan_host.nbytes,
                       q.data_ptr(), kv_cache.data_ptr(), kv_scales.data_ptr(), block, page_table.data_ptr(),
                       page_table.shape[1], rows // 64,

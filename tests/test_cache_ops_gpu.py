@@ -260,6 +260,159 @@ def test_key_weights_sum_to_the_rows():
     assert np.abs(total / [48, 24] - 1).max() < 1e-4
 
 
+@pytest.mark.parametrize("kind,block", [("bf16", 0), ("e4m3", 16)])
+def test_timeouts_are_reported_not_hung(kind, block):
+    """A plan whose test-only option keeps one copy from being issued and shortens every bounded
+    wait to ~2 ms: the decode and the key weights give up, report it, and the next calls are exact."""
+    batch = ref.Batch(12, [64 * 40 + 7], [4], kind, block, seed=27)
+    _, t, _, lse = decode(batch)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bad = VerifyDecoder(batch.seq_lens, batch.q_lens, 12, "bf16" if kind == "bf16" else "fp8",
+                        options=binding.PlanOptions(force_splits=4, debug_skip_copy=3))
+    if block:
+        bad.run(t["q"], t["kv"], t["table"], torch.empty((4, 12, 512), dtype=torch.bfloat16, device="cuda"),
+                status=status, kv_scales=t["scales"])
+        torch.cuda.synchronize()
+        assert int(status.item()) & binding.MLA_DEVICE_WAIT_TIMEOUT
+        status.zero_()
+    bad.key_weights(t["q"], t["kv"], t["table"], lse, torch.zeros((1, 2567), device="cuda"), kv_scales=t["scales"],
+                    status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) & binding.MLA_DEVICE_WAIT_TIMEOUT
+    old = np.zeros((1, 2567))
+    w, lse = run_weights(batch, 1.0, old)
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 1.0, old)
+    assert (np.abs(w.cpu().double().numpy() - want) <= bound + 1e-30).all()
+
+
+@pytest.mark.parametrize("kind,block", [("bf16", 0), ("e4m3", 0), ("e4m3", 64)])
+def test_bad_pages_are_reported(kind, block):
+    """A page id outside the cache is reported and touches nothing else: the other request's sums
+    and rows stay exact."""
+    batch = ref.Batch(12, [300, 200], [2, 1], kind, block, seed=28, extra_pages=20, poison=False)
+    d, t, _, lse = decode(batch)
+    table = batch.table.copy()
+    table[0, 2] = batch.pages
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = torch.zeros((2, 300), device="cuda")
+    d.key_weights(t["q"], t["kv"], dev(table), lse, w, kv_scale=batch.kv_scale, kv_scales=t["scales"], status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == binding.MLA_DEVICE_BAD_PAGE
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 1.0, np.zeros((2, 300)))
+    assert (np.abs(w.cpu().double().numpy() - want)[1] <= bound[1]).all()
+    if block:
+        status.zero_()
+        out = torch.empty((3, 12, 512), dtype=torch.bfloat16, device="cuda")
+        d.run(t["q"], t["kv"], dev(table), out, status=status, kv_scales=t["scales"])
+        torch.cuda.synchronize()
+        assert int(status.item()) == binding.MLA_DEVICE_BAD_PAGE
+        want_out, out_bound, _, _ = ref.attend(batch)
+        assert (np.abs(out[2].cpu().double().numpy() - want_out[2]) <= out_bound[2]).all()
+    # eviction: an old page of request 0 and a new page of request 1 out of range
+    table_dst = batch.free[:4].reshape(2, 2).copy()
+    bad_dst = table_dst.copy()
+    bad_dst[1, 1] = -1
+    weights = np.random.default_rng(1).random((2, 300)).astype(np.float32)
+    kept, lens = torch.empty((2, 100), dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    status.zero_()
+    cache.evict(dev(weights), dev(batch.seq_lens), 100, 0, 0, t["kv"], dev(table), t["kv"], dev(bad_dst), kept, lens,
+                scales=t["scales"], scales_dst=t["scales"], status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == binding.MLA_DEVICE_BAD_PAGE
+    assert lens.tolist() == [100, 100]
+    as_values = (lambda x: x.double().numpy()) if kind == "bf16" else ref.code_values
+    values, values_dst = as_values(batch.kv), as_values(batch.kv)
+    s = None if block == 0 else batch.scales.double().numpy()
+    want = ref.evict(weights[1:], batch.seq_lens[1:], 100, 0, 0, values, s, batch.table[1:], values_dst,
+                     None if s is None else s.copy(), table_dst[1:], block)
+    assert kept[1].cpu().tolist() == want[0].tolist()
+    got = as_values(t["kv"].cpu())
+    assert np.array_equal(got[table_dst[1, 0]], values_dst[table_dst[1, 0]])
+    assert np.array_equal(got[table_dst[1, 1]], values[table_dst[1, 1]])  # (named by nobody: as it was)
+
+
+def test_key_weights_with_a_plan_for_cta_pairs():
+    batch = ref.Batch(12, [700], [8], "bf16", seed=29)
+    d, t, _, lse = decode(batch, binding.PlanOptions(cta_pair=1))
+    assert d.cta_pair
+    w, _ = run_weights(batch, 1.0, np.zeros((1, 700)), lse=lse, d=d, t=t)
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 1.0, np.zeros((1, 700)))
+    assert (np.abs(w.cpu().double().numpy() - want) <= bound + 1e-30).all()
+
+
+def test_offsets_beyond_32_bits():
+    """A pool of 2.9 GB of codes whose pages in use lie at its end, as uint8 and as float8, gives
+    what a small pool gives: append, decode, key weights and eviction."""
+    big, n, q, H = 80000, 500, 3, 12
+    gen = torch.Generator().manual_seed(30)
+    rows = torch.randn((n, D), generator=gen).to(torch.bfloat16).cuda()
+    queries = torch.randn((q, H, D), generator=gen).to(torch.bfloat16).cuda()
+    weights = torch.rand((1, n), generator=gen).cuda()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    d = VerifyDecoder([n], [q], H, "fp8")
+    results = []
+    for pages in (12, big):
+        base = pages - 12
+        codes = torch.zeros((pages, PAGE, D), dtype=torch.uint8, device="cuda")
+        scales = torch.ones((pages, 4), device="cuda")
+        table = (base + torch.arange(8, device="cuda")).int().view(1, 8)
+        dst = (base + 8 + torch.arange(4, device="cuda")).int().view(1, 4)
+        out, lse = torch.empty((q, H, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((q, H), device="cuda")
+        w, kept, lens = torch.zeros((1, n), device="cuda"), torch.empty((1, 200), dtype=torch.int32, device="cuda"), i32([0])
+        status = i32([0])
+        view = codes.view(F8) if pages == big else codes
+        cache.append(rows, view, scales, table, i32([n]), i32([0, n]), n, status)
+        d.run(queries, view, table, out, lse, status=status, kv_scales=scales)
+        d.key_weights(queries, view, table, lse, w, kv_scales=scales, status=status)
+        cache.evict(weights, i32([n]), 200, 4, 8, view, table, view, dst, kept, lens, scales=scales, scales_dst=scales,
+                    status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        results.append([x.clone() for x in (out, lse, w, kept, lens, codes[base:], scales[base:])])
+        assert not codes[:base].any() if pages == 12 else not codes[:1000].any()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_refused_tensors():
+    """Wrong types, shapes and layouts on the GPU are refused before anything is launched."""
+    z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    rows, codes, scales = z(4, D, t=torch.bfloat16), z(3, PAGE, D, t=torch.uint8), z(3, 4, t=torch.float32)
+    good = dict(rows=rows, codes=codes, scales=scales, page_table=z(1, 2), seq_lens=z(1), cu_new=z(2), max_new=4)
+    for name, t in (("rows", rows.float()), ("rows", z(D, 4, t=torch.bfloat16).t()), ("rows", rows[0]), ("codes", codes[:, :32]),
+                    ("codes", codes.float()), ("scales", z(3, 3, t=torch.float32)), ("scales", z(2, 4, t=torch.float32)),
+                    ("scales", z(3, 128, t=torch.float32)), ("page_table", z(2)), ("page_table", z(2, 2, t=torch.int64)),
+                    ("seq_lens", z(2)), ("cu_new", z(1)), ("seq_lens", z(1).cpu())):
+        with pytest.raises(ValueError):
+            cache.append(**dict(good, **{name: t}))
+    with pytest.raises(binding.MlaError):
+        cache.append(**dict(good, max_new=5))
+    f32 = torch.float32
+    good = dict(weights=z(1, 64, t=f32), seq_lens=z(1), budget=8, n_first=0, n_last=0, kv=codes, page_table=z(1, 1),
+                kv_dst=codes, page_table_dst=z(1, 1), kept=z(1, 8), seq_lens_dst=z(1), scales=scales, scales_dst=scales)
+    for name, t in (("weights", z(64, t=f32)), ("weights", z(64, 2, t=f32).t()[:1]), ("seq_lens", z(2)), ("kv", codes.float()),
+                    ("kv_dst", codes.to(torch.bfloat16)), ("scales", None), ("scales_dst", z(3, 2, t=f32)), ("kept", z(1, 7)),
+                    ("page_table_dst", z(2, 1)), ("seq_lens_dst", z(1, t=torch.int64))):
+        with pytest.raises(ValueError):
+            cache.evict(**dict(good, **{name: t}))
+    with pytest.raises(binding.MlaError):
+        cache.evict(**dict(good, n_first=9))
+    d = VerifyDecoder([64], [1], 12, "fp8")
+    good = dict(q=z(1, 12, D, t=torch.bfloat16), kv_cache=codes, page_table=z(1, 1), lse=z(1, 12, t=f32), weights=z(1, 64, t=f32))
+    for name, t in (("q", z(1, 11, D, t=torch.bfloat16)), ("kv_cache", codes.to(torch.bfloat16)), ("kv_cache", codes[0, :32]),
+                    ("lse", z(12, 2, t=f32).t()[:1]), ("weights", z(64, t=f32)), ("page_table", z(1)), ("kv_scales", z(2, 1, t=f32)),
+                    ("counted", z(2))):
+        with pytest.raises(ValueError):
+            d.key_weights(**dict(good, **{name: t}))
+    with pytest.raises(binding.MlaError):
+        d.key_weights(**dict(good, weights=z(1, 63, t=f32)))
+    out = z(1, 12, 512, t=torch.bfloat16)
+    with pytest.raises(ValueError):
+        d.run(good["q"], codes, z(1, 1), out, kv_scales=z(3, 5, t=f32))
+    with pytest.raises(ValueError):
+        VerifyDecoder([64], [1], 12, "bf16").run(good["q"], codes.to(torch.bfloat16), z(1, 1), out, kv_scales=scales)
+
+
 @pytest.mark.parametrize("kind,block", [("bf16", 0), ("e4m3", 32)])
 def test_key_weights_of_many_requests(kind, block):
     """More requests than a warp looks at together, several of them in one CTA's share and some
@@ -314,12 +467,13 @@ def test_key_weights_long(kind, heads, q):
     assert ((w[0].double() - want).abs() <= bound).all()
 
 
-def test_two_graphs_at_once():
+@pytest.mark.parametrize("n", [20000, 70000])
+def test_two_graphs_at_once(n):
     """Graphs of one decoder, captured one after the other and replayed on two streams at the same
-    time, share no scratch: the key weights of an e4m3 cache, and an eviction of a long request."""
+    time, share no scratch: the key weights of an e4m3 cache, and an eviction of a request that a
+    cluster, or the whole GPU, selects from."""
     batch = ref.Batch(24, [3000, 900], [4, 2], "e4m3", 16, seed=26)
     d, t, _, lse = decode(batch)
-    n = 70000
     wide = torch.rand((1, n), device="cuda")
     pages = (n + 63) // 64
     kv = torch.zeros((pages + 20, 64, D), dtype=torch.uint8, device="cuda")
