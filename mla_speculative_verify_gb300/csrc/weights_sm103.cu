@@ -108,6 +108,7 @@ constexpr int kMiscBytes = (sizeof(WeightsMisc) + 1023) / 1024 * 1024;
 
 struct WeightsParams {
   const PlanRequest* reqs;
+  PlanRequest first;       // reqs[0], so that a call with one request need not read it
   int batch, H, pt_stride, num_pages, block_log2;
   const int32_t* page_table;
   const float* kv_scales;  // NULL without block scales
@@ -155,7 +156,7 @@ struct Walk {
       b0 += 32;
       if (b0 >= p.batch || base >= hi) return false;
       const bool live = b0 + lane < p.batch;
-      r = live ? p.reqs[b0 + lane] : PlanRequest{0, 0, 0, 1};
+      r = !live ? PlanRequest{0, 0, 0, 1} : p.batch == 1 ? p.first : p.reqs[b0 + lane];
       const long long mine = (long long)((r.ctx + kKeys - 1) / kKeys) * groups(p, r.q);
       long long incl = mine;
 #pragma unroll
@@ -381,12 +382,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   walk.start(p);
   int b, t0, t1;
   PlanRequest req;
+  auto load_q = [&](int c, int row) {  // piece c of the group that begins at `row` (one lane)
+    ptx::mbar_arrive_expect_tx(&ms->q_full[c], q_piece);
+    ptx::tma_load_3d(sQ + c * q_piece, &tmap_q, &ms->q_full[c], 0, row, c);
+    if (kFp8) ptx::tma_load_3d(sQ + c * q_piece + n * 64, &tmap_q, &ms->q_full[c], 0, p.total_rows + row, c);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
     Ring ring(p.stages);
-    uint32_t qfill = 0;  // Q groups loaded so far
+    uint32_t qfill = 0;  // Q groups loaded so far (the first by the issuers)
     int fill = 0;        // parts copied so far
     bool ok = true;
     while (ok && walk.next(p, b, req, t0, t1)) {
@@ -423,15 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (2 * tn + 1 < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, next1 * kPage, 0);
             }
             for (int c0 = 0; ok && c0 < kPieces; c0 += kPer) {
-              for (int c = c0; new_q && t == s0 && c < c0 + kPer; ++c) {
-                if (qfill > 0) ok = warp_wait(&ms->q_empty[c], (qfill - 1) & 1, abort, p);
+              for (int c = c0; new_q && qfill > 0 && t == s0 && c < c0 + kPer; ++c) {
+                ok = warp_wait(&ms->q_empty[c], (qfill - 1) & 1, abort, p);
                 if (!ok) break;
-                if (ptx::elect_one()) {
-                  const int row = req.tok0 * p.H + g * n;
-                  ptx::mbar_arrive_expect_tx(&ms->q_full[c], q_piece);
-                  ptx::tma_load_3d(sQ + c * q_piece, &tmap_q, &ms->q_full[c], 0, row, c);
-                  if (kFp8) ptx::tma_load_3d(sQ + c * q_piece + n * 64, &tmap_q, &ms->q_full[c], 0, p.total_rows + row, c);
-                }
+                if (ptx::elect_one()) load_q(c, req.tok0 * p.H + g * n);
                 __syncwarp();
               }
               if (ok && ring.phase > 0) ok = warp_wait(&ms->kv_empty[ring.at], (ring.phase - 1) & 1, abort, p);
@@ -483,10 +484,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       slots.step();
     }
     uint32_t qphase = 0;
-    bool ok = true, issued = false;
+    bool ok = true, issued = false, loaded = false;
+    if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
     while (ok && walk.next(p, b, req, t0, t1)) {
       const int rows = counted_rows(p, b, req.q), groups = (rows + n - 1) / n;
       if (groups == 0 || t0 >= t1) continue;
+      // the first group's Q: each issuer its own pieces, while warp 0 asks for the keys
+      if (!loaded && ptx::elect_one())
+        for (int u = u0; u < R::kCount; u += kIssuers)
+          for (int c = kPer * u; c < kPer * (u + 1); ++c) load_q(c, req.tok0 * p.H);
+      __syncwarp();
+      loaded = true;
       const int sub = groups > 1 ? p.sub_tiles : kMaxSub;
       for (int s0 = t0; ok && s0 < t1; s0 += sub) {
         const int s1 = min(t1, s0 + sub);
@@ -718,6 +726,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   }
   const unsigned grid = (unsigned)std::min<long long>(tiles, sms);
   prm.reqs = (const PlanRequest*)((const uint8_t*)plan_dev + h->req_off);
+  prm.first = reqs[0];
   prm.batch = h->batch;
   prm.H = h->num_heads;
   prm.pt_stride = page_table_stride;
