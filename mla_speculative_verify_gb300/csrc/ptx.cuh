@@ -200,6 +200,15 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// A warpgroup gives registers back down to N per thread, or takes up to N (all of its warps).
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 // Named barrier that also returns the OR of `pred` over all participating threads.
 __device__ __forceinline__ bool bar_red_or(uint32_t id, uint32_t nthreads, bool pred) {
   uint32_t r;

@@ -36,13 +36,14 @@
 // so one part is read while the next are computed.
 //
 // Warp roles (one CTA per SM): warp 0 loads (TMA), warps 1-3 issue the products, warps 4-7 and
-// 8-11 take the scores out, each half of the rows. All of them walk the same work list
+// 8-11 take the scores out, a tile each in turns. All of them walk the same work list
 // (Walk). Waits are bounded as in the decode kernel.
 //
-// Measured: 96 rows over 1M bf16 keys 200 us, 6.0 TB/s, 0.89 of the measured copy rate: bound by
-// HBM, and by the slowest of 152 equal shares (CTAs end 171 to 193 us after the start). 128 to 512
-// rows over 32 x 8k-16k e4m3 keys 137 us: bound by the exponentials' warps and the products'
-// operand reads, in turns; HBM would need 38 us and the products 86.
+// Measured: 96 rows over 1M bf16 keys 204 us, 5.9 TB/s, 0.87 of the measured copy rate: bound by
+// HBM, and by the slowest of 152 equal shares. 128 to 512 rows over 32 x 8k-16k e4m3 keys 129 us:
+// bound by the products' operand reads (128 rows x 128 keys read shared memory as long as they
+// compute, and the keys' arrival and the rows' tables want it too; without the keys' copies it is
+// 109); HBM would need 38 us and the products 86.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -76,32 +77,43 @@ constexpr int kMaxSlots = 6;        // accumulators, taken in turns by the parts
 
 // The parts of a tile; a part is a stage of the ring. One thread issues a product only every ~125
 // cycles and loses ~300 to a stage's waits and commits, more than the products themselves take,
-// so three warps issue parts in turns (bf16, 768 rows: 172 us with one, 159 with three). An issuer
-// waits for a stage's or an accumulator's next phase, which says nothing while the phase before
-// it is open; so each of them belongs to one issuer: their numbers are multiples of three. e4m3
-// pieces are half as large, so three make a part (batch of 128 heads 207 -> 179 us); bf16 parts
-// of three would leave two stages (a million keys 202 -> 208 us).
-constexpr int kIssuers = 3;  // warps 1-3; warp 0 loads
+// so several warps issue parts in turns. An issuer waits for a stage's or an accumulator's next
+// phase, which says nothing while the phase before it is open; so each of them belongs to one
+// issuer: their numbers are multiples of the issuers'. At 128 rows beside Q there is room for four
+// bf16 stages and 512 columns are four accumulators, so two issuers use all of both (768 rows over
+// 131k keys: one issuer 150 us, two 131, three 145). e4m3 pieces are half as large, so three make
+// a part, and a tile's three parts are the three stages of three issuers (batch of 128 heads
+// against parts of one piece: 207 -> 179 us); bf16 parts of three would leave two stages (a
+// million keys 202 -> 208 us).
+constexpr int kMaxIssuers = 3;  // of warps 1-3; warp 0 loads
 template <bool kFp8>
 struct Parts {
-  static constexpr int kCount = kFp8 ? 3 : 9;    // parts of a score's 576 columns
-  static constexpr int kPer = kPieces / kCount;  // pieces of a part
+  static constexpr int kCount = kFp8 ? 3 : 9;     // parts of a score's 576 columns
+  static constexpr int kPer = kPieces / kCount;   // pieces of a part
+  static constexpr int kIssuers = kFp8 ? 3 : 2;
+  static constexpr bool kFixed = kCount % kIssuers == 0;  // a piece is always multiplied by the same issuer
+  static_assert(kFixed || (kPer == 1 && kIssuers == 2), "the pieces' barriers expect one of these");
 };
 constexpr int kMaxSub = 32;         // tiles of one sub-range: a loading warp holds a page id in each lane
 constexpr int kMaxSubSums = 8;      // of those when sums wait in shared memory (G > 1)
 constexpr int kThreads = 384;
 constexpr int kSmemCap = 232448;    // 227 KB per CTA
 
+// Registers of a thread at the launch, and after the warpgroup of warps 0-3 has given some to the
+// other two, whose threads hold 128 sums and two reads of 32 columns (with 208 for those some of
+// them go through memory: batch of 128 heads, e4m3, 131 -> 143 us).
+constexpr int kRegsLaunch = 168, kRegsWork = 56, kRegsWeights = 224;
+static_assert(128 * kRegsWork + 256 * kRegsWeights <= kThreads * kRegsLaunch, "the launch's registers must cover the split");
+
 struct WeightsMisc {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[kPieces], q_empty[kPieces];
-  uint64_t d_full[kMaxSlots], d_empty[kMaxSlots], mma_done[kIssuers];
+  uint64_t d_full[2][kMaxSlots], d_empty[kMaxSlots], mma_done[kMaxIssuers];
   uint32_t tmem_base;
   int abort;
-  alignas(16) float nlse[kMaxRows];    // -lse of the current group's rows
-  alignas(16) float rscale[kMaxRows];  // e4m3: each row's part of its scores' scale
-  alignas(16) int lim[kMaxRows];       // keys that each row sees
-  float half[2][kKeys];                // one warpgroup's sums of a tile, for the other
+  alignas(16) float nlse[2][kMaxRows];    // of each warpgroup's current group: -lse of the rows
+  alignas(16) float rscale[2][kMaxRows];  // e4m3: each row's part of its scores' scale
+  alignas(16) int lim[2][kMaxRows];       // keys that each row sees
   alignas(16) float sums[kMaxSubSums][kKeys];
 };
 constexpr int kMiscBytes = (sizeof(WeightsMisc) + 1023) / 1024 * 1024;
@@ -191,35 +203,47 @@ struct Walk {
 struct Ring {
   uint32_t n, at, phase;
   __device__ __forceinline__ explicit Ring(uint32_t n_) : n(n_), at(0), phase(0) {}
-  __device__ __forceinline__ void step() {
-    if (++at == n) {
-      at = 0;
+  __device__ __forceinline__ void step(uint32_t by = 1) {  // (a divisor of n, from a place below it)
+    at += by;
+    if (at >= n) {
+      at -= n;
       ++phase;
     }
   }
 };
 
+// A value that all lanes of the warp hold, as one the compiler knows to be such. Whatever a branch,
+// an address or a descriptor of the loading and issuing warps depends on comes through here or
+// through a vote: their loops are chains of single instructions, and kept in per-lane registers
+// such values slowed those warps by a tenth (768 rows over 131k bf16 keys 147 against 131 us).
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 // Rows of request b that count (its first counted[b] tokens).
 __device__ __forceinline__ int counted_rows(const WeightsParams& p, int b, int q) {
-  const int c = p.counted ? max(0, min(q, p.counted[b])) : q;
+  const int c = p.counted ? uniform(max(0, min(q, p.counted[b]))) : q;
   return c * p.H;
 }
 
-// The epilogue warpgroups (wg 0 and 1, warps of quadrant qd): rows [16 NC wg, 16 NC (wg + 1))
-// of each group, N = 32 NC. A thread owns the key of its tensor-memory lane. One warpgroup
-// hands its half of a tile's sums to the other, in turns.
+// The epilogue warpgroups (wg 0 and 1, warps of quadrant qd) take a sub-range's tiles in turns:
+// while one adds the parts of its tile, the other's exponentials are computed. A thread owns the
+// key of its tensor-memory lane and all N = 32 NC rows of the group. (With half of a tile's rows
+// each, the two were at the same work at the same time and met at a barrier after every tile:
+// 768 rows over 131k e4m3 keys 85 us, in turns 76.)
 template <int NC, bool kFp8>
 __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc* ms, Walk& walk, uint32_t tmem, int wg,
                                              int qd, int lane) {
-  constexpr int kCols = 16 * NC, n = 32 * NC;
-  const int key_in = 32 * qd + lane, col0 = kCols * wg;
-  const uint32_t acc0 = tmem + col0 + ((uint32_t)(32 * qd) << 16);
-  const float* nlse = ms->nlse + col0;
-  const float* rscale = ms->rscale + col0;
-  const int* lim = ms->lim + col0;
+  constexpr int n = 32 * NC;
+  const int key_in = 32 * qd + lane;
+  const uint32_t acc0 = tmem + ((uint32_t)(32 * qd) << 16);
+  const float* nlse = ms->nlse[wg];
+  const float* rscale = ms->rscale[wg];
+  const int* lim = ms->lim[wg];
   volatile int* abort = &ms->abort;
   Ring slots(p.slots);
-  uint32_t tiles = 0;  // tiles done so far
+  uint32_t parity = 0;  // bit i: of this warpgroup's next wait for accumulator i
   bool ok = true;
   int b, t0, t1;
   PlanRequest req;
@@ -238,92 +262,124 @@ __device__ __forceinline__ void weights_role(const WeightsParams& p, WeightsMisc
     for (int s0 = t0; s0 < t1; s0 += sub) {
       const int s1 = min(t1, s0 + sub);
       for (int g = 0; g < groups; ++g) {
-        const int mine = min(n, rows - g * n) - col0;  // rows of this warpgroup that are there (or none)
+        const int mine = min(n, rows - g * n);  // rows of the group that are there
         if (groups > 1 || s0 == t0) {
-          const int row0 = req.tok0 * p.H + g * n + col0;
+          const int row0 = req.tok0 * p.H + g * n;
           ptx::bar_sync(1 + wg, 128);  // this warpgroup is done with the old table
-          if (key_in < kCols) {
+          if (key_in < n) {
             const bool live = key_in < mine;
             const float l = live ? p.lse[row0 + key_in] : INFINITY;
-            ms->nlse[col0 + key_in] = l == -INFINITY ? -INFINITY : -l;  // a row that saw nothing adds nothing
-            if (kFp8) ms->rscale[col0 + key_in] = live ? p.sm_scale * p.q_scale[row0 + key_in] : 0.f;
-            ms->lim[col0 + key_in] = live ? req.ctx - req.q + (g * n + col0 + key_in) / p.H + 1 : 0;
+            ms->nlse[wg][key_in] = l == -INFINITY ? -INFINITY : -l;  // a row that saw nothing adds nothing
+            if (kFp8) ms->rscale[wg][key_in] = live ? p.sm_scale * p.q_scale[row0 + key_in] : 0.f;
+            ms->lim[wg][key_in] = live ? req.ctx - req.q + (g * n + key_in) / p.H + 1 : 0;
           }
           ptx::bar_sync(1 + wg, 128);
         }
         const int lim_min = req.ctx - req.q + g * n / p.H + 1;  // what the group's first row sees
-        for (int t = s0; t < s1; ++t, ++tiles) {
+        for (int t = s0; t < s1; ++t) {
+          if (((t - s0) & 1) != wg) {  // the other warpgroup's tile
+            for (int u = 0; u < Parts<kFp8>::kCount; ++u) slots.step();
+            continue;
+          }
           const int key = t * kKeys + key_in;
-          const bool live = key < req.ctx, writes = ((t - s0) & 1) == wg;
+          const bool live = key < req.ctx;
           float old = 0.f, ks = kFp8 ? p.kv_scale : p.sm_scale;  // the key's part of its scores' scale
-          if (writes && g == groups - 1 && live && p.decay != 0.f) old = wrow[key] * p.decay;
+          if (g == groups - 1 && live && p.decay != 0.f) old = wrow[key] * p.decay;
           if (kFp8 && p.kv_scales && live) {
             int id = ids[key / kPage];
             id = id >= 0 && id < p.num_pages ? id : 0;
             ks = p.kv_scales[((size_t)id * kPage + key % kPage) >> p.block_log2];
           }
-          float x[kCols];
+          float x[n], y[2][32];  // the parts' sums; 32 columns are added while the next are read
+          auto load = [&](uint32_t acc, float* to) {
+            ptx::tmem_ld16(acc, to);
+            ptx::tmem_ld16(acc + 16, to + 16);
+          };
+          auto add = [&](int c) {
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) x[j] = 0.f;
-#pragma unroll (kFp8 ? Parts<kFp8>::kCount : 1)
-          for (int u = 0; u < Parts<kFp8>::kCount; ++u, slots.step()) {
-            const uint32_t slot = slots.at;
-            if (ok) ok = warp_wait(&ms->d_full[slot], slots.phase & 1, abort, p);
-            if (ok && mine > 0) {
-              ptx::tc_fence_after();
-              float y[kCols];
-#pragma unroll
-              for (int c = 0; c < NC; ++c) ptx::tmem_ld16(acc0 + slot * n + 16 * c, y + 16 * c);
-              ptx::tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < kCols; j += 2) {
-                float2 v = make_float2(y[j], y[j + 1]);
-                if (!kFp8 || u > 0) v = ptx::add2(v, make_float2(x[j], x[j + 1]));
-                x[j] = v.x;
-                x[j + 1] = v.y;
-              }
-              ptx::tc_fence_before();
+            for (int j = 0; j < 32; j += 2) {
+              const float2 v = ptx::add2(make_float2(x[32 * c + j], x[32 * c + j + 1]),
+                                         make_float2(y[c & 1][j], y[c & 1][j + 1]));
+              x[32 * c + j] = v.x;
+              x[32 * c + j + 1] = v.y;
             }
+          };
+          auto wait = [&]() {
+            if (ok) ok = warp_wait(&ms->d_full[wg][slots.at], parity >> slots.at & 1, abort, p);
+            parity ^= 1u << slots.at;
+            ptx::tc_fence_after();
+            return acc0 + slots.at * n;
+          };
+          auto done = [&]() {
+            ptx::tc_fence_before();
             __syncwarp();
-            if (ok && lane == 0) ptx::mbar_arrive(&ms->d_empty[slot]);
+            if (ok && lane == 0) ptx::mbar_arrive(&ms->d_empty[slots.at]);
+            slots.step();
+          };
+          {
+            const uint32_t acc = wait();
+#pragma unroll
+            for (int c = 0; c < NC; ++c) load(acc + 32 * c, x + 32 * c);
+            ptx::tmem_ld_wait();
+            done();
+          }
+#pragma unroll 1
+          for (int u = 1; u < Parts<kFp8>::kCount; ++u) {
+            const uint32_t acc = wait();
+            load(acc, y[0]);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int c = 1; c < NC; ++c) {
+              load(acc + 32 * c, y[c & 1]);
+              add(c - 1);
+              ptx::tmem_ld_wait();
+            }
+            done();
+            add(NC - 1);
           }
           float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          if (ok && mine > 0) {
-            const bool all = (t + 1) * kKeys <= lim_min;  // every row sees every key of the tile
+          if (ok) {
             const float2 ks2 = make_float2(ks, ks);
+            // exp(score - lse) of rows j, j + 1; score - lse is rounded once, at its own size, before
+            // it goes to base 2: a score and an lse of 40 rounded apart would each put 2e-6 into it
+            auto weight2 = [&](int j, float2 r, float2 l) {
+              float2 v = make_float2(x[j], x[j + 1]);
+              if (kFp8) v = ptx::mul2(v, r);
+              v = ptx::fma2(v, ks2, l);
+              v = ptx::mul2(v, make_float2(1.4426950408889634f, 1.4426950408889634f));
+              return make_float2(ex2(v.x), ex2(v.y));
+            };
+            if ((t + 1) * kKeys <= lim_min && mine == n) {  // every row sees every key of the tile
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              if (16 * c >= mine) break;
-              const bool whole = all && 16 * c + 16 <= mine;
+              for (int j = 0; j < n; j += 4) {
+                const float4 r = kFp8 ? *reinterpret_cast<const float4*>(rscale + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 l = *reinterpret_cast<const float4*>(nlse + j);
+                s[0] = ptx::add2(s[0], weight2(j, make_float2(r.x, r.y), make_float2(l.x, l.y)));
+                s[1] = ptx::add2(s[1], weight2(j + 2, make_float2(r.z, r.w), make_float2(l.z, l.w)));
+              }
+            } else {
+              // a row past the group, or one that does not see this key, holds anything
 #pragma unroll
-              for (int j = 16 * c; j < 16 * c + 16; j += 2) {
-                float2 v = make_float2(x[j], x[j + 1]);
-                if constexpr (kFp8) v = ptx::mul2(v, *reinterpret_cast<const float2*>(rscale + j));
-                // score - lse is rounded once, at its own size, before it goes to base 2: a score
-                // and an lse of 40 rounded apart would each put 2e-6 into the weight
-                v = ptx::fma2(v, ks2, *reinterpret_cast<const float2*>(nlse + j));
-                v = ptx::mul2(v, make_float2(1.4426950408889634f, 1.4426950408889634f));
-                float2 e = make_float2(ex2(v.x), ex2(v.y));
-                if (!whole) {  // a row past the group, or one that does not see this key, holds anything
+              for (int c = 0; c < 2 * NC; ++c) {
+                if (16 * c >= mine) break;
+#pragma unroll
+                for (int j = 16 * c; j < 16 * c + 16; j += 2) {
+                  float2 e = weight2(j, kFp8 ? *reinterpret_cast<const float2*>(rscale + j) : make_float2(0.f, 0.f),
+                                     *reinterpret_cast<const float2*>(nlse + j));
                   e.x = key < lim[j] ? e.x : 0.f;
                   e.y = key < lim[j + 1] ? e.y : 0.f;
+                  s[(j >> 1) & 1] = ptx::add2(s[(j >> 1) & 1], e);
                 }
-                s[(j >> 1) & 1] = ptx::add2(s[(j >> 1) & 1], e);
               }
             }
           }
           float w = (s[0].x + s[1].x) + (s[0].y + s[1].y);
-          if (!writes) ms->half[tiles & 1][key_in] = w;
-          ptx::bar_sync(3, 256);  // alternate buffers: the next tile's barrier closes this one's
-          if (writes) {
-            w += ms->half[tiles & 1][key_in];
-            if (groups > 1) {
-              float* slot = &ms->sums[t - s0][key_in];  // this thread's own, through all groups
-              if (g > 0) w += *slot;
-              *slot = w;
-            }
-            if (ok && g == groups - 1 && live) wrow[key] = old + w;
+          if (groups > 1) {
+            float* slot = &ms->sums[t - s0][key_in];  // this thread's own, through all groups
+            if (g > 0) w += *slot;
+            *slot = w;
           }
+          if (ok && g == groups - 1 && live) wrow[key] = old + w;
         }
       }
     }
@@ -349,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = p.rows_n;
   const int q_piece = n * 128;                           // bytes of a Q piece (e4m3: n hi rows, then n lo rows)
   uint8_t* sK = sQ + kPieces * q_piece;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   volatile int* abort = &ms->abort;
 
   if (warp == 0 && lane == 0) {
@@ -360,13 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kPieces; ++i) {
       ptx::mbar_init(&ms->q_full[i], 1);
-      ptx::mbar_init(&ms->q_empty[i], 1);
+      ptx::mbar_init(&ms->q_empty[i], Parts<kFp8>::kFixed ? 1 : Parts<kFp8>::kIssuers);
     }
     for (int i = 0; i < p.slots; ++i) {
-      ptx::mbar_init(&ms->d_full[i], 1);
-      ptx::mbar_init(&ms->d_empty[i], 8);
+      ptx::mbar_init(&ms->d_full[0][i], 1);
+      ptx::mbar_init(&ms->d_full[1][i], 1);
+      ptx::mbar_init(&ms->d_empty[i], 4);
     }
-    for (int i = 0; i < kIssuers; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
+    for (int i = 0; i < kMaxIssuers; ++i) ptx::mbar_init(&ms->mma_done[i], 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmap_q);
     ptx::prefetch_tmap(&tmap_kv);
@@ -377,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ms->tmem_base;
+  const uint32_t tmem = uniform(ms->tmem_base);
   Walk walk;
   walk.start(p);
   int b, t0, t1;
@@ -388,6 +445,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kFp8) ptx::tma_load_3d(sQ + c * q_piece + n * 64, &tmap_q, &ms->q_full[c], 0, p.total_rows + row, c);
   };
 
+  if (warp < 4) {
+    ptx::regs_down<kRegsWork>();
+  } else {
+    ptx::regs_up<kRegsWeights>();
+  }
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
@@ -471,18 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncwarp();
-  } else if (warp <= kIssuers) {
+  } else if (warp <= R::kIssuers) {
     // ------------------------------------------------------------ products
-    // Warp 1 + i issues parts i, i + 3, .. Each accumulator is written by one thread in order,
-    // so the sums repeat.
+    // The issuers take the parts in turns. Each accumulator is written by one thread in order, so
+    // the sums repeat. Where a piece of Q is not always the same issuer's, each of them waits for
+    // all new pieces, and says of each when its products with it are over.
     const uint32_t sq = ptx::smem_addr(sQ), sk = ptx::smem_addr(sK);
     const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kKeys, n, 0, 0) : ptx::idesc_bf16(kKeys, n, 0, 0);
     const int u0 = warp - 1;
     Ring ring(p.stages), slots(p.slots);
-    for (int i = 0; i < u0; ++i) {
-      ring.step();
-      slots.step();
-    }
+    ring.at = slots.at = u0;
+    int first = u0;  // this issuer's first part of the tile
     uint32_t qphase = 0;
     bool ok = true, issued = false, loaded = false;
     if (kFp8) ptx::pdl_wait_primary();  // Q's parts come from the kernel before
@@ -491,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (groups == 0 || t0 >= t1) continue;
       // the first group's Q: each issuer its own pieces, while warp 0 asks for the keys
       if (!loaded && ptx::elect_one())
-        for (int u = u0; u < R::kCount; u += kIssuers)
+        for (int u = u0; u < R::kCount; u += R::kIssuers)
           for (int c = kPer * u; c < kPer * (u + 1); ++c) load_q(c, req.tok0 * p.H);
       __syncwarp();
       loaded = true;
@@ -501,12 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g = 0; ok && g < groups; ++g) {
           const bool new_q = groups > 1 || s0 == t0, last_q = groups > 1 || s1 == t1;
           for (int t = s0; ok && t < s1; ++t) {
-            for (int u = u0; ok && u < R::kCount; u += kIssuers) {
-              // what the accumulator held has been read
-              if (slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
+            const bool last = last_q && t == s1 - 1;  // the group's last products
+            const bool fresh = new_q && t == s0;      // and its first
+            int u = first;
+            for (; ok && u < R::kCount; u += R::kIssuers) {
               const int c0 = kPer * u;
-              for (int c = c0; ok && new_q && t == s0 && c < c0 + kPer; ++c)
-                ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
+              if (fresh) {
+                for (int c = R::kFixed || u == 0 ? c0 : c0 - 1; ok && c < c0 + kPer; ++c)
+                  ok = warp_wait(&ms->q_full[c], qphase & 1, abort, p);
+              }
+              // what the accumulator held has been read
+              if (ok && slots.phase > 0) ok = warp_wait(&ms->d_empty[slots.at], (slots.phase - 1) & 1, abort, p);
               if (ok) ok = warp_wait(&ms->kv_full[ring.at], ring.phase & 1, abort, p);
               if (!ok) break;
               ptx::tc_fence_after();
@@ -529,16 +595,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
                 ptx::mma_commit(&ms->kv_empty[ring.at]);
-                if (last_q && t == s1 - 1)
+                if (last) {
                   for (int j = 0; j < kPer; ++j) ptx::mma_commit(&ms->q_empty[c0 + j]);
-                ptx::mma_commit(&ms->d_full[slots.at]);
+                  if (!R::kFixed && u > 0) ptx::mma_commit(&ms->q_empty[c0 - 1]);
+                }
+                ptx::mma_commit(&ms->d_full[(t - s0) & 1][slots.at]);
               }
               __syncwarp();
               issued = true;
-              for (int i = 0; i < kIssuers; ++i) {  // past the other issuers' parts
-                ring.step();
-                slots.step();
-              }
+              ring.step(R::kIssuers);
+              slots.step(R::kIssuers);
+            }
+            first = u - R::kCount;
+            if (!R::kFixed && first == 0) {  // another issuer had the last piece
+              if (ok && fresh) ok = warp_wait(&ms->q_full[kPieces - 1], qphase & 1, abort, p);
+              if (ok && last && ptx::elect_one()) ptx::mma_commit(&ms->q_empty[kPieces - 1]);
+              __syncwarp();
             }
           }
           if (new_q) ++qphase;
@@ -641,6 +713,12 @@ cudaError_t set_weights_kernel_attributes() {
   cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(key_weights_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
+  // a build that launches with fewer registers than the warpgroups share out would wait for them forever
+  for (const void* fn : {(const void*)key_weights_kernel<false>, (const void*)key_weights_kernel<true>}) {
+    cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, fn);
+    if (e == cudaSuccess && a.numRegs < kRegsLaunch) e = cudaErrorInvalidKernelImage;
+  }
   return e;
 }
 
@@ -710,7 +788,8 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   const int piece = fp8 ? 8192 : 16384, tile_bytes = kPieces * piece;
   const int fixed = 1024 + kMiscBytes + kPieces * most_rows * 128;
   const int per = fp8 ? Parts<true>::kPer : Parts<false>::kPer;
-  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / (per * piece)) / kIssuers * kIssuers;
+  const int issuers = fp8 ? Parts<true>::kIssuers : Parts<false>::kIssuers;
+  const int stages = std::min(kMaxStages, (kSmemCap - fixed) / (per * piece)) / issuers * issuers;
   const int smem = fixed + stages * per * piece;
   auto fn = fp8 ? key_weights_kernel<true> : key_weights_kernel<false>;
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -743,9 +822,11 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   prm.kv_scale = kv_scale;
   prm.rows_n = most_rows;
   prm.stages = stages;
-  prm.slots = std::min(kMaxSlots, 512 / most_rows) / kIssuers * kIssuers;
-  // tiles that all CTAs together keep in L2 while the groups pass over them
-  prm.sub_tiles = std::max(1, std::min<int>(kMaxSubSums, (int)((80LL << 20) / ((long long)tile_bytes * grid))));
+  prm.slots = std::min(kMaxSlots, 512 / most_rows) / issuers * issuers;
+  // tiles that all CTAs together keep in L2 while the groups pass over them: 2 (bf16) and 4 (e4m3)
+  // give 149 and 82 us for 768 rows over 131k keys, 4 and 8 give 145 and 77
+  // (an even number, as two warpgroups take turns)
+  prm.sub_tiles = std::max(2, std::min<int>(kMaxSubSums, (int)((90LL << 20) / ((long long)tile_bytes * grid))) / 2 * 2);
   prm.status = status_dev;
   prm.wait_budget = h->debug_skip_copy > 0 ? kWaitBudgetTest : kWaitBudget;
   prm.skip_copy = h->debug_skip_copy - 1;
