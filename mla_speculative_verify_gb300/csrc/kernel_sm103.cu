@@ -353,6 +353,10 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
   for (int i = 0; i < NC; ++i) l_acc[i] = 0.f;
 #pragma unroll
   for (int i = 0; i < (kFp8 ? NP : 1); ++i) rref[i] = -INFINITY;
+  // kScaled holds the references negated, as its sums of pairs want them
+  float nref[kScaled ? NP : 1];
+#pragma unroll
+  for (int i = 0; i < (kScaled ? NP : 1); ++i) nref[i] = INFINITY;
   // e4m3: the columns' score scales (fixed for the unit; the barrier above published them)
   float csr[kFp8 ? NP : 1];
 #pragma unroll
@@ -373,6 +377,15 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
     const int sb = t & 1;
     float inv_ks[2];  // kScaled: 1 / v of this thread's two keys
     float x[NC];
+    float xr[kScaled ? NC : 1];  // kScaled: x relative to the references
+    auto relative = [&]() {
+#pragma unroll
+      for (int i = 0; i < NC; i += 2) {
+        const float2 v = ptx::add2(make_float2(x[i], x[i + 1]), make_float2(nref[2 * (i / 4)], nref[2 * (i / 4) + 1]));
+        xr[kScaled ? i : 0] = v.x;
+        xr[kScaled ? i + 1 : 0] = v.y;
+      }
+    };
     bool need = false;
     bool unmasked = false;  // this tile: every key visible to every row
     // S^T(t): e4m3 buffer t % 2; bf16 the one buffer (its phase flips every tile)
@@ -433,9 +446,21 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
             x[e + 1] = v.y;
           }
         }
+        if (!unmasked) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            const int key = key0 + 8 * ((i >> 1) & 1);
+            x[i] = (key < a.kv_end && key < ms->lim[16 * (i / 4) + cp + (i & 1)]) ? x[i] : -INFINITY;
+          }
+        }
+        relative();
+        float top = xr[0];  // (a masked score before a reference is set gives a NaN, which fmaxf passes over)
+#pragma unroll
+        for (int i = 1; i < NC; ++i) top = fmaxf(top, xr[kScaled ? i : 0]);
+        need = top > kMoveAbove;
       }
 #pragma unroll
-      for (int c = 0; c < NCH; ++c) {
+      for (int c = 0; c < (kScaled ? 0 : NCH); ++c) {
         const int n0 = 16 * c + cp;
         float rrv[4];
         ref4(c, rrv);
@@ -446,7 +471,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float v = kScaled ? x[4 * c + j] : x[4 * c + j] * csv[j];
+          float v = x[4 * c + j] * csv[j];
           const int key = key0 + 8 * (j >> 1);
           if (!unmasked) v = (key < a.kv_end && key < ms->lim[n0 + (j & 1)]) ? v : -INFINITY;
           x[4 * c + j] = v;
@@ -482,6 +507,11 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
 #pragma unroll
         for (int i = 0; i < NP; ++i) rref[i] = ms->ref[16 * (i / 2) + cp + (i % 2)];
       }
+      if constexpr (kScaled) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) nref[i] = -rref[i];
+        relative();
+      }
       if (t >= 1) {
         // this warp: value blocks 2 grp and 2 grp + 1 of its lane quadrant
         fail = !warp_wait(&ms->pt_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort, p);
@@ -516,13 +546,12 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         float rrv[4];
-        ref4(c, rrv);
-        if (kScaled && unmasked) {
+        if constexpr (!kScaled) ref4(c, rrv);
+        if constexpr (kScaled) {
 #pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            const float2 v = ptx::add2(make_float2(x[4 * c + j], x[4 * c + j + 1]), make_float2(-rrv[j], -rrv[j + 1]));
-            pv[4 * c + j] = ex2(v.x);
-            pv[4 * c + j + 1] = ex2(v.y);
+          for (int j = 0; j < 4; ++j) {
+            const float e = ex2(xr[4 * c + j]);
+            pv[4 * c + j] = unmasked || x[4 * c + j] != -INFINITY ? e : 0.f;
           }
         } else if (unmasked) {  // no masked score (a reference may still be -inf: then a move follows)
 #pragma unroll
