@@ -120,8 +120,8 @@ struct Geo {
 //          own (the softmax adds the three); O^T is issued by four of the softmax warps,
 //          one value block each (it is on the critical path of the two-stage page ring)
 //   e4m3:  two S^T warps that take alternate pages (all K-steps of a page each); value
-//          blocks 0 and 1 of O^T come from an O^T warp, blocks 2 and 3 from the producer
-//          warp, just before it waits for the page's slot to refill it (the softmax warps
+//          blocks 0 and 1 (block scales: and 2) of O^T come from an O^T warp, the others from the
+//          producer warp, just before it waits for the page's slot to refill it (the softmax warps
 //          are the busiest role there, and twelve warps keep ~170 registers per thread)
 template <bool kFp8>
 struct Roles {
@@ -810,6 +810,10 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
   const int nmma = (nrows + 15) & ~15;   // MMA N (rows rounded up to 16)
   const int nch = nmma / 16;             // 16-column chunks of S^T / O^T
   const uint32_t tmem = ms->tmem_base;
+  // e4m3: value blocks of O^T that the O^T warp issues; the producer issues the others. With block
+  // scales to prepare the producer is the slower one: 2^20 keys, q = 8, with 2 blocks of the warp's
+  // 256 us, 3: 237, 4: 236 (32 requests of 16k-32k keys 242, 226, 230).
+  constexpr int kWarpBlocks = kScaled ? 3 : 2;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -832,7 +836,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
         return pid;
       };
       auto load_ids = [&](int t0) { return checked(t0 + lane < ntiles ? pt_row[t0 + lane] : 0, t0 + lane); };
-      // e4m3: O^T(u) += V^T . P^T(u) for value blocks 2 and 3, once P^T(u) is written (the
+      // e4m3: O^T(u) += V^T . P^T(u) for the value blocks from kWarpBlocks on, once P^T(u) is written (the
       // whole warp waits, lane 0 issues)
       auto producer_ot = [&](int u) -> int {
         if (!warp_wait(&ms->p_full[u & 1], (u >> 1) & 1, abort, p)) return 0;
@@ -840,7 +844,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
         if (lane == 0) {
           const uint32_t skv = ptx::smem_addr(sKv), spt = ptx::smem_addr(sPt);
 #pragma unroll
-          for (int blk = 2; blk < 4; ++blk)
+          for (int blk = kWarpBlocks; blk < 4; ++blk)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -876,8 +880,8 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
           const int tp = i + S;  // the page after the ring (index relative to t0)
           const int page_pf = __shfl_sync(0xffffffffu, tp < 32 ? pid_cur : pid_next, tp & 31);
           const int t = t0 + i, slot = t % S;
-          // e4m3: this warp also issues value blocks 2 and 3 of O^T(t - S), the page whose
-          // slot the copy of page t reuses (blocks 0 and 1 come from the O^T warp). The
+          // e4m3: this warp also issues its value blocks of O^T(t - S), the page whose slot
+          // the copy of page t reuses (the others come from the O^T warp). The
           // waits are the whole warp's; lane 0 issues.
           bool ok = true;
           if (kFp8 && t >= S) ok = producer_ot(t - S) != 0;
@@ -922,7 +926,7 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
         pid_cur = pid_next;
         pid_next = (t0 + 64 < ntiles) ? load_ids(t0 + 64) : 0;
       }
-      // e4m3: blocks 2 and 3 of O^T for the last S pages (no copy follows them)
+      // e4m3: this warp's blocks of O^T for the last S pages (no copy follows them)
       if (kFp8 && issued == ntiles) {
         int ok = 1;
         for (int u = max(0, ntiles - S); ok && u < ntiles; ++u) ok = producer_ot(u);
@@ -1000,16 +1004,15 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
         issued = true;
       }
     } else if constexpr (kFp8) {
-      // e4m3: O^T(t) += V^T . P^T(t) for value blocks 0 and 1 (the producer issues 2 and 3),
+      // e4m3: O^T(t) += V^T . P^T(t) for the first kWarpBlocks value blocks (the producer issues the others),
       // once the softmax warps have written P^T(t)
-      const int ow = mi - Roles<kFp8>::kSWarps;  // 0
       for (int t = 0; ok && t < ntiles; ++t) {
         ok = warp_wait(&ms->p_full[t & 1], (t >> 1) & 1, abort, p);
         if (!ok) break;
         ptx::tc_fence_after();
         if (lane == 0) {
 #pragma unroll
-          for (int blk = 2 * ow; blk < 2 * ow + 2; ++blk)
+          for (int blk = 0; blk < kWarpBlocks; ++blk)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
