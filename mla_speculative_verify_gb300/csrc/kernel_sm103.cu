@@ -482,7 +482,8 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
     // Moving the references (rare once a row has seen its largest scores): column maxima
     // over this tile's keys (the quadrant's 16 keys: 2 per thread, 8 threads per column),
     // each row's reference up to its maximum, l and O^T (tiles < t, once PV(t-1) is done)
-    // rescaled by alpha.
+    // rescaled by alpha. With block scales O^T follows after P^T(t) has been written, so that
+    // PV(t-1) ends meanwhile.
     auto move_refs = [&]() {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -512,6 +513,8 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
         for (int i = 0; i < NP; ++i) nref[i] = -rref[i];
         relative();
       }
+    };
+    auto rescale_o = [&]() {
       if (t >= 1) {
         // this warp: value blocks 2 grp and 2 grp + 1 of its lane quadrant
         fail = !warp_wait(&ms->pt_empty[(t - 1) & 1], ((t - 1) >> 1) & 1, abort, p);
@@ -607,12 +610,17 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
       // e4m3: the vote comes first, then P^T; the O^T warp issues O^T(t) once all softmax
       // warps have arrived (a warp that gave up a wait leaves the loop with the others at
       // the next tile's vote)
+      bool moved = false;
       if (softmax_any(need || fail)) {
         if (softmax_any(fail || *abort != 0)) {
           stop = true;
           break;
         }
         move_refs();
+        if (kScaled)
+          moved = true;
+        else
+          rescale_o();
       }
       if (!fail) {
         make_p();
@@ -633,8 +641,12 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
           }
         }
         store_p();
+        if (kScaled && moved) {
+          rescale_o();
+          ptx::tc_fence_before();
+        }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&ms->p_full[sb]);
+        if ((!kScaled || !fail) && lane == 0) ptx::mbar_arrive(&ms->p_full[sb]);
       }
       continue;
     }
@@ -654,6 +666,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
         break;
       }
       move_refs();
+      rescale_o();
       if (!fail) {
         make_p();
         store_p();
