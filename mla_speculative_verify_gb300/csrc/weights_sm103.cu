@@ -39,11 +39,11 @@
 // 8-11 take the scores out, a tile each in turns. All of them walk the same work list
 // (Walk). Waits are bounded as in the decode kernel.
 //
-// Measured: 96 rows over 1M bf16 keys 204 us, 5.9 TB/s, 0.87 of the measured copy rate: bound by
-// HBM, and by the slowest of 152 equal shares. 128 to 512 rows over 32 x 8k-16k e4m3 keys 129 us:
-// bound by the products' operand reads (128 rows x 128 keys read shared memory as long as they
-// compute, and the keys' arrival and the rows' tables want it too; without the keys' copies it is
-// 109); HBM would need 38 us and the products 86.
+// Measured: 96 rows over 1M bf16 keys 188 us, 6.4 TB/s, 0.95 of the measured copy rate: bound by
+// HBM. 128 to 512 rows over 32 x 8k-16k e4m3 keys 125 us: bound by the products' operand reads
+// (128 rows x 128 keys read shared memory as long as they compute, and the keys' arrival and the
+// rows' tables want it too; without the keys' copies it is 109); HBM would need 38 us and the
+// products 86.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -481,14 +481,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = s0; ok && t < s1; ++t) {
             const bool two = 2 * t + 1 < npages;  // (the last tile may have one page)
             const int id0 = __shfl_sync(0xffffffffu, cur0, t - s0), id1 = __shfl_sync(0xffffffffu, cur1, t - s0);
-            // ask L2 for the whole pages of the next tile that HBM has to deliver
-            const bool in = t + 1 < s1;
-            const int tn = g == 0 && in ? t + 1 : g == groups - 1 && !in ? s1 : t1;
-            const int next0 = __shfl_sync(0xffffffffu, in ? cur0 : nxt0, in ? t + 1 - s0 : 0);
-            const int next1 = __shfl_sync(0xffffffffu, in ? cur1 : nxt1, in ? t + 1 - s0 : 0);
-            if (tn < t1 && ptx::elect_one()) {
-              ptx::tma_prefetch_l2_3d(&tmap_page, 0, next0 * kPage, 0);
-              if (2 * tn + 1 < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, next1 * kPage, 0);
+            // A ring of one e4m3 tile: ask L2 for the whole pages of the next tile that HBM has to
+            // deliver. 512k keys, 96 rows: 61 us, without 66; where the ring holds two tiles (64
+            // rows) the requests only stand in the copies' way, 59 against 56; with bf16 parts
+            // they do at any size (96 rows 110 against 101, 128 rows 117 against 106).
+            if (kFp8 && p.stages == R::kIssuers) {
+              const bool in = t + 1 < s1;
+              const int tn = g == 0 && in ? t + 1 : g == groups - 1 && !in ? s1 : t1;
+              const int next0 = __shfl_sync(0xffffffffu, in ? cur0 : nxt0, in ? t + 1 - s0 : 0);
+              const int next1 = __shfl_sync(0xffffffffu, in ? cur1 : nxt1, in ? t + 1 - s0 : 0);
+              if (tn < t1 && ptx::elect_one()) {
+                ptx::tma_prefetch_l2_3d(&tmap_page, 0, next0 * kPage, 0);
+                if (2 * tn + 1 < npages) ptx::tma_prefetch_l2_3d(&tmap_page, 0, next1 * kPage, 0);
+              }
             }
             for (int c0 = 0; ok && c0 < kPieces; c0 += kPer) {
               for (int c = c0; new_q && qfill > 0 && t == s0 && c < c0 + kPer; ++c) {
@@ -823,10 +828,12 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
   prm.rows_n = most_rows;
   prm.stages = stages;
   prm.slots = std::min(kMaxSlots, 512 / most_rows) / issuers * issuers;
-  // tiles that all CTAs together keep in L2 while the groups pass over them: 2 (bf16) and 4 (e4m3)
-  // give 149 and 82 us for 768 rows over 131k keys, 4 and 8 give 145 and 77
-  // (an even number, as two warpgroups take turns)
-  prm.sub_tiles = std::max(2, std::min<int>(kMaxSubSums, (int)((90LL << 20) / ((long long)tile_bytes * grid))) / 2 * 2);
+  // Tiles that all CTAs together keep in L2 while the groups pass over them, an even number as two
+  // warpgroups take turns. Where HBM refills L2 meanwhile, less than half of it: 32 requests of 16k
+  // keys, 512 rows, bf16 325 us at 90 MB, 312 at 50 (e4m3 223, 213). Keys that all fit stay there
+  // anyhow, and longer passes load Q less often (768 rows over 131k e4m3 keys 72 us, 79 at 50 MB).
+  const long long room = tiles * tile_bytes <= (80LL << 20) ? 90LL << 20 : 50LL << 20;
+  prm.sub_tiles = std::max(2, std::min<int>(kMaxSubSums, (int)(room / ((long long)tile_bytes * grid))) / 2 * 2);
   prm.status = status_dev;
   prm.wait_budget = h->debug_skip_copy > 0 ? kWaitBudgetTest : kWaitBudget;
   prm.skip_copy = h->debug_skip_copy - 1;
