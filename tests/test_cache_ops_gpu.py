@@ -698,3 +698,85 @@ def test_a_server_step(block):
         torch.cuda.synchronize()
         for a, b in zip(got, (out, out2, w, kept, lens_dst, codes, scales)):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------------------- passes and turns
+@pytest.mark.parametrize("splits", [1, 3])
+def test_decode_scaled_scores_that_keep_rising(splits):
+    """Every page's scores exceed all before it by octaves, so every tile moves the references."""
+    batch = ref.Batch(12, [64 * 30 + 5], [8], "e4m3", 64, spread=0.0, seed=41)
+    for t in range(30):
+        batch.scales[batch.table[0][t], 0] = 0.04 * (t + 1)
+    want, bound, lse, lse_bound = ref.attend(batch)
+    _, _, out, got_lse = decode(batch, binding.PlanOptions(force_splits=splits))
+    assert (np.abs(got_lse.cpu().double().numpy() - lse) <= lse_bound).all()
+    assert (np.abs(out.cpu().double().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("kind,block", [("bf16", 0), ("e4m3", 16)])
+@pytest.mark.parametrize("heads,q", [(16, 2), (24, 2), (80, 1), (128, 1), (128, 3), (100, 7)])
+def test_key_weights_every_group_size(heads, q, kind, block):
+    """32, 64, 96 and 128 rows to a group, one group or several, over one to eight tiles a request."""
+    seq = [7, 128, 129, 400, 520, 769, 1000, 300]
+    batch = ref.Batch(heads, seq, [q] * len(seq), kind, block, seed=heads + q)
+    old = np.random.default_rng(2).random((len(seq), max(seq)))
+    counted = [q, q, 1, q, 0, q, max(1, q - 1), q]
+    w, lse = run_weights(batch, 0.5, old, counted)
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 0.5, old, counted)
+    got = w.cpu().double().numpy()
+    for b, n in enumerate(seq):
+        assert (np.abs(got[b, :n] - want[b, :n]) <= bound[b, :n] + 1e-30).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("total", [20000, 170000])
+def test_key_weights_of_a_batch_are_those_of_its_requests(kind, total):
+    """A key's sum is taken in the same order whatever the batch around it: requests alone, in few
+    and in many tiles at a time, give the batch's bits. (Caches that fit L2, and that do not.)"""
+    n = [total // 8 + 37 * i for i in range(8)]
+    heads, q = 48, 8  # three groups of rows
+    per = [-(-k // 64) for k in n]
+    g = torch.Generator(device="cuda").manual_seed(43)
+    kv = torch.randn((sum(per), 64, 576), generator=g, device="cuda").to(torch.bfloat16)
+    if kind == "fp8":
+        kv = kv.to(torch.float8_e4m3fn)
+    pages = torch.randperm(sum(per), generator=g, device="cuda").int()
+    table = torch.zeros((8, max(per)), dtype=torch.int32, device="cuda")
+    for b in range(8):
+        table[b, :per[b]] = pages[sum(per[:b]):sum(per[:b + 1])]
+    queries = torch.randn((8 * q, heads, 576), generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.empty((8 * q, heads, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((8 * q, heads), device="cuda")
+    d = VerifyDecoder(n, [q] * 8, heads, kind)
+    d.run(queries, kv, table, out, lse)
+    w = torch.zeros((8, max(n)), device="cuda")
+    d.key_weights(queries, kv, table, lse, w)
+    again = torch.zeros((8, max(n)), device="cuda")
+    d.key_weights(queries, kv, table, lse, again)
+    assert torch.equal(w, again)
+    for b in range(8):
+        rows = slice(b * q, b * q + q)
+        one = VerifyDecoder([n[b]], [q], heads, kind)
+        alone = torch.zeros((1, n[b]), device="cuda")
+        one.key_weights(queries[rows], kv, table[b:b + 1], lse[rows], alone)
+        assert torch.equal(alone[0], w[b, :n[b]])
+        assert abs(w[b].double().sum().item() / (heads * q) - 1) < 1e-4
+        assert (w[b, n[b]:] == 0).all()
+
+
+@pytest.mark.parametrize("kind,block,q", [("bf16", 0, 4), ("e4m3", 16, 4)])
+def test_timeouts_with_several_groups_of_rows(kind, block, q):
+    """As above with three groups of rows, where pieces of Q pass between the issuing warps."""
+    batch = ref.Batch(96, [64 * 20 + 7], [q], kind, block, seed=44)
+    _, t, _, lse = decode(batch)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bad = VerifyDecoder(batch.seq_lens, batch.q_lens, 96, "bf16" if kind == "bf16" else "fp8",
+                        options=binding.PlanOptions(force_splits=4, debug_skip_copy=8))
+    bad.key_weights(t["q"], t["kv"], t["table"], lse, torch.zeros((1, 1287), device="cuda"), kv_scales=t["scales"],
+                    status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) & binding.MLA_DEVICE_WAIT_TIMEOUT
+    old = np.zeros((1, 1287))
+    w, lse = run_weights(batch, 1.0, old)
+    want, bound = ref.weights(batch, lse.cpu().double().numpy(), 1.0, old)
+    assert (np.abs(w.cpu().double().numpy() - want) <= bound + 1e-30).all()
