@@ -40,7 +40,7 @@
 // (Walk). Waits are bounded as in the decode kernel.
 //
 // Measured: 96 rows over 1M bf16 keys 188 us, 6.4 TB/s, 0.95 of the measured copy rate: bound by
-// HBM. 128 to 512 rows over 32 x 8k-16k e4m3 keys 125 us: bound by the products' operand reads
+// HBM. 128 to 512 rows over 32 x 8k-16k e4m3 keys 130 us: bound by the products' operand reads
 // (128 rows x 128 keys read shared memory as long as they compute, and the keys' arrival and the
 // rows' tables want it too; without the keys' copies it is 109); HBM would need 38 us and the
 // products 86.
