@@ -51,8 +51,9 @@
 //
 // For an e4m3 cache the products run on kind::f8f6f4 MMAs straight from the cached
 // codes: each Q row is scaled by a power of two and split into two e4m3 parts (hi and
-// lo), and P into two e4m3 parts as well, so no page is ever expanded to bf16 and the
-// only rounding beyond fp32 accumulation is that of the lo parts (~2^-8 relative).
+// lo), and P into an e4m3 part and its remainder in e5m2, so no page is ever expanded to
+// bf16 and the only rounding beyond fp32 accumulation is that of the lo parts (P: 2^-8
+// relative; split_p below says how small P are held).
 //
 // Every mbarrier wait is bounded; on expiry the kernel ORs MLA_DEVICE_WAIT_TIMEOUT into
 // the status word, stops the unit, drains its in-flight copies and frees its TMEM.
@@ -88,7 +89,7 @@ static_assert(kChunks * kQ8ChunkBytes <= kQBytes, "e4m3 Q fits the Q region");
 constexpr int kKvChunkBytes = kTileKeys * 128;     // 8192 (bf16 page chunk: 64 keys x 64 columns)
 constexpr int kSlotBytes = kChunks * kKvChunkBytes;  // 73728 (bf16 page)
 constexpr int kKvBytes = 2 * kSlotBytes;           // page ring: two bf16 stages or four e4m3 stages
-constexpr int kPtBytes = kTileKeys * 128;          // P^T tile: 64 keys x (<= 64 rows) bf16, or e4m3 hi + lo
+constexpr int kPtBytes = kTileKeys * 128;          // P^T tile: 64 keys x (<= 64 rows) bf16, or 8-bit hi + lo
 constexpr int kOffQ = 0;
 constexpr int kOffKv = kOffQ + kQBytes;
 constexpr int kOffPt = kOffKv + kKvBytes;
@@ -138,9 +139,9 @@ constexpr uint32_t kTmemS = 256;
 constexpr float kRefSlack = 8.0f;    // octaves a score may exceed the row reference before it moves
 // e4m3 path: a smaller slack (p <= 16) so that P can be stored times 2^4 (<= 256 < 448,
 // the largest e4m3); probabilities down to 2^-10 of the reference stay in e4m3's normal
-// range, smaller ones keep an absolute error below 2^-14. The 2^4 is applied by keeping
-// the stored reference kPShiftFp8 octaves below the row's reference, so exp2(s - ref) is
-// already P times 2^4; l carries the same factor, which cancels in O / l and in the LSE.
+// range (split_p has the smaller ones). The 2^4 is applied by keeping the stored reference
+// kPShiftFp8 octaves below the row's reference, so exp2(s - ref) is already P times 2^4; l
+// carries the same factor, which cancels in O / l and in the LSE.
 constexpr float kRefSlackFp8 = 4.0f;
 constexpr float kPShiftFp8 = 4.0f;
 struct Misc {
@@ -172,17 +173,34 @@ __device__ __forceinline__ float round_to_e4m3_precision(float x) {
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-// Two fp32 values (<= 448) -> hi and lo e4m3 pairs with hi + lo ~ the values: through f16x2
-// (11 significant bits, more than hi + lo keep), hi = the e4m3 rounding, lo = the e4m3
-// rounding of the f16 remainder. Each result holds the first value in its low byte.
-__device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+// Two P of one key (<= 256; P times 2^kPShiftFp8) -> an e4m3 part (hi) and the remainder in
+// e5m2 (lo), through f16x2 (11 significant bits, and exact down to 2^-25). Each result holds
+// the first value in its low byte.
+//
+// From 2^-6 on, where e4m3 is normal, lo is rounded to nearest and hi + lo is within 2^-8 of P.
+// Below that hi ends on its grid of 2^-9 and lo has only its own 3 bits left, and what counts is
+// the sum over many keys: a few strong keys beside a long, nearly flat rest, each of it 2^-15 of
+// the largest, the rest as heavy as they are. Rounded to nearest, equal small P would all be off
+// by the same up to 1/8 (with both parts in e4m3 everything below 2^-10 was lost: half of the
+// output over 64k keys). So there lo is rounded up or down by comparing what is cut with a
+// number that the key's position gives: f16's upper byte is an e5m2, so adding d in [0, 256) to
+// the f16's bits and taking that byte rounds up with d's odds. d runs through a sequence that is
+// evenly spread over any stretch of keys (multiples of the golden ratio, modulo 1), so the errors
+// of a sum's keys cancel (64k flat keys beside a strong one: output off by 1.8e-3, its own bf16
+// rounding), and equal calls give equal bits. It costs 1 to 2 % (2^20 keys, q = 8: block scales
+// 220 -> 223 us, one scale 220 -> 225).
+constexpr uint32_t kDitherStep = 0x9E3779B1u;  // 2^32 times the golden ratio's fraction, odd
+__device__ __forceinline__ uint32_t dither_of(uint32_t at) { return __byte_perm(at, 0u, 0x4343u); }  // at's top byte, in both halves
+__device__ __forceinline__ void split_p(float a, float b, uint32_t dither, uint32_t& hi, uint32_t& lo) {
   const __half2 w = __floats2half2_rn(a, b);
   const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&w), __NV_SATFINITE,
                                                            __NV_E4M3);
   const __half2_raw hb = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
   const __half2 r = __hsub2(w, *reinterpret_cast<const __half2*>(&hb));
+  const uint32_t normal = __hge2_mask(w, __half2half2(__ushort_as_half(0x2400)));  // >= 2^-6
+  const uint32_t bits = *reinterpret_cast<const uint32_t*>(&r) + ((normal & 0x00800080u) | (~normal & dither));
   hi = (uint32_t)h;
-  lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E4M3);
+  lo = __byte_perm(bits, 0u, 0x4431u);  // the upper bytes
 }
 // Byte offset of (row, column) in a 64-byte-swizzled e4m3 region with 64-byte rows.
 __device__ __forceinline__ int sw64_offset(int row, int col) {
@@ -209,11 +227,11 @@ __device__ __forceinline__ void issue_ot_block_bf16(uint32_t tmem, uint32_t skv,
   }
 }
 // e4m3: one MMA of O^T += V^T . P^T(t): value block blk, K-step k (32 keys), P^T part
-// (0 = hi, 1 = lo; each 64 keys x 64 bytes).
+// (0 = hi, e4m3; 1 = lo, e5m2; each 64 keys x 64 bytes).
 __device__ __forceinline__ void issue_ot_mma_e4m3(uint32_t tmem, uint32_t skv, uint32_t spt, int t, int nmma, int blk,
                                                   int k, int part) {
   using G = Geo<true>;
-  const uint32_t idesc_o = ptx::idesc_e4m3(128, nmma, 1, 1);
+  const uint32_t idesc_o = ptx::idesc_e4m3(128, nmma, 1, 1) | (part ? ptx::kB_E5M2 : 0u);
   const uint32_t pt0 = spt + (t & 1) * kPtBytes;
   const uint32_t v0 = skv + (t % G::kStages) * G::kSlot + 2 * blk * G::kChunkBytes;
   const uint64_t ad = ptx::smem_desc(v0 + 2048 * k, G::kChunkBytes, 512, ptx::kSwizzle64B);
@@ -249,7 +267,7 @@ struct SoftmaxArgs {
 // page: looked up by every softmax thread for its two keys they cost the busiest role ~100
 // instructions a tile (1M keys q=8 301 us). Pairs of columns share fp32 instructions, and the
 // scores are taken relative to the references once, for the vote and for the weights (268 -> 256
-// us with one maximum for the vote). Now 220 us: 0.51 of the measured copy rate, bound by this
+// us with one maximum for the vote). Now 223 us: 0.40 of the measured copy rate, bound by this
 // chain of steps, ~1400 of a tile's 2000 cycles.
 template <int NCH, bool kFp8, bool kScaled>
 __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params& p) {
@@ -544,11 +562,13 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
       }
     };
     // probabilities relative to the current references (pv, kept until l takes them),
-    // packed to bf16, or for the e4m3 path times 2^4 and split into hi + lo e4m3 parts
+    // packed to bf16, or for the e4m3 path times 2^4 and split into hi + lo parts
     float pv[NC];
     uint32_t pk[NC / 2];           // bf16: pk[2 c + k] = the 2 columns of key kr0 + 8 k in chunk c
     uint32_t ph[NC / 2], pl[NC / 2];  // e4m3: the same pairs as hi and lo bytes (low 16 bits)
     auto make_p = [&]() {
+      const uint32_t at = kDitherStep * (uint32_t)(a.kv_begin + t * kTileKeys + kr0);
+      const uint32_t dither[2] = {dither_of(at), dither_of(at + 8 * kDitherStep)};  // e4m3: of the two keys
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         float rrv[4];
@@ -570,8 +590,8 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
           }
         }
         if constexpr (kFp8) {
-          split_e4m3x2(pv[4 * c], pv[4 * c + 1], ph[2 * c], pl[2 * c]);
-          split_e4m3x2(pv[4 * c + 2], pv[4 * c + 3], ph[2 * c + 1], pl[2 * c + 1]);
+          split_p(pv[4 * c], pv[4 * c + 1], dither[0], ph[2 * c], pl[2 * c]);
+          split_p(pv[4 * c + 2], pv[4 * c + 3], dither[1], ph[2 * c + 1], pl[2 * c + 1]);
         } else {
           pk[2 * c] = pack_bf16(pv[4 * c], pv[4 * c + 1]);
           pk[2 * c + 1] = pack_bf16(pv[4 * c + 2], pv[4 * c + 3]);
@@ -583,7 +603,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
       for (int k = 0; k < 2; ++k) {
         const int kr = kr0 + 8 * k;
         if constexpr (kFp8) {
-          // e4m3 P^T hi and lo, MN-major with 64-byte rows (64-byte swizzle): key kr's row
+          // P^T hi and lo, MN-major with 64-byte rows (64-byte swizzle): key kr's row
           uint8_t* line_hi = a.sPt + sb * kPtBytes + kr * 64;
           uint8_t* line_lo = line_hi + kTileKeys * 64;
 #pragma unroll
