@@ -291,7 +291,7 @@ int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* 
  *                 same cache; its pages named by page_table_dst must not be pages that the
  *                 call reads, nor be named twice
  *   kept          int32 [batch, budget]: the kept indices in order, then -1
- *   seq_lens_dst  int32 [batch]: the new lengths
+ *   seq_lens_dst  int32 [batch]: the new lengths; may be seq_lens itself (not overlap it otherwise)
  *   weights_dst   NULL, or fp32 [batch, weights_dst_stride]: the kept keys' weights in order (a
  *                 -0 may come back as 0, a NaN as another NaN)
  *   workspace     mla_cache_evict_workspace bytes for this batch and max_seq (0 unless max_seq is
@@ -300,7 +300,8 @@ int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* 
  * A new block's scale is the largest among its rows' old ones; codes of a row from a block
  * with another scale are multiplied by old / new and rounded. Rows of the new pages behind the
  * new length are left as they are. Pages out of range are skipped and reported as
- * MLA_DEVICE_BAD_PAGE. Enqueue only, as mla_decode_run; weights_dst must not overlap weights.
+ * MLA_DEVICE_BAD_PAGE. Enqueue only, as mla_decode_run. weights_dst must not overlap weights, nor
+ * page_table_dst be page_table where the caches are the same (both refused).
  */
 int mla_cache_evict(const float* weights, long long weights_stride, const int32_t* seq_lens, int batch, int max_seq,
                     int budget, int n_first, int n_last, int kv_dtype, const void* kv_cache, const float* kv_scales,

@@ -123,7 +123,8 @@ def evict(weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, n_first: i
 
     Written: ``kept`` [batch, budget] int32 (indices in order, then -1), ``seq_lens_dst``
     [batch] int32, ``weights_dst`` [batch, >= new length] fp32 if given, and the new pages.
-    ``kv_dst`` may be ``kv`` itself; the new pages must not be among the old ones. ``max_seq``
+    ``kv_dst`` may be ``kv`` itself and ``seq_lens_dst`` may be ``seq_lens``; ``weights_dst`` must
+    not overlap ``weights``, and the new pages must not be among the old ones. ``max_seq``
     (default: what ``weights`` and ``page_table`` have room for) is at least the longest length.
     """
     index = _cuda_index(weights)

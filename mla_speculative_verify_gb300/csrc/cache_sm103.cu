@@ -271,11 +271,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
   const int gtid = rank * kSelThreads + tid, gthreads = ctas * kSelThreads;
   const bool bad = n < 0 || n > a.max_seq;
   const int out = bad ? 0 : min(n, a.budget);
-  if (gtid == 0) {
+  // lens_dst may be lens: the new length is written behind a barrier that the whole cluster reaches
+  // with the old one
+  auto write_length = [&] {
+    if (gtid != 0) return;
     a.lens_dst[b] = out;
     if (bad) report(a.status, MLA_DEVICE_PLAN_MISMATCH);
-  }
+  };
   if (out < a.budget || n == a.budget) {  // everything stays (the whole cluster leaves here)
+    sync_all();
+    write_length();
     for (int r = gtid; r < a.budget; r += gthreads) {
       kept[r] = r < out ? r : -1;
       if (wd && r < out) wd[r] = w[r];
@@ -291,7 +296,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     kept[a.budget - a.n_last + r] = n - a.n_last + r;
     if (wd) wd[a.budget - a.n_last + r] = w[n - a.n_last + r];
   }
-  if (k == 0) return;  // the whole cluster again
+  if (k == 0) {  // the whole cluster again
+    sync_all();
+    write_length();
+    return;
+  }
   const int per = ((m + ctas * kSelWarps - 1) / (ctas * kSelWarps) + kSelStep - 1) / kSelStep * kSelStep;
   const long long i0 = ((long long)rank * kSelWarps + warp) * per;  // this warp's first key
   const float* wm = w + lo;
@@ -367,6 +376,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
       if (lane == 0) coarse[pass & 1][warp] = s64;
     }
     sync_all();
+    if (pass == 0) write_length();
     // Coarse to fine, so that few words cross the cluster: first the 64 bins that hold the
     // wanted rank, by the counts of 64 bins each, then the one among them. Warp r reads CTA r's;
     // then every warp finds the same.
@@ -544,6 +554,7 @@ constexpr int kWideMaxChunks = kSelMaxKeys / kWideKeys;
 struct alignas(256) WideState {  // per request, in the workspace; zero before step 0
   uint32_t hist[3][kBins];
   uint2 found[3];  // bits found by step s + 1, rank among the keys that match them
+  int len;         // the old length, from step 3 for step 4, which writes the new one, perhaps over it
   uint2 counts[kWideMaxChunks];
 };
 
@@ -557,8 +568,9 @@ __global__ void __launch_bounds__(kWideThreads) evict_wide_kernel(SelectArgs a, 
   // (the warp's index as a value known to be the same in all lanes: 2^20 keys 127.7 -> 124.2 us)
   const int b = blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int n = a.lens[b];
   WideState& st = states[b];
+  const int n = kStep == 4 ? st.len : a.lens[b];
+  if (kStep == 3 && chunk == 0 && tid == 0) st.len = n;
   const float* w = a.weights + (size_t)b * a.w_stride;
   const bool bad = n < 0 || n > a.max_seq;
   const int out = bad ? 0 : min(n, a.budget);
@@ -828,6 +840,25 @@ __global__ void __launch_bounds__(kGatherThreads, 3) evict_gather_kernel(GatherA
   }
 }
 
+// Whether a row of [batch, a_stride] (of which a_row entries are used) overlaps one of [batch,
+// b_stride]. Rows of both are in order, so one walk over the two lists finds it.
+bool rows_overlap(const float* a, long long a_stride, int a_row, const float* b, long long b_stride, int b_row, int batch) {
+  auto at = [](const float* p, long long stride, int i) { return (uintptr_t)p + 4ull * (uintptr_t)stride * (uintptr_t)i; };
+  const uintptr_t a_bytes = 4ull * (uintptr_t)a_row, b_bytes = 4ull * (uintptr_t)b_row;
+  if (a_bytes == 0 || b_bytes == 0) return false;
+  if (at(a, a_stride, batch - 1) + a_bytes <= (uintptr_t)b || at(b, b_stride, batch - 1) + b_bytes <= (uintptr_t)a) return false;
+  for (int i = 0, j = 0; i < batch && j < batch;) {
+    const uintptr_t x = at(a, a_stride, i), y = at(b, b_stride, j);
+    if (x + a_bytes <= y)
+      ++i;
+    else if (y + b_bytes <= x)
+      ++j;
+    else
+      return true;
+  }
+  return false;
+}
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
@@ -937,6 +968,13 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   if (need > 0 && (!workspace || workspace_bytes < need))
     return set_error(MLA_ERR_BUFFER, "workspace needs %zu bytes (got %zu)", need, workspace ? workspace_bytes : (size_t)0);
   if (need > 0 && ((uintptr_t)workspace & 255u)) return set_error(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  // what the kernels read must not be what other CTAs of theirs write
+  if (weights_dst && rows_overlap(weights, weights_stride, max_seq, weights_dst, weights_dst_stride, most, batch))
+    return set_error(MLA_ERR_INVALID_ARG, "weights_dst must not overlap weights");
+  if (seq_lens_dst != seq_lens && seq_lens_dst < seq_lens + batch && seq_lens < seq_lens_dst + batch)
+    return set_error(MLA_ERR_INVALID_ARG, "seq_lens_dst must be seq_lens itself, or not overlap it");
+  if (kv_cache == kv_cache_dst && page_table == page_table_dst)
+    return set_error(MLA_ERR_INVALID_ARG, "the new pages must not be the old ones: page_table_dst is page_table");
   int sms = 0;
   const int rc = current_device_ready(&sms);
   if (rc != MLA_OK) return rc;
