@@ -25,8 +25,8 @@
 
 namespace mla {
 
-int current_device_ready(int* sms);   // defined next to the decode kernel
-int block_log2_of(int block_tokens);  // defined with the plan
+int current_device_ready(DeviceKernels* out);  // defined next to the decode kernel
+int block_log2_of(int block_tokens);           // defined with the plan
 
 namespace {
 
@@ -864,7 +864,7 @@ bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 }  // namespace
 
-cudaError_t set_cache_kernel_attributes() {
+cudaError_t set_select_kernel_attributes() {
   cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCacheBytes);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCacheBytes);
@@ -895,8 +895,8 @@ extern "C" int mla_cache_append(const void* rows, int total_rows, const int32_t*
     return set_error(MLA_ERR_INVALID_ARG, "rows and kv_cache must be 16-byte aligned");
   if (!aligned4(cu_new) || !aligned4(seq_lens) || !aligned4(kv_scales) || !aligned4(page_table) || !aligned4(status_dev))
     return set_error(MLA_ERR_INVALID_ARG, "cu_new, seq_lens, kv_scales, page_table and status_dev must be 4-byte aligned");
-  int sms = 0;
-  const int rc = current_device_ready(&sms);
+  DeviceKernels device;
+  const int rc = current_device_ready(&device);
   if (rc != MLA_OK) return rc;
   const AppendArgs a{(const uint4*)rows, total_rows, page_table, page_table_stride, num_pages, max_new, bl,
                      seq_lens, cu_new, (uint8_t*)kv_cache, kv_scales, status_dev};
@@ -975,9 +975,11 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
     return set_error(MLA_ERR_INVALID_ARG, "seq_lens_dst must be seq_lens itself, or not overlap it");
   if (kv_cache == kv_cache_dst && page_table == page_table_dst)
     return set_error(MLA_ERR_INVALID_ARG, "the new pages must not be the old ones: page_table_dst is page_table");
-  int sms = 0;
-  const int rc = current_device_ready(&sms);
+  DeviceKernels device;
+  const int rc = current_device_ready(&device);
   if (rc != MLA_OK) return rc;
+  if (device.select != cudaSuccess)
+    return set_error(MLA_ERR_CUDA, "selection kernel attributes: %s", cudaGetErrorString(device.select));
 
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -1017,7 +1019,7 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   const GatherArgs g{kept, seq_lens_dst, budget, max_seq, (const uint4*)kv_cache, (uint4*)kv_cache_dst, kv_scales,
                      kv_scales_dst, bl, page_table, page_table_dst, page_table_stride, page_table_dst_stride, num_pages,
                      num_pages_dst, (int)pages_dst, batch, status_dev};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(pages_dst * batch, 3LL * sms), 1, 1);
+  cfg.gridDim = dim3((unsigned)std::min<long long>(pages_dst * batch, 3LL * device.sms), 1, 1);
   cfg.blockDim = dim3(kGatherThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;

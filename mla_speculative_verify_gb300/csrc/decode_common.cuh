@@ -14,6 +14,14 @@ namespace mla {
 constexpr long long kWaitBudget = 2000000000LL;  // cycles (~1 s) before a wait gives up
 constexpr long long kWaitBudgetTest = 4000000LL; // ~2 ms: the budget of a call that tests the timeout path
 
+// What the entry points beside the decode need to know of a device: its SMs, and how their own
+// kernels' attributes could be set. A failure there refuses the entry point that it belongs to.
+struct DeviceKernels {
+  int sms = 0;
+  cudaError_t select = cudaSuccess, weights = cudaSuccess;
+  int weights_regs = 0;  // registers a thread of the key weights' kernel, the lower of its two forms
+};
+
 struct Params {
   const PlanUnit* units;   // the plan's unit table (one record per CTA, or per CTA pair)
   const __nv_bfloat16* q;  // the e4m3 path converts its Q tile from global memory

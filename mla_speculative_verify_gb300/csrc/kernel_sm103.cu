@@ -1286,13 +1286,14 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 struct DeviceInfo {
   bool checked = false, ok = false, attrs_set = false;
-  int major = 0, minor = 0, sms = 0;
+  int major = 0, minor = 0;
+  DeviceKernels kernels;
 };
 static DeviceInfo g_dev[64];
 static std::mutex g_dev_mu;
 
-cudaError_t set_weights_kernel_attributes();  // defined next to those kernels
-cudaError_t set_cache_kernel_attributes();
+cudaError_t set_weights_kernel_attributes(int* regs);  // defined next to those kernels
+cudaError_t set_select_kernel_attributes();
 
 static int prepare_device(int dev) {
   if (dev < 0 || dev >= 64) return set_error(MLA_ERR_CUDA, "device ordinal %d out of range", dev);
@@ -1301,7 +1302,7 @@ static int prepare_device(int dev) {
   if (!d.checked) {
     cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev);
     cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev);
-    cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaDeviceGetAttribute(&d.kernels.sms, cudaDevAttrMultiProcessorCount, dev);
     d.ok = (d.major == 10 && d.minor == 3);
     d.checked = true;
   }
@@ -1313,22 +1314,22 @@ static int prepare_device(int dev) {
       const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesScaled);
       if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
     }
-    cudaError_t e = set_weights_kernel_attributes();
-    if (e == cudaSuccess) e = set_cache_kernel_attributes();
-    if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
+    d.kernels.weights = set_weights_kernel_attributes(&d.kernels.weights_regs);
+    d.kernels.select = set_select_kernel_attributes();
+    if (d.kernels.weights != cudaSuccess || d.kernels.select != cudaSuccess)
+      (void)cudaGetLastError();  // (it would show at the next launch)
     d.attrs_set = true;
   }
   return MLA_OK;
 }
 
-// The current device, checked to be one this library runs on, and its SMs (for the other entry
-// points).
-int current_device_ready(int* sms) {
+// The current device, checked to be one this library runs on (for the other entry points).
+int current_device_ready(DeviceKernels* out) {
   int dev = 0;
   const cudaError_t ce = cudaGetDevice(&dev);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(ce));
   const int rc = prepare_device(dev);
-  if (rc == MLA_OK) *sms = g_dev[dev].sms;
+  if (rc == MLA_OK) *out = g_dev[dev].kernels;
   return rc;
 }
 

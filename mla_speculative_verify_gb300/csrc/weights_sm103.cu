@@ -62,7 +62,7 @@
 
 namespace mla {
 
-int current_device_ready(int* sms);                         // defined next to the decode kernel
+int current_device_ready(DeviceKernels* out);               // defined next to the decode kernel
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();     // defined next to the decode kernel
 int block_log2_of(int block_tokens);                        // defined with the plan
 int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out);
@@ -714,17 +714,16 @@ CUresult encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const v
 
 }  // namespace
 
-cudaError_t set_weights_kernel_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(key_weights_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
-  // a build that launches with fewer registers than the warpgroups share out would wait for them forever
+cudaError_t set_weights_kernel_attributes(int* regs) {
+  *regs = 255;
   for (const void* fn : {(const void*)key_weights_kernel<false>, (const void*)key_weights_kernel<true>}) {
     cudaFuncAttributes a;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, fn);
-    if (e == cudaSuccess && a.numRegs < kRegsLaunch) e = cudaErrorInvalidKernelImage;
+    if (e != cudaSuccess) return e;
+    *regs = std::min(*regs, a.numRegs);
   }
-  return e;
+  return cudaSuccess;
 }
 
 }  // namespace mla
@@ -787,9 +786,15 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
     return set_error(MLA_ERR_BUFFER, "workspace needs %zu bytes (got %zu)", need, workspace ? workspace_bytes : (size_t)0);
   if (need > 0 && ((uintptr_t)workspace & 255u)) return set_error(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
 
-  int sms = 0;
-  rc = current_device_ready(&sms);
+  DeviceKernels device;
+  rc = current_device_ready(&device);
   if (rc != MLA_OK) return rc;
+  if (device.weights != cudaSuccess)
+    return set_error(MLA_ERR_CUDA, "key weights kernel attributes: %s", cudaGetErrorString(device.weights));
+  // launched with fewer registers than its warpgroups share out, the kernel would wait for them forever
+  if (device.weights_regs < kRegsLaunch)
+    return set_error(MLA_ERR_UNSUPPORTED, "the key weights kernel was compiled to %d registers a thread and needs %d",
+                     device.weights_regs, kRegsLaunch);
   const int piece = fp8 ? 8192 : 16384, tile_bytes = kPieces * piece;
   const int fixed = 1024 + kMiscBytes + kPieces * most_rows * 128;
   const int per = fp8 ? Parts<true>::kPer : Parts<false>::kPer;
@@ -808,7 +813,7 @@ extern "C" int mla_key_weights(const void* plan_dev, const void* plan_host, size
     tiles += t;
     prm.total_work += t * ((reqs[i].q * h->num_heads + most_rows - 1) / most_rows);
   }
-  const unsigned grid = (unsigned)std::min<long long>(tiles, sms);
+  const unsigned grid = (unsigned)std::min<long long>(tiles, device.sms);
   prm.reqs = (const PlanRequest*)((const uint8_t*)plan_dev + h->req_off);
   prm.first = reqs[0];
   prm.batch = h->batch;
