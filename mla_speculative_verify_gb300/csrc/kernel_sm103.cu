@@ -247,7 +247,7 @@ struct SoftmaxArgs {
   uint32_t tmem, skv, spt;
   int qd, grp, lane, sidx, nmma, b, nrows, qrow0, kv_begin, kv_end, ntiles, part_row0, ctx, qlen, tok0;
   volatile int* abort;
-  const float4* scales;  // block-scaled cache: (v, log2 v, 1 / v) of each key, by stage
+  const float4* scales;  // block-scaled cache: (v, log2 v, 1 / v) of each key, by stage (the latter two of at least 2^-60)
 };
 
 // Softmax warps for a tile of 16 NCH packed rows. Warp (qd, grp) owns the 16 key rows of
@@ -931,8 +931,9 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
             float4* dst = reinterpret_cast<float4*>(smem + kOffScales) + slot * kTileKeys + 2 * lane;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float v = sc[k] < 0x1p-60f ? 0x1p-60f : sc[k];  // a block of zeros may have the scale 0
-              dst[k] = make_float4(v, lg2(v), 1.f / v, 0.f);
+              // a block of zeros may have the scale 0: it scores 0 and weighs what the least scale does
+              const float v = fmaxf(sc[k], 0x1p-60f);
+              dst[k] = make_float4(sc[k], lg2(v), 1.f / v, 0.f);
             }
             const int page_n = __shfl_sync(0xffffffffu, i + 1 < 32 ? pid_cur : pid_next, (i + 1) & 31);
             if (t + 1 < ntiles) load_scales(t + 1, page_n);
