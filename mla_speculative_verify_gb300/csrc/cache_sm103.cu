@@ -538,8 +538,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
 }
 
 // ------------------------------------------------------------------ eviction: long requests
-// The same selection spread over the whole GPU, for requests so long that a cluster's 16 CTAs
-// take longer than a few launches (the sweeps of 1M keys on 16 CTAs: 45 us). A CTA takes 4096
+// The same selection spread over the whole GPU, for requests of more keys than a cluster's 8 CTAs
+// hold in shared memory (wide_selection below has both sides' times). A CTA takes 4096
 // keys, eight to a thread, and every pass is a launch of its own, which sees the counts of the
 // one before:
 //   step 0..2  counts of the next 11, 11, 10 bits among the keys that match the bits found so far
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(kWideThreads) evict_wide_kernel(SelectArgs a, 
 struct GatherArgs {
   const int32_t* kept;
   const int32_t* lens_dst;
-  int budget, max_seq;
+  int budget;
   const uint4* src;
   uint4* dst;
   const float* scales_src;
@@ -911,8 +911,8 @@ extern "C" int mla_cache_append(const void* rows, int total_rows, const int32_t*
 namespace mla {
 // Long requests are selected by the five launches, others by clusters. Whole calls that keep 64
 // keys, clusters against launches: 1 x 64k keys 19 against 19 us, 8 x 64k 19 against 25, 1 x 128k
-// 23 against 19, 4 x 128k 23 against 23, 8 x 128k 37 against 27, 1 x 1M 42 against 27 (in
-// clusters of 16, of which eight do not run at once).
+// 23 against 19, 4 x 128k 23 against 23, 8 x 128k 37 against 27, 1 x 1M 42 against 27 (the
+// longer ones then in clusters of 16, of which eight do not run at once; kSelMaxCtas is 8).
 static bool wide_selection(int max_seq) { return max_seq > kWideFrom; }
 }  // namespace mla
 
@@ -1016,7 +1016,7 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction selection launch: %s", cudaGetErrorString(ce));
   if (pages_dst == 0) return MLA_OK;
 
-  const GatherArgs g{kept, seq_lens_dst, budget, max_seq, (const uint4*)kv_cache, (uint4*)kv_cache_dst, kv_scales,
+  const GatherArgs g{kept, seq_lens_dst, budget, (const uint4*)kv_cache, (uint4*)kv_cache_dst, kv_scales,
                      kv_scales_dst, bl, page_table, page_table_dst, page_table_stride, page_table_dst_stride, num_pages,
                      num_pages_dst, (int)pages_dst, batch, status_dev};
   cfg.gridDim = dim3((unsigned)std::min<long long>(pages_dst * batch, 3LL * device.sms), 1, 1);

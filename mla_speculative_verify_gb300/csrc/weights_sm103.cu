@@ -148,7 +148,6 @@ struct Walk {
   PlanRequest r;           // this lane's request
   long long at;            // its place
   uint32_t todo;           // lanes of the current 32 requests that hold work of this CTA
-  bool loaded;
 
   __device__ __forceinline__ void start(const WeightsParams& p) {
     lo = p.total_work * blockIdx.x / gridDim.x;
@@ -156,7 +155,6 @@ struct Walk {
     base = 0;
     b0 = -32;
     todo = 0;
-    loaded = false;
   }
   static __device__ __forceinline__ int groups(const WeightsParams& p, int q) {
     return (q * p.H + p.rows_n - 1) / p.rows_n;
