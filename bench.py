@@ -147,8 +147,8 @@ def profiled_traffic(profile_md: str) -> dict:
 
 def mma_dtype(prob) -> str:
     """Arithmetic type of a call's tensor-core products: bf16 x bf16 for a bf16 cache; for
-    an e4m3 cache e4m3 x e4m3 on the stored codes and on two-part (hi + lo) e4m3 operands
-    of Q and P; fp32 accumulation and softmax either way."""
+    an e4m3 cache the stored codes against two-part (hi + lo) 8-bit operands of Q (both e4m3)
+    and P (e4m3 and e5m2); fp32 accumulation and softmax either way."""
     return "bf16" if prob.kv_dtype == inputs.KV_BF16 else "e4m3 (hi+lo operands)"
 
 

@@ -37,9 +37,10 @@
  * Errors: every entry point returns an mla_status; on failure mla_last_error()
  * describes the cause. Arguments are checked on the host before any launch.
  * Device-side problems (a bounded wait that ran out, seq_lens/q_lens that differ
- * from the plan, a page id outside [0, num_pages)) never trap: the kernels stop
- * the affected work item and OR a code into *status_dev (if given), which the
- * caller reads after synchronising.
+ * from the plan, a page id outside [0, num_pages)) never trap: the kernels OR a
+ * code into *status_dev (if given), which the caller reads after synchronising.
+ * They stop the affected work item; in the place of a bad page the decode and the
+ * key weights read page 0, so that the results of its request are not to be used.
  */
 #ifndef MLA_DECODE_H_
 #define MLA_DECODE_H_
@@ -147,8 +148,12 @@ int mla_decode_plan_info(const void* plan_host, size_t plan_bytes, int* n_units,
  *   sm_scale             : score scale (1/sqrt(192) for the Kimi-K3 / DeepSeek head sizes)
  *   kv_scale             : per-tensor dequantisation scale of an fp8 cache (ignored for bf16)
  *   workspace            : device scratch of at least the plan's workspace bytes (may be
- *                          NULL when that size is 0)
+ *                          NULL when that size is 0); calls that may overlap need one each
  *   status_dev           : optional device int32 the kernels OR MLA_DEVICE_* bits into
+ *
+ * With an fp8 cache a softmax weight enters the value product to 2^-8 of itself; one that is
+ * below 2^-10 of the row's largest is rounded up or down with odds that go by its key's
+ * position, so that the sums over many of them come out right. The row sums are fp32.
  *
  * Enqueue only: no allocation, no host synchronisation, no host reads of device
  * memory, so the call can be captured in a CUDA graph (the tensor maps are built on
@@ -217,7 +222,8 @@ int mla_device_pair_slots(int device, int* slots);
  *                 (none is allowed)
  *   seq_lens      device int32 [batch]: the length of each request with its new rows, which
  *                 are its last ones
- *   max_new       host: at least the largest number of new rows of a request
+ *   max_new       host: at least the largest number of new rows of a request; with 0 the call
+ *                 does nothing, and reads neither cu_new nor the lengths
  *   kv_cache, kv_scales   the cache, written in place
  *
  * A block whose first token is new gets the least power of two 2^e, -60 <= e <= 60, with
@@ -226,6 +232,10 @@ int mla_device_pair_slots(int device, int* slots);
  * rounded to it. Codes are round-to-nearest-even of x / scale; infinities and larger values
  * become +-448, NaN stays NaN. Rows behind a request's last token are left as they are.
  * No page may be named twice among those that a call writes.
+ *
+ * A scale only grows while its block holds older tokens. Where draft tokens are rejected and
+ * overwritten by the next append, the scale that they asked for stays with the block, and the
+ * older codes stay rounded to it. (With blocks of one token no append touches an older token.)
  *
  * Requests whose lengths do not fit (more than max_new rows, more rows than tokens, more
  * pages than page_table_stride, cu_new outside rows) write nothing and report
@@ -263,7 +273,9 @@ int mla_decode_run_scaled(const void* plan_dev, const void* plan_host, size_t pl
  *                 NULL for all; values are cut to [0, q_len]
  *   decay         finite; with 0 the old sums are not read
  *   weights       fp32 [batch, weights_stride], weights_stride >= the longest request; entries
- *                 at and behind seq_lens[b] are left as they are
+ *                 at and behind seq_lens[b] are left as they are. With a decay other than 0 the
+ *                 entry of a new token starts from what its place holds: the caller zeroes
+ *                 the places that an append fills, and those of rejected drafts
  *   workspace     mla_key_weights_workspace bytes (0 for a bf16 plan), 256-byte aligned; calls
  *                 that may overlap need one each
  *
@@ -279,7 +291,8 @@ int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* 
 
 /*
  * mla_cache_evict -- shorten each request to at most `budget` keys and move them, in order,
- * to new pages. A request of n <= budget keys keeps all. A longer one keeps its first n_first,
+ * to new pages. A request of n <= budget keys keeps all, and is moved too: page_table_dst has to
+ * name pages for every request of the call. A longer one keeps its first n_first,
  * its last n_last and, of the others, the budget - n_first - n_last with the largest weights
  * (ties: the lower index; -0 equals 0; NaN counts as the lowest).
  *
@@ -295,7 +308,8 @@ int mla_key_weights_workspace(const void* plan_host, size_t plan_bytes, size_t* 
  *   kept          int32 [batch, budget]: the kept indices in order, then -1
  *   seq_lens_dst  int32 [batch]: the new lengths; may be seq_lens itself (not overlap it otherwise)
  *   weights_dst   NULL, or fp32 [batch, weights_dst_stride]: the kept keys' weights in order (a
- *                 -0 may come back as 0, a NaN as another NaN)
+ *                 -0 may come back as 0, a NaN as another NaN). Entries behind the new length are
+ *                 left as they are: zero them before tokens are appended there
  *   workspace     mla_cache_evict_workspace bytes for this batch and max_seq (0 unless max_seq is
  *                 large), 256-byte aligned; calls that may overlap need one each
  *

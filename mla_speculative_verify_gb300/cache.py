@@ -5,8 +5,9 @@ Both only check shapes, dtypes and devices and pass raw pointers through to
 ``mla_cache_append`` / ``mla_cache_evict``; what they compute is stated in
 include/mla_decode.h. They enqueue on ``stream`` (default: torch's current stream of the
 tensors' device) and do not synchronise, so they can be captured in a CUDA graph; what scratch
-``evict`` needs comes from torch's allocator, call by call. Device-side faults (lengths that do not fit, pages out of range) are OR-ed into
-``status``, an int32 tensor, as ``binding.MLA_DEVICE_*`` bits.
+``evict`` needs comes from torch's allocator, call by call. Device-side faults (lengths that do not
+fit, pages out of range) are OR-ed into ``status``, an int32 tensor, as ``binding.MLA_DEVICE_*``
+bits.
 """
 from __future__ import annotations
 
@@ -93,7 +94,11 @@ def append(rows: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, page_t
 
     Request b's rows are rows[cu_new[b]:cu_new[b + 1]] (int32, device) and become its last
     tokens: its length with them is seq_lens[b] (int32, device). ``max_new`` is at least the
-    largest number of new rows of a request.
+    largest number of new rows of a request; with 0 the call does nothing.
+
+    A block's scale never shrinks while it holds older tokens, so the scale that a rejected draft
+    asked for stays with the older tokens of its block. Where key weights are added up, the
+    caller zeroes the places of the new tokens.
     """
     index = _cuda_index(rows)
     check_tensor("rows", rows, torch.bfloat16, rows.shape[:1] + (D_QK,), index)
@@ -124,7 +129,9 @@ def evict(weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, n_first: i
     Written: ``kept`` [batch, budget] int32 (indices in order, then -1), ``seq_lens_dst``
     [batch] int32, ``weights_dst`` [batch, >= new length] fp32 if given, and the new pages.
     ``kv_dst`` may be ``kv`` itself and ``seq_lens_dst`` may be ``seq_lens``; ``weights_dst`` must
-    not overlap ``weights``, and the new pages must not be among the old ones. ``max_seq``
+    not overlap ``weights``, and the new pages must not be among the old ones. A request that is
+    short enough already moves to its new pages too. Entries of ``weights_dst`` behind the new
+    length are left as they are; zero them before tokens are appended there. ``max_seq``
     (default: what ``weights`` and ``page_table`` have room for) is at least the longest length.
     """
     index = _cuda_index(weights)

@@ -66,7 +66,9 @@ class VerifyDecoder:
             seq_lens_dev: torch.Tensor | None = None, q_lens_dev: torch.Tensor | None = None,
             kv_scales: torch.Tensor | None = None) -> None:
         """The verify decode. With ``kv_scales`` [pages, 64 / block_tokens] fp32 the e4m3 cache
-        is block-scaled: code * scale of its block (``kv_scale`` is then not used)."""
+        is block-scaled: code * scale of its block (``kv_scale`` is then not used). A decoder's
+        calls share its workspace: those that may overlap (on two streams, or in two graphs that
+        are replayed at once) need a decoder each."""
         H = self.num_heads
         want_kv = torch.bfloat16 if self.kv_dtype == "bf16" else torch.uint8
         if q.dtype != torch.bfloat16 or tuple(q.shape) != (self.total_q, H, 576) or not q.is_contiguous():
@@ -116,7 +118,8 @@ class VerifyDecoder:
         """After ``run``: add to ``weights`` [batch, >= longest request] fp32 what every cached
         key received, weights = decay * weights + sum over rows of exp(score - lse), with the
         ``lse`` that ``run`` wrote. ``counted`` [batch] int32: only the first so many verify
-        tokens of a request count (the accepted ones). Its scratch comes from torch's allocator,
+        tokens of a request count (the accepted ones). A new token's sum starts from what
+        ``weights`` holds in its place, so zero the places that an append fills. Its scratch comes from torch's allocator,
         call by call, so calls on several streams or captured in several graphs share none."""
         if self.device.type != "cuda":
             raise ValueError("key_weights runs on a CUDA device")
