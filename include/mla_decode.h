@@ -211,9 +211,10 @@ int mla_device_pair_slots(int device, int* slots);
  * An e4m3 cache may carry an fp32 scale for each block of block_tokens consecutive tokens of
  * a page instead of one per tensor: kv_scales [num_pages, 64 / block_tokens], block_tokens 1,
  * 2, 4, .. 64, and code c of a row of that block stands for c * scale. Scales are finite and
- * >= 0 (0 stands for a block of zeros); between 2^-60 and 2^60 they may lie any distance apart.
- * Scores take a smaller scale as it is, the decode's output takes it as 2^-60 (such a block's
- * values are below 2^-51).
+ * >= 0 (0 stands for a block of zeros). Those between 2^-60 and 2^60 may lie up to 2^90 apart in
+ * a request; with more, keys of the small scales whose softmax weight is below 2^-40 of the
+ * largest key's, or up to 2^-10 with 2^120, are left out of the row's sum. Scores take a scale
+ * below 2^-60 as it is, the decode's output takes it as 2^-60 (such a block's values are below 2^-51).
  *
  * mla_cache_append -- write new latent rows into such a cache.
  *

@@ -262,7 +262,8 @@ struct SoftmaxArgs {
 // the products run on the raw codes. With s_j the score and v_j the scale of key j, the
 // softmax works on s_j + log2 v_j: P'_j = 2^(s_j + log2 v_j - ref) is what the code of key j
 // is weighted with in O^T, and l adds P'_j / v_j, so out = O / l and the reference follows
-// the terms that O is made of, however far the blocks' scales lie apart. The producer warp
+// the terms that O is made of. (P' is an fp32 down to 2^-126, 2^-130 of the largest: with scales
+// 2^90 apart l still has every key of 2^-40 of the largest weight.) The producer warp
 // reads a page's scales one page ahead and leaves (v, log2 v, 1 / v) of each key beside the
 // page: looked up by every softmax thread for its two keys they cost the busiest role ~100
 // instructions a tile (1M keys q=8 301 us). Pairs of columns share fp32 instructions, and the

@@ -1,9 +1,11 @@
-"""Block scales below 2^-60: the decode's scores and the key weights' are the same, those of the
-scales as they are."""
+"""Block scales at the ends of their range: below 2^-60 the decode's scores and the key weights' are
+the same, those of the scales as they are; scales far apart leave every key its weight."""
+import math
+
 import pytest
 import torch
 
-from mla_speculative_verify_gb300 import inputs
+from mla_speculative_verify_gb300 import binding, inputs
 from mla_speculative_verify_gb300.decoder import VerifyDecoder
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +44,34 @@ def test_scores_of_small_scales(mixed):
         want[:n - q + i + 1] += torch.exp(s - exact[:, None]).sum(0)
     assert ((w[0].double() - want).abs() <= 0.02 * want + 1e-12).all()  # ds and lse's: below 1 % of a weight
     assert torch.isfinite(out).all() and out.float().abs().max() < 2.0 ** -51
+
+
+@pytest.mark.parametrize("octaves", [0, 52, 90])
+def test_scales_far_apart(octaves):
+    """A key with half of the weight in a block whose scale is 2^octaves of all others', whose keys
+    share the other half (52: a block of zeros, which an append gives 2^-60, beside rows of size 1)."""
+    n, H = 20000, 2
+    pages = -(-n // 64)
+    g = torch.Generator(device="cuda").manual_seed(62)
+    codes = (torch.randn((pages, 64, 576), generator=g, device="cuda") * 60).clamp(-448, 448)
+    codes[..., 512:] = 0.0
+    codes[0, 1:] = 0.0
+    codes[0, 0, 512] = 64.0
+    scales = torch.full((pages, 1), 2.0 ** -(octaves // 2), device="cuda")
+    scales[0] = 2.0 ** (octaves - octaves // 2)
+    queries = torch.zeros((1, H, 576), device="cuda")
+    queries[..., 512] = torch.tensor([1.0, 1.1], device="cuda") * math.log(n) / (inputs.SM_SCALE * 64.0 * scales[0, 0].item())
+    queries = queries.to(torch.bfloat16)
+    codes = codes.to(torch.float8_e4m3fn)
+    d = VerifyDecoder([n], [1], H, "fp8", options=binding.PlanOptions(force_splits=1))
+    out, lse = torch.empty((1, H, 512), dtype=torch.bfloat16, device="cuda"), torch.empty((1, H), device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
+    d.run(queries, codes, table, out, lse, kv_scales=scales)
+    torch.cuda.synchronize()
+    k = (codes.double() * scales.double()[:, :, None]).view(-1, 576)[:n]
+    s = inputs.SM_SCALE * (queries[0].double() @ k.T)
+    want = torch.softmax(s, 1) @ k[:, :512]
+    assert ((lse[0].double() - torch.logsumexp(s, 1)).abs() <= 1e-4).all()
+    # the strong key's weight to 2^-8, the output's rounding 2^-8, the others' 2^-3 of theirs, independent: 6 deviations
+    noise = 6 * 2.0 ** -3 / n * k[1:, :512].norm()
+    assert ((out[0].double() - want).norm(dim=1) <= 2.0 ** -7 * want.norm(dim=1) + noise).all()
