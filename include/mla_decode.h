@@ -155,6 +155,10 @@ int mla_decode_plan_info(const void* plan_host, size_t plan_bytes, int* n_units,
  * below 2^-10 of the row's largest is rounded up or down with odds that go by its key's
  * position, so that the sums over many of them come out right. The row sums are fp32.
  *
+ * What lies behind a request's last key may be anything, NaN too. A NaN or an infinity in the
+ * values of one of its keys may reach all of its verify tokens, those that do not see the key
+ * included (a weight of zero times a NaN).
+ *
  * Enqueue only: no allocation, no host synchronisation, no host reads of device
  * memory, so the call can be captured in a CUDA graph (the tensor maps are built on
  * the host and passed by value).
