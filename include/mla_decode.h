@@ -67,6 +67,7 @@ typedef enum { MLA_KV_BF16 = 0, MLA_KV_FP8_E4M3 = 1 } mla_kv_dtype;
 #define MLA_DEVICE_WAIT_TIMEOUT 0x1     /* a bounded mbarrier wait ran out */
 #define MLA_DEVICE_PLAN_MISMATCH 0x2    /* seq_lens / q_lens on the device differ from the plan */
 #define MLA_DEVICE_BAD_PAGE 0x4         /* a page id outside [0, num_pages) */
+#define MLA_DEVICE_BAD_TREE 0x8         /* a parent that is not before its node, a path that does not rise */
 
 #define MLA_HEAD_DIM_QK 576
 #define MLA_HEAD_DIM_V 512
@@ -332,6 +333,141 @@ int mla_cache_evict(const float* weights, long long weights_stride, const int32_
                     float* weights_dst, long long weights_dst_stride, void* workspace, size_t workspace_bytes,
                     int32_t* status_dev, void* stream);
 int mla_cache_evict_workspace(int batch, int max_seq, size_t* workspace_bytes_out);
+
+/*
+ * ---- Trees of drafted tokens ----
+ *
+ * A request's verify tokens may be a tree instead of a chain: node 0 is the root (the last token
+ * that is certain), every other node i has a parent before it, and sees the keys before the
+ * request's verify tokens, its ancestors' keys and its own. A step of a server: mla_tree_masks,
+ * then in each layer the append and mla_decode_run_tree, then mla_tree_verify on the logits, then
+ * mla_cache_commit, after which the cache holds the accepted path as a chain.
+ *
+ *   parents    [total_nodes] int32, index within the request; node 0's, and that of a node which
+ *              hangs on nothing (padding), is negative
+ *   cu_nodes   device int32 [batch + 1]: request b's nodes are cu_nodes[b] .. cu_nodes[b + 1] - 1
+ *              (none is allowed); in the decode's order, cu_nodes are the sums of q_lens
+ *   max_nodes  host: at least the largest number of nodes of a request, at most MLA_TREE_MAX_NODES
+ *
+ * A parent at or behind its own node reports MLA_DEVICE_BAD_TREE and counts as negative. Requests
+ * whose cu_nodes do not fit (outside [0, total_nodes], falling, more than max_nodes) report
+ * MLA_DEVICE_PLAN_MISMATCH.
+ */
+#define MLA_TREE_MAX_NODES 1024
+
+/*
+ * mla_tree_masks -- parents to visibility words.
+ *
+ *   masks   [total_nodes, mask_words] uint32, mask_words >= max_nodes / 32 rounded up: bit a % 32
+ *           of word a / 32 of a node's row is set where a is the node or one of its ancestors
+ *   depths  NULL, or [total_nodes] int32: a node's number of ancestors (its position is that of
+ *           the root plus this)
+ *
+ * Rows of requests that do not fit, and of nodes in none, are left as they are. Enqueue only, as
+ * mla_decode_run. masks and depths must not overlap the other arrays (refused).
+ */
+int mla_tree_masks(const int32_t* parents, const int32_t* cu_nodes, int batch, int total_nodes, int max_nodes,
+                   uint32_t* masks, int mask_words, int32_t* depths, int32_t* status_dev, void* stream);
+
+/*
+ * mla_decode_plan_tree -- mla_decode_plan_ex for trees: the row tiles are cut from all of a
+ * request's q * H rows, where the fold rule asks for a divisor of q. force_fold and cta_pair are
+ * refused. Such a plan runs chains too, and mla_key_weights takes it.
+ */
+int mla_decode_plan_tree(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads, int page_size,
+                         int kv_dtype, int num_sms, const mla_plan_options* opts, void* plan_buf,
+                         size_t plan_buf_bytes, size_t* plan_bytes_out, size_t* workspace_bytes_out);
+
+/*
+ * mla_decode_run_tree -- mla_decode_run (with kv_scales NULL) or mla_decode_run_scaled, in which
+ * verify token i of request b sees key j < seq_lens[b] - q_lens[b], and key seq_lens[b] -
+ * q_lens[b] + a where bit a of its row of tree_masks is set.
+ *
+ *   plan         of any entry point, but not one for two-CTA tiles (cta_pair)
+ *   tree_masks   [sum(q_lens), mask_words] uint32 as mla_tree_masks writes it, or any other
+ *                choice of keys; bits from q_lens[b] on are not looked at
+ *
+ * A row that sees no key gets zeros and an lse of -inf. With the masks of a chain the results are
+ * mla_decode_run's of the same plan, bit for bit.
+ */
+int mla_decode_run_tree(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
+                        const void* kv_cache, const float* kv_scales, int block_tokens, const int32_t* page_table,
+                        int page_table_stride, int num_pages, const int32_t* seq_lens, const int32_t* q_lens,
+                        const uint32_t* tree_masks, int mask_words, float sm_scale, float kv_scale, void* out,
+                        float* lse, void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream);
+
+/*
+ * mla_tree_verify -- how far the target model's distribution accepts a draft, and the next token.
+ *
+ *   target_logits  [total_nodes, target_stride] bf16 or fp32 (logits_dtype), the first vocab of a
+ *                  row: row u is the target's at node u
+ *   draft_logits   NULL, or [total_nodes, draft_stride] of the same type: row u's distribution is
+ *                  what the children of u were drawn from, each by itself (rows of nodes without
+ *                  children are not read). NULL: the children are certain (the draft's best tokens)
+ *   tokens         [total_nodes] int32: the drafted token of each node (node 0's is not read). A
+ *                  node whose token lies outside [0, vocab) is never accepted and changes nothing
+ *   temperature    NULL (1 for all), or fp32 [batch]. Below 2^-20, or NaN: greedy; cut to 2^20
+ *   uniforms       fp32 [total_nodes], in [0, 1): decides on node i
+ *   noise          fp32 [batch, noise_stride >= vocab], drawn from the exponential distribution;
+ *                  0, negative numbers and NaN count as the least normal number. uniforms and noise
+ *                  both NULL: all requests are greedy
+ *   path           int32 [batch, path_stride]: the accepted nodes, from node 0 on, then -1
+ *   out_tokens     int32 [batch, path_stride]: the tokens that follow each of them: the accepted
+ *                  nodes' own and last the next token, then -1
+ *   accepted       int32 [batch]: nodes on the path (0 for a request without nodes, or one that
+ *                  does not fit)
+ *
+ * At node u, with p = softmax(target_logits[u] / T), the children are tried in order. Draft NULL:
+ * r is p without the tokens tried before, R its sum, and child i with token x is accepted where
+ * uniforms[i] * R < r(x). Otherwise, with q = softmax(draft_logits[u] / T), r = p and R = 1 at
+ * first, it is accepted where uniforms[i] * R * q(x) < r(x); after a rejection r becomes
+ * max(r - R q, 0) and R its sum. Where no child is accepted (or path is full: then none is tried)
+ * the next token is argmax r / noise, of equal ones the lowest; where r has nothing left, argmax
+ * p / noise. So each token that comes out is distributed as p. Greedy: the token of the largest
+ * logit (of equal ones the lowest) follows, and a child is accepted where it has that token.
+ *
+ * NaN logits count as -inf, infinite ones as the largest number. A row of -inf alone accepts
+ * nothing, and its next token is -1. Sums are taken in fp32 in a fixed order: equal inputs give
+ * equal results; one that hangs on less than about 1e-6 of a probability may fall either way.
+ * path, out_tokens and accepted must not overlap one another or the inputs (refused), and the
+ * inputs must not change while the call runs. Enqueue only, as mla_decode_run.
+ */
+typedef enum { MLA_LOGITS_BF16 = 0, MLA_LOGITS_FP32 = 1 } mla_logits_dtype;
+int mla_tree_verify(int logits_dtype, const void* target_logits, long long target_stride, const void* draft_logits,
+                    long long draft_stride, int vocab, const int32_t* tokens, const int32_t* parents,
+                    const int32_t* cu_nodes, int batch, int total_nodes, int max_nodes, const float* temperature,
+                    const float* uniforms, const float* noise, long long noise_stride, int32_t* path,
+                    int32_t* out_tokens, int path_stride, int32_t* accepted, int32_t* status_dev, void* stream);
+
+/*
+ * mla_cache_commit -- after mla_tree_verify: in every layer, the rows of the accepted nodes move
+ * to the front of the request's verify tokens, so that its last keys are the accepted path.
+ *
+ *   kv_dtype, kv_cache   [layers, num_pages, 64, 576], written in place; kv_scales NULL, or
+ *                 [layers, num_pages, 64 / block_tokens] of a block-scaled e4m3 cache
+ *   page_table    one for all layers
+ *   seq_lens      device int32 [batch]: lengths with all verify tokens
+ *   cu_nodes      device int32 [batch + 1]: request b has cu_nodes[b + 1] - cu_nodes[b] of them
+ *   path          device int32 [batch, path_stride], path_stride <= 1024; accepted device int32
+ *                 [batch], as mla_tree_verify writes them: row path[k] of the verify tokens becomes
+ *                 row k, for k < accepted
+ *   seq_lens_dst  int32 [batch]: seq_lens without the tokens that were not accepted. Not seq_lens
+ *                 itself, nor overlapping path, accepted or cu_nodes (refused)
+ *
+ * A block that receives rows gets the largest of their scales, and of its own where rows before
+ * them stay in it; codes of a row or block with a smaller scale are rounded to it. Rows behind the
+ * new length are left as they are, and so are blocks that receive nothing.
+ *
+ * A path that does not rise from a node >= 0 to one within the request reports
+ * MLA_DEVICE_BAD_TREE, lengths that do not fit (fewer tokens than nodes, more accepted than nodes or
+ * path_stride, more pages than page_table_stride) MLA_DEVICE_PLAN_MISMATCH: such a request stays as
+ * it is, with its old length. Rows of pages outside [0, num_pages) do not move, reported as
+ * MLA_DEVICE_BAD_PAGE. No page may be named twice. Enqueue only, as mla_decode_run.
+ */
+int mla_cache_commit(int kv_dtype, void* kv_cache, float* kv_scales, int block_tokens, int layers,
+                     const int32_t* page_table, int page_table_stride, int num_pages, const int32_t* seq_lens,
+                     const int32_t* cu_nodes, int batch, const int32_t* path, int path_stride, const int32_t* accepted,
+                     int32_t* seq_lens_dst, int32_t* status_dev, void* stream);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* mla_last_error(void);

@@ -26,6 +26,10 @@ MLA_KV_FP8_E4M3 = 1
 MLA_DEVICE_WAIT_TIMEOUT = 0x1
 MLA_DEVICE_PLAN_MISMATCH = 0x2
 MLA_DEVICE_BAD_PAGE = 0x4
+MLA_DEVICE_BAD_TREE = 0x8
+MLA_LOGITS_BF16 = 0
+MLA_LOGITS_FP32 = 1
+MLA_TREE_MAX_NODES = 1024
 MLA_STATIC_WORKSPACE_BYTES = 16 << 20
 
 _P = ctypes.c_void_p
@@ -73,6 +77,18 @@ SIGNATURES = {
                                        ctypes.c_int, ctypes.c_int, _P, _P, _P, ctypes.c_int, ctypes.c_int, _P, _P, _P,
                                        ctypes.c_longlong, _P, ctypes.c_size_t, _P, _P]),
     "mla_cache_evict_workspace": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _SZP]),
+    "mla_tree_masks": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, ctypes.c_int, _P, _P, _P]),
+    "mla_decode_plan_tree": (ctypes.c_int, [_I32P, _I32P, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                            ctypes.c_int, ctypes.POINTER(PlanOptions), _P, ctypes.c_size_t, _SZP,
+                                            _SZP]),
+    "mla_decode_run_tree": (ctypes.c_int, [_P, _P, ctypes.c_size_t, _P, _P, _P, ctypes.c_int, _P, ctypes.c_int,
+                                           ctypes.c_int, _P, _P, _P, ctypes.c_int, ctypes.c_float, ctypes.c_float, _P,
+                                           _P, _P, ctypes.c_size_t, _P, _P]),
+    "mla_tree_verify": (ctypes.c_int, [ctypes.c_int, _P, ctypes.c_longlong, _P, ctypes.c_longlong, ctypes.c_int, _P, _P,
+                                       _P, ctypes.c_int, ctypes.c_int, ctypes.c_int, _P, _P, _P, ctypes.c_longlong, _P,
+                                       _P, ctypes.c_int, _P, _P, _P]),
+    "mla_cache_commit": (ctypes.c_int, [ctypes.c_int, _P, _P, ctypes.c_int, ctypes.c_int, _P, ctypes.c_int,
+                                        ctypes.c_int, _P, _P, ctypes.c_int, _P, ctypes.c_int, _P, _P, _P, _P]),
     "mla_device_pair_slots": (ctypes.c_int, [ctypes.c_int, _IP]),
     "mla_last_error": (ctypes.c_char_p, []),
     "mla_version": (ctypes.c_int, []),
@@ -122,20 +138,21 @@ def _i32(a) -> np.ndarray:
 
 
 def plan(seq_lens, q_lens, num_heads: int, kv_dtype: int, num_sms: int, options: PlanOptions | None = None,
-         page_size: int = 64):
-    """mla_decode_plan(_ex): returns (plan bytes as a uint8 numpy array, workspace bytes)."""
+         page_size: int = 64, tree: bool = False):
+    """mla_decode_plan(_ex), or with ``tree`` mla_decode_plan_tree: returns (plan bytes as a uint8 numpy
+    array, workspace bytes)."""
     lib = load()
+    make = lib.mla_decode_plan_tree if tree else lib.mla_decode_plan_ex
     s, q = _i32(seq_lens), _i32(q_lens)
     nbytes, ws = ctypes.c_size_t(0), ctypes.c_size_t(0)
     args = (s.ctypes.data_as(_I32P), q.ctypes.data_as(_I32P), int(s.shape[0]), int(num_heads), int(page_size),
             int(kv_dtype), int(num_sms))
     opt = ctypes.byref(options) if options is not None else None
-    rc = lib.mla_decode_plan_ex(*args, opt, None, 0, ctypes.byref(nbytes), ctypes.byref(ws))
+    rc = make(*args, opt, None, 0, ctypes.byref(nbytes), ctypes.byref(ws))
     if rc != MLA_ERR_BUFFER:
         check(rc, lib)
     buf = np.zeros(nbytes.value, dtype=np.uint8)
-    rc = lib.mla_decode_plan_ex(*args, opt, buf.ctypes.data_as(_P), buf.nbytes, ctypes.byref(nbytes),
-                                ctypes.byref(ws))
+    rc = make(*args, opt, buf.ctypes.data_as(_P), buf.nbytes, ctypes.byref(nbytes), ctypes.byref(ws))
     check(rc, lib)
     return buf, int(ws.value)
 
@@ -192,6 +209,31 @@ def run_scaled(*args) -> None:
     e4m3 cache with a scale for each block of tokens."""
     lib = _lib or load()
     check(lib.mla_decode_run_scaled(*args), lib)
+
+
+def run_tree(*args) -> None:
+    """mla_decode_run_tree, arguments as in the header (pointers as ints): the decode of trees of
+    verify tokens."""
+    lib = _lib or load()
+    check(lib.mla_decode_run_tree(*args), lib)
+
+
+def tree_masks(*args) -> None:
+    """mla_tree_masks, arguments as in the header (pointers as ints)."""
+    lib = _lib or load()
+    check(lib.mla_tree_masks(*args), lib)
+
+
+def tree_verify(*args) -> None:
+    """mla_tree_verify, arguments as in the header (pointers as ints)."""
+    lib = _lib or load()
+    check(lib.mla_tree_verify(*args), lib)
+
+
+def cache_commit(*args) -> None:
+    """mla_cache_commit, arguments as in the header (pointers as ints)."""
+    lib = _lib or load()
+    check(lib.mla_cache_commit(*args), lib)
 
 
 def key_weights_workspace(plan_host: np.ndarray) -> int:

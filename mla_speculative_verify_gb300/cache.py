@@ -1,8 +1,9 @@
 """The paged latent cache's own operators on torch tensors: ``append`` writes rows into a
-block-scaled e4m3 cache, ``evict`` keeps the keys with the largest accumulated weight.
+block-scaled e4m3 cache, ``evict`` keeps the keys with the largest accumulated weight, ``commit``
+keeps the accepted path of a tree of drafted tokens.
 
-Both only check shapes, dtypes and devices and pass raw pointers through to
-``mla_cache_append`` / ``mla_cache_evict``; what they compute is stated in
+They only check shapes, dtypes and devices and pass raw pointers through to
+``mla_cache_append`` / ``mla_cache_evict`` / ``mla_cache_commit``; what they compute is stated in
 include/mla_decode.h. They enqueue on ``stream`` (default: torch's current stream of the
 tensors' device) and do not synchronise, so they can be captured in a CUDA graph; what scratch
 ``evict`` needs comes from torch's allocator, call by call. Device-side faults (lengths that do not
@@ -171,3 +172,44 @@ def evict(weights: torch.Tensor, seq_lens: torch.Tensor, budget: int, n_first: i
               block, page_table.data_ptr(), stride, pages, kv_dst.data_ptr(), _ptr(scales_dst),
               page_table_dst.data_ptr(), stride_dst, pages_dst, kept.data_ptr(), seq_lens_dst.data_ptr(),
               _ptr(weights_dst), wd_stride, _ptr(scratch), need, _ptr(status), stream_handle(index, stream))
+
+
+def commit(kv: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, cu_nodes: torch.Tensor,
+           path: torch.Tensor, accepted: torch.Tensor, seq_lens_dst: torch.Tensor, scales: torch.Tensor | None = None,
+           status: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> None:
+    """After ``tree.verify``: in every layer of ``kv`` [layers, pages, 64, 576] (or one layer's
+    [pages, 64, 576]; bf16, or e4m3 as uint8 or float8_e4m3fn, with ``scales`` [layers, pages, 64 /
+    block_tokens] if block-scaled) the rows of the accepted nodes move to the front of the
+    request's verify tokens, in place, and become its last keys.
+
+    ``seq_lens`` [batch] int32 are the lengths with all verify tokens, of which request b has
+    ``cu_nodes[b + 1] - cu_nodes[b]``; ``path`` [batch, width] and ``accepted`` [batch] int32 are
+    what ``tree.verify`` wrote. ``seq_lens_dst`` [batch] int32 receives the lengths without the
+    tokens that were not accepted; it must not be ``seq_lens`` itself. A block that receives rows
+    gets the largest of their scales (and of its own, where older rows stay in it).
+    """
+    index = _cuda_index(kv)
+    bf16 = kv.dtype == torch.bfloat16
+    layers, pages = (1, kv.shape[0]) if kv.dim() == 3 else (kv.shape[0], kv.shape[1]) if kv.dim() == 4 else (0, 0)
+    lead = (pages,) if kv.dim() == 3 else (layers, pages)
+    check_tensor("kv", kv, torch.bfloat16 if bf16 else E4M3, (*lead, *ROW), index)
+    block = 0
+    if scales is not None:
+        if scales.dim() != kv.dim() - 1:
+            raise ValueError(f"scales must be float32 {[*lead, '64 / block_tokens']}, got {list(scales.shape)}")
+        check_tensor("scales", scales, torch.float32, (*lead, scales.shape[-1]), index)
+        block = check_scales("scales", scales.view(-1, scales.shape[-1]), layers * pages, index)
+    batch = page_table.shape[0] if page_table.dim() else 0
+    stride = check_table("page_table", page_table, batch, index)
+    check_tensor("seq_lens", seq_lens, torch.int32, (batch,), index)
+    check_tensor("cu_nodes", cu_nodes, torch.int32, (batch + 1,), index)
+    width = path.shape[1] if path.dim() == 2 else 0
+    check_tensor("path", path, torch.int32, (batch, width), index)
+    check_tensor("accepted", accepted, torch.int32, (batch,), index)
+    check_tensor("seq_lens_dst", seq_lens_dst, torch.int32, (batch,), index)
+    if status is not None:
+        check_tensor("status", status, torch.int32, (1,), index)
+    on_device(index, binding.cache_commit, binding.MLA_KV_BF16 if bf16 else binding.MLA_KV_FP8_E4M3, kv.data_ptr(),
+              _ptr(scales), block, layers, page_table.data_ptr(), stride, pages, seq_lens.data_ptr(),
+              cu_nodes.data_ptr(), batch, path.data_ptr(), width, accepted.data_ptr(), seq_lens_dst.data_ptr(),
+              _ptr(status), stream_handle(index, stream))

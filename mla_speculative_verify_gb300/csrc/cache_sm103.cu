@@ -840,6 +840,153 @@ __global__ void __launch_bounds__(kGatherThreads, 3) evict_gather_kernel(GatherA
   }
 }
 
+// ------------------------------------------------------------------ commit
+// Accepted rows path[k] of a request's verify tokens become its tokens k, in every layer. As path
+// rises, path[k] >= k: rows are taken in order, a batch of them into registers, one barrier, and
+// written; a later batch's sources lie behind all of an earlier one's places. A CTA takes some layers
+// of one request, so that the path and the page ids are read once for them and many rows are in
+// flight together.
+constexpr int kCommitThreads = 288;   // 4 bf16 rows of 72 16-byte pieces, or 8 e4m3 rows of 36
+constexpr int kCommitDeep = 4;        // rows in flight to a thread's piece
+constexpr int kCommitMaxPath = 1024;  // accepted nodes of a request
+constexpr int kCommitEntries = 1024;  // (layer, row) pairs whose scales a CTA holds at a time
+
+struct CommitArgs {
+  uint4* kv;
+  float* scales;
+  const int32_t* page_table;
+  int pt_stride, num_pages, layers, layers_cta, block_log2, path_stride;
+  const int32_t* seq_lens;
+  const int32_t* cu;
+  const int32_t* path;
+  const int32_t* accepted;
+  int32_t* new_lens;
+  int32_t* status;
+};
+
+template <int P, bool kScaled>
+__global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
+  constexpr int kGroups = kCommitThreads / P;  // rows at a time
+  __shared__ int src_row[kCommitMaxPath], dst_row[kCommitMaxPath];  // cache rows, or -1
+  __shared__ float s_of[kScaled ? kCommitEntries : 1], r_of[kScaled ? kCommitEntries : 1];
+  __shared__ float old_ratio[kScaled ? kCommitEntries : 1];
+  __shared__ int first_moved;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int q = a.cu[b + 1] - a.cu[b], len = a.seq_lens[b], acc = a.accepted[b];
+  const int n0 = len - q;
+  const bool fits = q >= 0 && n0 >= 0 && acc >= 0 && acc <= q && acc <= a.path_stride &&
+                    (len == 0 || (len - 1) / kPage < a.pt_stride);
+  if (blockIdx.y == 0 && tid == 0) {
+    a.new_lens[b] = fits ? n0 + acc : len;
+    if (!fits) report(a.status, MLA_DEVICE_PLAN_MISMATCH);
+  }
+  if (!fits) return;
+  if (tid == 0) first_moved = acc;
+  __syncthreads();
+  const int32_t* path = a.path + (size_t)b * a.path_stride;
+  const int32_t* table = a.page_table + (size_t)b * a.pt_stride;
+  bool bad = false;
+  for (int k = tid; k < acc; k += kCommitThreads) {
+    const int p = path[k];
+    bad |= p < 0 || p >= q || (k > 0 && path[k - 1] >= p);
+    if (p != k) atomicMin(&first_moved, k);
+  }
+  if (__syncthreads_or(bad)) {  // not a rising path: the rows stay
+    if (blockIdx.y == 0 && tid == 0) {
+      a.new_lens[b] = len;
+      report(a.status, MLA_DEVICE_BAD_TREE);
+    }
+    return;
+  }
+  const int k0 = first_moved, m = acc - k0;  // path[k] = k before k0, and nowhere from there on
+  if (m == 0) return;
+  bool bad_page = false;
+  auto row_of = [&](int pos) {
+    const int page = table[pos / kPage];
+    if (page < 0 || page >= a.num_pages) {
+      bad_page = true;
+      return -1;
+    }
+    return page * kPage + pos % kPage;
+  };
+  for (int i = tid; i < m; i += kCommitThreads) {
+    src_row[i] = row_of(n0 + path[k0 + i]);
+    dst_row[i] = row_of(n0 + k0 + i);
+  }
+  if (bad_page && blockIdx.y == 0) report(a.status, MLA_DEVICE_BAD_PAGE);
+  const int stay = n0 + k0;  // rows before this position keep their places
+  const int tokens = 1 << a.block_log2;
+  const int n_old = kScaled ? stay & (tokens - 1) : 0;  // of them, in the first new row's block
+  __syncthreads();
+  const size_t layer_rows = (size_t)a.num_pages * kPage;
+  const int l_end = min(a.layers, (int)(blockIdx.y + 1) * a.layers_cta);
+  const int l_step = kScaled ? max(1, kCommitEntries / m) : a.layers_cta;
+  const int piece = tid % P, grp = tid / P;
+  for (int l0 = blockIdx.y * a.layers_cta; l0 < l_end; l0 += l_step) {
+    const int items = min(l_step, l_end - l0) * m;
+    if constexpr (kScaled) {
+      // the largest scale among a new block's rows, its own too where it holds rows that stay
+      auto scale_at = [&](int l, int row) -> float* {
+        return a.scales + ((layer_rows * (size_t)(l0 + l) + (size_t)row) >> a.block_log2);
+      };
+      for (int e = tid; e < items; e += kCommitThreads) {
+        const int row = src_row[e % m];
+        s_of[e] = row < 0 ? 0.f : *scale_at(e / m, row);
+      }
+      if (tid < items / m) old_ratio[tid] = n_old > 0 && dst_row[0] >= 0 ? *scale_at(tid, dst_row[0]) : 0.f;
+      __syncthreads();
+      for (int e = tid; e < items; e += kCommitThreads) {
+        const int l = e / m, i = e % m;
+        // rows of the same block: positions stay + j with the same number of the block
+        const int blk = (stay + i) >> a.block_log2;
+        const int j0 = max(0, (blk << a.block_log2) - stay), j1 = min(m, ((blk + 1) << a.block_log2) - stay);
+        float top = j0 == 0 && n_old > 0 ? old_ratio[l] : 0.f;
+        for (int j = j0; j < j1; ++j) top = fmaxf(top, s_of[l * m + j]);
+        r_of[e] = top > 0.f ? s_of[e] / top : 1.f;
+        if (i == j0 && dst_row[i] >= 0) *scale_at(l, dst_row[i]) = top;
+      }
+      __syncthreads();
+      // codes of the rows that stay in a block whose scale has grown
+      if (n_old > 0 && dst_row[0] >= 0) {
+        const int row0 = dst_row[0] - n_old;
+        for (int e = grp; e < items / m * n_old; e += kGroups) {
+          const int l = e / n_old;
+          const float was = old_ratio[l], now = *scale_at(l, dst_row[0]);
+          if (grp >= kGroups || was == now || !(now > 0.f)) continue;
+          uint4* at = a.kv + (layer_rows * (size_t)(l0 + l) + (size_t)(row0 + e % n_old)) * P + piece;
+          const Rescale to(was / now);
+          const uint4 v = *at;
+          *at = make_uint4(to(v.x), to(v.y), to(v.z), to(v.w));
+        }
+      }
+    }
+    for (int e0 = 0; e0 < items; e0 += kGroups * kCommitDeep) {
+      uint4 v[kCommitDeep];
+#pragma unroll
+      for (int d = 0; d < kCommitDeep; ++d) {
+        const int e = e0 + kGroups * d + grp;
+        if (grp < kGroups && e < items && src_row[e % m] >= 0)
+          v[d] = a.kv[(layer_rows * (size_t)(l0 + e / m) + (size_t)src_row[e % m]) * P + piece];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int d = 0; d < kCommitDeep; ++d) {
+        const int e = e0 + kGroups * d + grp;
+        if (grp < kGroups && e < items && src_row[e % m] >= 0 && dst_row[e % m] >= 0) {
+          if constexpr (kScaled) {
+            if (r_of[e] != 1.f) {
+              const Rescale to(r_of[e]);
+              v[d] = make_uint4(to(v[d].x), to(v[d].y), to(v[d].z), to(v[d].w));
+            }
+          }
+          a.kv[(layer_rows * (size_t)(l0 + e / m) + (size_t)dst_row[e % m]) * P + piece] = v[d];
+        }
+      }
+    }
+    if (kScaled) __syncthreads();  // (the next layers' scales go where these are read)
+  }
+}
+
 // Whether a row of [batch, a_stride] (of which a_row entries are used) overlaps one of [batch,
 // b_stride]. Rows of both are in order, so one walk over the two lists finds it.
 bool rows_overlap(const float* a, long long a_stride, int a_row, const float* b, long long b_stride, int b_row, int batch) {
@@ -1030,5 +1177,58 @@ extern "C" int mla_cache_evict(const float* weights, long long weights_stride, c
                                     : evict_gather_kernel<36, false>;
   ce = cudaLaunchKernelEx(&cfg, fn, g);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "eviction gather kernel launch: %s", cudaGetErrorString(ce));
+  return MLA_OK;
+}
+
+extern "C" int mla_cache_commit(int kv_dtype, void* kv_cache, float* kv_scales, int block_tokens, int layers,
+                                const int32_t* page_table, int page_table_stride, int num_pages,
+                                const int32_t* seq_lens, const int32_t* cu_nodes, int batch, const int32_t* path,
+                                int path_stride, const int32_t* accepted, int32_t* seq_lens_dst, int32_t* status_dev,
+                                void* stream) {
+  clear_error();
+  if (batch < 1) return set_error(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
+  if (layers < 1 || layers > 65535) return set_error(MLA_ERR_INVALID_ARG, "layers must be in [1, 65535] (got %d)", layers);
+  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3)
+    return set_error(MLA_ERR_INVALID_ARG, "kv_dtype must be MLA_KV_BF16 or MLA_KV_FP8_E4M3 (got %d)", kv_dtype);
+  const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
+  if (!kv_cache || !page_table || !seq_lens || !cu_nodes || !path || !accepted || !seq_lens_dst)
+    return set_error(MLA_ERR_INVALID_ARG,
+                     "kv_cache, page_table, seq_lens, cu_nodes, path, accepted and seq_lens_dst must not be NULL");
+  if (!aligned16(kv_cache)) return set_error(MLA_ERR_INVALID_ARG, "kv_cache must be 16-byte aligned");
+  for (const void* p : {(const void*)kv_scales, (const void*)page_table, (const void*)seq_lens, (const void*)cu_nodes,
+                        (const void*)path, (const void*)accepted, (const void*)seq_lens_dst, (const void*)status_dev})
+    if (!aligned4(p)) return set_error(MLA_ERR_INVALID_ARG, "scales, tables, lengths, path and status_dev must be 4-byte aligned");
+  if (kv_scales && !fp8) return set_error(MLA_ERR_INVALID_ARG, "block scales belong to an fp8 e4m3 cache");
+  const int bl = kv_scales ? block_log2_of(block_tokens) : 0;
+  if (bl < 0) return set_error(MLA_ERR_UNSUPPORTED, "block_tokens must be 1, 2, 4, .. 64 (got %d)", block_tokens);
+  if (num_pages < 1 || (long long)num_pages * kPage > INT32_MAX)
+    return set_error(MLA_ERR_INVALID_ARG, "num_pages out of range (got %d)", num_pages);
+  if (page_table_stride < 1) return set_error(MLA_ERR_INVALID_ARG, "page_table_stride must be >= 1 (got %d)", page_table_stride);
+  if (path_stride < 1 || path_stride > kCommitMaxPath)
+    return set_error(MLA_ERR_INVALID_ARG, "path_stride must be in [1, %d] (got %d)", kCommitMaxPath, path_stride);
+  // every CTA of a request reads these while one of them writes the new length
+  const uintptr_t d0 = (uintptr_t)seq_lens_dst, d1 = d0 + 4ull * (size_t)batch;
+  auto meets = [&](const void* p, size_t n) { return (uintptr_t)p < d1 && d0 < (uintptr_t)p + n; };
+  if (meets(seq_lens, 4ull * (size_t)batch) || meets(accepted, 4ull * (size_t)batch) || meets(cu_nodes, 4ull * ((size_t)batch + 1)) ||
+      meets(path, 4ull * (size_t)batch * (size_t)path_stride))
+    return set_error(MLA_ERR_INVALID_ARG, "seq_lens_dst must not overlap seq_lens, cu_nodes, path or accepted");
+  DeviceKernels device;
+  const int rc = current_device_ready(&device);
+  if (rc != MLA_OK) return rc;
+  // layers to a CTA: enough CTAs for all SMs several times over first, then fewer reads of the path
+  const long long waves = 6LL * device.sms;
+  const int per = (int)std::min<long long>(16, std::max<long long>(1, (long long)layers * batch / waves));
+  CommitArgs a{(uint4*)kv_cache, kv_scales, page_table, page_table_stride, num_pages, layers, per, bl, path_stride,
+               seq_lens, cu_nodes, path, accepted, seq_lens_dst, status_dev};
+  const dim3 grid((unsigned)batch, (unsigned)((layers + per - 1) / per));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (kv_scales)
+    commit_kernel<36, true><<<grid, kCommitThreads, 0, st>>>(a);
+  else if (fp8)
+    commit_kernel<36, false><<<grid, kCommitThreads, 0, st>>>(a);
+  else
+    commit_kernel<72, false><<<grid, kCommitThreads, 0, st>>>(a);
+  const cudaError_t ce = cudaGetLastError();
+  if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "commit kernel launch: %s", cudaGetErrorString(ce));
   return MLA_OK;
 }

@@ -18,7 +18,7 @@ constexpr long long kWaitBudgetTest = 4000000LL; // ~2 ms: the budget of a call 
 // kernels' attributes could be set. A failure there refuses the entry point that it belongs to.
 struct DeviceKernels {
   int sms = 0;
-  cudaError_t select = cudaSuccess, weights = cudaSuccess;
+  cudaError_t select = cudaSuccess, weights = cudaSuccess, verify = cudaSuccess;
   int weights_regs = 0;  // registers a thread of the key weights' kernel, the lower of its two forms
 };
 
@@ -41,6 +41,8 @@ struct Params {
   int skip_copy;          // page of the first unit whose copy is never issued (timeout test), or -1
   const float* kv_scales; // block-scaled e4m3 cache: [num_pages, 64 >> block_log2], else NULL
   int block_log2;         // log2 of the tokens that share a scale
+  const uint32_t* tree_masks;  // a tree of verify tokens: [sum q_lens, mask_words] visibility bits, else NULL
+  int mask_words;
 };
 
 __device__ __forceinline__ void report(int32_t* status, int bits) {

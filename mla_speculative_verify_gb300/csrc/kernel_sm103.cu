@@ -270,7 +270,11 @@ struct SoftmaxArgs {
 // scores are taken relative to the references once, for the vote and for the weights (268 -> 256
 // us with one maximum for the vote). Now 223 us: 0.40 of the measured copy rate, bound by this
 // chain of steps, ~1400 of a tile's 2000 cycles.
-template <int NCH, bool kFp8, bool kScaled>
+//
+// kTree: verify token i sees the keys before the request's verify tokens, and of those the ones
+// whose bit its mask has. Only tiles that reach into the verify tokens' own keys look at masks;
+// each thread gathers the bits of its elements while it would wait for the scores.
+template <int NCH, bool kFp8, bool kScaled, bool kTree>
 __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params& p) {
   constexpr int NC = 4 * NCH;
   using G = Geo<kFp8>;
@@ -304,7 +308,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
     int lim = 0;
     if (sidx < a.nrows) {
       const int i = (a.qrow0 + sidx) / p.H - a.tok0;  // verify token of this packed row
-      lim = a.ctx - a.qlen + i + 1;
+      lim = a.ctx - a.qlen + (kTree ? 0 : i + 1);
     }
     ms->lim[sidx] = lim;
     ms->ref[sidx] = -INFINITY;
@@ -397,6 +401,24 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
   const float scale = p.score_scale_log2;
   for (int t = 0; !stop && t < a.ntiles; ++t) {
     const int sb = t & 1;
+    uint32_t sees = 0;  // kTree: bit e: element e of a tile that is not wholly visible
+    if constexpr (kTree) {
+      if (a.kv_begin + (t + 1) * kTileKeys > lim_min) {
+        const int draft0 = a.kv_begin + t * kTileKeys + kr0 - (a.ctx - a.qlen);  // this thread's first key among the verify tokens
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const int row = 16 * (i >> 1) + cp + (i & 1);
+          const uint32_t* words = p.tree_masks + (size_t)((a.qrow0 + row) / p.H) * p.mask_words;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int d = draft0 + 8 * k;
+            bool on = row < a.nrows && d < a.qlen;
+            if (on && d >= 0) on = (__ldg(words + (d >> 5)) >> (d & 31)) & 1u;
+            sees |= (uint32_t)on << (4 * (i >> 1) + 2 * k + (i & 1));
+          }
+        }
+      }
+    }
     float inv_ks[2];  // kScaled: 1 / v of this thread's two keys
     float x[NC];
     float xr[kScaled ? NC : 1];  // kScaled: x relative to the references
@@ -472,7 +494,8 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
             const int key = key0 + 8 * ((i >> 1) & 1);
-            x[i] = (key < a.kv_end && key < ms->lim[16 * (i / 4) + cp + (i & 1)]) ? x[i] : -INFINITY;
+            const bool on = kTree ? (sees >> i) & 1u : key < ms->lim[16 * (i / 4) + cp + (i & 1)];
+            x[i] = (key < a.kv_end && on) ? x[i] : -INFINITY;
           }
         }
         relative();
@@ -495,7 +518,10 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
         for (int j = 0; j < 4; ++j) {
           float v = x[4 * c + j] * csv[j];
           const int key = key0 + 8 * (j >> 1);
-          if (!unmasked) v = (key < a.kv_end && key < ms->lim[n0 + (j & 1)]) ? v : -INFINITY;
+          if (!unmasked) {
+            const bool on = kTree ? (sees >> (4 * c + j)) & 1u : key < ms->lim[n0 + (j & 1)];
+            v = (key < a.kv_end && on) ? v : -INFINITY;
+          }
           x[4 * c + j] = v;
           need |= v > rrv[j] + kMoveAbove;
         }
@@ -774,7 +800,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
   return issued_ot;
 }
 
-template <bool kFp8, bool kScaled>
+template <bool kFp8, bool kScaled, bool kTree>
 __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
     fold_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_kv, Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1079,11 +1105,11 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
                         reinterpret_cast<const float4*>(smem + kOffScales)};
     bool issued_ot;
     if (nch == 1)
-      issued_ot = softmax_role<1, kFp8, kScaled>(a, p);
+      issued_ot = softmax_role<1, kFp8, kScaled, kTree>(a, p);
     else if (nch == 2)
-      issued_ot = softmax_role<2, kFp8, kScaled>(a, p);
+      issued_ot = softmax_role<2, kFp8, kScaled, kTree>(a, p);
     else
-      issued_ot = softmax_role<3, kFp8, kScaled>(a, p);
+      issued_ot = softmax_role<3, kFp8, kScaled, kTree>(a, p);
     // the O^T MMAs this lane issued must retire before TMEM is released
     if (issued_ot) drain_mmas(&ms->mma_done[4 + (warp - 1 - kMma)], p.wait_budget);
     __syncwarp();
@@ -1200,7 +1226,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) lse_merge_kernel(cons
       const float4 a = acc_s[i][lane];
       r.x += f * a.x; r.y += f * a.y; r.z += f * a.z; r.w += f * a.w;
     }
-    const float inv = 1.f / l;
+    const float inv = l > 0.f ? 1.f / l : 0.f;  // (a tree's mask may leave a row without keys)
     const int qr = m.qrow0 + row;
     if constexpr (kCols == 4)
       *reinterpret_cast<uint2*>(out + (size_t)qr * kDv + col) =
@@ -1296,6 +1322,7 @@ static std::mutex g_dev_mu;
 
 cudaError_t set_weights_kernel_attributes(int* regs);  // defined next to those kernels
 cudaError_t set_select_kernel_attributes();
+cudaError_t set_verify_kernel_attributes();
 
 static int prepare_device(int dev) {
   if (dev < 0 || dev >= 64) return set_error(MLA_ERR_CUDA, "device ordinal %d out of range", dev);
@@ -1312,13 +1339,16 @@ static int prepare_device(int dev) {
     return set_error(MLA_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a (GB300)", dev, d.major,
                      d.minor);
   if (!d.attrs_set) {
-    for (auto fn : {fold_decode_kernel<false, false>, fold_decode_kernel<true, false>, fold_decode_kernel<true, true>}) {
+    for (auto fn : {fold_decode_kernel<false, false, false>, fold_decode_kernel<true, false, false>,
+                    fold_decode_kernel<true, true, false>, fold_decode_kernel<false, false, true>,
+                    fold_decode_kernel<true, false, true>, fold_decode_kernel<true, true, true>}) {
       const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesScaled);
       if (e != cudaSuccess) return set_error(MLA_ERR_CUDA, "cudaFuncSetAttribute failed: %s", cudaGetErrorString(e));
     }
     d.kernels.weights = set_weights_kernel_attributes(&d.kernels.weights_regs);
     d.kernels.select = set_select_kernel_attributes();
-    if (d.kernels.weights != cudaSuccess || d.kernels.select != cudaSuccess)
+    d.kernels.verify = set_verify_kernel_attributes();
+    if (d.kernels.weights != cudaSuccess || d.kernels.select != cudaSuccess || d.kernels.verify != cudaSuccess)
       (void)cudaGetLastError();  // (it would show at the next launch)
     d.attrs_set = true;
   }
@@ -1352,12 +1382,13 @@ static CUresult encode_chunked(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMa
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// mla_decode_run, and with kv_scales (the caller has checked them) mla_decode_run_scaled.
+// mla_decode_run, and with kv_scales or tree_masks (the caller has checked them) mla_decode_run_scaled
+// and mla_decode_run_tree.
 static int decode_run(const void* plan_dev, const void* plan_host, const PlanHeader* h, const void* q,
                       const void* kv_cache, const float* kv_scales, int block_log2, const int32_t* page_table,
                       int page_table_stride, int num_pages, const int32_t* seq_lens, const int32_t* q_lens,
-                      float sm_scale, float kv_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
-                      int32_t* status_dev, void* stream) {
+                      const uint32_t* tree_masks, int mask_words, float sm_scale, float kv_scale, void* out, float* lse,
+                      void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
   int rc = MLA_OK;
   if (!plan_dev || !q || !kv_cache || !page_table || !seq_lens || !q_lens || !out)
     return set_error(MLA_ERR_INVALID_ARG, "plan_dev, q, kv_cache, page_table, seq_lens, q_lens and out must not be NULL");
@@ -1417,18 +1448,19 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
   prm.skip_copy = h->debug_skip_copy - 1;
   prm.kv_scales = kv_scales;
   prm.block_log2 = block_log2;
+  prm.tree_masks = tree_masks;
+  prm.mask_words = mask_words;
   cudaStream_t st = (cudaStream_t)stream;
   if (h->cta_pair) {
     if (fp8) return set_error(MLA_ERR_PLAN, "a two-CTA plan needs a bf16 cache");
     rc = launch_pair_kernel(dev, h, q, kv_cache, num_pages, prm, st);
     if (rc != MLA_OK) return rc;
   } else {
-    if (kv_scales)
-      fold_decode_kernel<true, true><<<h->n_units, Roles<true>::kThreads, kSmemBytesScaled, st>>>(tq, tkv, prm);
-    else if (fp8)
-      fold_decode_kernel<true, false><<<h->n_units, Roles<true>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
-    else
-      fold_decode_kernel<false, false><<<h->n_units, Roles<false>::kThreads, kSmemBytes, st>>>(tq, tkv, prm);
+    auto fn = kv_scales ? (tree_masks ? fold_decode_kernel<true, true, true> : fold_decode_kernel<true, true, false>)
+              : fp8     ? (tree_masks ? fold_decode_kernel<true, false, true> : fold_decode_kernel<true, false, false>)
+                        : (tree_masks ? fold_decode_kernel<false, false, true> : fold_decode_kernel<false, false, false>);
+    fn<<<h->n_units, fp8 ? Roles<true>::kThreads : Roles<false>::kThreads, kv_scales ? kSmemBytesScaled : kSmemBytes,
+         st>>>(tq, tkv, prm);
     ce = cudaGetLastError();
     if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "fold kernel launch: %s", cudaGetErrorString(ce));
   }
@@ -1483,7 +1515,7 @@ extern "C" int mla_decode_run(const void* plan_dev, const void* plan_host, size_
   const int rc = check_plan(plan_host, plan_bytes, &h);
   if (rc != MLA_OK) return rc;
   return decode_run(plan_dev, plan_host, h, q, kv_cache, nullptr, 0, page_table, page_table_stride, num_pages, seq_lens,
-                    q_lens, sm_scale, kv_scale, out, lse, workspace, workspace_bytes, status_dev, stream);
+                    q_lens, nullptr, 0, sm_scale, kv_scale, out, lse, workspace, workspace_bytes, status_dev, stream);
 }
 
 extern "C" int mla_decode_run_scaled(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
@@ -1503,7 +1535,35 @@ extern "C" int mla_decode_run_scaled(const void* plan_dev, const void* plan_host
   if (!kv_scales || ((uintptr_t)kv_scales & 3u))
     return set_error(MLA_ERR_INVALID_ARG, "kv_scales must be a 4-byte aligned pointer and not NULL");
   return decode_run(plan_dev, plan_host, h, q, kv_cache, kv_scales, bl, page_table, page_table_stride, num_pages,
-                    seq_lens, q_lens, sm_scale, 1.0f, out, lse, workspace, workspace_bytes, status_dev, stream);
+                    seq_lens, q_lens, nullptr, 0, sm_scale, 1.0f, out, lse, workspace, workspace_bytes, status_dev, stream);
+}
+
+extern "C" int mla_decode_run_tree(const void* plan_dev, const void* plan_host, size_t plan_bytes, const void* q,
+                                   const void* kv_cache, const float* kv_scales, int block_tokens,
+                                   const int32_t* page_table, int page_table_stride, int num_pages,
+                                   const int32_t* seq_lens, const int32_t* q_lens, const uint32_t* tree_masks,
+                                   int mask_words, float sm_scale, float kv_scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, int32_t* status_dev, void* stream) {
+  clear_error();
+  const PlanHeader* h = nullptr;
+  const int rc = check_plan(plan_host, plan_bytes, &h);
+  if (rc != MLA_OK) return rc;
+  if (kv_scales && h->kv_dtype != MLA_KV_FP8_E4M3)
+    return set_error(MLA_ERR_INVALID_ARG, "block scales belong to an fp8 e4m3 cache: plan with MLA_KV_FP8_E4M3");
+  const int bl = kv_scales ? block_log2_of(block_tokens) : 0;
+  if (bl < 0) return set_error(MLA_ERR_UNSUPPORTED, "block_tokens must be 1, 2, 4, .. 64 (got %d)", block_tokens);
+  if ((uintptr_t)kv_scales & 3u) return set_error(MLA_ERR_INVALID_ARG, "kv_scales must be 4-byte aligned");
+  if (!tree_masks || ((uintptr_t)tree_masks & 3u))
+    return set_error(MLA_ERR_INVALID_ARG, "tree_masks must be a 4-byte aligned pointer and not NULL");
+  if (h->cta_pair) return set_error(MLA_ERR_UNSUPPORTED, "a two-CTA plan takes no tree");
+  const PlanRequest* reqs = (const PlanRequest*)((const uint8_t*)plan_host + h->req_off);
+  int most = 0;
+  for (int i = 0; i < h->batch; ++i) most = std::max(most, reqs[i].q);
+  if (mask_words < (most + 31) / 32)
+    return set_error(MLA_ERR_INVALID_ARG, "mask_words %d is too few for the %d tokens of the widest request", mask_words, most);
+  return decode_run(plan_dev, plan_host, h, q, kv_cache, kv_scales, bl, page_table, page_table_stride, num_pages, seq_lens,
+                    q_lens, tree_masks, mask_words, sm_scale, kv_scales ? 1.0f : kv_scale, out, lse, workspace,
+                    workspace_bytes, status_dev, stream);
 }
 
 extern "C" int mla_device_pair_slots(int device, int* slots) {

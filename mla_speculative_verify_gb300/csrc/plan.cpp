@@ -56,10 +56,10 @@ size_t workspace_bytes_for(int n_part_rows) {
 
 using namespace mla;
 
-extern "C" int mla_decode_plan_ex(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads,
-                                  int page_size, int kv_dtype, int num_sms, const mla_plan_options* opts,
-                                  void* plan_buf, size_t plan_buf_bytes, size_t* plan_bytes_out,
-                                  size_t* workspace_bytes_out) {
+// mla_decode_plan_ex, and with whole_requests mla_decode_plan_tree: a fold group is all of a request's tokens.
+static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads, int page_size,
+                     int kv_dtype, int num_sms, const mla_plan_options* opts, bool whole_requests, void* plan_buf,
+                     size_t plan_buf_bytes, size_t* plan_bytes_out, size_t* workspace_bytes_out) {
   clear_error();
   if (!seq_lens_h || !q_lens_h) return set_error(MLA_ERR_INVALID_ARG, "seq_lens_h and q_lens_h must not be NULL");
   if (batch < 1) return set_error(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
@@ -83,6 +83,8 @@ extern "C" int mla_decode_plan_ex(const int32_t* seq_lens_h, const int32_t* q_le
     return set_error(MLA_ERR_INVALID_ARG, "plan options must be >= 0");
   if (o.force_splits > 0 && o.unit_pages > 0)
     return set_error(MLA_ERR_INVALID_ARG, "force_splits and unit_pages exclude each other");
+  if (whole_requests && (o.force_fold > 0 || o.cta_pair > 0))
+    return set_error(MLA_ERR_INVALID_ARG, "a plan for trees takes neither force_fold nor cta_pair");
 
   long long total_q = 0;
   int max_pages = 0;
@@ -117,7 +119,7 @@ extern "C" int mla_decode_plan_ex(const int32_t* seq_lens_h, const int32_t* q_le
   int tok0 = 0;
   for (int b = 0; b < batch; ++b) {
     int ctx = seq_lens_h[b], q = q_lens_h[b];
-    int F = o.force_fold > 0 ? o.force_fold : fold_factor(q, num_heads);
+    int F = whole_requests ? q : o.force_fold > 0 ? o.force_fold : fold_factor(q, num_heads);
     reqs[b] = PlanRequest{ctx, q, tok0, F};
     int R = F * num_heads;                       // packed rows per fold group
     int n_rt = (R + cap - 1) / cap;
@@ -298,6 +300,24 @@ extern "C" int mla_decode_plan_ex(const int32_t* seq_lens_h, const int32_t* q_le
   if (!units.empty()) memcpy(base + units_off, units.data(), sizeof(PlanUnit) * units.size());
   if (!merges.empty()) memcpy(base + merge_off, merges.data(), sizeof(PlanMerge) * merges.size());
   return MLA_OK;
+}
+
+extern "C" int mla_decode_plan_ex(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads,
+                                  int page_size, int kv_dtype, int num_sms, const mla_plan_options* opts,
+                                  void* plan_buf, size_t plan_buf_bytes, size_t* plan_bytes_out,
+                                  size_t* workspace_bytes_out) {
+  return make_plan(seq_lens_h, q_lens_h, batch, num_heads, page_size, kv_dtype, num_sms, opts, false, plan_buf,
+                   plan_buf_bytes, plan_bytes_out, workspace_bytes_out);
+}
+
+// A tree's size has any divisors: folded by the largest one a tree of 29 tokens would run as 29 tiles
+// of one token each. A row's mask is its own, so the tiles are cut from all of a request's rows.
+extern "C" int mla_decode_plan_tree(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads,
+                                    int page_size, int kv_dtype, int num_sms, const mla_plan_options* opts,
+                                    void* plan_buf, size_t plan_buf_bytes, size_t* plan_bytes_out,
+                                    size_t* workspace_bytes_out) {
+  return make_plan(seq_lens_h, q_lens_h, batch, num_heads, page_size, kv_dtype, num_sms, opts, true, plan_buf,
+                   plan_buf_bytes, plan_bytes_out, workspace_bytes_out);
 }
 
 extern "C" int mla_decode_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads,

@@ -26,7 +26,9 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 class VerifyDecoder:
     def __init__(self, seq_lens, q_lens, num_heads: int, kv_dtype: str, device="cuda", num_sms: int | None = None,
-                 options: binding.PlanOptions | None = None):
+                 options: binding.PlanOptions | None = None, tree: bool = False):
+        """``tree``: plan for trees of verify tokens (``run`` with ``tree_masks``), whose sizes need
+        no handy divisors; such a decoder runs chains as well."""
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
@@ -47,7 +49,7 @@ class VerifyDecoder:
                 opts.pair_slots = binding.device_pair_slots(self.device.index)
             options = opts
         self.plan_host, self.workspace_bytes = binding.plan(self.seq_lens, self.q_lens, self.num_heads,
-                                                            KV_DTYPES[kv_dtype], self.num_sms, options)
+                                                            KV_DTYPES[kv_dtype], self.num_sms, options, tree=tree)
         self.info = binding.plan_info(self.plan_host)
         self._plan_host_ptr = self.plan_host.ctypes.data
         self.weights_workspace_bytes = binding.key_weights_workspace(self.plan_host)
@@ -64,11 +66,13 @@ class VerifyDecoder:
             lse: torch.Tensor | None = None, sm_scale: float = SM_SCALE, kv_scale: float = 1.0,
             status: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None,
             seq_lens_dev: torch.Tensor | None = None, q_lens_dev: torch.Tensor | None = None,
-            kv_scales: torch.Tensor | None = None) -> None:
+            kv_scales: torch.Tensor | None = None, tree_masks: torch.Tensor | None = None) -> None:
         """The verify decode. With ``kv_scales`` [pages, 64 / block_tokens] fp32 the e4m3 cache
         is block-scaled: code * scale of its block (``kv_scale`` is then not used). A decoder's
         calls share its workspace: those that may overlap (on two streams, or in two graphs that
-        are replayed at once) need a decoder each."""
+        are replayed at once) need a decoder each. ``tree_masks`` [total_q, words] int32, as
+        ``tree.masks`` writes them: verify token i sees the keys before the request's verify tokens,
+        and of those the ones whose bit is set (a row that sees none gets zeros)."""
         H = self.num_heads
         want_kv = torch.bfloat16 if self.kv_dtype == "bf16" else torch.uint8
         if q.dtype != torch.bfloat16 or tuple(q.shape) != (self.total_q, H, 576) or not q.is_contiguous():
@@ -89,6 +93,22 @@ class VerifyDecoder:
         for t in (q, kv_cache, out, page_table, lse, status):
             if t is not None and t.device != self.device:
                 raise ValueError("all tensors must be on the decoder's device")
+        if tree_masks is not None:
+            index, block = self.device.index, 0
+            words = tree_masks.shape[1] if tree_masks.dim() == 2 else 0
+            check_tensor("tree_masks", tree_masks, torch.int32, (self.total_q, words), index)
+            if kv_scales is not None:
+                if self.kv_dtype != "fp8":
+                    raise ValueError("block scales belong to an fp8 cache")
+                block = check_scales("kv_scales", kv_scales, rows // 64, index)
+            stride = check_table("page_table", page_table, self.seq_lens.shape[0], index)
+            on_device(index, binding.run_tree, self.plan_dev.data_ptr(), self._plan_host_ptr, self.plan_host.nbytes,
+                      q.data_ptr(), kv_cache.data_ptr(), _ptr(kv_scales), block, page_table.data_ptr(), stride,
+                      rows // 64, (seq_lens_dev if seq_lens_dev is not None else self.seq_lens_dev).data_ptr(),
+                      (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(), tree_masks.data_ptr(),
+                      words, sm_scale, kv_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
+                      _ptr(status), stream_handle(index, stream))
+            return
         if kv_scales is not None:
             if self.kv_dtype != "fp8":
                 raise ValueError("block scales belong to an fp8 cache")
