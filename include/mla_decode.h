@@ -426,7 +426,7 @@ int mla_decode_run_tree(const void* plan_dev, const void* plan_host, size_t plan
  * p / noise. So each token that comes out is distributed as p. Greedy: the token of the largest
  * logit (of equal ones the lowest) follows, and a child is accepted where it has that token.
  *
- * NaN logits count as -inf, infinite ones as the largest number. A row of -inf alone accepts
+ * NaN logits count as -inf, infinite ones as the largest number of their type. A row of -inf alone accepts
  * nothing, and its next token is -1. Sums are taken in fp32 in a fixed order: equal inputs give
  * equal results; one that hangs on less than about 1e-6 of a probability may fall either way.
  * path, out_tokens and accepted must not overlap one another or the inputs (refused), and the

@@ -197,8 +197,11 @@ def commit(kv: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, c
     if scales is not None:
         if scales.dim() != kv.dim() - 1:
             raise ValueError(f"scales must be float32 {[*lead, '64 / block_tokens']}, got {list(scales.shape)}")
-        check_tensor("scales", scales, torch.float32, (*lead, scales.shape[-1]), index)
-        block = check_scales("scales", scales.view(-1, scales.shape[-1]), layers * pages, index)
+        per_page = scales.shape[-1]
+        check_tensor("scales", scales, torch.float32, (*lead, per_page), index)
+        if per_page < 1 or PAGE_SIZE % per_page:
+            raise ValueError(f"scales must hold 1, 2, 4, .. 64 scales a page, got {list(scales.shape)}")
+        block = PAGE_SIZE // per_page
     batch = page_table.shape[0] if page_table.dim() else 0
     stride = check_table("page_table", page_table, batch, index)
     check_tensor("seq_lens", seq_lens, torch.int32, (batch,), index)
