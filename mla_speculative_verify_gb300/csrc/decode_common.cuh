@@ -18,7 +18,7 @@ constexpr long long kWaitBudgetTest = 4000000LL; // ~2 ms: the budget of a call 
 // kernels' attributes could be set. A failure there refuses the entry point that it belongs to.
 struct DeviceKernels {
   int sms = 0;
-  cudaError_t select = cudaSuccess, weights = cudaSuccess, verify = cudaSuccess;
+  cudaError_t select = cudaSuccess, weights = cudaSuccess, verify = cudaSuccess, wide = cudaSuccess;
   int weights_regs = 0;  // registers a thread of the key weights' kernel, the lower of its two forms
 };
 

@@ -72,6 +72,7 @@
 #include "plan_format.h"
 #include "decode_common.cuh"
 #include "ptx.cuh"
+#include "softmax_parts.cuh"
 #include "status.h"
 
 namespace mla {
@@ -136,14 +137,6 @@ constexpr uint32_t kTmemO = 0;       // O^T block b at columns 64 b (N <= 64)
 // S^T: bf16: one buffer, partial p of the three at columns 256 + 64 p (N <= 48);
 //       e4m3: two buffers, buffer b at columns 256 + 128 b (Q_hi and Q_lo products, 2 N <= 96)
 constexpr uint32_t kTmemS = 256;
-constexpr float kRefSlack = 8.0f;    // octaves a score may exceed the row reference before it moves
-// e4m3 path: a smaller slack (p <= 16) so that P can be stored times 2^4 (<= 256 < 448,
-// the largest e4m3); probabilities down to 2^-10 of the reference stay in e4m3's normal
-// range (split_p has the smaller ones). The 2^4 is applied by keeping the stored reference
-// kPShiftFp8 octaves below the row's reference, so exp2(s - ref) is already P times 2^4; l
-// carries the same factor, which cancels in O / l and in the LSE.
-constexpr float kRefSlackFp8 = 4.0f;
-constexpr float kPShiftFp8 = 4.0f;
 struct Misc {
   uint64_t bar_q;
   uint64_t kv_full[4], kv_empty[4];
@@ -162,50 +155,6 @@ struct Misc {
 };
 static_assert(offsetof(Misc, ref) % 16 == 0, "float4 reads of ref need 16-byte alignment");
 static_assert(sizeof(Misc) <= kMiscBytes, "misc block too small");
-
-// An fp32 rounded to the precision of e4m3 (4 significant bits, round to nearest even),
-// still as fp32; exact for magnitudes in e4m3's normal range.
-__device__ __forceinline__ float round_to_e4m3_precision(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return __uint_as_float((u + 0x7FFFFu + ((u >> 20) & 1u)) & 0xFFF00000u);
-}
-// Two fp32 -> two e4m3 codes (round to nearest even, saturating), first in the low byte.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-// Two P of one key (<= 256; P times 2^kPShiftFp8) -> an e4m3 part (hi) and the remainder in
-// e5m2 (lo), through f16x2 (11 significant bits, and exact down to 2^-25). Each result holds
-// the first value in its low byte.
-//
-// From 2^-6 on, where e4m3 is normal, lo is rounded to nearest and hi + lo is within 2^-8 of P.
-// Below that hi ends on its grid of 2^-9 and lo has only its own 3 bits left, and what counts is
-// the sum over many keys: a few strong keys beside a long, nearly flat rest, each of it 2^-15 of
-// the largest, the rest as heavy as they are. Rounded to nearest, equal small P would all be off
-// by the same up to 1/8 (with both parts in e4m3 everything below 2^-10 was lost: half of the
-// output over 64k keys). So there lo is rounded up or down by comparing what is cut with a
-// number that the key's position gives: f16's upper byte is an e5m2, so adding d in [0, 256) to
-// the f16's bits and taking that byte rounds up with d's odds. d runs through a sequence that is
-// evenly spread over any stretch of keys (multiples of the golden ratio, modulo 1), so the errors
-// of a sum's keys cancel (64k flat keys beside a strong one: output off by 1.8e-3, its own bf16
-// rounding), and equal calls give equal bits. It costs 1 to 2 % (2^20 keys, q = 8: block scales
-// 220 -> 223 us, one scale 220 -> 225).
-constexpr uint32_t kDitherStep = 0x9E3779B1u;  // 2^32 times the golden ratio's fraction, odd
-__device__ __forceinline__ uint32_t dither_of(uint32_t at) { return __byte_perm(at, 0u, 0x4343u); }  // at's top byte, in both halves
-__device__ __forceinline__ void split_p(float a, float b, uint32_t dither, uint32_t& hi, uint32_t& lo) {
-  const __half2 w = __floats2half2_rn(a, b);
-  const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&w), __NV_SATFINITE,
-                                                           __NV_E4M3);
-  const __half2_raw hb = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
-  const __half2 r = __hsub2(w, *reinterpret_cast<const __half2*>(&hb));
-  const uint32_t normal = __hge2_mask(w, __half2half2(__ushort_as_half(0x2400)));  // >= 2^-6
-  const uint32_t bits = *reinterpret_cast<const uint32_t*>(&r) + ((normal & 0x00800080u) | (~normal & dither));
-  hi = (uint32_t)h;
-  lo = __byte_perm(bits, 0u, 0x4431u);  // the upper bytes
-}
-// Byte offset of (row, column) in a 64-byte-swizzled e4m3 region with 64-byte rows.
-__device__ __forceinline__ int sw64_offset(int row, int col) {
-  return row * 64 + ((((col >> 4) ^ (row >> 1)) & 3) << 4) + (col & 15);
-}
 
 // O^T is zeroed in tensor memory before the first tile, so every O^T MMA accumulates and
 // the MMAs of one value block may come from different threads in any order.
@@ -1295,6 +1244,8 @@ int max_splits_for_merge() { return kMergeMaxSplits; }
 size_t workspace_bytes_for(int n_part_rows);
 int block_log2_of(int block_tokens);  // defined with the plan
 int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out);
+int launch_wide_kernel(const PlanHeader* h, const void* q, const void* kv_cache, int num_pages, const Params& prm,
+                       cudaStream_t st);
 int launch_pair_kernel(int dev, const PlanHeader* h, const void* q, const void* kv_cache, int num_pages,
                        const Params& prm, cudaStream_t st);
 int pair_slots_on_device(int dev, int* slots);
@@ -1323,6 +1274,7 @@ static std::mutex g_dev_mu;
 cudaError_t set_weights_kernel_attributes(int* regs);  // defined next to those kernels
 cudaError_t set_select_kernel_attributes();
 cudaError_t set_verify_kernel_attributes();
+cudaError_t set_wide_kernel_attributes();
 
 static int prepare_device(int dev) {
   if (dev < 0 || dev >= 64) return set_error(MLA_ERR_CUDA, "device ordinal %d out of range", dev);
@@ -1348,7 +1300,9 @@ static int prepare_device(int dev) {
     d.kernels.weights = set_weights_kernel_attributes(&d.kernels.weights_regs);
     d.kernels.select = set_select_kernel_attributes();
     d.kernels.verify = set_verify_kernel_attributes();
-    if (d.kernels.weights != cudaSuccess || d.kernels.select != cudaSuccess || d.kernels.verify != cudaSuccess)
+    d.kernels.wide = set_wide_kernel_attributes();
+    if (d.kernels.weights != cudaSuccess || d.kernels.select != cudaSuccess || d.kernels.verify != cudaSuccess ||
+        d.kernels.wide != cudaSuccess)
       (void)cudaGetLastError();  // (it would show at the next launch)
     d.attrs_set = true;
   }
@@ -1451,7 +1405,12 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
   prm.tree_masks = tree_masks;
   prm.mask_words = mask_words;
   cudaStream_t st = (cudaStream_t)stream;
-  if (h->cta_pair) {
+  if (h->wide) {
+    if (g_dev[dev].kernels.wide != cudaSuccess)
+      return set_error(MLA_ERR_CUDA, "wide kernel attributes: %s", cudaGetErrorString(g_dev[dev].kernels.wide));
+    rc = launch_wide_kernel(h, q, kv_cache, num_pages, prm, st);
+    if (rc != MLA_OK) return rc;
+  } else if (h->cta_pair) {
     if (fp8) return set_error(MLA_ERR_PLAN, "a two-CTA plan needs a bf16 cache");
     rc = launch_pair_kernel(dev, h, q, kv_cache, num_pages, prm, st);
     if (rc != MLA_OK) return rc;

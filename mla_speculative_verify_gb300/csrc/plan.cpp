@@ -14,6 +14,7 @@
 //      per-SM share of the work; split units write partial (O, LSE) rows that the
 //      merge kernel combines.
 #include <algorithm>
+#include <cmath>
 #include <functional>
 #include <queue>
 #include <cstdio>
@@ -30,6 +31,7 @@ namespace mla {
 int rows_cap_for(int kv_dtype);  // defined next to the kernel
 int max_splits_for_merge();       // defined next to the merge kernel
 int pair_rows_cap();              // defined next to the two-CTA kernel
+int wide_rows_cap();              // defined next to the wide kernel
 
 static int fold_factor(int q, int H) {
   int best = 1;
@@ -72,7 +74,8 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   mla_plan_options o{};
   if (opts) o = *opts;
   int cap = rows_cap_for(kv_dtype);
-  if (o.max_rows_per_cta > 0) {
+  const bool force_wide = whole_requests && o.max_rows_per_cta == wide_rows_cap();
+  if (o.max_rows_per_cta > 0 && !force_wide) {
     if (o.max_rows_per_cta % 16 != 0 || o.max_rows_per_cta > cap)
       return set_error(MLA_ERR_INVALID_ARG, "max_rows_per_cta must be a multiple of 16 and <= %d (got %d)", cap,
                        o.max_rows_per_cta);
@@ -110,7 +113,21 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
     pair = R > cap && R <= pair_rows_cap();
   }
   if (pair) cap = pair_rows_cap();
-  const int slots = pair ? (o.pair_slots > 0 ? o.pair_slots : std::max(1, num_sms / 2)) : num_sms;
+  // Trees of many rows run in tiles of 128 rows on clusters of two CTAs, where those take less of the
+  // SMs' time: a page of such a tile keeps two SMs as long as kWidePage pages of a 48-row tile keep one.
+  bool wide = force_wide;
+  if (whole_requests && o.max_rows_per_cta == 0) {
+    const double kWidePage = kv_dtype == MLA_KV_BF16 ? 1.0 : 1.4;
+    double narrow_cost = 0, wide_cost = 0;
+    for (int b = 0; b < batch; ++b) {
+      const double rows = (double)q_lens_h[b] * num_heads, pages = (seq_lens_h[b] + kPage - 1) / kPage;
+      narrow_cost += std::ceil(rows / cap) * pages;
+      wide_cost += kWidePage * std::ceil(rows / wide_rows_cap()) * pages;
+    }
+    wide = wide_cost < narrow_cost;
+  }
+  if (wide) cap = wide_rows_cap();
+  const int slots = pair || wide ? (o.pair_slots > 0 ? o.pair_slots : std::max(1, num_sms / 2)) : num_sms;
 
   // --- row tiles ----------------------------------------------------------------------
   struct RowTile { int b, qrow0, nrows, pages; };
@@ -166,8 +183,8 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   const int min_pages = o.min_pages_per_split > 0 ? o.min_pages_per_split : 4;
   const int max_splits = max_splits_for_merge();
   const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
-  const double start_cost = fp8 ? 16.0 : 6.0;
-  auto row_cost = [&](int nrows) { return (fp8 && nrows <= 32) ? 0.9 : 1.0; };
+  const double start_cost = wide ? 10.0 : fp8 ? 16.0 : 6.0;
+  auto row_cost = [&](int nrows) { return (!wide && fp8 && nrows <= 32) ? 0.9 : 1.0; };
   long long tile_pages = 0;
   for (const Group& g : groups) tile_pages += (long long)(g.t1 - g.t0) * g.pages;
   auto assign = [&](long long T) {
@@ -295,6 +312,7 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   h.total_bytes = (int32_t)total;
   h.debug_skip_copy = o.debug_skip_copy;
   h.cta_pair = pair ? 1 : 0;
+  h.wide = wide ? 1 : 0;
   memcpy(base, &h, sizeof h);
   memcpy(base + req_off, reqs.data(), sizeof(PlanRequest) * batch);
   if (!units.empty()) memcpy(base + units_off, units.data(), sizeof(PlanUnit) * units.size());

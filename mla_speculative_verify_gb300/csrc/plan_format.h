@@ -30,7 +30,8 @@ struct PlanHeader {
   int32_t total_bytes;
   int32_t debug_skip_copy;  // mla_plan_options.debug_skip_copy (0 in production plans)
   int32_t cta_pair;         // 1: every unit is one fold group of 49..96 rows for a cluster of two CTAs
-  int32_t reserved[3];
+  int32_t wide;             // 1: units of up to 128 rows for clusters of two CTAs (kernel_wide_sm103.cu)
+  int32_t reserved[2];
 };
 static_assert(sizeof(PlanHeader) == 80, "plan header is 80 bytes");
 

@@ -321,9 +321,9 @@ __host__ __device__ __forceinline__ uint32_t idesc_bf16(int M, int N, int a_mn, 
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Instruction descriptor of tcgen05.mma kind::f8f6f4 with e4m3 A/B and fp32 D; kB_E5M2 makes B
-// e5m2 (the operands' types are independent in this kind).
-enum : uint32_t { kB_E5M2 = 1u << 10 };
+// Instruction descriptor of tcgen05.mma kind::f8f6f4 with e4m3 A/B and fp32 D; kA_E5M2 makes A and
+// kB_E5M2 B e5m2 (the operands' types are independent in this kind).
+enum : uint32_t { kA_E5M2 = 1u << 7, kB_E5M2 = 1u << 10 };
 __host__ __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | (0u << 7) | (0u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);

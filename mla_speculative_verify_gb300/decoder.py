@@ -44,7 +44,7 @@ class VerifyDecoder:
         if self.device.type == "cuda":
             # clusters of two CTAs the device runs at once, for plans that use them
             opts = binding.PlanOptions() if options is None else options
-            if opts.pair_slots == 0 and kv_dtype == "bf16":
+            if opts.pair_slots == 0 and (kv_dtype == "bf16" or tree):
                 opts = binding.PlanOptions.from_buffer_copy(opts)
                 opts.pair_slots = binding.device_pair_slots(self.device.index)
             options = opts
