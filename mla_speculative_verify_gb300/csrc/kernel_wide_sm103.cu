@@ -20,7 +20,8 @@
 // Tensor memory (columns): O at 0-127 (values 0-255) and 128-255 (values 256-511), S in two buffers
 // at 256 and 320. Shared memory: Q, the page ring (bf16: one page in three pieces of three 64-column
 // chunks, so that a piece is refilled while the product goes on; e4m3: two pages), the value columns
-// in two halves, P.
+// of a tile's two pages, P of the two pages. O takes the pages one after the other, so that P and the
+// values of one are replaced while the other's product runs.
 //
 // Warps: 0 copies of pages, 3 of value columns. 1: in CTA 0 issues S, in CTA 1 tells CTA 0 that its
 // pieces have landed; 2 the same for O. 4-11 softmax: warp (lane quadrant, group) has 32 of the 64 keys
@@ -50,6 +51,11 @@ constexpr int kRows = 128, kHalfRows = 64;
 constexpr int kTileKeys = 128;  // two pages
 constexpr int kChunks = 9;
 constexpr int kThreads = 384;
+// Octaves that a score may pass its row's reference by before that moves (bf16 P). P and the sums are
+// floating-point numbers, so a late reference costs no bits, only range: P up to 2^32. With the 8
+// octaves of the narrow kernel most tiles had one of 128 rows move (4 x 64 nodes, 16 heads, 32768
+// keys: 325 us; with 32 SLACK_US).
+constexpr float kRefSlackWide = 32.0f;
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemCols = 512;
 
 template <bool kFp8>
@@ -61,11 +67,11 @@ struct Geo {
   static constexpr int kPieceChunks = kChunks / kPieces;
   static constexpr int kSlots = kFp8 ? 2 : 3;               // of the page ring, a piece each
   static constexpr int kSlotBytes = kPieceChunks * kChunkBytes;
-  static constexpr int kVHalf = 4 * kChunkBytes;            // 128 keys x 128 values of one half
+  static constexpr int kVPage = 4 * kChunkBytes;            // a page's 64 keys x 128 values of either half
   static constexpr int kPBytes = 2 * kHalfRows * 128;       // 64 rows x 128 keys, bf16 or two 8-bit parts
   static constexpr int kOffK = kChunks * kQChunkBytes;
   static constexpr int kOffV = kOffK + kSlots * kSlotBytes;
-  static constexpr int kOffP = kOffV + 2 * kVHalf;
+  static constexpr int kOffP = kOffV + 2 * kVPage;
   static constexpr int kOffScales = kOffP + kPBytes;        // e4m3: a float4 per key of two tiles
   static constexpr int kOffMisc = kOffScales + (kFp8 ? 2 * kTileKeys * 16 : 0);
   static constexpr int kMiscBytes = 3072;
@@ -77,9 +83,9 @@ struct Geo {
 struct Misc {
   uint64_t q_full;
   uint64_t k_full[3], k_empty[3], k_peer[3];  // pieces: landed here; read by S; landed in CTA 1
-  uint64_t v_full[2], v_empty[2], v_peer[2];
+  uint64_t v_full[2], v_empty[2], v_peer[2];  // by page of the tile
   uint64_t s_full[2], s_empty[2];
-  uint64_t p_ready, o_done;
+  uint64_t p_ready[2], o_done[2];             // by page of the tile
   uint64_t sc_full[2], sc_free[2];            // a tile's scales
   uint64_t drained[2];
   uint32_t tmem_base;
@@ -140,12 +146,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Arrive on a barrier of CTA 0 (this thread's writes released).
+// Arrive on a barrier of CTA 0. What it announces (P, copies that have landed, scores that have been
+// read) lies in this CTA's own shared and tensor memory and is only touched there, by its own SM's tensor
+// core, to which fence.proxy.async or tcgen05.fence has handed it over before; so the arrival releases
+// at CTA scope, also from CTA 1. (A release at cluster scope waits for all of a warp's stores to be
+// seen by the other SM: ARRIVE_US.)
 __device__ __forceinline__ void arrive_first(uint64_t* bar, uint32_t rank) {
   if (rank == 0)
     ptx::mbar_arrive(bar);
   else
-    ptx::mbar_arrive_remote(ptx::mapa(ptx::smem_addr(bar), 0));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ptx::mapa(ptx::smem_addr(bar), 0)) : "memory");
 }
 
 template <bool kFp8, bool kScaled>
@@ -153,7 +163,7 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
                                              int grp, int lane, int sidx) {
   using G = Geo<kFp8>;
   constexpr float kPShift = kFp8 ? kPShiftFp8 : 0.f;
-  constexpr float kMoveAbove = (kFp8 ? kRefSlackFp8 : kRefSlack) + kPShift;
+  constexpr float kMoveAbove = (kFp8 ? kRefSlackFp8 : kRefSlackWide) + kPShift;
   volatile int* abort = &ms->abort;
   const int b = ms->unit[0], qrow0 = ms->unit[1] + kHalfRows * (int)rank;
   const int nrows = max(0, min(kHalfRows, ms->unit[2] - kHalfRows * (int)rank));
@@ -283,19 +293,24 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
       need = top > ref + kMoveAbove;
       ms->red[2 * pg + grp][row] = top;  // (read only if some row moves)
     }
-    if (softmax_any(need || fail)) {
+    const bool moved = softmax_any(need || fail);
+    float alpha = 1.f;
+    if (moved) {
       if (softmax_any(fail || *abort != 0)) {
         stop = true;
         break;
       }
       const float m = fmaxf(fmaxf(ms->red[0][row], ms->red[1][row]), fmaxf(ms->red[2][row], ms->red[3][row]));
       const float nw = fmaxf(ref, m - kPShift);
-      const float alpha = nw == ref ? 1.f : ex2(ref - nw);
+      alpha = nw == ref ? 1.f : ex2(ref - nw);
       ref = nw;
       l *= alpha;
-      if (t >= 1) {
-        fail = !warp_wait(&ms->o_done, (t - 1) & 1, abort, p);
-        if (!fail) {
+    }
+    // O of the rows that move, between O(t - 1) and O(t); all warps' before any P(t) is handed on
+    auto rescale = [&]() {
+      if (t >= 1 && !fail) {
+        for (int k = 0; k < 2 && !fail; ++k) fail = !warp_wait(&ms->o_done[k], (t - 1) & 1, abort, p);
+        if (!fail && __any_sync(0xffffffffu, alpha != 1.f)) {
           ptx::tc_fence_after();
           // this thread's row in half `grp` of the values
 #pragma unroll 1
@@ -310,10 +325,11 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
             ptx::tmem_st16(at + 16, o + 16);
           }
           ptx::tmem_st_wait();
+          ptx::tc_fence_before();
         }
       }
-      softmax_any(false);  // `red` is read before the next tile writes it
-    }
+      softmax_any(false);  // (`red` too is read before the next tile writes it)
+    };
     if (!fail) {
       float s = 0.f;
       uint32_t w[kFp8 ? 8 : 16], wl[kFp8 ? 8 : 1];
@@ -341,8 +357,10 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&ms->sc_free[sb]);
       }
-      if (t >= 1) fail = !warp_wait(&ms->o_done, (t - 1) & 1, abort, p);
-      if (!fail) {
+      if (moved) rescale();
+      const bool any = kv_begin + t * kTileKeys + kPage * pg < kv_end;  // (a unit's last tile may have one page)
+      if (t >= 1 && any) fail = !warp_wait(&ms->o_done[pg], (t - 1) & 1, abort, p);
+      if (!fail && any) {
         if constexpr (kFp8) {
           uint8_t* hi = smem + G::kOffP + pg * (kHalfRows * 64);
 #pragma unroll
@@ -357,24 +375,22 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4*>(line + (((4 * grp + j) ^ (row & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
-        if (kv_begin + (t + 1) * kTileKeys > kv_end) {
-          // values behind the key range: zero, so that P = 0 meets V = 0 (8 warps: 128 keys x 2 halves)
-          for (int h = 0; h < 2 && !fail; ++h) fail = !warp_wait(&ms->v_full[h], t & 1, abort, p);
-          if (!fail) {
-            const int key = sidx & 127, h = sidx >> 7;  // key of the tile, half of the values
-            if (kv_begin + t * kTileKeys + key >= kv_end) {
-              uint8_t* at = smem + G::kOffV + h * G::kVHalf + (key >> 6) * (2 * G::kChunkBytes) + (key & 63) * G::kRowBytes;
+        if (kv_begin + t * kTileKeys + kPage * (pg + 1) > kv_end) {
+          // values behind the key range: zero, so that P = 0 meets V = 0 (a key and a half to a thread)
+          fail = !warp_wait(&ms->v_full[pg], t & 1, abort, p);
+          if (!fail && kv_begin + t * kTileKeys + kPage * pg + row >= kv_end) {
+            uint8_t* at = smem + G::kOffV + pg * G::kVPage + grp * (2 * G::kChunkBytes) + row * G::kRowBytes;
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int j = 0; j < G::kRowBytes / 16; ++j) *reinterpret_cast<uint4*>(at + c * G::kChunkBytes + 16 * j) = make_uint4(0, 0, 0, 0);
-            }
+              for (int j = 0; j < G::kRowBytes / 16; ++j) *reinterpret_cast<uint4*>(at + c * G::kChunkBytes + 16 * j) = make_uint4(0, 0, 0, 0);
           }
+          __syncwarp();
         }
         ptx::fence_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
-        if (!fail && lane == 0) arrive_first(&ms->p_ready, rank);
+        if (!fail && lane == 0) arrive_first(&ms->p_ready[pg], rank);
       }
     }
   }
@@ -385,7 +401,9 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
       ms->red[2 * pg + grp][row] = l;
       softmax_sync();
       l = (ms->red[0][row] + ms->red[1][row]) + (ms->red[2][row] + ms->red[3][row]);
-      fail = !warp_wait(&ms->o_done, (ntiles - 1) & 1, abort, p);
+      const int npages = (kv_end - kv_begin + kPage - 1) / kPage;
+      fail = !warp_wait(&ms->o_done[0], (ntiles - 1) & 1, abort, p);
+      if (!fail && npages >= 2) fail = !warp_wait(&ms->o_done[1], (npages / 2 - 1) & 1, abort, p);
       stop = softmax_any(fail || *abort != 0);
     }
   }
@@ -445,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(&ms->s_empty[i], 16);
         ptx::mbar_init(&ms->sc_full[i], 1);
         ptx::mbar_init(&ms->sc_free[i], 8);
+        ptx::mbar_init(&ms->p_ready[i], 8);
+        ptx::mbar_init(&ms->o_done[i], 1);
         ptx::mbar_init(&ms->drained[i], 1);
       }
-      ptx::mbar_init(&ms->p_ready, 16);
-      ptx::mbar_init(&ms->o_done, 1);
       ptx::fence_mbar_init();
     }
     if (lane < 12) ms->unit[lane] = reinterpret_cast<const int32_t*>(p.units + (blockIdx.x >> 1))[lane];
@@ -543,26 +561,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------------------ copies of this CTA's value columns
-    int issued = 0;
     bool ok = !*abort;
-    int pa = page_at(0), pb = page_at(1);
-    for (int t = 0; ok && t < ntiles; ++t) {
-      const bool two = 2 * t + 1 < npages;
-      const int na = t + 1 < ntiles ? page_at(2 * t + 2) : 0, nb = t + 1 < ntiles ? page_at(2 * t + 3) : 0;
-      for (int h = 0; ok && h < 2; ++h) {
-        if (t >= 1) ok = warp_wait(&ms->v_empty[h], (t - 1) & 1, abort, p);
-        if (!ok) break;
-        if (lane == 0) {
-          uint8_t* dst = smem + G::kOffV + h * G::kVHalf;
-          ptx::mbar_arrive_expect_tx(&ms->v_full[h], (two ? 4 : 2) * G::kChunkBytes);
-          ptx::tma_load_3d(dst, &tmap_v, &ms->v_full[h], 0, pa * kPage, 4 * h + 2 * (int)rank);
-          if (two) ptx::tma_load_3d(dst + 2 * G::kChunkBytes, &tmap_v, &ms->v_full[h], 0, pb * kPage, 4 * h + 2 * (int)rank);
-        }
-        __syncwarp();
-        issued = 2 * t + h + 1;
+    int issued = 0, page = page_at(0);
+    for (; ok && issued < npages; ++issued) {
+      const int pg = issued & 1, t = issued >> 1;
+      const int next = issued + 1 < npages ? page_at(issued + 1) : 0;
+      if (t >= 1) ok = warp_wait(&ms->v_empty[pg], (t - 1) & 1, abort, p);
+      if (!ok) break;
+      if (lane == 0) {
+        uint8_t* dst = smem + G::kOffV + pg * G::kVPage;
+        ptx::mbar_arrive_expect_tx(&ms->v_full[pg], G::kVPage);
+        ptx::tma_load_3d(dst, &tmap_v, &ms->v_full[pg], 0, page * kPage, 2 * (int)rank);
+        ptx::tma_load_3d(dst + 2 * G::kChunkBytes, &tmap_v, &ms->v_full[pg], 0, page * kPage, 4 + 2 * (int)rank);
       }
-      pa = na;
-      pb = nb;
+      __syncwarp();
+      page = next;
     }
     if (lane == 0) {
       for (int n = max(0, issued - 2); n < issued; ++n) {
@@ -582,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2 && rank == 1) {
     bool ok = !*abort;
-    for (int n = 0; ok && n < 2 * ntiles; ++n) {
+    for (int n = 0; ok && n < npages; ++n) {
       ok = warp_wait(&ms->v_full[n & 1], (n >> 1) & 1, abort, p);
       if (ok && lane == 0) arrive_first(&ms->v_peer[n & 1], rank);
       __syncwarp();
@@ -639,40 +652,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ O += P(t) . V(t)
     bool ok = !*abort, issued = false;
     const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kRows, 256, 0, 1) : ptx::idesc_bf16(kRows, 256, 0, 1);
-    for (int t = 0; ok && t < ntiles; ++t) {
-      ok = warp_wait<true>(&ms->p_ready, t & 1, abort, p);
-      const int pages = 2 * t + 1 < npages ? 2 : 1;
-      for (int h = 0; ok && h < 2; ++h) {
-        ok = warp_wait(&ms->v_full[h], t & 1, abort, p);
-        if (ok) ok = warp_wait<true>(&ms->v_peer[h], t & 1, abort, p);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        ptx::fence_async_smem_cluster();
-        if (ptx::elect_one()) {
-          const uint32_t v0 = s0 + G::kOffV + h * G::kVHalf, p0 = s0 + G::kOffP, d = tmem + kTmemO + 128 * h;
-          for (int pg = 0; pg < pages; ++pg) {
-            if constexpr (kFp8) {
+    for (int n = 0; ok && n < npages; ++n) {
+      const int pg = n & 1, t = n >> 1;
+      ok = warp_wait(&ms->v_full[pg], t & 1, abort, p);
+      if (ok) ok = warp_wait<true>(&ms->v_peer[pg], t & 1, abort, p);
+      if (ok) ok = warp_wait<true>(&ms->p_ready[pg], t & 1, abort, p);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      ptx::fence_async_smem_cluster();
+      if (ptx::elect_one()) {
+        const uint32_t v0 = s0 + G::kOffV + pg * G::kVPage, p0 = s0 + G::kOffP;
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t d = tmem + kTmemO + 128 * h, vh = v0 + h * (2 * G::kChunkBytes);
+          if constexpr (kFp8) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-                  mma2<true>(d, ptx::smem_desc(p0 + part * (kHalfRows * 128) + pg * (kHalfRows * 64) + 32 * k, 16, 512, ptx::kSwizzle64B),
-                             ptx::smem_desc(v0 + pg * (2 * G::kChunkBytes) + 2048 * k, G::kChunkBytes, 512, ptx::kSwizzle64B),
-                             idesc | (part ? ptx::kA_E5M2 : 0u), (t | pg | k | part) != 0 ? 1u : 0u);
-            } else {
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma2<false>(d, ptx::smem_desc(p0 + pg * (kHalfRows * 128) + 32 * k, 16, 1024, ptx::kSwizzle128B),
-                            ptx::smem_desc(v0 + pg * (2 * G::kChunkBytes) + 2048 * k, G::kChunkBytes, 1024, ptx::kSwizzle128B), idesc,
-                            (t | pg | k) != 0 ? 1u : 0u);
-            }
+              for (int part = 0; part < 2; ++part)
+                mma2<true>(d, ptx::smem_desc(p0 + part * (kHalfRows * 128) + pg * (kHalfRows * 64) + 32 * k, 16, 512, ptx::kSwizzle64B),
+                           ptx::smem_desc(vh + 2048 * k, G::kChunkBytes, 512, ptx::kSwizzle64B), idesc | (part ? ptx::kA_E5M2 : 0u),
+                           (n | k | part) != 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma2<false>(d, ptx::smem_desc(p0 + pg * (kHalfRows * 128) + 32 * k, 16, 1024, ptx::kSwizzle128B),
+                          ptx::smem_desc(vh + 2048 * k, G::kChunkBytes, 1024, ptx::kSwizzle128B), idesc, (n | k) != 0 ? 1u : 0u);
           }
-          commit_both(&ms->v_empty[h]);
-          if (h == 1) commit_both(&ms->o_done);
         }
-        __syncwarp();
-        issued = true;
+        commit_both(&ms->v_empty[pg]);
+        commit_both(&ms->o_done[pg]);
       }
+      __syncwarp();
+      issued = true;
     }
     if (issued) {
       if (ptx::elect_one()) {
