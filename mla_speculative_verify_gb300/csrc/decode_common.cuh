@@ -34,7 +34,7 @@ struct Params {
   float out_scale;         // kv_scale (1 for a bf16 cache)
   __nv_bfloat16* out;
   float* lse;
-  __nv_bfloat16* part_o;  // split partials of O (bf16, each normalised by its split's l)
+  void* part_o;  // split partials of O, each normalised by its split's l: bf16, those of the wide kernel fp32
   float* part_lse;
   int32_t* status;
   long long wait_budget;  // cycles a bounded wait may take (kWaitBudget; kWaitBudgetTest in a timeout test)

@@ -389,7 +389,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, const Params& p) {
   ptx::tc_fence_after();
   // O(row, dv) = O^T(dv, row) * oscale(row): this thread holds dv = 256 crank + 128 grp +
   // 32 qd + lane, every row of the unit
-  __nv_bfloat16* dst = a.part_row0 < 0 ? p.out + (size_t)a.qrow0 * kDv : p.part_o + (size_t)a.part_row0 * kDv;
+  __nv_bfloat16* dst = a.part_row0 < 0 ? p.out + (size_t)a.qrow0 * kDv : (__nv_bfloat16*)p.part_o + (size_t)a.part_row0 * kDv;
   const int dv = 256 * (int)a.crank + 128 * grp + 32 * qd + lane;
 #pragma unroll 1
   for (int c = 0; c < NM; ++c) {

@@ -67,6 +67,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "mla_decode.h"
 #include "plan_format.h"
@@ -723,7 +724,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
   // O^T(dv, row) / l(row): this thread holds dv = 128 blk + 32 qd + lane of value blocks
   // 2 grp, 2 grp + 1; a warp's stores of one row cover 32 consecutive dv (bf16 out, or
   // the bf16 split partial)
-  __nv_bfloat16* dst = a.part_row0 < 0 ? p.out + (size_t)a.qrow0 * kDv : p.part_o + (size_t)a.part_row0 * kDv;
+  __nv_bfloat16* dst = a.part_row0 < 0 ? p.out + (size_t)a.qrow0 * kDv : (__nv_bfloat16*)p.part_o + (size_t)a.part_row0 * kDv;
   const int dv_in_blk = qd * 32 + lane;
 #pragma unroll 1
   for (int blk = 2 * grp; blk < 2 * grp + 2; ++blk) {
@@ -1084,18 +1085,32 @@ constexpr int kMergeBatch = 10;  // partial-O loads in flight per lane (16 warps
 constexpr int kMergeMaxSplits = 2048;
 constexpr long long kMergeWideSlicesMaxCtas = 200;  // 8 slices per row up to this many merge CTAs
 
-// Four bf16 partial-O values (8 bytes, streamed: read once) as fp32.
-__device__ __forceinline__ float4 load_part4(const __nv_bfloat16* ptr) {
-  const uint2 raw = __ldcs(reinterpret_cast<const uint2*>(ptr));
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
+// kN partial-O values of a split, as they lie in memory (streamed: read once) and as fp32. P is their
+// type: bf16, or fp32 (those of the wide kernel).
+template <typename P, int kN>
+struct PartValues {
+  alignas(kN * sizeof(P)) uint32_t w[kN * sizeof(P) / 4];
+  __device__ __forceinline__ void load(const P* ptr) {
+    if constexpr (sizeof(w) == 16) {
+      *reinterpret_cast<uint4*>(w) = __ldcs(reinterpret_cast<const uint4*>(ptr));
+    } else if constexpr (sizeof(w) == 8) {
+      *reinterpret_cast<uint2*>(w) = __ldcs(reinterpret_cast<const uint2*>(ptr));
+    } else {
+      w[0] = __ldcs(reinterpret_cast<const unsigned int*>(ptr));
+    }
+  }
+  __device__ __forceinline__ float2 pair(int k) const {
+    if constexpr (sizeof(P) == 4)
+      return make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    else
+      return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
+  }
+};
 
 // 64 registers per thread (the minimum-blocks bound): two 16-warp CTAs per SM, so the
 // merge CTAs of a 48-row tile with ~150 splits (192 of them) run in one wave.
-template <int W, int SL>
-__global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) lse_merge_kernel(const PlanMerge* merges, const __nv_bfloat16* part_o,
+template <int W, int SL, typename P>
+__global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) lse_merge_kernel(const PlanMerge* merges, const P* part_o,
                                                                  const float* part_lse, __nv_bfloat16* out, float* lse) {
   static_assert(SL == 4 || SL == 8, "4 or 8 column slices per row");
   constexpr int kCols = kDv / SL / 32;  // value columns per lane: 4 or 2
@@ -1110,7 +1125,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) lse_merge_kernel(cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ns = m.n_splits;  // the planner keeps this <= kMergeMaxSplits
   const int col = slice * (kDv / SL) + kCols * lane;
-  const __nv_bfloat16* base = part_o + (size_t)(m.part_row0 + row) * kDv + col;
+  const P* base = part_o + (size_t)(m.part_row0 + row) * kDv + col;
   const size_t split_stride = (size_t)m.nrows * kDv;
   // Warp w folds its splits w, w + W, ... into a running (max M_w, sum l_w = sum_s e^(L_s -
   // M_w), acc_w = sum_s e^(L_s - M_w) O_s), kMergeBatch splits per round trip (their
@@ -1118,35 +1133,33 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) lse_merge_kernel(cons
   // L = M + ln l, O = acc / l. A split that the row cannot see has L_s = -inf: weight 0.
   float mw = -INFINITY, lw = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = warp; s0 < ns; s0 += W * kMergeBatch) {
-    uint2 v[kMergeBatch];  // kCols bf16 partial-O values each, unpacked when used
-    float x[kMergeBatch];
+  constexpr int kBatch = sizeof(P) == 4 ? kMergeBatch / 2 : kMergeBatch;  // (registers)
+  for (int s0 = warp; s0 < ns; s0 += W * kBatch) {
+    PartValues<P, kCols> v[kBatch];
+    float x[kBatch];
 #pragma unroll
-    for (int u = 0; u < kMergeBatch; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       const int s = s0 + W * u;
-      if constexpr (kCols == 4) {
-        v[u] = s < ns ? __ldcs(reinterpret_cast<const uint2*>(base + (size_t)s * split_stride)) : make_uint2(0u, 0u);
-      } else {
-        v[u].x = s < ns ? __ldcs(reinterpret_cast<const unsigned int*>(base + (size_t)s * split_stride)) : 0u;
-        v[u].y = 0u;
-      }
+#pragma unroll
+      for (uint32_t& w : v[u].w) w = 0u;
+      if (s < ns) v[u].load(base + (size_t)s * split_stride);
       x[u] = s < ns ? part_lse[m.part_row0 + s * m.nrows + row] : -INFINITY;
     }
     float mb = mw;
 #pragma unroll
-    for (int u = 0; u < kMergeBatch; ++u) mb = fmaxf(mb, x[u]);
+    for (int u = 0; u < kBatch; ++u) mb = fmaxf(mb, x[u]);
     if (mb == -INFINITY) continue;  // nothing visible so far
     const float sc = mw == -INFINITY ? 0.f : __expf(mw - mb);
     lw *= sc;
     acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
 #pragma unroll
-    for (int u = 0; u < kMergeBatch; ++u) {
+    for (int u = 0; u < kBatch; ++u) {
       const float w = x[u] == -INFINITY ? 0.f : __expf(x[u] - mb);
-      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v[u].x));
+      const float2 a = v[u].pair(0);
       lw += w;
       acc.x += w * a.x; acc.y += w * a.y;
       if constexpr (kCols == 4) {
-        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v[u].y));
+        const float2 b = v[u].pair(1);
         acc.z += w * b.x; acc.w += w * b.y;
       }
     }
@@ -1193,8 +1206,8 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) lse_merge_kernel(cons
 constexpr int kMergeSmallSplits = 16;
 constexpr int kMergeSmallWarps = 8;
 
-__global__ void __launch_bounds__(32 * kMergeSmallWarps) lse_merge_small_kernel(const PlanMerge* merges,
-                                                                                const __nv_bfloat16* part_o,
+template <typename P>
+__global__ void __launch_bounds__(32 * kMergeSmallWarps) lse_merge_small_kernel(const PlanMerge* merges, const P* part_o,
                                                                                 const float* part_lse,
                                                                                 __nv_bfloat16* out, float* lse) {
   const PlanMerge m = merges[blockIdx.y];  // plan data: read before the wait, as above
@@ -1205,12 +1218,15 @@ __global__ void __launch_bounds__(32 * kMergeSmallWarps) lse_merge_small_kernel(
   if (row >= m.nrows) return;
   const int ns = m.n_splits;  // <= kMergeSmallSplits (checked on the host)
   const int col = quarter * 128 + 4 * lane;
-  const __nv_bfloat16* base = part_o + (size_t)(m.part_row0 + row) * kDv + col;
+  const P* base = part_o + (size_t)(m.part_row0 + row) * kDv + col;
   const size_t split_stride = (size_t)m.nrows * kDv;
-  float4 v[kMergeSmallSplits];
+  PartValues<P, 4> v[kMergeSmallSplits];
 #pragma unroll
-  for (int s = 0; s < kMergeSmallSplits; ++s)
-    v[s] = s < ns ? load_part4(base + (size_t)s * split_stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < kMergeSmallSplits; ++s) {
+#pragma unroll
+    for (uint32_t& w : v[s].w) w = 0u;
+    if (s < ns) v[s].load(base + (size_t)s * split_stride);
+  }
   const float x = lane < ns ? part_lse[m.part_row0 + lane * m.nrows + row] : -INFINITY;
   float mx = x;
 #pragma unroll
@@ -1225,7 +1241,8 @@ __global__ void __launch_bounds__(32 * kMergeSmallWarps) lse_merge_small_kernel(
   for (int s = 0; s < kMergeSmallSplits; ++s) {
     const float ws = __shfl_sync(0xffffffffu, w, s);
     if (s < ns) {
-      acc.x += ws * v[s].x; acc.y += ws * v[s].y; acc.z += ws * v[s].z; acc.w += ws * v[s].w;
+      const float2 a = v[s].pair(0), b = v[s].pair(1);
+      acc.x += ws * a.x; acc.y += ws * a.y; acc.z += ws * b.x; acc.w += ws * b.y;
     }
   }
   const int qr = m.qrow0 + row;
@@ -1241,7 +1258,7 @@ int rows_cap_for(int kv_dtype) {
 int max_splits_for_merge() { return kMergeMaxSplits; }
 
 // ------------------------------------------------------------------ host side
-size_t workspace_bytes_for(int n_part_rows);
+size_t workspace_bytes_for(int n_part_rows, bool wide);
 int block_log2_of(int block_tokens);  // defined with the plan
 int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out);
 int launch_wide_kernel(const PlanHeader* h, const void* q, const void* kv_cache, int num_pages, const Params& prm,
@@ -1357,7 +1374,7 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
                      page_table_stride, h->max_pages);
   if (!(sm_scale > 0.f) || !(kv_scale > 0.f) || !isfinite(sm_scale) || !isfinite(kv_scale))
     return set_error(MLA_ERR_INVALID_ARG, "sm_scale and kv_scale must be finite and > 0");
-  const size_t ws_need = workspace_bytes_for(h->n_part_rows);
+  const size_t ws_need = workspace_bytes_for(h->n_part_rows, h->wide != 0);
   if (ws_need > 0 && (!workspace || workspace_bytes < ws_need))
     return set_error(MLA_ERR_BUFFER, "workspace needs %zu bytes (got %zu)", ws_need, workspace ? workspace_bytes : (size_t)0);
   if (ws_need > 0 && ((uintptr_t)workspace & 255u)) return set_error(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -1394,9 +1411,9 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
   prm.out_scale = ks;
   prm.out = (__nv_bfloat16*)out;
   prm.lse = lse;
-  prm.part_o = (__nv_bfloat16*)workspace;
-  prm.part_lse =
-      ws_need ? (float*)((uint8_t*)workspace + ((size_t)h->n_part_rows * kDv * kPartOElemBytes + 255) / 256 * 256) : nullptr;
+  prm.part_o = workspace;
+  const size_t part_bytes = (size_t)h->n_part_rows * kDv * (h->wide ? kWidePartOElemBytes : kPartOElemBytes);
+  prm.part_lse = ws_need ? (float*)((uint8_t*)workspace + (part_bytes + 255) / 256 * 256) : nullptr;
   prm.status = status_dev;
   prm.wait_budget = h->debug_skip_copy > 0 ? kWaitBudgetTest : kWaitBudget;
   prm.skip_copy = h->debug_skip_copy - 1;
@@ -1447,15 +1464,19 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto merge_fn = small ? lse_merge_small_kernel
-                    : slices == 8 ? (large_warps == 4   ? lse_merge_kernel<4, 8>
-                                     : large_warps == 8 ? lse_merge_kernel<8, 8>
-                                                        : lse_merge_kernel<kMergeWarps, 8>)
-                                  : (large_warps == 4   ? lse_merge_kernel<4, 4>
-                                     : large_warps == 8 ? lse_merge_kernel<8, 4>
-                                                        : lse_merge_kernel<kMergeWarps, 4>);
-    ce = cudaLaunchKernelEx(&cfg, merge_fn, (const PlanMerge*)((const uint8_t*)plan_dev + h->merge_off),
-                            (const __nv_bfloat16*)prm.part_o, (const float*)prm.part_lse, (__nv_bfloat16*)out, lse);
+    auto launch = [&](auto* part) {
+      using P = std::remove_pointer_t<decltype(part)>;
+      auto merge_fn = small ? lse_merge_small_kernel<P>
+                      : slices == 8 ? (large_warps == 4   ? lse_merge_kernel<4, 8, P>
+                                       : large_warps == 8 ? lse_merge_kernel<8, 8, P>
+                                                          : lse_merge_kernel<kMergeWarps, 8, P>)
+                                    : (large_warps == 4   ? lse_merge_kernel<4, 4, P>
+                                       : large_warps == 8 ? lse_merge_kernel<8, 4, P>
+                                                          : lse_merge_kernel<kMergeWarps, 4, P>);
+      return cudaLaunchKernelEx(&cfg, merge_fn, (const PlanMerge*)((const uint8_t*)plan_dev + h->merge_off), (const P*)part,
+                                (const float*)prm.part_lse, (__nv_bfloat16*)out, lse);
+    };
+    ce = h->wide ? launch((float*)prm.part_o) : launch((__nv_bfloat16*)prm.part_o);
     if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "merge kernel launch: %s", cudaGetErrorString(ce));
   }
   return MLA_OK;

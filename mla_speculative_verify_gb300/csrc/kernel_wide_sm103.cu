@@ -54,7 +54,7 @@ constexpr int kThreads = 384;
 // Octaves that a score may pass its row's reference by before that moves (bf16 P). P and the sums are
 // floating-point numbers, so a late reference costs no bits, only range: P up to 2^32. With the 8
 // octaves of the narrow kernel most tiles had one of 128 rows move (4 x 64 nodes, 16 heads, 32768
-// keys: 325 us; with 32 SLACK_US).
+// keys: 325 us; with 32 314, and most of what else was then won).
 constexpr float kRefSlackWide = 32.0f;
 constexpr uint32_t kTmemO = 0, kTmemS = 256, kTmemCols = 512;
 
@@ -65,27 +65,32 @@ struct Geo {
   static constexpr int kQChunkBytes = kHalfRows * 128;      // bf16, or e4m3 in two parts of 4096
   static constexpr int kPieces = kFp8 ? 1 : 3;              // of a page
   static constexpr int kPieceChunks = kChunks / kPieces;
-  static constexpr int kSlots = kFp8 ? 2 : 3;               // of the page ring, a piece each
+  static constexpr int kSlots = kFp8 ? 2 : 3;             // of the page ring, a piece each
   static constexpr int kSlotBytes = kPieceChunks * kChunkBytes;
   static constexpr int kVPage = 4 * kChunkBytes;            // a page's 64 keys x 128 values of either half
   static constexpr int kPBytes = 2 * kHalfRows * 128;       // 64 rows x 128 keys, bf16 or two 8-bit parts
   static constexpr int kOffK = kChunks * kQChunkBytes;
   static constexpr int kOffV = kOffK + kSlots * kSlotBytes;
   static constexpr int kOffP = kOffV + 2 * kVPage;
-  static constexpr int kOffScales = kOffP + kPBytes;        // e4m3: a float4 per key of two tiles
-  static constexpr int kOffMisc = kOffScales + (kFp8 ? 2 * kTileKeys * 16 : 0);
+  static constexpr int kOffScales = kOffP + kPBytes;        // e4m3: block scales of two tiles
+  static constexpr int kScaleBytes = kTileKeys / 2 * 24;    // of a tile, by pairs of keys
+  static constexpr int kOffMisc = kOffScales + (kFp8 ? 2 * kScaleBytes : 0);
   static constexpr int kMiscBytes = 3072;
   static constexpr int kSmem = kOffMisc + kMiscBytes;
   static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory");
   static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
 };
 
+// Scales of an e4m3 cache: one for all; a thread's 32 keys in one block, so that they come with one load;
+// smaller blocks, with a load for each pair of keys.
+enum : int { kOneScale = 0, kLargeBlocks = 1, kSmallBlocks = 2 };
+
 struct Misc {
   uint64_t q_full;
   uint64_t k_full[3], k_empty[3], k_peer[3];  // pieces: landed here; read by S; landed in CTA 1
   uint64_t v_full[2], v_empty[2], v_peer[2];  // by page of the tile
   uint64_t s_full[2], s_empty[2];
-  uint64_t p_ready[2], o_done[2];             // by page of the tile
+  uint64_t p_ready[2][2], o_done[2][2];       // by page of the tile, the tile's parity
   uint64_t sc_full[2], sc_free[2];            // a tile's scales
   uint64_t drained[2];
   uint32_t tmem_base;
@@ -146,11 +151,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+               "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])), "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])),
+               "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])), "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])), "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
+               "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])), "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])), "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
+               : "memory");
+}
+
 // Arrive on a barrier of CTA 0. What it announces (P, copies that have landed, scores that have been
 // read) lies in this CTA's own shared and tensor memory and is only touched there, by its own SM's tensor
 // core, to which fence.proxy.async or tcgen05.fence has handed it over before; so the arrival releases
 // at CTA scope, also from CTA 1. (A release at cluster scope waits for all of a warp's stores to be
-// seen by the other SM: ARRIVE_US.)
+// seen by the other SM: 4 x 64 nodes over 32768 bf16 keys 314 us, 247 so.)
 __device__ __forceinline__ void arrive_first(uint64_t* bar, uint32_t rank) {
   if (rank == 0)
     ptx::mbar_arrive(bar);
@@ -158,10 +172,19 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ptx::mapa(ptx::smem_addr(bar), 0)) : "memory");
 }
 
-template <bool kFp8, bool kScaled>
+// The dither of split_p for keys j and j + 1 in the upper bytes of two halves: multiples of the golden
+// ratio, modulo 1, in 16 bits (an even j's half may carry into its neighbour's, which is as good).
+constexpr uint32_t kDither16 = 0x9E37u, kDither2Step = (2u * kDither16 & 0xFFFFu) * 0x10001u;
+__device__ __forceinline__ uint32_t dither2_of(int j) {
+  const uint32_t a = kDither16 * (uint32_t)j;
+  return (a & 0xFFFFu) | (a + kDither16) << 16;
+}
+
+template <bool kFp8, int kScales>
 __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Params& p, uint32_t tmem, uint32_t rank, int qd,
                                              int grp, int lane, int sidx) {
   using G = Geo<kFp8>;
+  constexpr bool kScaled = kScales != kOneScale;
   constexpr float kPShift = kFp8 ? kPShiftFp8 : 0.f;
   constexpr float kMoveAbove = (kFp8 ? kRefSlackFp8 : kRefSlackWide) + kPShift;
   volatile int* abort = &ms->abort;
@@ -232,12 +255,21 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
   }
   bool stop = softmax_any(*abort != 0), fail = false;
   if (kFp8) cs = ms->colscale[row];
+  float4 one = make_float4(0.f, 0.f, 0.f, 0.f);  // kLargeBlocks: the scale of this thread's keys, times cs; its logarithm in .z
+  // x (v cs) + log2 v of keys i and i + 1
+  auto in_octaves = [&](float2 v, const float4* scales, int i) {
+    if constexpr (kScales == kOneScale) return ptx::mul2(v, make_float2(cs, cs));
+    if constexpr (kScales == kLargeBlocks) return ptx::fma2(v, make_float2(one.x, one.x), make_float2(one.z, one.z));
+    const float4 a = scales[i / 2];
+    return ptx::fma2(ptx::mul2(v, make_float2(cs, cs)), make_float2(a.x, a.y), make_float2(a.z, a.w));
+  };
+  auto o_done = [&](int k, int u) { return warp_wait(&ms->o_done[k][u & 1], (u >> 1) & 1, abort, p); };  // O of page k of tile u
   float ref = -INFINITY, l = 0.f;
   for (int t = 0; !stop && t < ntiles; ++t) {
     const int sb = t & 1;
     const int key0 = kv_begin + t * kTileKeys + kPage * pg + 32 * grp;  // this thread's 32 keys
     uint32_t sees = 0xffffffffu;
-    if (kv_begin + (t + 1) * kTileKeys > all_see) {
+    if (__builtin_expect(kv_begin + (t + 1) * kTileKeys > all_see, 0)) {
       // up to 32 bits: keys before the verify tokens, then the mask's or the chain's
       const int d = key0 - n0;
       const int left = kv_end - key0;
@@ -261,11 +293,14 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
       if (left < 32) sees &= left <= 0 ? 0u : (1u << left) - 1u;
       if (!live) sees = 0u;
     }
-    float x[32];
+    float x[32], top = -INFINITY;
     bool need = false;
     if (!fail) fail = !warp_wait(&ms->s_full[sb], (t >> 1) & 1, abort, p);
     if (kScaled && !fail) fail = !warp_wait(&ms->sc_full[sb], (t >> 1) & 1, abort, p);
-    const float4* scales = reinterpret_cast<const float4*>(smem + G::kOffScales) + sb * kTileKeys + kPage * pg + 32 * grp;
+    // block scales of this thread's pairs of keys: (v, v', log2 v, log2 v'), and (1 / v, 1 / v')
+    const uint8_t* table = smem + G::kOffScales + sb * G::kScaleBytes;
+    const float4* scales = reinterpret_cast<const float4*>(table) + (kPage * pg + 32 * grp) / 2;
+    const float2* inverse = reinterpret_cast<const float2*>(table + kTileKeys / 2 * 16) + (kPage * pg + 32 * grp) / 2;
     if (!fail) {
       ptx::tc_fence_after();
       tmem_ld32(tmem + kTmemS + 64 * sb + 32 * grp + lanes, x);
@@ -273,29 +308,55 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_first(&ms->s_empty[sb], rank);
+      if constexpr (kScales == kLargeBlocks) {
+        one = scales[0];
+        one.x *= cs;
+      }
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        float2 v = ptx::mul2(make_float2(x[i], x[i + 1]), make_float2(cs, cs));
-        if constexpr (kScaled) {
-          const float4 a = scales[i], c = scales[i + 1];
-          v = ptx::fma2(v, make_float2(a.x, c.x), make_float2(a.y, c.y));
-        }
+        const float2 v = in_octaves(make_float2(x[i], x[i + 1]), scales, i);
         x[i] = v.x;
         x[i + 1] = v.y;
       }
-      if (sees != 0xffffffffu) {
+      if (__builtin_expect(sees != 0xffffffffu, 0)) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = (sees >> i) & 1u ? x[i] : -INFINITY;
       }
-      float top = x[0];
+      top = x[0];
 #pragma unroll
       for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
       need = top > ref + kMoveAbove;
-      ms->red[2 * pg + grp][row] = top;  // (read only if some row moves)
     }
     const bool moved = softmax_any(need || fail);
     float alpha = 1.f;
     if (moved) {
+      if constexpr (kFp8) {
+        // With little room above a reference (P is 8 bits wide) moves are frequent: look at the next
+        // tile's scores too, where all rows see all of it; it would move many of the same rows (29 nodes, 12 heads, 2^18 keys 157 -> 150 us).
+        if (!fail && kv_begin + (t + 2) * kTileKeys <= all_see) {
+          const int nb = (t + 1) & 1;
+          fail = !warp_wait(&ms->s_full[nb], ((t + 1) >> 1) & 1, abort, p);
+          if (kScaled && !fail) fail = !warp_wait(&ms->sc_full[nb], ((t + 1) >> 1) & 1, abort, p);
+          if (!fail) {
+            float y[32];
+            const float4* next = reinterpret_cast<const float4*>(smem + G::kOffScales + nb * G::kScaleBytes) + (kPage * pg + 32 * grp) / 2;
+            ptx::tc_fence_after();
+            tmem_ld32(tmem + kTmemS + 64 * nb + 32 * grp + lanes, y);
+            ptx::tmem_ld_wait();
+            ptx::tc_fence_before();
+            if constexpr (kScales == kLargeBlocks) {
+              one = next[0];
+              one.x *= cs;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 v = in_octaves(make_float2(y[i], y[i + 1]), next, i);
+              top = fmaxf(top, fmaxf(v.x, v.y));
+            }
+          }
+        }
+      }
+      ms->red[2 * pg + grp][row] = top;
       if (softmax_any(fail || *abort != 0)) {
         stop = true;
         break;
@@ -309,20 +370,21 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
     // O of the rows that move, between O(t - 1) and O(t); all warps' before any P(t) is handed on
     auto rescale = [&]() {
       if (t >= 1 && !fail) {
-        for (int k = 0; k < 2 && !fail; ++k) fail = !warp_wait(&ms->o_done[k], (t - 1) & 1, abort, p);
+        for (int k = 0; k < 2 && !fail; ++k) fail = !o_done(k, t - 1);
         if (!fail && __any_sync(0xffffffffu, alpha != 1.f)) {
           ptx::tc_fence_after();
           // this thread's row in half `grp` of the values
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            float o[32];
+          for (int c = 0; c < 128; c += 64) {
+            float o[64];
             const uint32_t at = tmem + kTmemO + 128 * grp + c + lanes;
             tmem_ld32(at, o);
+            tmem_ld32(at + 32, o + 32);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            ptx::tmem_st16(at, o);
-            ptx::tmem_st16(at + 16, o + 16);
+            for (int i = 0; i < 64; ++i) o[i] *= alpha;
+#pragma unroll
+            for (int i = 0; i < 64; i += 32) tmem_st32(at + i, o + i);
           }
           ptx::tmem_st_wait();
           ptx::tc_fence_before();
@@ -331,35 +393,36 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
       softmax_any(false);  // (`red` too is read before the next tile writes it)
     };
     if (!fail) {
-      float s = 0.f;
+      float2 s = make_float2(0.f, 0.f);
       uint32_t w[kFp8 ? 8 : 16], wl[kFp8 ? 8 : 1];
       const float nref = ref == -INFINITY ? 0.f : -ref;  // (a row that has seen no key yet: all scores are -inf)
+      uint32_t dither = dither2_of(key0);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
         const float2 v = ptx::add2(make_float2(x[i], x[i + 1]), make_float2(nref, nref));
-        const float p0 = ex2(v.x), p1 = ex2(v.y);
-        if constexpr (kScaled)
-          s += p0 * scales[i].z + p1 * scales[i + 1].z;
+        const float2 pv = make_float2(ex2(v.x), ex2(v.y));
+        if constexpr (kScales == kSmallBlocks)
+          s = ptx::fma2(pv, inverse[i / 2], s);
         else
-          s += p0 + p1;
+          s = ptx::add2(s, pv);
         if constexpr (kFp8) {
-          const uint32_t at = kDitherStep * (uint32_t)(key0 + i);
           uint32_t hi, lo;
-          split_p(p0, p1, __byte_perm(at, at + kDitherStep, 0x4743) & 0x00ff00ffu, hi, lo);
-          w[i / 4] = i % 4 ? w[i / 4] | hi << 16 : hi & 0xffffu;
-          wl[i / 4] = i % 4 ? wl[i / 4] | lo << 16 : lo & 0xffffu;
+          split_p(pv.x, pv.y, __byte_perm(dither, 0u, 0x4341), hi, lo);
+          dither += kDither2Step;
+          w[i / 4] = i % 4 ? __byte_perm(w[i / 4], hi, 0x5410) : hi;
+          wl[i / 4] = i % 4 ? __byte_perm(wl[i / 4], lo, 0x5410) : lo;
         } else {
-          w[i / 2] = pack_bf16(p0, p1);
+          w[i / 2] = pack_bf16(pv.x, pv.y);
         }
       }
-      l += s;
+      l += kScales == kLargeBlocks ? (s.x + s.y) * inverse[0].x : s.x + s.y;
       if (kScaled) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&ms->sc_free[sb]);
       }
       if (moved) rescale();
       const bool any = kv_begin + t * kTileKeys + kPage * pg < kv_end;  // (a unit's last tile may have one page)
-      if (t >= 1 && any) fail = !warp_wait(&ms->o_done[pg], (t - 1) & 1, abort, p);
+      if (t >= 1 && any) fail = !o_done(pg, t - 1);  // (P and the values of the page are single: the next ones follow O)
       if (!fail && any) {
         if constexpr (kFp8) {
           uint8_t* hi = smem + G::kOffP + pg * (kHalfRows * 64);
@@ -375,7 +438,7 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
           for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4*>(line + (((4 * grp + j) ^ (row & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
-        if (kv_begin + t * kTileKeys + kPage * (pg + 1) > kv_end) {
+        if (__builtin_expect(kv_begin + t * kTileKeys + kPage * (pg + 1) > kv_end, 0)) {
           // values behind the key range: zero, so that P = 0 meets V = 0 (a key and a half to a thread)
           fail = !warp_wait(&ms->v_full[pg], t & 1, abort, p);
           if (!fail && kv_begin + t * kTileKeys + kPage * pg + row >= kv_end) {
@@ -390,7 +453,7 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
         ptx::fence_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
-        if (!fail && lane == 0) arrive_first(&ms->p_ready[pg], rank);
+        if (!fail && lane == 0) arrive_first(&ms->p_ready[pg][sb], rank);
       }
     }
   }
@@ -402,8 +465,8 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
       softmax_sync();
       l = (ms->red[0][row] + ms->red[1][row]) + (ms->red[2][row] + ms->red[3][row]);
       const int npages = (kv_end - kv_begin + kPage - 1) / kPage;
-      fail = !warp_wait(&ms->o_done[0], (ntiles - 1) & 1, abort, p);
-      if (!fail && npages >= 2) fail = !warp_wait(&ms->o_done[1], (npages / 2 - 1) & 1, abort, p);
+      fail = !o_done(0, ntiles - 1);
+      if (!fail && npages >= 2) fail = !o_done(1, npages / 2 - 1);
       stop = softmax_any(fail || *abort != 0);
     }
   }
@@ -417,27 +480,35 @@ __device__ __forceinline__ void softmax_role(uint8_t* smem, Misc* ms, const Para
       p.lse[qrow0 + row] = lse;
   }
   const float os = l > 0.f ? p.out_scale / l : 0.f;
-  __nv_bfloat16* dst = part_row0 < 0 ? p.out + (size_t)(qrow0 + row) * kDv : p.part_o + (size_t)(part_row0 + row) * kDv;
-  dst += 256 * grp + 128 * pg;
+  const int dv = 256 * grp + 128 * pg;
+  __nv_bfloat16* dst = p.out + (size_t)(qrow0 + row) * kDv + dv;
+  float* part = (float*)p.part_o + (size_t)(part_row0 + row) * kDv + dv;
 #pragma unroll 1
   for (int c = 0; c < 128; c += 32) {
     float o[32];
     tmem_ld32(tmem + kTmemO + 128 * grp + c + lanes, o);
     ptx::tmem_ld_wait();
-    if (live) {
+    if (!live) continue;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] *= os;
+    if (part_row0 < 0) {
 #pragma unroll
       for (int i = 0; i < 32; i += 8)
-        *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(pack_bf16(o[i] * os, o[i + 1] * os), pack_bf16(o[i + 2] * os, o[i + 3] * os),
-                                                            pack_bf16(o[i + 4] * os, o[i + 5] * os), pack_bf16(o[i + 6] * os, o[i + 7] * os));
+        *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]),
+                                                            pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(part + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
     }
   }
 }
 
-template <bool kFp8, bool kScaled>
+template <bool kFp8, int kScales>
 __global__ void __launch_bounds__(kThreads, 1)
     wide_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, Params p) {
   using G = Geo<kFp8>;
+  constexpr bool kScaled = kScales != kOneScale;
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc* ms = (Misc*)(smem + G::kOffMisc);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -463,8 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(&ms->s_empty[i], 16);
         ptx::mbar_init(&ms->sc_full[i], 1);
         ptx::mbar_init(&ms->sc_free[i], 8);
-        ptx::mbar_init(&ms->p_ready[i], 8);
-        ptx::mbar_init(&ms->o_done[i], 1);
+        for (int k = 0; k < 2; ++k) {
+          ptx::mbar_init(&ms->p_ready[i][k], 8);
+          ptx::mbar_init(&ms->o_done[i][k], 1);
+        }
         ptx::mbar_init(&ms->drained[i], 1);
       }
       ptx::fence_mbar_init();
@@ -485,13 +558,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int npages = (kv_end - kv_begin + kPage - 1) / kPage;
   const int32_t* table = p.page_table + (size_t)ms->unit[0] * p.pt_stride + kv_begin / kPage;
   const uint32_t s0 = ptx::smem_addr(smem);
-  auto page_at = [&](int i) {  // page i of the unit (a tile's missing second page: the first one again)
-    const int page = table[i < npages ? i : npages - 1];
-    if (page < 0 || page >= p.num_pages) {
-      report(p.status, MLA_DEVICE_BAD_PAGE);
-      return 0;
-    }
-    return page;
+  // page i of the unit (a tile's missing second page: the first one again). An id is checked where it is
+  // used, so that its load is not waited for before.
+  auto page_id = [&](int i) { return table[i < npages ? i : npages - 1]; };
+  auto checked = [&](int page) {
+    if (page >= 0 && page < p.num_pages) return page;
+    report(p.status, MLA_DEVICE_BAD_PAGE);
+    return 0;
   };
 
   if (warp == 0) {
@@ -503,32 +576,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_arrive_expect_tx(&ms->q_full, kChunks * G::kQChunkBytes);
       ptx::tma_load_3d(smem, &tmap_q, &ms->q_full, 0, ms->unit[1] + kHalfRows * (int)rank, 0);
     }
-    int page = page_at((int)rank), next = ntiles > 1 ? page_at(2 + (int)rank) : 0;
+    // lanes 0-15 hold the ids of the tiles' first pages, lanes 16-31 of the second ones, two tiles ahead
+    int id = checked(page_id(lane >> 4)), id1 = ntiles > 1 ? page_id(2 + (lane >> 4)) : 0;
     float sc[4];
-    auto load_scales = [&](int t) {  // of four keys of the tile
+    auto load_scales = [&](int t, int page) {  // of four keys of the tile
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int key = 4 * lane + k;
         const bool in = kv_begin + t * kTileKeys + key < kv_end;
-        sc[k] = in ? p.kv_scales[((size_t)page_at(2 * t + (key >> 6)) * kPage + (key & 63)) >> p.block_log2] : 1.f;
+        sc[k] = in ? p.kv_scales[((size_t)page * kPage + (key & 63)) >> p.block_log2] : 1.f;
       }
     };
-    if (kScaled && ok) load_scales(0);
+    if (kScaled && ok) load_scales(0, id);
     for (int t = 0; ok && t < ntiles; ++t) {
-      if constexpr (kScaled) {
-        if (t >= 2) ok = warp_wait(&ms->sc_free[t & 1], ((t - 2) >> 1) & 1, abort, p);
-        if (!ok) break;
-        float4* dst = reinterpret_cast<float4*>(smem + G::kOffScales) + (t & 1) * kTileKeys + 4 * lane;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float v = fmaxf(sc[k], 0x1p-60f);
-          dst[k] = make_float4(sc[k], lg2(v), 1.f / v, 0.f);
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&ms->sc_full[t & 1]);
-        if (t + 1 < ntiles) load_scales(t + 1);
-      }
-      const int after = t + 2 < ntiles ? page_at(2 * (t + 2) + (int)rank) : 0;
+      const int page = __shfl_sync(0xffffffffu, id, 16 * (int)rank);
+      if (t + 1 < ntiles) id1 = checked(id1);
+      const int next = __shfl_sync(0xffffffffu, id1, 16 * (int)rank);
       for (int g = 0; ok && g < G::kPieces; ++g) {
         const int n = t * G::kPieces + g, slot = n % G::kSlots;
         if (n >= G::kSlots) ok = warp_wait(&ms->k_empty[slot], ((n / G::kSlots) - 1) & 1, abort, p);
@@ -541,8 +604,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         issued = n + 1;
       }
-      page = next;
-      next = after;
+      const int id2 = t + 2 < ntiles ? page_id(2 * (t + 2) + (lane >> 4)) : 0;
+      if constexpr (kScaled) {
+        if (ok && t >= 2) ok = warp_wait(&ms->sc_free[t & 1], ((t - 2) >> 1) & 1, abort, p);
+        if (!ok) break;
+        uint8_t* tables = smem + G::kOffScales + (t & 1) * G::kScaleBytes;
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const float v0 = fmaxf(sc[k], 0x1p-60f), v1 = fmaxf(sc[k + 1], 0x1p-60f);
+          reinterpret_cast<float4*>(tables)[2 * lane + k / 2] = make_float4(sc[k], sc[k + 1], lg2(v0), lg2(v1));
+          reinterpret_cast<float2*>(tables + kTileKeys / 2 * 16)[2 * lane + k / 2] = make_float2(1.f / v0, 1.f / v1);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ms->sc_full[t & 1]);
+        if (t + 1 < ntiles) load_scales(t + 1, id1);
+      }
+      id = id1;
+      id1 = id2;
     }
     // every copy lands before the CTA may exit
     if (lane == 0) {
@@ -562,10 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 3) {
     // ------------------------------------------------------------ copies of this CTA's value columns
     bool ok = !*abort;
-    int issued = 0, page = page_at(0);
+    int issued = 0, page = page_id(0);
     for (; ok && issued < npages; ++issued) {
       const int pg = issued & 1, t = issued >> 1;
-      const int next = issued + 1 < npages ? page_at(issued + 1) : 0;
+      page = checked(page);
       if (t >= 1) ok = warp_wait(&ms->v_empty[pg], (t - 1) & 1, abort, p);
       if (!ok) break;
       if (lane == 0) {
@@ -575,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tma_load_3d(dst + 2 * G::kChunkBytes, &tmap_v, &ms->v_full[pg], 0, page * kPage, 4 + 2 * (int)rank);
       }
       __syncwarp();
-      page = next;
+      page = page_id(issued + 1);
     }
     if (lane == 0) {
       for (int n = max(0, issued - 2); n < issued; ++n) {
@@ -585,118 +663,112 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1 && rank == 1) {
-    // ------------------------------------------------------------ CTA 1: tell CTA 0 what has landed
-    bool ok = !*abort && warp_wait(&ms->q_full, 0, abort, p);
-    for (int n = 0; ok && n < ntiles * G::kPieces; ++n) {
-      ok = warp_wait(&ms->k_full[n % G::kSlots], (n / G::kSlots) & 1, abort, p);
-      if (ok && lane == 0) arrive_first(&ms->k_peer[n % G::kSlots], rank);
-      __syncwarp();
-    }
-  } else if (warp == 2 && rank == 1) {
-    bool ok = !*abort;
-    for (int n = 0; ok && n < npages; ++n) {
-      ok = warp_wait(&ms->v_full[n & 1], (n >> 1) & 1, abort, p);
-      if (ok && lane == 0) arrive_first(&ms->v_peer[n & 1], rank);
-      __syncwarp();
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S(t) = Q . K^T into buffer t % 2
-    bool ok = !*abort && warp_wait(&ms->q_full, 0, abort, p), issued = false;
-    const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kRows, kTileKeys, 0, 0) : ptx::idesc_bf16(kRows, kTileKeys, 0, 0);
-    for (int t = 0; ok && t < ntiles; ++t) {
-      if (t >= 2) ok = warp_wait<true>(&ms->s_empty[t & 1], ((t - 2) >> 1) & 1, abort, p);
-      const uint32_t d = tmem + kTmemS + 64 * (t & 1);
-      for (int g = 0; ok && g < G::kPieces; ++g) {
-        const int n = t * G::kPieces + g, slot = n % G::kSlots;
-        ok = warp_wait(&ms->k_full[slot], (n / G::kSlots) & 1, abort, p);
-        if (ok) ok = warp_wait<true>(&ms->k_peer[slot], (n / G::kSlots) & 1, abort, p);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint32_t k0 = s0 + G::kOffK + slot * G::kSlotBytes, q0 = s0 + g * G::kPieceChunks * G::kQChunkBytes;
-          if constexpr (kFp8) {
+  } else if (warp <= 2) {
+    // One thread of the warp does all of the role's waiting and issuing (a whole warp that polls takes
+    // ~100 cycles a barrier: 4 x 64 nodes over 32768 bf16 keys 247 us, with one thread 187).
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+      const long long t0 = clock64();
+      while (!*abort) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > p.wait_budget) {
+          *abort = 1;
+          report(p.status, MLA_DEVICE_WAIT_TIMEOUT);
+        }
+      }
+      return false;
+    };
+    if (ptx::elect_one()) {
+      bool ok = !*abort, issued = false;
+      if (warp == 1 && rank == 1) {
+        // ---------------------------------------------------------- CTA 1: tell CTA 0 what has landed
+        ok = ok && wait(&ms->q_full, 0);
+        for (int n = 0; ok && n < ntiles * G::kPieces; ++n) {
+          ok = wait(&ms->k_full[n % G::kSlots], (n / G::kSlots) & 1);
+          if (ok) arrive_first(&ms->k_peer[n % G::kSlots], rank);
+        }
+      } else if (rank == 1) {
+        for (int n = 0; ok && n < npages; ++n) {
+          ok = wait(&ms->v_full[n & 1], (n >> 1) & 1);
+          if (ok) arrive_first(&ms->v_peer[n & 1], rank);
+        }
+      } else if (warp == 1) {
+        // ---------------------------------------------------------- S(t) = Q . K^T into buffer t % 2
+        ok = ok && wait(&ms->q_full, 0);
+        const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kRows, kTileKeys, 0, 0) : ptx::idesc_bf16(kRows, kTileKeys, 0, 0);
+        for (int t = 0; ok && t < ntiles; ++t) {
+          if (t >= 2) ok = wait(&ms->s_empty[t & 1], ((t - 2) >> 1) & 1);
+          const uint32_t d = tmem + kTmemS + 64 * (t & 1);
+          for (int g = 0; ok && g < G::kPieces; ++g) {
+            const int n = t * G::kPieces + g, slot = n % G::kSlots;
+            ok = wait(&ms->k_full[slot], (n / G::kSlots) & 1) && wait(&ms->k_peer[slot], (n / G::kSlots) & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t k0 = s0 + G::kOffK + slot * G::kSlotBytes, q0 = s0 + g * G::kPieceChunks * G::kQChunkBytes;
+            if constexpr (kFp8) {
+#pragma unroll 1
+              for (int c = 0; c < G::kPieceChunks; ++c)
 #pragma unroll
-            for (int c = 0; c < G::kPieceChunks; ++c)
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                  for (int part = 0; part < 2; ++part)
+                    mma2<true>(d, ptx::smem_desc(q0 + c * G::kQChunkBytes + part * (kHalfRows * 64) + 32 * k, 16, 512, ptx::kSwizzle64B),
+                               ptx::smem_desc(k0 + c * G::kChunkBytes + 32 * k, 16, 512, ptx::kSwizzle64B), idesc, (c | k | part) != 0 ? 1u : 0u);
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < G::kPieceChunks; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma2<false>(d, ptx::smem_desc(q0 + c * G::kQChunkBytes + 32 * k, 16, 1024, ptx::kSwizzle128B),
+                              ptx::smem_desc(k0 + c * G::kChunkBytes + 32 * k, 16, 1024, ptx::kSwizzle128B), idesc, (g | c | k) != 0 ? 1u : 0u);
+            }
+            commit_both(&ms->k_empty[slot]);
+            if (g == G::kPieces - 1) commit_both(&ms->s_full[t & 1]);
+            issued = true;
+          }
+        }
+      } else {
+        // ---------------------------------------------------------- O += P(t) . V(t), a page at a time
+        const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kRows, 256, 0, 1) : ptx::idesc_bf16(kRows, 256, 0, 1);
+        for (int n = 0; ok && n < npages; ++n) {
+          const int pg = n & 1, t = n >> 1;
+          ok = wait(&ms->v_full[pg], t & 1) && wait(&ms->v_peer[pg], t & 1) && wait(&ms->p_ready[pg][t & 1], (t >> 1) & 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t v0 = s0 + G::kOffV + pg * G::kVPage, p0 = s0 + G::kOffP;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t d = tmem + kTmemO + 128 * h, vh = v0 + h * (2 * G::kChunkBytes);
+            if constexpr (kFp8) {
 #pragma unroll
               for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
-                  mma2<true>(d, ptx::smem_desc(q0 + c * G::kQChunkBytes + part * (kHalfRows * 64) + 32 * k, 16, 512, ptx::kSwizzle64B),
-                             ptx::smem_desc(k0 + c * G::kChunkBytes + 32 * k, 16, 512, ptx::kSwizzle64B), idesc, (c | k | part) != 0 ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int c = 0; c < G::kPieceChunks; ++c)
+                  mma2<true>(d, ptx::smem_desc(p0 + part * (kHalfRows * 128) + pg * (kHalfRows * 64) + 32 * k, 16, 512, ptx::kSwizzle64B),
+                             ptx::smem_desc(vh + 2048 * k, G::kChunkBytes, 512, ptx::kSwizzle64B), idesc | (part ? ptx::kA_E5M2 : 0u),
+                             (n | k | part) != 0 ? 1u : 0u);
+            } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                mma2<false>(d, ptx::smem_desc(q0 + c * G::kQChunkBytes + 32 * k, 16, 1024, ptx::kSwizzle128B),
-                            ptx::smem_desc(k0 + c * G::kChunkBytes + 32 * k, 16, 1024, ptx::kSwizzle128B), idesc, (g | c | k) != 0 ? 1u : 0u);
+                mma2<false>(d, ptx::smem_desc(p0 + pg * (kHalfRows * 128) + 32 * k, 16, 1024, ptx::kSwizzle128B),
+                            ptx::smem_desc(vh + 2048 * k, G::kChunkBytes, 1024, ptx::kSwizzle128B), idesc, (n | k) != 0 ? 1u : 0u);
+            }
           }
-          commit_both(&ms->k_empty[slot]);
-          if (g == G::kPieces - 1) commit_both(&ms->s_full[t & 1]);
+          commit_both(&ms->v_empty[pg]);
+          commit_both(&ms->o_done[pg][t & 1]);
+          issued = true;
         }
-        __syncwarp();
-        issued = true;
       }
-    }
-    if (issued) {
-      if (ptx::elect_one()) {
-        commit_here(&ms->drained[0]);
+      if (issued) {  // every product retires before tensor memory is released
+        commit_here(&ms->drained[warp - 1]);
         const long long t0 = clock64();
-        while (!ptx::mbar_try_wait(&ms->drained[0], 0) && clock64() - t0 < p.wait_budget) {
+        while (!ptx::mbar_try_wait(&ms->drained[warp - 1], 0) && clock64() - t0 < p.wait_budget) {
         }
       }
-      __syncwarp();
     }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ O += P(t) . V(t)
-    bool ok = !*abort, issued = false;
-    const uint32_t idesc = kFp8 ? ptx::idesc_e4m3(kRows, 256, 0, 1) : ptx::idesc_bf16(kRows, 256, 0, 1);
-    for (int n = 0; ok && n < npages; ++n) {
-      const int pg = n & 1, t = n >> 1;
-      ok = warp_wait(&ms->v_full[pg], t & 1, abort, p);
-      if (ok) ok = warp_wait<true>(&ms->v_peer[pg], t & 1, abort, p);
-      if (ok) ok = warp_wait<true>(&ms->p_ready[pg], t & 1, abort, p);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      ptx::fence_async_smem_cluster();
-      if (ptx::elect_one()) {
-        const uint32_t v0 = s0 + G::kOffV + pg * G::kVPage, p0 = s0 + G::kOffP;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t d = tmem + kTmemO + 128 * h, vh = v0 + h * (2 * G::kChunkBytes);
-          if constexpr (kFp8) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-                mma2<true>(d, ptx::smem_desc(p0 + part * (kHalfRows * 128) + pg * (kHalfRows * 64) + 32 * k, 16, 512, ptx::kSwizzle64B),
-                           ptx::smem_desc(vh + 2048 * k, G::kChunkBytes, 512, ptx::kSwizzle64B), idesc | (part ? ptx::kA_E5M2 : 0u),
-                           (n | k | part) != 0 ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma2<false>(d, ptx::smem_desc(p0 + pg * (kHalfRows * 128) + 32 * k, 16, 1024, ptx::kSwizzle128B),
-                          ptx::smem_desc(vh + 2048 * k, G::kChunkBytes, 1024, ptx::kSwizzle128B), idesc, (n | k) != 0 ? 1u : 0u);
-          }
-        }
-        commit_both(&ms->v_empty[pg]);
-        commit_both(&ms->o_done[pg]);
-      }
-      __syncwarp();
-      issued = true;
-    }
-    if (issued) {
-      if (ptx::elect_one()) {
-        commit_here(&ms->drained[1]);
-        const long long t0 = clock64();
-        while (!ptx::mbar_try_wait(&ms->drained[1], 0) && clock64() - t0 < p.wait_budget) {
-        }
-      }
-      __syncwarp();
-    }
+    __syncwarp();
   } else {
-    softmax_role<kFp8, kScaled>(smem, ms, p, tmem, rank, warp & 3, (warp - 4) >> 2, lane, tid - 128);
+    softmax_role<kFp8, kScales>(smem, ms, p, tmem, rank, warp & 3, (warp - 4) >> 2, lane, tid - 128);
     __syncwarp();
   }
   ptx::tc_fence_before();
@@ -730,9 +802,9 @@ static CUresult encode_wide(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* 
 }
 
 cudaError_t set_wide_kernel_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(wide::wide_decode_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::Geo<false>::kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(wide::wide_decode_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::Geo<true>::kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(wide::wide_decode_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::Geo<true>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(wide::wide_decode_kernel<false, wide::kOneScale>, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::Geo<false>::kSmem);
+  for (auto fn : {wide::wide_decode_kernel<true, wide::kOneScale>, wide::wide_decode_kernel<true, wide::kLargeBlocks>, wide::wide_decode_kernel<true, wide::kSmallBlocks>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::Geo<true>::kSmem);
   return e;
 }
 
@@ -756,7 +828,10 @@ int launch_wide_kernel(const PlanHeader* h, const void* q, const void* kv_cache,
   attr[0].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto fn = prm.kv_scales ? wide::wide_decode_kernel<true, true> : fp8 ? wide::wide_decode_kernel<true, false> : wide::wide_decode_kernel<false, false>;
+  auto fn = !fp8             ? wide::wide_decode_kernel<false, wide::kOneScale>
+            : !prm.kv_scales ? wide::wide_decode_kernel<true, wide::kOneScale>
+            : prm.block_log2 >= 5 ? wide::wide_decode_kernel<true, wide::kLargeBlocks>
+                                  : wide::wide_decode_kernel<true, wide::kSmallBlocks>;
   const cudaError_t ce = cudaLaunchKernelEx(&cfg, fn, tq, tk, tv, prm);
   if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "wide kernel launch: %s", cudaGetErrorString(ce));
   return MLA_OK;

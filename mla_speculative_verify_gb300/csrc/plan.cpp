@@ -49,9 +49,9 @@ int block_log2_of(int block_tokens) {
   return -1;
 }
 
-size_t workspace_bytes_for(int n_part_rows) {
+size_t workspace_bytes_for(int n_part_rows, bool wide) {
   if (n_part_rows <= 0) return 0;
-  return align_up((size_t)n_part_rows * kDv * kPartOElemBytes, 256) + align_up((size_t)n_part_rows * sizeof(float), 256);
+  return align_up((size_t)n_part_rows * kDv * (wide ? kWidePartOElemBytes : kPartOElemBytes), 256) + align_up((size_t)n_part_rows * sizeof(float), 256);
 }
 
 }  // namespace mla
@@ -114,10 +114,12 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   }
   if (pair) cap = pair_rows_cap();
   // Trees of many rows run in tiles of 128 rows on clusters of two CTAs, where those take less of the
-  // SMs' time: a page of such a tile keeps two SMs as long as kWidePage pages of a 48-row tile keep one.
+  // SMs' time: a page of such a tile takes as much of it as kWidePage pages of a 48-row tile. (64 rows, 32
+  // requests of 4k to 8k keys: 55 us in wide tiles, 79 in narrow ones with a bf16 cache, 57 and 63 with an
+  // e4m3 one; 96 rows over 2^17 keys 40 and 60, 40 and 52; 512 to 1024 rows 2.0 and 1.5 times as fast.)
   bool wide = force_wide;
   if (whole_requests && o.max_rows_per_cta == 0) {
-    const double kWidePage = kv_dtype == MLA_KV_BF16 ? 1.0 : 1.4;
+    const double kWidePage = kv_dtype == MLA_KV_BF16 ? 1.4 : 1.8;
     double narrow_cost = 0, wide_cost = 0;
     for (int b = 0; b < batch; ++b) {
       const double rows = (double)q_lens_h[b] * num_heads, pages = (seq_lens_h[b] + kPage - 1) / kPage;
@@ -176,14 +178,15 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   // epilogue and its split partial) plus its pages, each weighted by its row tile's cost
   // (a tile of <= 32 rows of an e4m3 cache takes less than a 48-row tile). The model's
   // constants were fitted to measured call times over forced piece lengths on GB300
-  // (bf16: a unit start ~ 6 page-times; e4m3: ~ 16). It sees each request's q, so a batch
+  // (bf16: a unit start ~ 6 page-times; e4m3: ~ 16; tiles of 128 rows, whose page takes a cluster half
+  // as long: ~ 24, by sweeps over ten batches: 32 trees of 48 heads 418 us with 10, 393 with 24). It sees each request's q, so a batch
   // of ragged query lengths, whose fold groups differ in tile count, gets other piece
   // lengths than a uniform one of the same total work. A split keeps at least min_pages
   // pages.
-  const int min_pages = o.min_pages_per_split > 0 ? o.min_pages_per_split : 4;
+  const int min_pages = o.min_pages_per_split > 0 ? o.min_pages_per_split : wide ? 2 : 4;
   const int max_splits = max_splits_for_merge();
   const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
-  const double start_cost = wide ? 10.0 : fp8 ? 16.0 : 6.0;
+  const double start_cost = wide ? 24.0 : fp8 ? 16.0 : 6.0;
   auto row_cost = [&](int nrows) { return (!wide && fp8 && nrows <= 32) ? 0.9 : 1.0; };
   long long tile_pages = 0;
   for (const Group& g : groups) tile_pages += (long long)(g.t1 - g.t0) * g.pages;
@@ -295,7 +298,7 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   size_t total = align_up(merge_off + sizeof(PlanMerge) * merges.size(), 64);
   if (total > (size_t)INT32_MAX) return set_error(MLA_ERR_INVALID_ARG, "plan too large");
   if (plan_bytes_out) *plan_bytes_out = total;
-  if (workspace_bytes_out) *workspace_bytes_out = workspace_bytes_for(part_rows);
+  if (workspace_bytes_out) *workspace_bytes_out = workspace_bytes_for(part_rows, wide);
   if (!plan_buf || plan_buf_bytes < total)
     return set_error(MLA_ERR_BUFFER, "plan buffer needs %zu bytes (got %zu)", total, plan_buf ? plan_buf_bytes : (size_t)0);
 

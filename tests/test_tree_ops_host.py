@@ -120,12 +120,16 @@ def test_tensors_off_the_gpu_are_refused():
 @pytest.mark.parametrize("heads,seq,q", [(12, [4096], [29]), (12, [100, 64, 5000], [1, 64, 7]), (128, [700], [13]),
                                          (48, [16384, 9000, 300], [5, 16, 11]), (1, [65], [65]), (33, [5000], [96])])
 @pytest.mark.parametrize("kv", [0, 1])
-def test_tree_plan_covers_every_row_and_key_once(heads, seq, q, kv):
-    buf, ws = binding.plan(seq, q, heads, kv, 152, tree=True)
+@pytest.mark.parametrize("cap", [0, 48, 128])
+def test_tree_plan_covers_every_row_and_key_once(heads, seq, q, kv, cap):
+    """Of the planner's choice, in tiles of 48 rows, in tiles of 128."""
+    buf, ws = binding.plan(seq, q, heads, kv, 152, binding.PlanOptions(max_rows_per_cta=cap), tree=True)
     pl = read_plan(buf)
+    wide = pl["header"]["reserved0"]
+    assert wide == {0: wide, 48: 0, 128: 1}[cap]
     rows = np.zeros((sum(q) * heads, max(seq)), np.int32)
     for u in pl["units"]:
-        assert u["kv_begin"] % 64 == 0 and 0 < u["nrows"] <= 48
+        assert u["kv_begin"] % 64 == 0 and 0 < u["nrows"] <= (128 if wide else 48)
         rows[u["qrow0"]:u["qrow0"] + u["nrows"], u["kv_begin"]:u["kv_end"]] += 1
         lo = pl["requests"][u["b"]]["tok0"] * heads
         assert lo <= u["qrow0"] and u["qrow0"] + u["nrows"] <= lo + u["q"] * heads
@@ -140,10 +144,19 @@ def test_tree_plan_covers_every_row_and_key_once(heads, seq, q, kv):
 
 
 def test_a_prime_tree_is_cut_into_full_tiles():
-    """29 tokens of 12 heads: 348 rows in 8 tiles of 48, where the fold rule would make 29 of 12."""
-    pl = read_plan(binding.plan([8192], [29], 12, 0, 152, binding.PlanOptions(force_splits=1), tree=True)[0])
-    assert sorted(u["nrows"] for u in pl["units"]) == [12] + [48] * 7
-    assert len(read_plan(binding.plan([8192], [29], 12, 0, 152, binding.PlanOptions(force_splits=1))[0])["units"]) == 29
+    """29 tokens of 12 heads: 348 rows in 8 tiles of 48 or 3 of 128, where the fold rule would make 29 of 12."""
+    def rows(cap, tree):
+        return sorted(u["nrows"] for u in read_plan(binding.plan([8192], [29], 12, 0, 152, binding.PlanOptions(
+            force_splits=1, max_rows_per_cta=cap), tree=tree)[0])["units"])
+    assert rows(48, True) == [12] + [48] * 7 and rows(128, True) == [92, 128, 128] == rows(0, True)
+    assert rows(0, False) == [12] * 29
+
+
+def test_few_rows_stay_in_narrow_tiles():
+    for kv in (0, 1):
+        wide = [read_plan(binding.plan([4096], [q], 12, kv, 152, tree=True)[0])["header"]["reserved0"] for q in (1, 4, 5, 8, 64)]
+        assert wide == [0, 0, 1, 1, 1]
+        assert read_plan(binding.plan([4096], [64], 12, kv, 152)[0])["header"]["reserved0"] == 0
 
 
 def test_tree_plan_refusals():
