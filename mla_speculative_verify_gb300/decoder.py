@@ -58,6 +58,8 @@ class VerifyDecoder:
         self.plan_dev = torch.from_numpy(self.plan_host).to(self.device)
         self.workspace = (torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
                           if self.workspace_bytes else None)
+        self._plan_dev_ptr, self._plan_bytes = self.plan_dev.data_ptr(), self.plan_host.nbytes
+        self._workspace_ptr = _ptr(self.workspace)
         self.seq_lens_dev = torch.from_numpy(self.seq_lens).to(self.device)
         self.q_lens_dev = torch.from_numpy(self.q_lens).to(self.device)
         self.total_q = int(self.q_lens.sum())
@@ -73,6 +75,10 @@ class VerifyDecoder:
         are replayed at once) need a decoder each. ``tree_masks`` [total_q, words] int32, as
         ``tree.masks`` writes them: verify token i sees the keys before the request's verify tokens,
         and of those the ones whose bit is set (a row that sees none gets zeros)."""
+        if tree_masks is not None:
+            self._run_tree(q, kv_cache, page_table, out, lse, sm_scale, kv_scale, status, stream, seq_lens_dev, q_lens_dev,
+                           kv_scales, tree_masks)
+            return
         H = self.num_heads
         want_kv = torch.bfloat16 if self.kv_dtype == "bf16" else torch.uint8
         if q.dtype != torch.bfloat16 or tuple(q.shape) != (self.total_q, H, 576) or not q.is_contiguous():
@@ -93,22 +99,6 @@ class VerifyDecoder:
         for t in (q, kv_cache, out, page_table, lse, status):
             if t is not None and t.device != self.device:
                 raise ValueError("all tensors must be on the decoder's device")
-        if tree_masks is not None:
-            index, block = self.device.index, 0
-            words = tree_masks.shape[1] if tree_masks.dim() == 2 else 0
-            check_tensor("tree_masks", tree_masks, torch.int32, (self.total_q, words), index)
-            if kv_scales is not None:
-                if self.kv_dtype != "fp8":
-                    raise ValueError("block scales belong to an fp8 cache")
-                block = check_scales("kv_scales", kv_scales, rows // 64, index)
-            stride = check_table("page_table", page_table, self.seq_lens.shape[0], index)
-            on_device(index, binding.run_tree, self.plan_dev.data_ptr(), self._plan_host_ptr, self.plan_host.nbytes,
-                      q.data_ptr(), kv_cache.data_ptr(), _ptr(kv_scales), block, page_table.data_ptr(), stride,
-                      rows // 64, (seq_lens_dev if seq_lens_dev is not None else self.seq_lens_dev).data_ptr(),
-                      (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(), tree_masks.data_ptr(),
-                      words, sm_scale, kv_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
-                      _ptr(status), stream_handle(index, stream))
-            return
         if kv_scales is not None:
             if self.kv_dtype != "fp8":
                 raise ValueError("block scales belong to an fp8 cache")
@@ -130,6 +120,43 @@ class VerifyDecoder:
                     (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(),
                     sm_scale, kv_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
                     _ptr(status), st.cuda_stream)
+
+    def _run_tree(self, q, kv_cache, page_table, out, lse, sm_scale, kv_scale, status, stream, seq_lens_dev, q_lens_dev,
+                  kv_scales, tree_masks) -> None:
+        """``run`` with ``tree_masks``."""
+        H, index, batch, total = self.num_heads, self.device.index, self.seq_lens.shape[0], self.total_q
+        check_tensor("q", q, torch.bfloat16, (total, H, 576), index)
+        shape = kv_cache.shape
+        if shape[-1:] != (576,) or kv_cache.numel() % (64 * 576):
+            raise ValueError("kv_cache must hold whole 64-row pages [..., 576]")
+        pages = kv_cache.numel() // (64 * 576)
+        check_tensor("kv_cache", kv_cache, torch.bfloat16 if self.kv_dtype == "bf16" else E4M3, shape, index)
+        check_tensor("out", out, torch.bfloat16, (total, H, 512), index)
+        if lse is not None:
+            check_tensor("lse", lse, torch.float32, (total, H), index)
+        block = 0
+        if kv_scales is not None:
+            if self.kv_dtype != "fp8":
+                raise ValueError("block scales belong to an fp8 cache")
+            block = check_scales("kv_scales", kv_scales, pages, index)
+        stride = check_table("page_table", page_table, batch, index)
+        words = tree_masks.shape[1] if tree_masks.dim() == 2 else 0
+        check_tensor("tree_masks", tree_masks, torch.int32, (total, words), index)
+        if status is not None:
+            check_tensor("status", status, torch.int32, (1,), index)
+        if seq_lens_dev is None:
+            seq_lens_dev = self.seq_lens_dev
+        else:
+            check_tensor("seq_lens_dev", seq_lens_dev, torch.int32, (batch,), index)
+        if q_lens_dev is None:
+            q_lens_dev = self.q_lens_dev
+        else:
+            check_tensor("q_lens_dev", q_lens_dev, torch.int32, (batch,), index)
+        on_device(index, binding.run_tree, self._plan_dev_ptr, self._plan_host_ptr, self._plan_bytes, q.data_ptr(),
+                  kv_cache.data_ptr(), _ptr(kv_scales), block, page_table.data_ptr(), stride, pages,
+                  seq_lens_dev.data_ptr(), q_lens_dev.data_ptr(), tree_masks.data_ptr(), words, sm_scale, kv_scale,
+                  out.data_ptr(), _ptr(lse), self._workspace_ptr, self.workspace_bytes, _ptr(status),
+                  stream_handle(index, stream))
 
     def key_weights(self, q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor, lse: torch.Tensor,
                     weights: torch.Tensor, decay: float = 1.0, counted: torch.Tensor | None = None,
