@@ -54,6 +54,159 @@ size_t workspace_bytes_for(int n_part_rows, bool wide) {
   return align_up((size_t)n_part_rows * kDv * (wide ? kWidePartOElemBytes : kPartOElemBytes), 256) + align_up((size_t)n_part_rows * sizeof(float), 256);
 }
 
+namespace {
+
+struct RowTile { int b, qrow0, nrows, pages; };
+// tiles [t0, t1) of one fold group: consecutive, same request, qrow0 contiguous
+struct Group { size_t t0, t1; int b, pages, n_split, cap; };  // cap: piece length in pages (0: equal pieces)
+
+int piece_pages(const Group& g, int s) {
+  if (g.cap > 0) return std::min(g.pages, (s + 1) * g.cap) - s * g.cap;
+  return (int)((long long)g.pages * (s + 1) / g.n_split - (long long)g.pages * s / g.n_split);
+}
+
+// What a partition is made of: the kernel's tiles, and what the model of their time knows.
+struct Geometry {
+  bool wide, whole_requests;
+  int cap;            // rows of a tile
+  int slots;          // units that run at once
+  int min_pages;      // of a piece
+  double start_cost;  // of a unit, in page-times
+  double page_us;     // a page-time (only compared between geometries)
+};
+
+struct Partition {
+  std::vector<RowTile> tiles;
+  std::vector<PlanRequest> reqs;
+  std::vector<Group> groups;
+  double end_us;  // when the model's last unit ends
+};
+
+Partition cut_batch(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads, bool fp8,
+                    const mla_plan_options& o, const Geometry& geo) {
+  Partition out;
+  std::vector<RowTile>& tiles = out.tiles;
+  std::vector<PlanRequest>& reqs = out.reqs;
+  std::vector<Group>& groups = out.groups;
+  reqs.resize(batch);
+  const int cap = geo.cap, slots = geo.slots, min_pages = geo.min_pages;
+  const double start_cost = geo.start_cost;
+  // --- row tiles ----------------------------------------------------------------------
+  int tok0 = 0;
+  for (int b = 0; b < batch; ++b) {
+    int ctx = seq_lens_h[b], q = q_lens_h[b];
+    int F = geo.whole_requests ? q : o.force_fold > 0 ? o.force_fold : fold_factor(q, num_heads);
+    reqs[b] = PlanRequest{ctx, q, tok0, F};
+    int R = F * num_heads;                       // packed rows per fold group
+    int n_rt = (R + cap - 1) / cap;
+    int T = ((R + n_rt - 1) / n_rt + 15) / 16 * 16;
+    if (T > cap) T = cap;
+    int pages = (ctx + kPage - 1) / kPage;
+    for (int g = 0; g < q / F; ++g) {
+      int grow0 = (tok0 + g * F) * num_heads;
+      for (int r0 = 0; r0 < R; r0 += T) {
+        tiles.push_back(RowTile{b, grow0 + r0, std::min(T, R - r0), pages});
+      }
+    }
+    tok0 += q;
+  }
+
+  // --- fold groups ------------------------------------------------------------------
+  for (size_t i = 0; i < tiles.size();) {
+    size_t j = i;
+    int grp_rows = 0;
+    const int b = tiles[i].b;
+    const int R = reqs[b].fold * num_heads;
+    while (j < tiles.size() && tiles[j].b == b && grp_rows < R) { grp_rows += tiles[j].nrows; ++j; }
+    groups.push_back(Group{i, j, b, tiles[i].pages, 1, 1});
+    i = j;
+  }
+
+  // --- splits ----------------------------------------------------------------------
+  // Each group is cut into pieces of T pages (the last one shorter); all row tiles of the
+  // group are cut at the same boundaries. The units are ordered longest first (below), so
+  // the full-length units fill the SMs and the short tails run back to back on the SMs
+  // left over. T is the per-SM share of the tile-pages divided by k, for the k whose
+  // schedule ends first in a model of the hardware's in-order CTA dispatch: a unit costs
+  // a start-up of kStart page-times (its prologue, first copies and Q preparation, the
+  // epilogue and its split partial) plus its pages, each weighted by its row tile's cost
+  // (a tile of <= 32 rows of an e4m3 cache takes less than a 48-row tile). The model's
+  // constants were fitted to measured call times over forced piece lengths on GB300
+  // (bf16: a unit start ~ 6 page-times; e4m3: ~ 16). It sees each request's q, so a batch
+  // of ragged query lengths, whose fold groups differ in tile count, gets other piece
+  // lengths than a uniform one of the same total work. A split keeps at least min_pages
+  // pages.
+  const int max_splits = max_splits_for_merge();
+  auto row_cost = [&](int nrows) { return (!geo.wide && fp8 && nrows <= 32) ? 0.9 : 1.0; };
+  long long tile_pages = 0;
+  for (const Group& g : groups) tile_pages += (long long)(g.t1 - g.t0) * g.pages;
+  auto assign = [&](long long T) {
+    for (auto& g : groups) {
+      long long n = o.force_splits > 0 ? o.force_splits : (g.pages + T - 1) / T;
+      g.n_split = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(n, g.pages), max_splits));
+      // pieces of T pages, unless the split count was capped or forced: then equal pieces
+      g.cap = (o.force_splits <= 0 && (long long)g.n_split == (g.pages + T - 1) / T) ? (int)T : 0;
+    }
+  };
+  // the end of the schedule with pieces of T pages
+  std::vector<std::pair<int, double>> lens;  // (pages, per-page cost) of every unit
+  auto end_of = [&](long long T) {
+    assign(T);
+    lens.clear();
+    for (const Group& g : groups)
+      for (int s = 0; s < g.n_split; ++s)
+        for (size_t t = g.t0; t < g.t1; ++t) lens.emplace_back(piece_pages(g, s), row_cost(tiles[t].nrows));
+    std::stable_sort(lens.begin(), lens.end(),
+                     [](const std::pair<int, double>& a, const std::pair<int, double>& b) { return a.first > b.first; });
+    std::priority_queue<double, std::vector<double>, std::greater<double>> sm;
+    for (int i = 0; i < slots; ++i) sm.push(0.0);
+    double end = 0;
+    for (const auto& L : lens) {
+      const double t = sm.top() + start_cost + L.first * L.second;
+      sm.pop();
+      sm.push(t);
+      end = std::max(end, t);
+    }
+    return end;
+  };
+  long long best_T = std::max<long long>(min_pages, (tile_pages + slots - 1) / slots);
+  if (o.unit_pages > 0) best_T = o.unit_pages;
+  double best_end = -1;
+  if (o.force_splits > 0 || o.unit_pages > 0) {
+    best_end = end_of(best_T);
+  } else {
+    // candidates: the per-SM share divided by 1, 1.25, ... 8, and the longest group's
+    // pages divided into 1 .. 64 equal pieces
+    std::vector<long long> cands;
+    for (int k4 : {4, 5, 6, 8, 10, 12, 16, 20, 24, 32})
+      cands.push_back((4 * tile_pages + (long long)slots * k4 - 1) / ((long long)slots * k4));
+    int longest = 0;
+    for (const Group& g : groups) longest = std::max(longest, g.pages);
+    for (int n = 1; n <= 64; ++n) cands.push_back((longest + n - 1) / n);
+    std::sort(cands.begin(), cands.end());
+    cands.erase(std::unique(cands.begin(), cands.end()), cands.end());
+    for (long long c : cands) {
+      const long long T = std::max<long long>(min_pages, c);
+      // more than 16 waves of units (beyond one unit per row tile) never pays for its
+      // start-up costs; skipping those keeps the search cheap for very long batches
+      long long n_units = 0;
+      for (const Group& g : groups) n_units += (long long)(g.t1 - g.t0) * ((g.pages + T - 1) / T);
+      if (n_units > std::max<long long>(16LL * slots, (long long)tiles.size()) && !cands.empty() && c != cands.back())
+        continue;
+      const double end = end_of(T);
+      if (best_end < 0 || end < best_end - 1e-9) {
+        best_end = end;
+        best_T = T;
+      }
+    }
+  }
+  assign(best_T);
+  out.end_us = best_end * geo.page_us;
+  return out;
+}
+
+}  // namespace
+
 }  // namespace mla
 
 using namespace mla;
@@ -113,141 +266,45 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
     pair = R > cap && R <= pair_rows_cap();
   }
   if (pair) cap = pair_rows_cap();
-  // Trees of many rows run in tiles of 128 rows on clusters of two CTAs, where those take less of the
-  // SMs' time: a page of such a tile takes as much of it as kWidePage pages of a 48-row tile. (64 rows, 32
-  // requests of 4k to 8k keys: 55 us in wide tiles, 79 in narrow ones with a bf16 cache, 57 and 63 with an
-  // e4m3 one; 96 rows over 2^17 keys 40 and 60, 40 and 52; 512 to 1024 rows 2.0 and 1.5 times as fast.)
-  bool wide = force_wide;
-  if (whole_requests && o.max_rows_per_cta == 0) {
-    const double kWidePage = kv_dtype == MLA_KV_BF16 ? 1.4 : 1.8;
-    double narrow_cost = 0, wide_cost = 0;
-    for (int b = 0; b < batch; ++b) {
-      const double rows = (double)q_lens_h[b] * num_heads, pages = (seq_lens_h[b] + kPage - 1) / kPage;
-      narrow_cost += std::ceil(rows / cap) * pages;
-      wide_cost += kWidePage * std::ceil(rows / wide_rows_cap()) * pages;
-    }
-    wide = wide_cost < narrow_cost;
-  }
-  if (wide) cap = wide_rows_cap();
-  const int slots = pair || wide ? (o.pair_slots > 0 ? o.pair_slots : std::max(1, num_sms / 2)) : num_sms;
-
-  // --- row tiles ----------------------------------------------------------------------
-  struct RowTile { int b, qrow0, nrows, pages; };
-  std::vector<RowTile> tiles;
-  std::vector<PlanRequest> reqs(batch);
-  int tok0 = 0;
-  for (int b = 0; b < batch; ++b) {
-    int ctx = seq_lens_h[b], q = q_lens_h[b];
-    int F = whole_requests ? q : o.force_fold > 0 ? o.force_fold : fold_factor(q, num_heads);
-    reqs[b] = PlanRequest{ctx, q, tok0, F};
-    int R = F * num_heads;                       // packed rows per fold group
-    int n_rt = (R + cap - 1) / cap;
-    int T = ((R + n_rt - 1) / n_rt + 15) / 16 * 16;
-    if (T > cap) T = cap;
-    int pages = (ctx + kPage - 1) / kPage;
-    for (int g = 0; g < q / F; ++g) {
-      int grow0 = (tok0 + g * F) * num_heads;
-      for (int r0 = 0; r0 < R; r0 += T) {
-        tiles.push_back(RowTile{b, grow0 + r0, std::min(T, R - r0), pages});
-      }
-    }
-    tok0 += q;
-  }
-
-  // --- fold groups ------------------------------------------------------------------
-  // tiles [t0, t1) of one fold group: consecutive, same request, qrow0 contiguous
-  struct Group { size_t t0, t1; int b, pages, n_split, cap; };  // cap: piece length in pages (0: equal pieces)
-  std::vector<Group> groups;
-  for (size_t i = 0; i < tiles.size();) {
-    size_t j = i;
-    int grp_rows = 0;
-    const int b = tiles[i].b;
-    const int R = reqs[b].fold * num_heads;
-    while (j < tiles.size() && tiles[j].b == b && grp_rows < R) { grp_rows += tiles[j].nrows; ++j; }
-    groups.push_back(Group{i, j, b, tiles[i].pages, 1, 1});
-    i = j;
-  }
-
-  // --- splits ----------------------------------------------------------------------
-  // Each group is cut into pieces of T pages (the last one shorter); all row tiles of the
-  // group are cut at the same boundaries. The units are ordered longest first (below), so
-  // the full-length units fill the SMs and the short tails run back to back on the SMs
-  // left over. T is the per-SM share of the tile-pages divided by k, for the k whose
-  // schedule ends first in a model of the hardware's in-order CTA dispatch: a unit costs
-  // a start-up of kStart page-times (its prologue, first copies and Q preparation, the
-  // epilogue and its split partial) plus its pages, each weighted by its row tile's cost
-  // (a tile of <= 32 rows of an e4m3 cache takes less than a 48-row tile). The model's
-  // constants were fitted to measured call times over forced piece lengths on GB300
-  // (bf16: a unit start ~ 6 page-times; e4m3: ~ 16; tiles of 128 rows, whose page takes a cluster half
-  // as long: ~ 24, by sweeps over ten batches: 32 trees of 48 heads 418 us with 10, 393 with 24). It sees each request's q, so a batch
-  // of ragged query lengths, whose fold groups differ in tile count, gets other piece
-  // lengths than a uniform one of the same total work. A split keeps at least min_pages
-  // pages.
-  const int min_pages = o.min_pages_per_split > 0 ? o.min_pages_per_split : wide ? 2 : 4;
-  const int max_splits = max_splits_for_merge();
   const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
-  const double start_cost = wide ? 24.0 : fp8 ? 16.0 : 6.0;
-  auto row_cost = [&](int nrows) { return (!wide && fp8 && nrows <= 32) ? 0.9 : 1.0; };
-  long long tile_pages = 0;
-  for (const Group& g : groups) tile_pages += (long long)(g.t1 - g.t0) * g.pages;
-  auto assign = [&](long long T) {
-    for (auto& g : groups) {
-      long long n = o.force_splits > 0 ? o.force_splits : (g.pages + T - 1) / T;
-      g.n_split = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(n, g.pages), max_splits));
-      // pieces of T pages, unless the split count was capped or forced: then equal pieces
-      g.cap = (o.force_splits <= 0 && (long long)g.n_split == (g.pages + T - 1) / T) ? (int)T : 0;
-    }
-  };
-  auto piece_pages = [](const Group& g, int s) {
-    if (g.cap > 0) return std::min(g.pages, (s + 1) * g.cap) - s * g.cap;
-    return (int)((long long)g.pages * (s + 1) / g.n_split - (long long)g.pages * s / g.n_split);
-  };
-  long long best_T = std::max<long long>(min_pages, (tile_pages + slots - 1) / slots);
-  if (o.unit_pages > 0) best_T = o.unit_pages;
-  if (o.force_splits <= 0 && o.unit_pages <= 0) {
-    double best_end = -1;
-    std::vector<std::pair<int, double>> lens;  // (pages, per-page cost) of every unit
-    // candidates: the per-SM share divided by 1, 1.25, ... 8, and the longest group's
-    // pages divided into 1 .. 64 equal pieces
-    std::vector<long long> cands;
-    for (int k4 : {4, 5, 6, 8, 10, 12, 16, 20, 24, 32})
-      cands.push_back((4 * tile_pages + (long long)slots * k4 - 1) / ((long long)slots * k4));
-    int longest = 0;
-    for (const Group& g : groups) longest = std::max(longest, g.pages);
-    for (int n = 1; n <= 64; ++n) cands.push_back((longest + n - 1) / n);
-    std::sort(cands.begin(), cands.end());
-    cands.erase(std::unique(cands.begin(), cands.end()), cands.end());
-    for (long long c : cands) {
-      const long long T = std::max<long long>(min_pages, c);
-      // more than 16 waves of units (beyond one unit per row tile) never pays for its
-      // start-up costs; skipping those keeps the search cheap for very long batches
-      long long n_units = 0;
-      for (const Group& g : groups) n_units += (long long)(g.t1 - g.t0) * ((g.pages + T - 1) / T);
-      if (n_units > std::max<long long>(16LL * slots, (long long)tiles.size()) && !cands.empty() && c != cands.back())
-        continue;
-      assign(T);
-      lens.clear();
-      for (const Group& g : groups)
-        for (int s = 0; s < g.n_split; ++s)
-          for (size_t t = g.t0; t < g.t1; ++t) lens.emplace_back(piece_pages(g, s), row_cost(tiles[t].nrows));
-      std::stable_sort(lens.begin(), lens.end(),
-                       [](const std::pair<int, double>& a, const std::pair<int, double>& b) { return a.first > b.first; });
-      std::priority_queue<double, std::vector<double>, std::greater<double>> sm;
-      for (int i = 0; i < slots; ++i) sm.push(0.0);
-      double end = 0;
-      for (const auto& L : lens) {
-        const double t = sm.top() + start_cost + L.first * L.second;
-        sm.pop();
-        sm.push(t);
-        end = std::max(end, t);
-      }
-      if (best_end < 0 || end < best_end - 1e-9) {
-        best_end = end;
-        best_T = T;
+  const int pair_slots = o.pair_slots > 0 ? o.pair_slots : std::max(1, num_sms / 2);
+  const int asked = o.min_pages_per_split;
+  Geometry geo{false, whole_requests, cap, pair ? pair_slots : num_sms, asked > 0 ? asked : 4, fp8 ? 16.0 : 6.0, 1.0};
+  Partition part;
+  bool wide = force_wide;
+  if (whole_requests) {
+    // Trees run in tiles of 48 rows, or in tiles of 128 on clusters of two CTAs where the model's schedule
+    // of those ends first. Fitted to forced piece lengths over six short and ten long batches: a unit
+    // starts in 9 us (bf16) or 12 (e4m3) and takes 1.6 or 1.2 us a page in narrow tiles; 15 or 17 us and
+    // 0.65 or 0.72 in wide ones. (8 nodes, 12 heads: 11 us narrow, 15 wide over 4096 keys, 60 and 40 over
+    // 131072; 32 trees of 48 heads over block scales 584 and 393; pieces of a page instead of four, 4096 keys:
+    // 15.8 -> 10.9; 24 page-times to start a wide unit instead of 10, the 32 trees: 418 -> 393.)
+    Geometry narrow = geo, broad = geo;
+    narrow.min_pages = asked > 0 ? asked : 1;
+    narrow.start_cost = fp8 ? 10.0 : 6.0;
+    narrow.page_us = fp8 ? 1.2 : 1.6;
+    broad.wide = true;
+    broad.cap = wide_rows_cap();
+    broad.slots = pair_slots;
+    broad.min_pages = asked > 0 ? asked : 2;
+    broad.start_cost = 24.0;
+    broad.page_us = fp8 ? 0.72 : 0.65;
+    if (force_wide || o.max_rows_per_cta == 0) part = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, geo = broad);
+    if (!force_wide) {
+      Partition other = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, narrow);
+      wide = o.max_rows_per_cta == 0 && part.end_us < other.end_us;
+      if (!wide) {
+        part = std::move(other);
+        geo = narrow;
       }
     }
+  } else {
+    part = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, geo);
   }
-  assign(best_T);
+  const std::vector<RowTile>& tiles = part.tiles;
+  const std::vector<PlanRequest>& reqs = part.reqs;
+  const std::vector<Group>& groups = part.groups;
+  const int slots = geo.slots;
 
   std::vector<PlanUnit> units;
   std::vector<PlanMerge> merges;

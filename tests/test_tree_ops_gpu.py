@@ -567,7 +567,6 @@ class Step:
                          dev(cu_of(self.prefix)), int(self.prefix.max()))
         self.rows = torch.randn((layers, self.total, D), generator=g, device="cuda").to(torch.bfloat16)
         self.q = torch.randn((layers, self.total, heads, D), generator=g, device="cuda").to(torch.bfloat16)
-        self.head = torch.randn((heads * 512, vocab), generator=g, device="cuda") * 0.02
         self.parents, self.cu = dev(flat(self.trees)), dev(cu_of(self.nodes))
         self.tokens = torch.randint(0, 3, (self.total,), generator=g, device="cuda").int()
         self.temp = torch.full((3,), 2.0, device="cuda")
@@ -588,7 +587,8 @@ class Step:
             cache.append(self.rows[l], self.kv[l], self.scales[l], self.table, self.len_dev, self.cu, 13, self.status)
             self.decoder.run(self.q[l], self.kv[l], self.table, self.out[l], self.lse[l], kv_scales=self.scales[l],
                              tree_masks=self.masks, status=self.status)
-        self.logits.copy_(self.out[-1].view(self.total, -1).float() @ self.head)
+        # (elementwise: graphs that are replayed at once must not hold a library's product, whose workspace they share)
+        self.logits.copy_(self.out[-1].view(self.total, -1)[:, :self.logits.shape[1]]).mul_(30.0)
         self.logits[:, :3] += 20.0  # (three tokens that the drafts are made of)
         tree.verify(self.logits, self.tokens, self.parents, self.cu, self.path, self.tok, self.accepted, self.temp,
                     self.uniforms, self.noise, max_nodes=13, status=self.status)

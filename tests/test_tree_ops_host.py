@@ -152,11 +152,13 @@ def test_a_prime_tree_is_cut_into_full_tiles():
     assert rows(0, False) == [12] * 29
 
 
-def test_few_rows_stay_in_narrow_tiles():
+def test_few_rows_and_short_contexts_stay_in_narrow_tiles():
+    def wide(q, n, kv, tree=True):
+        return read_plan(binding.plan([n], [q], 12, kv, 152, tree=tree)[0])["header"]["reserved0"]
     for kv in (0, 1):
-        wide = [read_plan(binding.plan([4096], [q], 12, kv, 152, tree=True)[0])["header"]["reserved0"] for q in (1, 4, 5, 8, 64)]
-        assert wide == [0, 0, 1, 1, 1]
-        assert read_plan(binding.plan([4096], [64], 12, kv, 152)[0])["header"]["reserved0"] == 0
+        assert [wide(q, 131072, kv) for q in (1, 2, 4, 5, 8, 64)] == [0, 0, 0, 1, 1, 1]
+        assert [wide(8, n, kv) for n in (64, 4096, 131072)] == [0, 0, 1]
+        assert wide(64, 131072, kv, tree=False) == 0
 
 
 def test_tree_plan_refusals():
