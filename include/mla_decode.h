@@ -371,8 +371,11 @@ int mla_tree_masks(const int32_t* parents, const int32_t* cu_nodes, int batch, i
 
 /*
  * mla_decode_plan_tree -- mla_decode_plan_ex for trees: the row tiles are cut from all of a
- * request's q * H rows, where the fold rule asks for a divisor of q. force_fold and cta_pair are
- * refused. Such a plan runs chains too, and mla_key_weights takes it.
+ * request's q * H rows, where the fold rule asks for a divisor of q. Tiles of at most 48 rows on a
+ * CTA, or of 128 on clusters of two CTAs, whichever the planner's model of the time prefers
+ * (max_rows_per_cta: 16, 32 or 48 for the former, 128 for the latter; pair_slots for the latter as
+ * with cta_pair). force_fold and cta_pair are refused. Such a plan runs chains too, and
+ * mla_key_weights takes it.
  */
 int mla_decode_plan_tree(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads, int page_size,
                          int kv_dtype, int num_sms, const mla_plan_options* opts, void* plan_buf,
@@ -426,9 +429,9 @@ int mla_decode_run_tree(const void* plan_dev, const void* plan_host, size_t plan
  * p / noise. So each token that comes out is distributed as p. Greedy: the token of the largest
  * logit (of equal ones the lowest) follows, and a child is accepted where it has that token.
  *
- * NaN logits count as -inf, infinite ones as the largest number of their type. A row of -inf alone accepts
- * nothing, and its next token is -1. Sums are taken in fp32 in a fixed order: equal inputs give
- * equal results; one that hangs on less than about 1e-6 of a probability may fall either way.
+ * NaN logits count as -inf, infinite ones as the largest number of their type. A row of -inf alone
+ * accepts nothing, and its next token is -1. Sums are taken in fp32 in a fixed order: equal inputs
+ * give equal results; one that hangs on less than about 1e-6 of a probability may fall either way.
  * path, out_tokens and accepted must not overlap one another or the inputs (refused), and the
  * inputs must not change while the call runs. Enqueue only, as mla_decode_run.
  */

@@ -34,7 +34,7 @@ struct Params {
   float out_scale;         // kv_scale (1 for a bf16 cache)
   __nv_bfloat16* out;
   float* lse;
-  void* part_o;  // split partials of O, each normalised by its split's l: bf16, those of the wide kernel fp32
+  void* part_o;  // split partials of O, each normalised by its split's l: bf16, or (part_fp32) fp32
   float* part_lse;
   int32_t* status;
   long long wait_budget;  // cycles a bounded wait may take (kWaitBudget; kWaitBudgetTest in a timeout test)
@@ -43,6 +43,7 @@ struct Params {
   int block_log2;         // log2 of the tokens that share a scale
   const uint32_t* tree_masks;  // a tree of verify tokens: [sum q_lens, mask_words] visibility bits, else NULL
   int mask_words;
+  bool part_fp32;
 };
 
 __device__ __forceinline__ void report(int32_t* status, int bits) {

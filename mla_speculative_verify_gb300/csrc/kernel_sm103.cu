@@ -222,8 +222,10 @@ struct SoftmaxArgs {
 // chain of steps, ~1400 of a tile's 2000 cycles.
 //
 // kTree: verify token i sees the keys before the request's verify tokens, and of those the ones
-// whose bit its mask has. Only tiles that reach into the verify tokens' own keys look at masks;
-// each thread gathers the bits of its elements while it would wait for the scores.
+// whose bit its mask has, or, without masks, itself and the ones before it. Only tiles that reach
+// into the verify tokens' own keys look at masks; each thread gathers the bits of its elements while
+// it would wait for the scores. (8 nodes, 12 heads, 4096 bf16 keys: 12 us, most of it the fixed cost
+// of a split decode and its merge.)
 template <int NCH, bool kFp8, bool kScaled, bool kTree>
 __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params& p) {
   constexpr int NC = 4 * NCH;
@@ -358,12 +360,14 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           const int row = 16 * (i >> 1) + cp + (i & 1);
-          const uint32_t* words = p.tree_masks + (size_t)((a.qrow0 + row) / p.H) * p.mask_words;
+          const int token = (a.qrow0 + row) / p.H;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int d = draft0 + 8 * k;
             bool on = row < a.nrows && d < a.qlen;
-            if (on && d >= 0) on = (__ldg(words + (d >> 5)) >> (d & 31)) & 1u;
+            if (on && d >= 0)
+              on = p.tree_masks ? (__ldg(p.tree_masks + (size_t)token * p.mask_words + (d >> 5)) >> (d & 31)) & 1u
+                                : d <= token - a.tok0;
             sees |= (uint32_t)on << (4 * (i >> 1) + 2 * k + (i & 1));
           }
         }
@@ -725,6 +729,7 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
   // 2 grp, 2 grp + 1; a warp's stores of one row cover 32 consecutive dv (bf16 out, or
   // the bf16 split partial)
   __nv_bfloat16* dst = a.part_row0 < 0 ? p.out + (size_t)a.qrow0 * kDv : (__nv_bfloat16*)p.part_o + (size_t)a.part_row0 * kDv;
+  float* part = kTree && p.part_fp32 && a.part_row0 >= 0 ? (float*)p.part_o + (size_t)a.part_row0 * kDv : nullptr;
   const int dv_in_blk = qd * 32 + lane;
 #pragma unroll 1
   for (int blk = 2 * grp; blk < 2 * grp + 2; ++blk) {
@@ -742,7 +747,11 @@ __device__ __forceinline__ bool softmax_role(const SoftmaxArgs& a, const Params&
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int n = 16 * c + j + u;
-          if (n < a.nrows) dst[(size_t)n * kDv + dv] = __float2bfloat16_rn(v4[u]);
+          if (n >= a.nrows) continue;
+          if (kTree && part != nullptr)
+            part[(size_t)n * kDv + dv] = v4[u];
+          else
+            dst[(size_t)n * kDv + dv] = __float2bfloat16_rn(v4[u]);
         }
       }
     }
@@ -1086,7 +1095,7 @@ constexpr int kMergeMaxSplits = 2048;
 constexpr long long kMergeWideSlicesMaxCtas = 200;  // 8 slices per row up to this many merge CTAs
 
 // kN partial-O values of a split, as they lie in memory (streamed: read once) and as fp32. P is their
-// type: bf16, or fp32 (those of the wide kernel).
+// type: bf16, or fp32 (those of trees).
 template <typename P, int kN>
 struct PartValues {
   alignas(kN * sizeof(P)) uint32_t w[kN * sizeof(P) / 4];
@@ -1258,7 +1267,7 @@ int rows_cap_for(int kv_dtype) {
 int max_splits_for_merge() { return kMergeMaxSplits; }
 
 // ------------------------------------------------------------------ host side
-size_t workspace_bytes_for(int n_part_rows, bool wide);
+size_t workspace_bytes_for(int n_part_rows, bool tree);
 int block_log2_of(int block_tokens);  // defined with the plan
 int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out);
 int launch_wide_kernel(const PlanHeader* h, const void* q, const void* kv_cache, int num_pages, const Params& prm,
@@ -1374,7 +1383,7 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
                      page_table_stride, h->max_pages);
   if (!(sm_scale > 0.f) || !(kv_scale > 0.f) || !isfinite(sm_scale) || !isfinite(kv_scale))
     return set_error(MLA_ERR_INVALID_ARG, "sm_scale and kv_scale must be finite and > 0");
-  const size_t ws_need = workspace_bytes_for(h->n_part_rows, h->wide != 0);
+  const size_t ws_need = workspace_bytes_for(h->n_part_rows, h->tree != 0);
   if (ws_need > 0 && (!workspace || workspace_bytes < ws_need))
     return set_error(MLA_ERR_BUFFER, "workspace needs %zu bytes (got %zu)", ws_need, workspace ? workspace_bytes : (size_t)0);
   if (ws_need > 0 && ((uintptr_t)workspace & 255u)) return set_error(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -1412,7 +1421,7 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
   prm.out = (__nv_bfloat16*)out;
   prm.lse = lse;
   prm.part_o = workspace;
-  const size_t part_bytes = (size_t)h->n_part_rows * kDv * (h->wide ? kWidePartOElemBytes : kPartOElemBytes);
+  const size_t part_bytes = (size_t)h->n_part_rows * kDv * (h->tree ? kTreePartOElemBytes : kPartOElemBytes);
   prm.part_lse = ws_need ? (float*)((uint8_t*)workspace + (part_bytes + 255) / 256 * 256) : nullptr;
   prm.status = status_dev;
   prm.wait_budget = h->debug_skip_copy > 0 ? kWaitBudgetTest : kWaitBudget;
@@ -1421,6 +1430,7 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
   prm.block_log2 = block_log2;
   prm.tree_masks = tree_masks;
   prm.mask_words = mask_words;
+  prm.part_fp32 = h->tree != 0;
   cudaStream_t st = (cudaStream_t)stream;
   if (h->wide) {
     if (g_dev[dev].kernels.wide != cudaSuccess)
@@ -1432,9 +1442,10 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
     rc = launch_pair_kernel(dev, h, q, kv_cache, num_pages, prm, st);
     if (rc != MLA_OK) return rc;
   } else {
-    auto fn = kv_scales ? (tree_masks ? fold_decode_kernel<true, true, true> : fold_decode_kernel<true, true, false>)
-              : fp8     ? (tree_masks ? fold_decode_kernel<true, false, true> : fold_decode_kernel<true, false, false>)
-                        : (tree_masks ? fold_decode_kernel<false, false, true> : fold_decode_kernel<false, false, false>);
+    const bool tree = h->tree || tree_masks;
+    auto fn = kv_scales ? (tree ? fold_decode_kernel<true, true, true> : fold_decode_kernel<true, true, false>)
+              : fp8     ? (tree ? fold_decode_kernel<true, false, true> : fold_decode_kernel<true, false, false>)
+                        : (tree ? fold_decode_kernel<false, false, true> : fold_decode_kernel<false, false, false>);
     fn<<<h->n_units, fp8 ? Roles<true>::kThreads : Roles<false>::kThreads, kv_scales ? kSmemBytesScaled : kSmemBytes,
          st>>>(tq, tkv, prm);
     ce = cudaGetLastError();
@@ -1476,7 +1487,7 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
       return cudaLaunchKernelEx(&cfg, merge_fn, (const PlanMerge*)((const uint8_t*)plan_dev + h->merge_off), (const P*)part,
                                 (const float*)prm.part_lse, (__nv_bfloat16*)out, lse);
     };
-    ce = h->wide ? launch((float*)prm.part_o) : launch((__nv_bfloat16*)prm.part_o);
+    ce = prm.part_fp32 ? launch((float*)prm.part_o) : launch((__nv_bfloat16*)prm.part_o);
     if (ce != cudaSuccess) return set_error(MLA_ERR_CUDA, "merge kernel launch: %s", cudaGetErrorString(ce));
   }
   return MLA_OK;

@@ -49,9 +49,9 @@ int block_log2_of(int block_tokens) {
   return -1;
 }
 
-size_t workspace_bytes_for(int n_part_rows, bool wide) {
+size_t workspace_bytes_for(int n_part_rows, bool tree) {
   if (n_part_rows <= 0) return 0;
-  return align_up((size_t)n_part_rows * kDv * (wide ? kWidePartOElemBytes : kPartOElemBytes), 256) + align_up((size_t)n_part_rows * sizeof(float), 256);
+  return align_up((size_t)n_part_rows * kDv * (tree ? kTreePartOElemBytes : kPartOElemBytes), 256) + align_up((size_t)n_part_rows * sizeof(float), 256);
 }
 
 namespace {
@@ -355,7 +355,7 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   size_t total = align_up(merge_off + sizeof(PlanMerge) * merges.size(), 64);
   if (total > (size_t)INT32_MAX) return set_error(MLA_ERR_INVALID_ARG, "plan too large");
   if (plan_bytes_out) *plan_bytes_out = total;
-  if (workspace_bytes_out) *workspace_bytes_out = workspace_bytes_for(part_rows, wide);
+  if (workspace_bytes_out) *workspace_bytes_out = workspace_bytes_for(part_rows, whole_requests);
   if (!plan_buf || plan_buf_bytes < total)
     return set_error(MLA_ERR_BUFFER, "plan buffer needs %zu bytes (got %zu)", total, plan_buf ? plan_buf_bytes : (size_t)0);
 
@@ -373,6 +373,7 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   h.debug_skip_copy = o.debug_skip_copy;
   h.cta_pair = pair ? 1 : 0;
   h.wide = wide ? 1 : 0;
+  h.tree = whole_requests ? 1 : 0;
   memcpy(base, &h, sizeof h);
   memcpy(base + req_off, reqs.data(), sizeof(PlanRequest) * batch);
   if (!units.empty()) memcpy(base + units_off, units.data(), sizeof(PlanUnit) * units.size());

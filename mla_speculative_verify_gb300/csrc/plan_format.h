@@ -15,10 +15,10 @@ constexpr int kPage = 64;
 // Split partials of O are stored as bf16 (each split's O is already normalised by its
 // own l, so bf16 adds at most 2^-9 relative error before the merge's weighted sum).
 constexpr int kPartOElemBytes = 2;
-// Those of the wide kernel as fp32: with its longer pieces few partials of a row count, and their
-// rounding would show beside that of P and of the result (4 x 64 nodes over 32768 keys: error against
-// 64 bits 2.4e-3 with bf16, 2.0e-3 with fp32, of which the bf16 result is 1.5e-3).
-constexpr int kWidePartOElemBytes = 4;
+// Those of a tree as fp32: where few partials of a row count, their rounding shows beside that of P
+// and of the result (4 x 64 nodes over 32768 keys: error against 64 bits 2.4e-3 with bf16, 2.0e-3 with
+// fp32, of which the bf16 result is 1.5e-3).
+constexpr int kTreePartOElemBytes = 4;
 // PlanUnit.flags: the request's cache pages are read by this row tile only (one fold
 // group, one tile), so a page can leave L2 right after its copy into shared memory.
 constexpr int32_t kUnitKvReadOnce = 1;
@@ -35,7 +35,8 @@ struct PlanHeader {
   int32_t debug_skip_copy;  // mla_plan_options.debug_skip_copy (0 in production plans)
   int32_t cta_pair;         // 1: every unit is one fold group of 49..96 rows for a cluster of two CTAs
   int32_t wide;             // 1: units of up to 128 rows for clusters of two CTAs (kernel_wide_sm103.cu)
-  int32_t reserved[2];
+  int32_t tree;             // 1: a plan for trees: its workspace has room for fp32 partials
+  int32_t reserved[1];
 };
 static_assert(sizeof(PlanHeader) == 80, "plan header is 80 bytes");
 

@@ -19,7 +19,7 @@
 
 namespace mla {
 
-size_t workspace_bytes_for(int n_part_rows, bool wide);
+size_t workspace_bytes_for(int n_part_rows, bool tree);
 int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out);
 
 // Partial O rows and partial LSE of split units (same layout as a caller's workspace).
@@ -87,7 +87,7 @@ extern "C" int mla_decode_run_static_ws(const void* plan_dev, const void* plan_h
   const PlanHeader* h = nullptr;
   int rc = check_plan(plan_host, plan_bytes, &h);
   if (rc != MLA_OK) return rc;
-  const size_t need = workspace_bytes_for(h->n_part_rows, h->wide != 0);
+  const size_t need = workspace_bytes_for(h->n_part_rows, h->tree != 0);
   if (need > (size_t)MLA_STATIC_WORKSPACE_BYTES)
     return set_error(MLA_ERR_BUFFER,
                      "this plan needs %zu bytes of split-KV scratch but the static workspace holds %zu; plan with "

@@ -55,6 +55,8 @@ def masks(parents: torch.Tensor, cu_nodes: torch.Tensor, out: torch.Tensor, dept
     check_tensor("cu_nodes", cu_nodes, torch.int32, (batch + 1,), index)
     words = out.shape[1] if out.dim() == 2 else 0
     check_tensor("out", out, torch.int32, (total, words), index)
+    if total and not words:
+        raise ValueError("out must have room for a bit for each node of a request")
     if depths is not None:
         check_tensor("depths", depths, torch.int32, (total,), index)
     if status is not None:

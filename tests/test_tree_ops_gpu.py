@@ -51,6 +51,16 @@ def test_masks(sizes, words):
     assert torch.equal(only, out)
 
 
+def test_masks_refuses_tensors():
+    p, cu = i32([-1, 0, 1]), i32([0, 3])
+    for out, depths in ((i32([0, 0, 0]), None), (torch.zeros((3, 0), dtype=torch.int32, device="cuda"), None),
+                        (torch.zeros((2, 1), dtype=torch.int32, device="cuda"), None),
+                        (torch.zeros((3, 1), dtype=torch.int64, device="cuda"), None),
+                        (torch.zeros((3, 1), dtype=torch.int32, device="cuda"), i32([0, 0]))):
+        with pytest.raises(ValueError):
+            tree.masks(p, cu, out, depths)
+
+
 def test_masks_of_bad_trees():
     """A parent behind its node counts as none; a request that does not fit stays as it is."""
     out, depths, status = torch.full((9, 1), 7, dtype=torch.int32, device="cuda"), i32([7] * 9), i32([0])
@@ -298,6 +308,27 @@ def test_verify_greedy(sizes, vocab, dtype):
     d.check(max(sizes))
 
 
+def test_verify_greedy_looks_at_no_draft_distribution():
+    d = Draft([20] * 12, 257, torch.bfloat16, True, seed=15)
+    got = d.run(20, greedy=True)
+    d.draft.fill_(float("nan"))
+    assert all(np.array_equal(a, b) for a, b in zip(got[:3], d.run(20, greedy=True)[:3]))
+    d.check(20, greedy=True)
+
+
+def test_verify_of_nothing():
+    """Requests without nodes, and a batch of them alone; a draft that is the target's own distribution is accepted."""
+    d = Draft([0, 3, 0], 30, torch.float32, False, seed=16)
+    d.check(4)
+    d = Draft([0, 0], 30, torch.float32, False, seed=16)
+    path, out, accepted, status = d.run(4, max_nodes=1)
+    assert status == 0 and (path == -1).all() and (out == -1).all() and (accepted == 0).all()
+    d = Draft([6] * 40, 100, torch.float32, True, seed=17, width=1)
+    d.draft = d.logits.clone()
+    d.temp.fill_(0.8)
+    assert (d.run(6)[2] == 6).all()
+
+
 def test_verify_long_chains_and_padding():
     d = Draft([1024, 900], 50, torch.float32, False, seed=3, width=1)
     d.temp[0], d.temp[1] = 2.0, 0.5
@@ -408,6 +439,26 @@ def test_verify_rows_far_apart():
     torch.cuda.synchronize()
     (p, o, margin), = d.want(5)
     assert margin >= NEAR and path[0, :len(p)].tolist() == p and out[0, :len(o)].tolist() == o
+
+
+def test_verify_refuses_tensors():
+    d = Draft([4], 30, torch.float32, True, seed=11)
+    x, cu = d.logits.cuda(), i32([0, 4])
+    good = dict(logits=x, tokens=d.tokens.cuda(), parents=dev(flat(d.trees)), cu_nodes=cu, path=i32([[0] * 4]), out_tokens=i32([[0] * 4]),
+                accepted=i32([0]), uniforms=d.uniforms.cuda(), noise=d.noise.cuda(), draft_logits=d.draft.cuda())
+    tree.verify(**good)
+    wide_x = torch.zeros((4, 60), device="cuda")
+    for name, bad in (("logits", x.double()), ("logits", wide_x[:, ::2]), ("logits", x[:1].expand(4, 30)), ("logits", x[0]),
+                      ("draft_logits", x.bfloat16()), ("draft_logits", x[:3]), ("tokens", d.tokens.cuda().long()), ("cu_nodes", cu[:1]),
+                      ("path", i32([0] * 4)), ("out_tokens", i32([[0] * 3])), ("accepted", i32([0, 0])), ("noise", d.noise.cuda()[:, :29]),
+                      ("uniforms", d.uniforms), ("temperature", torch.ones(2, device="cuda"))):
+        with pytest.raises((ValueError, binding.MlaError)):
+            tree.verify(**{**good, name: bad})
+    for left_out in ("uniforms", "noise"):
+        with pytest.raises(binding.MlaError):
+            tree.verify(**{**good, left_out: None})
+    with pytest.raises(binding.MlaError):  # written over what other requests still read
+        tree.verify(**{**good, "accepted": good["tokens"][:1]})
 
 
 # ------------------------------------------------------------------------------- commit

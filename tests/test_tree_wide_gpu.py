@@ -127,3 +127,54 @@ def test_wide_bad_page_and_lengths():
     d.run(q, kv, dev(batch.table), out, lse, status=status, tree_masks=masks, seq_lens_dev=i32([999]))
     torch.cuda.synchronize()
     assert int(status.item()) & binding.MLA_DEVICE_PLAN_MISMATCH
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_other_entry_points_take_a_tree_plan(kind):
+    """The decode in the library's own scratch, and the key weights: as with a chain's plan."""
+    batch = ref.Batch(12, [700, 300], [16, 9], kind, 0, seed=51)
+    kv_name = "bf16" if kind == "bf16" else "fp8"
+    q, kv, table = batch.q.cuda(), batch.kv.cuda(), dev(batch.table)
+    chain, _ = tref.words([list(range(-1, n - 1)) for n in (16, 9)], 1)
+    out, lse = decode(batch, chain, wide())
+    d = VerifyDecoder(batch.seq_lens, batch.q_lens, 12, kv_name, tree=True, options=wide())
+    assert d.workspace_bytes > 0
+    o, e, status = torch.zeros_like(out), torch.zeros_like(lse), i32([0])
+    binding.run_static_ws(d.plan_dev.data_ptr(), d.plan_host, q.data_ptr(), kv.data_ptr(), table.data_ptr(), table.shape[1],
+                          batch.pages, d.seq_lens_dev.data_ptr(), d.q_lens_dev.data_ptr(), 1.0 / 192.0 ** 0.5, batch.kv_scale,
+                          o.data_ptr(), e.data_ptr(), status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and torch.equal(o, out) and torch.equal(e, lse)
+    plain = VerifyDecoder(batch.seq_lens, batch.q_lens, 12, kv_name)
+    w, w2 = torch.zeros((2, 704), device="cuda"), torch.zeros((2, 704), device="cuda")
+    d.key_weights(q, kv, table, lse, w, kv_scale=batch.kv_scale)
+    plain.key_weights(q, kv, table, lse, w2, kv_scale=batch.kv_scale)
+    torch.cuda.synchronize()
+    assert torch.equal(w, w2)
+
+
+def test_a_workspace_too_small_is_refused():
+    d = VerifyDecoder([5000], [16], 12, "bf16", tree=True, options=wide())
+    d.workspace_bytes -= 256
+    with pytest.raises(binding.MlaError) as e:
+        d.run(torch.zeros((16, 12, 576), dtype=torch.bfloat16, device="cuda"), torch.zeros((79, 64, 576), dtype=torch.bfloat16, device="cuda"),
+              torch.zeros((1, 79), dtype=torch.int32, device="cuda"), torch.zeros((16, 12, 512), dtype=torch.bfloat16, device="cuda"),
+              tree_masks=torch.zeros((16, 1), dtype=torch.int32, device="cuda"))
+    assert e.value.code == binding.MLA_ERR_BUFFER
+
+
+def test_wide_offsets_beyond_32_bits():
+    """Pages whose bytes lie behind 2^32, in either kernel; the results of the same pages at the front."""
+    pages = 62_000  # 4.6 GB
+    big = torch.zeros((pages, 64, 576), dtype=torch.bfloat16, device="cuda")
+    batch = ref.Batch(12, [400], [16], "bf16", 0, seed=52, poison=False)
+    masks, _ = tref.words([tref.random_tree(np.random.default_rng(2), 16)], 1)
+    far = np.array([[pages - 1 - int(p) for p in batch.table[0]]], np.int32)
+    big[dev(far[0]).long()] = batch.kv.cuda()[dev(batch.table[0]).long()]
+    for options in (wide(), None):
+        want = decode(batch, masks, options)
+        d = VerifyDecoder([400], [16], 12, "bf16", tree=True, options=options)
+        out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+        d.run(batch.q.cuda(), big, dev(far), out, lse, tree_masks=dev(masks))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
