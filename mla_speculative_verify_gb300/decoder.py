@@ -58,8 +58,6 @@ class VerifyDecoder:
         self.plan_dev = torch.from_numpy(self.plan_host).to(self.device)
         self.workspace = (torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
                           if self.workspace_bytes else None)
-        self._plan_dev_ptr, self._plan_bytes = self.plan_dev.data_ptr(), self.plan_host.nbytes
-        self._workspace_ptr = _ptr(self.workspace)
         self.seq_lens_dev = torch.from_numpy(self.seq_lens).to(self.device)
         self.q_lens_dev = torch.from_numpy(self.q_lens).to(self.device)
         self.total_q = int(self.q_lens.sum())
@@ -152,10 +150,10 @@ class VerifyDecoder:
             q_lens_dev = self.q_lens_dev
         else:
             check_tensor("q_lens_dev", q_lens_dev, torch.int32, (batch,), index)
-        on_device(index, binding.run_tree, self._plan_dev_ptr, self._plan_host_ptr, self._plan_bytes, q.data_ptr(),
+        on_device(index, binding.run_tree, self.plan_dev.data_ptr(), self._plan_host_ptr, self.plan_host.nbytes, q.data_ptr(),
                   kv_cache.data_ptr(), _ptr(kv_scales), block, page_table.data_ptr(), stride, pages,
                   seq_lens_dev.data_ptr(), q_lens_dev.data_ptr(), tree_masks.data_ptr(), words, sm_scale, kv_scale,
-                  out.data_ptr(), _ptr(lse), self._workspace_ptr, self.workspace_bytes, _ptr(status),
+                  out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes, _ptr(status),
                   stream_handle(index, stream))
 
     def key_weights(self, q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor, lse: torch.Tensor,

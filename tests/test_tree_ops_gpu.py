@@ -537,6 +537,16 @@ def test_commit_many_rows_and_layers():
     check_commit(batch, kv, None, lens, nodes, paths, 0)
 
 
+def test_commit_of_lengths_that_pass_32_bits():
+    """A negative length minus the nodes passes the lowest int32 and comes out positive."""
+    batch, kv, _, _ = commit_case([100], [20], 1, "bf16", 0, seed=8)
+    k, new_lens, status = kv.cuda().clone(), i32([7]), i32([0])
+    cache.commit(k, dev(batch.table), i32([-5]), i32([0, 2 ** 31 - 1]), i32([[0, 3, 7]]), i32([3]), new_lens, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == binding.MLA_DEVICE_PLAN_MISMATCH and int(new_lens.item()) == -5
+    assert torch.equal(k, kv.cuda())
+
+
 def test_commit_bad_requests_stay():
     lens, nodes = [100, 90, 80], [20, 20, 20]
     good = [0, 3, 7]
