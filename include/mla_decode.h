@@ -406,7 +406,7 @@ int mla_decode_run_tree(const void* plan_dev, const void* plan_host, size_t plan
  *                  row: row u is the target's at node u
  *   draft_logits   NULL, or [total_nodes, draft_stride] of the same type: row u's distribution is
  *                  what the children of u were drawn from, each by itself (rows of nodes without
- *                  children are not read). NULL: the children are certain (the draft's best tokens)
+ *                  children do not matter). NULL: the children are certain (the draft's best tokens)
  *   tokens         [total_nodes] int32: the drafted token of each node (node 0's is not read). A
  *                  node whose token lies outside [0, vocab) is never accepted and changes nothing
  *   temperature    NULL (1 for all), or fp32 [batch]. Below 2^-20, or NaN: greedy; cut to 2^20

@@ -482,7 +482,18 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) tree_verify_k
       continue;
     }
 
-    // ---- the first children's logits are asked for before the pass, which hides their way
+    // ---- the first groups, and while they are on their way the children and their logits
+    constexpr int kDeep = (kDraft ? 2 : 4) * 2 / (int)sizeof(T);
+    Raw<T> r[kDeep], w[kDraft ? kDeep : 1];
+    auto fetch = [&](int g) {
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int at = g + k * kVerThreads;
+        r[k] = at < g1 ? target8(at) : nothing<T>();
+        if (kDraft) w[kDraft ? k : 0] = at < g1 ? draft8(at) : nothing<T>();
+      }
+    };
+    fetch(g0 + tid);
     int n_kids = 0, kids_end = q, kid_i = -1, kid_x = -1;
     T kid_t{}, kid_d{};
     float coin = 1.f;
@@ -530,29 +541,16 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) tree_verify_k
       }
       p.s += s.x + s.y;
     };
-    {  // the next kDeep groups are on their way while these are added
-      constexpr int kDeep = (kDraft ? 2 : 4) * 2 / (int)sizeof(T);
-      Raw<T> r[kDeep], w[kDraft ? kDeep : 1];
-      auto fetch = [&](int g) {
+    for (int g = g0 + tid; g < g1; g += kDeep * kVerThreads) {  // the next groups are on their way while these are added
+      Raw<T> r1[kDeep], w1[kDraft ? kDeep : 1];
 #pragma unroll
-        for (int k = 0; k < kDeep; ++k) {
-          const int at = g + k * kVerThreads;
-          r[k] = at < g1 ? target8(at) : nothing<T>();
-          if (kDraft) w[kDraft ? k : 0] = at < g1 ? draft8(at) : nothing<T>();
-        }
-      };
-      fetch(g0 + tid);
-      for (int g = g0 + tid; g < g1; g += kDeep * kVerThreads) {
-        Raw<T> r1[kDeep], w1[kDraft ? kDeep : 1];
-#pragma unroll
-        for (int k = 0; k < kDeep; ++k) {
-          r1[k] = r[k];
-          if (kDraft) w1[kDraft ? k : 0] = w[kDraft ? k : 0];
-        }
-        if (g + kDeep * kVerThreads < g1) fetch(g + kDeep * kVerThreads);
-        add(pt, r1, kDeep);
-        if (kDraft) add(pd, w1, kDeep);
+      for (int k = 0; k < kDeep; ++k) {
+        r1[k] = r[k];
+        if (kDraft) w1[kDraft ? k : 0] = w[kDraft ? k : 0];
       }
+      if (g + kDeep * kVerThreads < g1) fetch(g + kDeep * kVerThreads);
+      add(pt, r1, kDeep);
+      if (kDraft) add(pd, w1, kDeep);
     }
     pt = warp_join<32>(pt);
     if (kDraft) pd = warp_join<32>(pd);
