@@ -79,7 +79,7 @@ struct Geo {
   static constexpr int kOffScales = kOffP + kPBytes;        // e4m3: block scales of two tiles
   static constexpr int kScaleBytes = kTileKeys / 2 * 24;    // of a tile, by pairs of keys
   static constexpr int kOffMisc = kOffScales + (kFp8 ? 2 * kScaleBytes : 0);
-  static constexpr int kMiscBytes = 3072;
+  static constexpr int kMiscBytes = 2816;
   static constexpr int kSmem = kOffMisc + kMiscBytes;
   static_assert(kSmem <= 232448, "exceeds the 227 KB per-CTA shared memory");
   static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
@@ -103,7 +103,7 @@ struct Misc {
   float red[4][kHalfRows];                    // by (page of the tile, group): maxima, then sums
   float colscale[kHalfRows];                  // e4m3: score scale of a row
 };
-static_assert(sizeof(Misc) <= 3072, "misc block too small");
+static_assert(sizeof(Misc) <= Geo<false>::kMiscBytes, "misc block too small");
 
 // ---------------------------------------------------------------- cta_group::2
 __device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t cols) {

@@ -682,7 +682,8 @@ __global__ void __launch_bounds__(kVerThreads, 1024 / kVerThreads) tree_verify_k
       auto fetch = [&](int g) {
         r = target8(g);
         if (less) w = draft8(g);
-        e = __builtin_expect(noise_alike && g >= f0 && g < f1, 1) ? whole_noise8(noise - head + 8 * (ptrdiff_t)g) : load_noise8(noise, 8 * g - head, a.vocab);
+        e = __builtin_expect(noise_alike && g >= f0 && g < f1, 1) ? whole_noise8(noise - head + 8 * (ptrdiff_t)g)
+                                                                  : load_noise8(noise, 8 * g - head, a.vocab);
       };
       if (g0 + tid < g1) fetch(g0 + tid);
       for (int g = g0 + tid; g < g1; g += kVerThreads) {  // (rising: of equal ones a thread keeps the lowest)
@@ -776,7 +777,8 @@ extern "C" int mla_tree_masks(const int32_t* parents, const int32_t* cu_nodes, i
   if (max_nodes == 0 || total_nodes == 0) return MLA_OK;
   if (!parents || !cu_nodes || !masks) return set_error(MLA_ERR_INVALID_ARG, "parents, cu_nodes and masks must not be NULL");
   for (const void* p : {(const void*)parents, (const void*)cu_nodes, (const void*)masks, (const void*)depths, (const void*)status_dev})
-    if ((uintptr_t)p & 3u) return set_error(MLA_ERR_INVALID_ARG, "parents, cu_nodes, masks, depths and status_dev must be 4-byte aligned");
+    if ((uintptr_t)p & 3u)
+      return set_error(MLA_ERR_INVALID_ARG, "parents, cu_nodes, masks, depths and status_dev must be 4-byte aligned");
   if (mask_words < (max_nodes + 31) / 32)
     return set_error(MLA_ERR_INVALID_ARG, "mask_words %d is too few for %d nodes", mask_words, max_nodes);
   const size_t nodes = 4 * (size_t)total_nodes, cu = 4 * ((size_t)batch + 1), words = nodes * (size_t)mask_words;
@@ -830,7 +832,8 @@ extern "C" int mla_tree_verify(int logits_dtype, const void* target_logits, long
                                                     {noise, noise ? 4 * ((size_t)noise_stride * (batch - 1) + vocab) : 0}},
                outs[] = {{path, paths}, {out_tokens, paths}, {accepted, rows}};
   for (const auto& i : in)
-    if ((uintptr_t)i.p & 3u) return set_error(MLA_ERR_INVALID_ARG, "tokens, parents, cu_nodes, temperature, uniforms and noise must be 4-byte aligned");
+    if ((uintptr_t)i.p & 3u)
+      return set_error(MLA_ERR_INVALID_ARG, "tokens, parents, cu_nodes, temperature, uniforms and noise must be 4-byte aligned");
   for (const auto& o : outs) {
     if ((uintptr_t)o.p & 3u) return set_error(MLA_ERR_INVALID_ARG, "path, out_tokens and accepted must be 4-byte aligned");
     for (const auto& i : in)
