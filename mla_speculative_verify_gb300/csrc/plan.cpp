@@ -276,7 +276,7 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
     // Trees run in tiles of 48 rows, or in tiles of 128 on clusters of two CTAs where the model's schedule
     // of those ends first. Fitted to forced piece lengths over six short and ten long batches: a unit
     // starts in 9 us (bf16) or 12 (e4m3) and takes 1.6 or 1.2 us a page in narrow tiles; 15 or 17 us and
-    // 0.65 or 0.72 in wide ones. (8 nodes, 12 heads: 11 us narrow, 15 wide over 4096 keys, 60 and 40 over
+    // 0.65 or 0.72 in wide ones. (8 nodes, 12 heads: 12 us narrow, 16 wide over 4096 keys, 60 and 40 over
     // 131072; 32 trees of 48 heads over block scales 584 and 393; pieces of a page instead of four, 4096 keys:
     // 15.8 -> 10.9; 24 page-times to start a wide unit instead of 10, the 32 trees: 418 -> 393.)
     Geometry narrow = geo, broad = geo;
