@@ -465,7 +465,8 @@ int mla_tree_verify(int logits_dtype, const void* target_logits, long long targe
  * MLA_DEVICE_BAD_TREE, lengths that do not fit (fewer tokens than nodes, more accepted than nodes or
  * path_stride, more pages than page_table_stride) MLA_DEVICE_PLAN_MISMATCH: such a request stays as
  * it is, with its old length. Rows of pages outside [0, num_pages) do not move, reported as
- * MLA_DEVICE_BAD_PAGE. No page may be named twice. Enqueue only, as mla_decode_run.
+ * MLA_DEVICE_BAD_PAGE: their scales do not count, a block that no other row enters keeps its own, and
+ * the codes in their places stay. No page may be named twice. Enqueue only, as mla_decode_run.
  */
 int mla_cache_commit(int kv_dtype, void* kv_cache, float* kv_scales, int block_tokens, int layers,
                      const int32_t* page_table, int page_table_stride, int num_pages, const int32_t* seq_lens,

@@ -942,9 +942,13 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
         const int blk = (stay + i) >> a.block_log2;
         const int j0 = max(0, (blk << a.block_log2) - stay), j1 = min(m, ((blk + 1) << a.block_log2) - stay);
         float top = j0 == 0 && n_old > 0 ? old_ratio[l] : 0.f;
-        for (int j = j0; j < j1; ++j) top = fmaxf(top, s_of[l * m + j]);
+        bool enters = false;  // (rows on bad pages bring no scale)
+        for (int j = j0; j < j1; ++j) {
+          top = fmaxf(top, s_of[l * m + j]);
+          enters |= src_row[j] >= 0;
+        }
         r_of[e] = top > 0.f ? s_of[e] / top : 1.f;
-        if (i == j0 && dst_row[i] >= 0) *scale_at(l, dst_row[i]) = top;
+        if (i == j0 && enters && dst_row[i] >= 0) *scale_at(l, dst_row[i]) = top;
       }
       __syncthreads();
       // codes of the rows that stay in a block whose scale has grown
