@@ -418,7 +418,7 @@ int mla_decode_run_tree(const void* plan_dev, const void* plan_host, size_t plan
  *   out_tokens     int32 [batch, path_stride]: the tokens that follow each of them: the accepted
  *                  nodes' own and last the next token, then -1
  *   accepted       int32 [batch]: nodes on the path (0 for a request without nodes, or one that
- *                  does not fit)
+ *                  does not fit, which mla_cache_commit then keeps as it is)
  *
  * At node u, with p = softmax(target_logits[u] / T), the children are tried in order. Draft NULL:
  * r is p without the tokens tried before, R its sum, and child i with token x is accepted where
@@ -463,8 +463,9 @@ int mla_tree_verify(int logits_dtype, const void* target_logits, long long targe
  *
  * A path that does not rise from a node >= 0 to one within the request reports
  * MLA_DEVICE_BAD_TREE, lengths that do not fit (fewer tokens than nodes, more accepted than nodes or
- * path_stride, more pages than page_table_stride) MLA_DEVICE_PLAN_MISMATCH: such a request stays as
- * it is, with its old length. Rows of pages outside [0, num_pages) do not move, reported as
+ * path_stride, none accepted of some nodes, more pages than page_table_stride)
+ * MLA_DEVICE_PLAN_MISMATCH: such a request stays as it is, with its old length, and so does one that
+ * mla_tree_verify refused: all its nodes are still its last keys. Rows of pages outside [0, num_pages) do not move, reported as
  * MLA_DEVICE_BAD_PAGE: their scales do not count, a block that no other row enters keeps its own, and
  * the codes in their places stay. No page may be named twice. Enqueue only, as mla_decode_run.
  */

@@ -186,7 +186,9 @@ def commit(kv: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor, c
     ``cu_nodes[b + 1] - cu_nodes[b]``; ``path`` [batch, width] and ``accepted`` [batch] int32 are
     what ``tree.verify`` wrote. ``seq_lens_dst`` [batch] int32 receives the lengths without the
     tokens that were not accepted; it must not be ``seq_lens`` itself. A block that receives rows
-    gets the largest of their scales (and of its own, where older rows stay in it).
+    gets the largest of their scales (and of its own, where older rows stay in it). A request with
+    nodes of which none is accepted (``tree.verify`` refused it) keeps its rows and its length,
+    reported as ``MLA_DEVICE_PLAN_MISMATCH``.
     """
     index = _cuda_index(kv)
     bf16 = kv.dtype == torch.bfloat16

@@ -875,7 +875,8 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
   const int b = blockIdx.x, tid = threadIdx.x;
   const int q = a.cu[b + 1] - a.cu[b], len = a.seq_lens[b], acc = a.accepted[b];
   const int n0 = len - q;
-  const bool fits = q >= 0 && len >= 0 && n0 >= 0 && acc >= 0 && acc <= q && acc <= a.path_stride &&
+  // (no node accepted of some: the verification refused the request, and the certain root is among them)
+  const bool fits = q >= 0 && len >= 0 && n0 >= 0 && acc >= (q > 0 ? 1 : 0) && acc <= q && acc <= a.path_stride &&
                     (len == 0 || (len - 1) / kPage < a.pt_stride);
   if (blockIdx.y == 0 && tid == 0) {
     a.new_lens[b] = fits ? n0 + acc : len;
