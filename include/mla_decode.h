@@ -285,6 +285,14 @@ int mla_decode_run_scaled(const void* plan_dev, const void* plan_host, size_t pl
  *   workspace     mla_key_weights_workspace bytes (0 for a bf16 plan), 256-byte aligned; calls
  *                 that may overlap need one each
  *
+ * The rows are a chain's: j is visible to i for j < seq_lens[b] - q_lens[b] + i + 1. After
+ * mla_decode_run_tree the call would be wrong: that lse does not hold a row's siblings and cousins,
+ * whose weights may then be far above 1, and counted names no path. Call it on the committed chain:
+ * after mla_cache_commit, with a plan for the new lengths and the accepted counts, it takes the accepted
+ * nodes' rows of q and of the tree's lse, since each sees there what it saw in the tree (over a
+ * block-scaled cache up to what the commit rounded in codes that moved to a larger scale; a decode of
+ * the chain gives its lse anew).
+ *
  * Sums are taken in fp32 in a fixed order: equal inputs give equal bits. A row whose lse is
  * -inf adds nothing. Enqueue only, as mla_decode_run.
  */
@@ -375,7 +383,7 @@ int mla_tree_masks(const int32_t* parents, const int32_t* cu_nodes, int batch, i
  * CTA, or of 128 on clusters of two CTAs, whichever the planner's model of the time prefers
  * (max_rows_per_cta: 16, 32 or 48 for the former, 128 for the latter; pair_slots for the latter as
  * with cta_pair). force_fold and cta_pair are refused. Such a plan runs chains too, and
- * mla_key_weights takes it.
+ * mla_key_weights takes it for a chain's lse (see there).
  */
 int mla_decode_plan_tree(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads, int page_size,
                          int kv_dtype, int num_sms, const mla_plan_options* opts, void* plan_buf,

@@ -61,6 +61,7 @@ class VerifyDecoder:
         self.seq_lens_dev = torch.from_numpy(self.seq_lens).to(self.device)
         self.q_lens_dev = torch.from_numpy(self.q_lens).to(self.device)
         self.total_q = int(self.q_lens.sum())
+        self._last_run_saw_tree = False
 
     def run(self, q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor, out: torch.Tensor,
             lse: torch.Tensor | None = None, sm_scale: float = SM_SCALE, kv_scale: float = 1.0,
@@ -110,6 +111,7 @@ class VerifyDecoder:
                       (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(),
                       sm_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
                       _ptr(status), stream_handle(index, stream))
+            self._last_run_saw_tree = False
             return
         st = stream if stream is not None else torch.cuda.current_stream(self.device)
         binding.run(self.plan_dev.data_ptr(), self.plan_host, q.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
@@ -118,6 +120,7 @@ class VerifyDecoder:
                     (q_lens_dev if q_lens_dev is not None else self.q_lens_dev).data_ptr(),
                     sm_scale, kv_scale, out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes,
                     _ptr(status), st.cuda_stream)
+        self._last_run_saw_tree = False
 
     def _run_tree(self, q, kv_cache, page_table, out, lse, sm_scale, kv_scale, status, stream, seq_lens_dev, q_lens_dev,
                   kv_scales, tree_masks) -> None:
@@ -155,6 +158,7 @@ class VerifyDecoder:
                   seq_lens_dev.data_ptr(), q_lens_dev.data_ptr(), tree_masks.data_ptr(), words, sm_scale, kv_scale,
                   out.data_ptr(), _ptr(lse), _ptr(self.workspace), self.workspace_bytes, _ptr(status),
                   stream_handle(index, stream))
+        self._last_run_saw_tree = True
 
     def key_weights(self, q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor, lse: torch.Tensor,
                     weights: torch.Tensor, decay: float = 1.0, counted: torch.Tensor | None = None,
@@ -165,9 +169,18 @@ class VerifyDecoder:
         ``lse`` that ``run`` wrote. ``counted`` [batch] int32: only the first so many verify
         tokens of a request count (the accepted ones). A new token's sum starts from what
         ``weights`` holds in its place, so zero the places that an append fills. Its scratch comes from torch's allocator,
-        call by call, so calls on several streams or captured in several graphs share none."""
+        call by call, so calls on several streams or captured in several graphs share none.
+
+        The rows count as a chain: row i gives weight to every key up to its own place. So it is
+        refused after a ``run`` with ``tree_masks``, whose ``lse`` does not hold the other branches
+        of a tree. The weights of a tree's accepted path are those of the committed chain:
+        after ``cache.commit`` a decoder of the new lengths and the accepted counts takes the
+        accepted nodes' rows of q and of the tree's ``lse`` (see ``tree``)."""
         if self.device.type != "cuda":
             raise ValueError("key_weights runs on a CUDA device")
+        if self._last_run_saw_tree:
+            raise ValueError("the last run took tree_masks: its lse holds what a tree's rows see, and key_weights counts a chain's "
+                             "rows; call it on the committed chain")
         H, batch, index = self.num_heads, self.seq_lens.shape[0], self.device.index
         check_tensor("q", q, torch.bfloat16, (self.total_q, H, 576), index)
         if kv_cache.shape[-1:] != (576,) or kv_cache.numel() % (64 * 576):

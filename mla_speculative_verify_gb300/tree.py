@@ -12,6 +12,9 @@ they can be captured in a CUDA graph. A step of a server:
     tree.verify(logits, tokens, parents, cu_nodes, path, out_tokens, accepted, ...)
     cache.commit(kv_of_all_layers, page_table, seq_lens, cu_nodes, path, accepted, new_lens, scales)
 
+The keys' weights, where an eviction goes by them, are taken after the commit: ``VerifyDecoder(new_lens,
+accepted, ..).key_weights`` with the accepted nodes' rows of q and of the tree's lse, each layer.
+
 Device-side faults (a parent that is not before its node, nodes that do not fit) are OR-ed into
 ``status``, an int32 tensor, as ``binding.MLA_DEVICE_*`` bits.
 """
