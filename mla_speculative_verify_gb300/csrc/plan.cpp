@@ -416,6 +416,13 @@ int check_plan(const void* plan_host, size_t plan_bytes, const PlanHeader** out)
     return set_error(MLA_ERR_PLAN, "plan bytes were not written by this library version");
   if ((size_t)h->total_bytes != plan_bytes)
     return set_error(MLA_ERR_PLAN, "plan_bytes %zu differs from the plan's size %d", plan_bytes, h->total_bytes);
+  // what chooses the kernel and its tiles
+  const auto flag = [](int32_t v) { return v == 0 || v == 1; };
+  const int cap = h->wide ? wide_rows_cap() : h->cta_pair ? pair_rows_cap() : rows_cap_for(h->kv_dtype);
+  if (!flag(h->wide) || !flag(h->tree) || !flag(h->cta_pair) || (h->wide && !h->tree) || (h->cta_pair && h->tree) ||
+      (h->cta_pair && h->kv_dtype != MLA_KV_BF16) || h->rows_cap < 1 || h->rows_cap > cap)
+    return set_error(MLA_ERR_PLAN, "the plan's header contradicts itself (wide %d, tree %d, cta_pair %d, kv_dtype %d, row tiles of %d)",
+                     h->wide, h->tree, h->cta_pair, h->kv_dtype, h->rows_cap);
   *out = h;
   return MLA_OK;
 }

@@ -8,7 +8,7 @@
 namespace mla {
 
 constexpr uint32_t kPlanMagic = 0x564C4D41u;  // "AMLV"
-constexpr uint32_t kPlanVersion = 5;
+constexpr uint32_t kPlanVersion = 6;  // 6: the fields `wide` and `tree`, which 5 took for reserved ones
 constexpr int kDqk = 576;
 constexpr int kDv = 512;
 constexpr int kPage = 64;
