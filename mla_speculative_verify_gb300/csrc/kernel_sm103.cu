@@ -1085,12 +1085,14 @@ __global__ void __launch_bounds__(Roles<kFp8>::kThreads, 1)
 // ------------------------------------------------------------------ LSE merge
 // One CTA per (packed row, slice of the 512 value columns: SL = 4 slices of 128 columns, or
 // 8 of 64 when the merge has few rows, so that more SMs share its loads): its W warps (4, 8
-// or 16, enough for all splits at kMergeBatch loads per lane) share the splits of the row;
-// fewer warps per CTA let more CTAs share an SM. L = ln sum_s exp(L_s),
+// or 16: enough for all splits of bf16 partials at kMergeBatch loads per lane) share the splits
+// of the row; fewer warps per CTA let more CTAs share an SM. L = ln sum_s exp(L_s),
 // O = sum_s exp(L_s - L) O_s.
 constexpr int kMergeThreads = 512;
 constexpr int kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeBatch = 10;  // partial-O loads in flight per lane (16 warps x 10 = 160 splits per round trip)
+// bf16 partial-O loads in flight per lane (16 warps x 10 = 160 splits per round trip). Of the trees'
+// fp32 partials, which take twice the registers, half as many: their splits may take two round trips.
+constexpr int kMergeBatch = 10;
 constexpr int kMergeMaxSplits = 2048;
 constexpr long long kMergeWideSlicesMaxCtas = 200;  // 8 slices per row up to this many merge CTAs
 
@@ -1137,7 +1139,7 @@ __global__ void __launch_bounds__(32 * W, 1024 / (32 * W)) lse_merge_kernel(cons
   const P* base = part_o + (size_t)(m.part_row0 + row) * kDv + col;
   const size_t split_stride = (size_t)m.nrows * kDv;
   // Warp w folds its splits w, w + W, ... into a running (max M_w, sum l_w = sum_s e^(L_s -
-  // M_w), acc_w = sum_s e^(L_s - M_w) O_s), kMergeBatch splits per round trip (their
+  // M_w), acc_w = sum_s e^(L_s - M_w) O_s), kBatch splits per round trip (their
   // partial O and LSE loads issued together); one barrier then combines the W warps:
   // L = M + ln l, O = acc / l. A split that the row cannot see has L_s = -inf: weight 0.
   float mw = -INFINITY, lw = 0.f;
@@ -1472,7 +1474,11 @@ static int decode_run(const void* plan_dev, const void* plan_host, const PlanHea
     cfg.gridDim = small ? dim3((unsigned)((h->rows_cap * 4 + kMergeSmallWarps - 1) / kMergeSmallWarps), (unsigned)h->n_merge, 1)
                         : dim3((unsigned)(h->rows_cap * slices), (unsigned)h->n_merge, 1);
     // CTA-per-row merge: just enough warps for one round trip of loads (fewer registers per
-    // CTA, so more of them fit on an SM as the fold kernel's CTAs leave)
+    // CTA, so more of them fit on an SM as the fold kernel's CTAs leave). For fp32 partials the
+    // same numbers, two round trips: twice the warps are faster in one of four shapes measured
+    // (8 nodes, 12 heads, 2048 bf16 keys in 32 splits 10.5 -> 10.0 us) and slower in the others
+    // (4096 keys in 64 splits 11.6 -> 11.9, 29 nodes over 8192 in 22 19.5 -> 20.7, over 2^18 e4m3
+    // keys in 25 137.9 -> 139.3), whose CTAs fill the SMs.
     const int large_warps = max_ns <= 4 * kMergeBatch ? 4 : max_ns <= 8 * kMergeBatch ? 8 : kMergeWarps;
     cfg.blockDim = dim3(small ? 32 * kMergeSmallWarps : 32 * large_warps, 1, 1);
     cfg.dynamicSmemBytes = 0;
