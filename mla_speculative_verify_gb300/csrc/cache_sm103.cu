@@ -868,6 +868,7 @@ struct CommitArgs {
 template <int P, bool kScaled>
 __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
   constexpr int kGroups = kCommitThreads / P;  // rows at a time
+  static_assert(kGroups * P == kCommitThreads, "every thread has a piece");
   __shared__ int src_row[kCommitMaxPath], dst_row[kCommitMaxPath];  // cache rows, or -1
   __shared__ float s_of[kScaled ? kCommitEntries : 1], r_of[kScaled ? kCommitEntries : 1];
   __shared__ float old_ratio[kScaled ? kCommitEntries : 1];
@@ -958,7 +959,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
         for (int e = grp; e < items / m * n_old; e += kGroups) {
           const int l = e / n_old;
           const float was = old_ratio[l], now = *scale_at(l, dst_row[0]);
-          if (grp >= kGroups || was == now || !(now > 0.f)) continue;
+          if (was == now || !(now > 0.f)) continue;
           uint4* at = a.kv + (layer_rows * (size_t)(l0 + l) + (size_t)(row0 + e % n_old)) * P + piece;
           const Rescale to(was / now);
           const uint4 v = *at;
@@ -985,7 +986,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
 #pragma unroll
       for (int d = 0; d < kCommitDeep; ++d) {
         to[d] = nullptr;
-        if (grp < kGroups && e < items) {
+        if (e < items) {
           const int src = src_row[i], dst = dst_row[i];
           if (src >= 0 && dst >= 0) {
             v[d] = layer[(long long)src * P];
