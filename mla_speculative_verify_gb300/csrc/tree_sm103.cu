@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kMaskThreads) tree_masks_kernel(MaskArgs a) {
 // search in r's running sum, where a border is nearer than fp32's sums are exact.
 //   What bounds it: few requests, the ~3 us that a node takes from its row's first load to the cluster's
 // decision, one node after the other (32 trees of up to 32 nodes over 131072 bf16 logits 27 us); many,
-// the issue of the pass's instructions, 64 % of the slots, at 4.1 TB/s (256 chains of 5 with both
-// distributions 145 us, where HBM would take 83).
+// the issue of the pass's instructions, 64 % of the slots, at 3.9 TB/s of the rows that are visited (256
+// chains of 5 with both distributions over 131072 tokens 145 us, where HBM would take 83).
 constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerMaxCluster = 16;
@@ -854,9 +854,10 @@ extern "C" int mla_tree_verify(int logits_dtype, const void* target_logits, long
                path_stride, tokens, parents, cu_nodes, temperature, uniforms, noise, path, out_tokens, accepted, status_dev};
   const bool draft = draft_logits != nullptr;
   // CTAs to a request, a power of two up to 16: as many as four to an SM, with three groups of eight to
-  // two threads at least; more where each then still has six to a thread. (131072 tokens, drafts:
-  // 64 requests 107, 68, 53, 63 us with 2, 4, 8, 16 CTAs; 256 requests 178, 150, 145, 195; 32000 tokens, 256
-  // requests 56, 61, 78, 146; without drafts, 32 requests 24, 19, 19, 22.)
+  // two threads at least; more where each then still has six to a thread. (us with 2, 4, 8, 16 CTAs, the
+  // rule's choice in brackets; bf16. Drafts, 131072 tokens: 64 requests 104, 66, [50], 60; 256 requests 155,
+  // 143, [142], 190; 32000 tokens, 256 requests [54], 58, 75, 141. Without drafts, 131072 tokens: 32 requests
+  // 51, 33, 26, [25]; 64 requests 53, 37, [29], 39; 32000 tokens, 32 requests 21, 17, [17], 18.)
   int c = 1;
   while (c < kVerMaxCluster) {
     const long long each = vocab / (8LL * 2 * c);  // groups
