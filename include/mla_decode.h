@@ -58,7 +58,8 @@ typedef enum {
   MLA_ERR_UNSUPPORTED = -2,   /* H outside [1, 128], page size other than 64, no sm_103 device */
   MLA_ERR_BUFFER = -3,        /* plan buffer or workspace too small */
   MLA_ERR_CUDA = -4,          /* a CUDA runtime/driver call failed */
-  MLA_ERR_PLAN = -5           /* plan bytes do not describe a plan of this library */
+  MLA_ERR_PLAN = -5,          /* plan bytes do not describe a plan of this library */
+  MLA_ERR_MEMORY = -6         /* the host has no memory for a plan */
 } mla_status;
 
 typedef enum { MLA_KV_BF16 = 0, MLA_KV_FP8_E4M3 = 1 } mla_kv_dtype;

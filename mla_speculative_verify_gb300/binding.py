@@ -21,6 +21,7 @@ MLA_ERR_UNSUPPORTED = -2
 MLA_ERR_BUFFER = -3
 MLA_ERR_CUDA = -4
 MLA_ERR_PLAN = -5
+MLA_ERR_MEMORY = -6
 MLA_KV_BF16 = 0
 MLA_KV_FP8_E4M3 = 1
 MLA_DEVICE_WAIT_TIMEOUT = 0x1

@@ -15,6 +15,7 @@
 //      merge kernel combines.
 #include <algorithm>
 #include <cmath>
+#include <exception>
 #include <functional>
 #include <queue>
 #include <cstdio>
@@ -212,10 +213,9 @@ Partition cut_batch(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batc
 using namespace mla;
 
 // mla_decode_plan_ex, and with whole_requests mla_decode_plan_tree: a fold group is all of a request's tokens.
-static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads, int page_size,
-                     int kv_dtype, int num_sms, const mla_plan_options* opts, bool whole_requests, void* plan_buf,
-                     size_t plan_buf_bytes, size_t* plan_bytes_out, size_t* workspace_bytes_out) {
-  clear_error();
+static int plan_batch(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads, int page_size,
+                      int kv_dtype, int num_sms, const mla_plan_options* opts, bool whole_requests, void* plan_buf,
+                      size_t plan_buf_bytes, size_t* plan_bytes_out, size_t* workspace_bytes_out) {
   if (!seq_lens_h || !q_lens_h) return set_error(MLA_ERR_INVALID_ARG, "seq_lens_h and q_lens_h must not be NULL");
   if (batch < 1) return set_error(MLA_ERR_INVALID_ARG, "batch must be >= 1 (got %d)", batch);
   if (num_heads < 1 || num_heads > MLA_MAX_HEADS)
@@ -379,6 +379,17 @@ static int make_plan(const int32_t* seq_lens_h, const int32_t* q_lens_h, int bat
   if (!units.empty()) memcpy(base + units_off, units.data(), sizeof(PlanUnit) * units.size());
   if (!merges.empty()) memcpy(base + merge_off, merges.data(), sizeof(PlanMerge) * merges.size());
   return MLA_OK;
+}
+
+// No exception leaves a C entry: the planner's vectors throw where the host has no memory for them.
+template <typename... Args>
+static int make_plan(Args... args) {
+  clear_error();
+  try {
+    return plan_batch(args...);
+  } catch (const std::exception& e) {
+    return set_error(MLA_ERR_MEMORY, "no host memory for the plan (%s)", e.what());
+  }
 }
 
 extern "C" int mla_decode_plan_ex(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads,
