@@ -80,11 +80,11 @@ struct Partition {
   std::vector<RowTile> tiles;
   std::vector<PlanRequest> reqs;
   std::vector<Group> groups;
-  double end_us;  // when the model's last unit ends
+  double end_us;  // when the model's last unit ends (known where the pieces are searched for, or if `compared`)
 };
 
 Partition cut_batch(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batch, int num_heads, bool fp8,
-                    const mla_plan_options& o, const Geometry& geo) {
+                    const mla_plan_options& o, const Geometry& geo, bool compared) {
   Partition out;
   std::vector<RowTile>& tiles = out.tiles;
   std::vector<PlanRequest>& reqs = out.reqs;
@@ -174,7 +174,7 @@ Partition cut_batch(const int32_t* seq_lens_h, const int32_t* q_lens_h, int batc
   if (o.unit_pages > 0) best_T = o.unit_pages;
   double best_end = -1;
   if (o.force_splits > 0 || o.unit_pages > 0) {
-    best_end = end_of(best_T);
+    if (compared) best_end = end_of(best_T);
   } else {
     // candidates: the per-SM share divided by 1, 1.25, ... 8, and the longest group's
     // pages divided into 1 .. 64 equal pieces
@@ -289,17 +289,18 @@ static int plan_batch(const int32_t* seq_lens_h, const int32_t* q_lens_h, int ba
     broad.min_pages = asked > 0 ? asked : 2;
     broad.start_cost = 24.0;
     broad.page_us = fp8 ? 0.72 : 0.65;
-    if (force_wide || o.max_rows_per_cta == 0) part = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, geo = broad);
+    const bool compared = o.max_rows_per_cta == 0;  // of both tiles, not the one that is asked for
+    if (force_wide || compared) part = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, geo = broad, compared);
     if (!force_wide) {
-      Partition other = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, narrow);
-      wide = o.max_rows_per_cta == 0 && part.end_us < other.end_us;
+      Partition other = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, narrow, compared);
+      wide = compared && part.end_us < other.end_us;
       if (!wide) {
         part = std::move(other);
         geo = narrow;
       }
     }
   } else {
-    part = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, geo);
+    part = cut_batch(seq_lens_h, q_lens_h, batch, num_heads, fp8, o, geo, false);
   }
   const std::vector<RowTile>& tiles = part.tiles;
   const std::vector<PlanRequest>& reqs = part.reqs;
