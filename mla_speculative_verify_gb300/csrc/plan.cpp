@@ -307,6 +307,12 @@ static int plan_batch(const int32_t* seq_lens_h, const int32_t* q_lens_h, int ba
   const std::vector<Group>& groups = part.groups;
   const int slots = geo.slots;
 
+  long long all_part_rows = 0;
+  for (const Group& g : groups)
+    if (g.n_split > 1)
+      for (size_t t = g.t0; t < g.t1; ++t) all_part_rows += (long long)g.n_split * tiles[t].nrows;
+  if (all_part_rows > INT32_MAX) return set_error(MLA_ERR_INVALID_ARG, "too many partial rows: fewer splits are needed");
+
   std::vector<PlanUnit> units;
   std::vector<PlanMerge> merges;
   int part_rows = 0;
