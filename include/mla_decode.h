@@ -105,7 +105,7 @@ typedef struct {
  * row tiles, and cuts each row tile's key range [0, seq_len) into page-aligned
  * splits so that the units fill the num_sms SMs.
  *
- *   seq_lens_h, q_lens_h : host int32 [batch]
+ *   seq_lens_h, q_lens_h : host int32 [batch], 1 <= q_len <= seq_len <= 2^30
  *   num_heads            : H, 1..128
  *   page_size            : must be 64
  *   kv_dtype             : MLA_KV_BF16 or MLA_KV_FP8_E4M3

@@ -57,6 +57,8 @@ size_t workspace_bytes_for(int n_part_rows, bool tree) {
 
 namespace {
 
+constexpr int kMaxKeys = 1 << 30;  // of a request
+
 struct RowTile { int b, qrow0, nrows, pages; };
 // tiles [t0, t1) of one fold group: consecutive, same request, qrow0 contiguous
 struct Group { size_t t0, t1; int b, pages, n_split, cap; };  // cap: piece length in pages (0: equal pieces)
@@ -248,6 +250,8 @@ static int plan_batch(const int32_t* seq_lens_h, const int32_t* q_lens_h, int ba
     int ctx = seq_lens_h[b], q = q_lens_h[b];
     if (q < 1) return set_error(MLA_ERR_INVALID_ARG, "q_lens[%d] = %d must be >= 1", b, q);
     if (ctx < q) return set_error(MLA_ERR_INVALID_ARG, "seq_lens[%d] = %d is smaller than q_lens[%d] = %d", b, ctx, b, q);
+    // (the kernels count keys in 32 bits, some tiles ahead)
+    if (ctx > kMaxKeys) return set_error(MLA_ERR_INVALID_ARG, "seq_lens[%d] = %d must be <= %d", b, ctx, kMaxKeys);
     if (o.force_fold > 0 && q % o.force_fold != 0)
       return set_error(MLA_ERR_INVALID_ARG, "force_fold %d does not divide q_lens[%d] = %d", o.force_fold, b, q);
     total_q += q;
