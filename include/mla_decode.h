@@ -373,7 +373,8 @@ int mla_cache_evict_workspace(int batch, int max_seq, size_t* workspace_bytes_ou
  *           the root plus this)
  *
  * Rows of requests that do not fit, and of nodes in none, are left as they are. Enqueue only, as
- * mla_decode_run. masks and depths must not overlap the other arrays (refused).
+ * mla_decode_run. masks and depths must not overlap the other arrays (refused). With max_nodes or
+ * total_nodes 0 nothing is launched, and so nothing reported.
  */
 int mla_tree_masks(const int32_t* parents, const int32_t* cu_nodes, int batch, int total_nodes, int max_nodes,
                    uint32_t* masks, int mask_words, int32_t* depths, int32_t* status_dev, void* stream);
@@ -443,6 +444,9 @@ int mla_decode_run_tree(const void* plan_dev, const void* plan_host, size_t plan
  * give equal results; one that hangs on less than about 1e-6 of a probability may fall either way.
  * path, out_tokens and accepted must not overlap one another or the inputs (refused), and the
  * inputs must not change while the call runs. Enqueue only, as mla_decode_run.
+ *
+ * Rows may start anywhere. What costs time is a row of draft_logits that starts elsewhere between
+ * 16-byte boundaries than the target's (its loads are of single elements): give both the same stride.
  */
 typedef enum { MLA_LOGITS_BF16 = 0, MLA_LOGITS_FP32 = 1 } mla_logits_dtype;
 int mla_tree_verify(int logits_dtype, const void* target_logits, long long target_stride, const void* draft_logits,

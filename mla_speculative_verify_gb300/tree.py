@@ -12,6 +12,10 @@ they can be captured in a CUDA graph. A step of a server:
     tree.verify(logits, tokens, parents, cu_nodes, path, out_tokens, accepted, ...)
     cache.commit(kv_of_all_layers, page_table, seq_lens, cu_nodes, path, accepted, new_lens, scales)
 
+A plan is made on the host (0.06 to 2.4 ms, by the batch) for exact lengths: a decoder serves all layers of a
+step, the next step needs a new one, and a captured step is good for its lengths alone. Lengths after a
+commit are on the device, so a copy to the host comes before the plan.
+
 The keys' weights, where an eviction goes by them, are taken after the commit: ``VerifyDecoder(new_lens,
 accepted, ..).key_weights`` with the accepted nodes' rows of q and of the tree's lse, each layer.
 
@@ -84,7 +88,8 @@ def verify(logits: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor, cu
     were drawn from; without it the draft counts as certain. ``temperature`` [batch] fp32 (default
     1) divides both; 0 is greedy. ``uniforms`` [total] in [0, 1) decide on the nodes, ``noise``
     [batch, vocab], exponentially distributed, draws the next token; without both all requests are
-    greedy.
+    greedy. Rows of ``logits`` and ``draft_logits`` are best equally far apart: where they start
+    differently between 16-byte boundaries, verification takes up to 1.7 times as long.
 
     Written: ``path`` [batch, width] int32, the accepted nodes from the root on, then -1;
     ``out_tokens`` [batch, width], the token behind each of them, the new one last, then -1;
